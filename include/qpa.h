@@ -43,6 +43,7 @@ extern "C" {
 #define QPA_ERR_WORKSPACE (-4)   /* workspace smaller than *_workspace_size() */
 #define QPA_ERR_PARTITIONS (-5)  /* num_partitions < 1 */
 #define QPA_ERR_CUDA (-6)        /* the CUDA runtime rejected a launch */
+#define QPA_ERR_OVERLAP (-7)     /* an output overlaps an input it may not overlap */
 
 #define QPA_OUT_F32 0
 #define QPA_OUT_BF16 1
@@ -59,7 +60,8 @@ int qpa_version(void);
  * after its time limit; 3: an invalid block id was met; 4: the fp8 work split
  * produced an out-of-range slot, which its own bounds rule out; 5: a value
  * outside what the hd256 kernel represents, see QPA_UQ_UE8M0_SCALES and the
- * centroid table). Returns QPA_ERR_CUDA
+ * centroid table; 6: paged_slot_map ran out of free blocks or of table
+ * columns). Returns QPA_ERR_CUDA
  * if the synchronisation fails. Diagnostic only; the decode entry points
  * never call it. */
 int qpa_kernel_error(void* stream);
@@ -411,6 +413,157 @@ int nvfp4_index_score(const uint8_t* q, const uint8_t* kv_pages, const int32_t* 
 int pa_decode_fp8_static(const void* q, const uint8_t* kv_cache, const int32_t* block_table,
                          const int32_t* seq_lens, const float* k_scale, const float* v_scale,
                          int num_partitions, void* out, const qpa_fp8_desc* d, void* stream);
+
+/* ========================================================================
+ * paged_slot_map -- the block table, slots and lengths of a step, from the
+ * requests' lengths
+ *
+ * Request r holds c = cached_lens[r] tokens in the cache and brings
+ * n = new_lens[r] new ones (negative values count as 0). One kernel writes
+ *   query_start [num_reqs+1]  the exclusive running sum of n (the first row of
+ *                             each request among the step's new tokens; the
+ *                             last entry is their number)
+ *   seq_lens    [num_reqs]    c + n
+ *   block_table               row r, columns ceil(c/block_size) up to
+ *                             ceil((c+n)/block_size): the next ids of
+ *                             free_blocks, in request order; every other
+ *                             entry is left as it was
+ *   slots       [max_tokens]  of new token i of request r, at position
+ *                             pos = c + i: block_table[r][pos / block_size] *
+ *                             block_size + pos % block_size; -1 for the rows
+ *                             behind the last token
+ *   positions   [max_tokens]  pos; 0 behind the last token
+ *   num_taken   [1]           ids taken from free_blocks
+ * query_start and seq_lens saturate at INT32_MAX. Tokens from the max_tokens-th
+ * on get no slot (query_start still counts them).
+ * A request that needs a column past max_blocks_per_seq, or an id past
+ * num_free, gets slot -1 for the tokens of the missing block (its table entry,
+ * if it has one, is left as it was) and the kernel raises error word 6;
+ * num_taken counts the ids that were needed, so num_taken > num_free says how
+ * many were short. A negative block id (in the table or the free list) gives
+ * slot -1 and error word 3. The call may be captured; repeated on the same
+ * inputs it gives the same result.
+ * The table rows that serve requests not in the batch are not touched. No
+ * output may overlap an input other than block_table itself
+ * (QPA_ERR_OVERLAP); cached_lens stays as it was, so a server passes seq_lens
+ * as the next step's cached_lens.
+ * Supported: num_reqs 0..16384, block_size 16/32/64/128/256, max_tokens >= 0,
+ * num_free >= 0. block_table row r starts at r * table_stride elements.
+ * Alignment: slots 8 bytes, the others 4 bytes.
+ * ====================================================================== */
+typedef struct qpa_slot_desc {
+  int32_t num_reqs;
+  int32_t block_size;
+  int32_t max_blocks_per_seq;
+  int32_t num_free;             /* ids in free_blocks */
+  int32_t max_tokens;           /* rows of slots and positions */
+  int32_t reserved;             /* 0 */
+  int64_t table_stride;         /* elements; 0 = max_blocks_per_seq */
+} qpa_slot_desc;
+
+int paged_slot_map(const int32_t* new_lens, const int32_t* cached_lens, int32_t* block_table,
+                   const int32_t* free_blocks, int32_t* query_start, int32_t* seq_lens, int64_t* slots,
+                   int32_t* positions, int32_t* num_taken, const qpa_slot_desc* d, void* stream);
+
+/* ========================================================================
+ * kv_append_fp8 -- new keys and values quantised into the paged cache
+ *
+ * For every row t with slots[t] >= 0, KV head h and dim d (slot = block *
+ * block_size + offset):
+ *     kv_cache[block][0][h][offset][d] = e4m3(k[t][h][d] / ks)
+ *     kv_cache[block][1][h][offset][d] = e4m3(v[t][h][d] / vs)
+ * where e4m3() is the nearest e4m3fn value of the exact quotient, ties to
+ * even, saturating at +-448 (NaN gives the code 0x7F, +-inf saturates), and
+ *   kv_scale_per_token = 0: ks = k_scale[0], vs = v_scale[0], read;
+ *   kv_scale_per_token = 1: ks, vs are computed per (row, head),
+ *       max(a / 448, 2^-126) in float32 with a the largest |x| of the head's
+ *       vector (NaN ignored, infinities as the largest bf16), and written to
+ *       k_scale / v_scale [num_blocks][num_kv_heads][block_size] at the slot:
+ *       the layout pa_decode_fp8_ext and pa_chunk_fp8 read.
+ * Rows with a negative slot (padding) are skipped; a slot at or past
+ * num_blocks * block_size is skipped and raises error word 3. Nothing else in
+ * the cache is written. Rows that share a slot: which one's bytes and scales
+ * end there is not defined. Scales are meant to be positive and finite; other
+ * values follow IEEE division.
+ *
+ * Layouts: k, v bf16 [num_tokens][num_kv_heads][head_dim] with the strides of
+ * the descriptor (elements, multiples of 8; slices of a fused QKV projection
+ * can be passed directly); kv_cache uint8 [num_blocks][2][num_kv_heads]
+ * [block_size][head_dim]; slots int64 [num_tokens] (as paged_slot_map writes).
+ * Supported: head_dim 64 or 128, block_size 16/32/64/128/256.
+ * Alignment: k, v and kv_cache 16 bytes, slots 8, scales 4 bytes.
+ * ====================================================================== */
+typedef struct qpa_append_desc {
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t kv_scale_per_token;   /* 0 = per-tensor (read), 1 = per-token (computed, written) */
+  int64_t k_stride_tok;         /* elements; 0 = num_kv_heads*head_dim */
+  int64_t k_stride_head;        /* elements; 0 = head_dim */
+  int64_t v_stride_tok;
+  int64_t v_stride_head;
+} qpa_append_desc;
+
+int kv_append_fp8(const void* k, const void* v, uint8_t* kv_cache, const int64_t* slots, float* k_scale,
+                  float* v_scale, const qpa_append_desc* d, void* stream);
+
+/* ========================================================================
+ * pa_chunk_fp8 -- attention of a chunk of new tokens per request over the
+ * fp8 paged cache (prompts, chunked prompts, and single tokens beside them)
+ *
+ * Request r owns the query rows query_start[r] .. query_start[r+1] - 1 (n of
+ * them) and L = seq_lens[r] cached tokens, which count the n new ones (their
+ * keys and values are in the cache already). Row i of the request, KV head h,
+ * group row g (query head h*query_group + g):
+ *     out = sum_t softmax_t(softmax_scale * q . k_t) v_t,   t = 0 .. L - n + i,
+ * with k_t and v_t as in pa_decode_fp8_ext (per-tensor or per-token scales). A
+ * row that sees no token (L - n + i < 0) gives 0; rows of `out` outside every
+ * request's range are left as they were. Codes and scales of tokens that a
+ * row does not see have no influence on it, NaN codes included.
+ * Precision: each query row, scaled by a power of two, enters the tensor core
+ * as 2 e4m3 terms (exact down to 2^-10 of the row's largest |q|, within 2^-18
+ * of it below), K and V exactly; the probabilities enter as f16 (times the
+ * token's V scale over the power of two of the largest scale so far, with
+ * per-token scales); sums and softmax statistics are float32. The output is
+ * bf16 only: probabilities of 11 bits would leave the rest of a float32
+ * output without meaning.
+ *
+ * Layouts: q bf16 [num_tokens][num_kv_heads*query_group][head_dim] with the
+ * descriptor's strides (elements, multiples of 8); out bf16, contiguous;
+ * kv_cache, k_scale, v_scale as for pa_decode_fp8_ext; block_table int32, row
+ * r at r * table_stride elements, only entries below ceil(L/block_size) are
+ * read; query_start int32 [num_reqs+1], its values clamped to [0, num_tokens];
+ * seq_lens int32 [num_reqs], clamped to [0, max_blocks_per_seq*block_size].
+ * workspace: pa_chunk_fp8_workspace_size() bytes, 256-byte aligned, no
+ * initialisation; calls that may overlap need a workspace each.
+ * Supported: head_dim 64 or 128, query_group 1..64, block_size
+ * 16/32/64/128/256. Alignment: q, kv_cache, out 16 bytes; per-token scales 16.
+ * Errors as pa_decode_fp8; an invalid block id reads block 0 and raises error
+ * word 3.
+ * ====================================================================== */
+typedef struct qpa_chunk_desc {
+  int32_t num_reqs;
+  int32_t num_tokens;           /* rows of q and out */
+  int32_t num_kv_heads;
+  int32_t query_group;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t max_blocks_per_seq;
+  int32_t kv_scale_per_token;   /* 0 = per-tensor, 1 = per-token */
+  float softmax_scale;          /* 0 = 1/sqrt(head_dim) */
+  int64_t q_stride_tok;         /* elements; 0 = num_kv_heads*query_group*head_dim */
+  int64_t q_stride_head;        /* elements; 0 = head_dim */
+  int64_t table_stride;         /* elements; 0 = max_blocks_per_seq */
+} qpa_chunk_desc;
+
+size_t pa_chunk_fp8_workspace_size(const qpa_chunk_desc* d);
+
+int pa_chunk_fp8(const void* q, const uint8_t* kv_cache, const int32_t* block_table, const int32_t* query_start,
+                 const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* out,
+                 const qpa_chunk_desc* d, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

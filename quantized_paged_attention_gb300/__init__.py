@@ -25,6 +25,7 @@ QPA_UQ_ROT_PERM = 4
 QPA_IDX_PER_TOKEN = 1
 QPA_IDX_SHARED_PAGES = 2
 QPA_TEST_WITHHOLD_ARRIVAL = 1
+SLOT_MAP_MAX_REQS = 16384
 _lib = None
 
 
@@ -69,6 +70,29 @@ class IdxDesc(ctypes.Structure):
                 ("s_stride_row", ctypes.c_int64)]
 
 
+class SlotDesc(ctypes.Structure):
+    _fields_ = [("num_reqs", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("max_blocks_per_seq", ctypes.c_int32), ("num_free", ctypes.c_int32),
+                ("max_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32), ("table_stride", ctypes.c_int64)]
+
+
+class AppendDesc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("kv_scale_per_token", ctypes.c_int32), ("k_stride_tok", ctypes.c_int64),
+                ("k_stride_head", ctypes.c_int64), ("v_stride_tok", ctypes.c_int64),
+                ("v_stride_head", ctypes.c_int64)]
+
+
+class ChunkDesc(ctypes.Structure):
+    _fields_ = [("num_reqs", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("query_group", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+                ("kv_scale_per_token", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("q_stride_tok", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _SIGS = {
     "qpa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -94,6 +118,11 @@ _SIGS = {
     "uq_decode_hd256_combine": (ctypes.c_int, [ctypes.c_int, _P, ctypes.POINTER(UqDesc), _P,
                                                ctypes.c_size_t, _P]),
     "nvfp4_index_score": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.POINTER(IdxDesc), _P]),
+    "paged_slot_map": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(SlotDesc), _P]),
+    "kv_append_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.POINTER(AppendDesc), _P]),
+    "pa_chunk_fp8_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(ChunkDesc)]),
+    "pa_chunk_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(ChunkDesc), _P,
+                                    ctypes.c_size_t, _P]),
 }
 
 
@@ -385,3 +414,190 @@ def nvfp4_index_score(q_codes, pages, block_table, seq_lens, query_len: int, num
                                ctypes.byref(desc), _stream(stream))
     _check("nvfp4_index_score", st)
     return scores
+
+
+# --------------------------------------------------------------------- serving step
+def _need(cond, msg):
+    if not cond:
+        raise ValueError(msg)
+
+
+def _need_all(dtype, dense, **ts):
+    """Each tensor: the dtype and, with dense, contiguous."""
+    for name, t in ts.items():
+        _need(t.dtype == dtype, f"{name} must be {dtype}, is {t.dtype}")
+        _need(not dense or t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _same_device(*ts):
+    _need_cuda(*ts)
+    _need(len({t.device for t in ts if t is not None}) == 1, "all tensors must be on one device")
+
+
+def _rows(block_table):
+    _need(block_table.dim() == 2, "block_table must be [num_reqs, max_blocks]")
+    R, maxb = block_table.shape
+    _need(R == 0 or maxb <= 1 or block_table.stride(1) == 1, "block_table must have contiguous rows")
+    _need(R <= 1 or block_table.stride(0) >= maxb, "block_table rows must not overlap")
+    return maxb, block_table.stride(0) if R > 1 else 0
+
+
+def _launch(fn, device, stream, *args):
+    """Call an entry point on `stream` (default: the device's current stream)
+    with the tensors' device current."""
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        _need(stream.device == device, "the stream must belong to the tensors' device")
+        _check(fn, getattr(load_library(), fn)(*args, ctypes.c_void_p(stream.cuda_stream)))
+
+
+def paged_slot_map(new_lens, cached_lens, block_table, free_blocks, block_size: int, max_tokens: int,
+                   query_start=None, seq_lens=None, slots=None, positions=None, num_taken=None, stream=None):
+    """Block table, slots and lengths of a step from the requests' lengths.
+
+    new_lens, cached_lens int32 [R] (R <= 16384); block_table int32
+    [R, max_blocks], rows contiguous, extended in place; free_blocks int32 [F]:
+    ids are taken from its front. Returns (query_start int32 [R+1], seq_lens
+    int32 [R], slots int64 [max_tokens], positions int32 [max_tokens],
+    num_taken int32 [1]), written into the tensors passed for them if any
+    (a captured graph keeps its own)."""
+    dev = new_lens.device
+    _need_all(torch.int32, True, new_lens=new_lens, cached_lens=cached_lens, free_blocks=free_blocks)
+    _need_all(torch.int32, False, block_table=block_table)
+    R = new_lens.numel()
+    maxb, stride = _rows(block_table)
+    _need(cached_lens.numel() == R and block_table.shape[0] == R,
+          "new_lens, cached_lens and block_table must have one entry per request")
+
+    def outp(t, n, dtype, name):
+        if t is None:
+            return torch.empty(n, dtype=dtype, device=dev)
+        _need_all(dtype, True, **{name: t})
+        _need(t.numel() == n, f"{name} must have {n} elements")
+        return t
+
+    query_start = outp(query_start, R + 1, torch.int32, "query_start")
+    seq_lens = outp(seq_lens, R, torch.int32, "seq_lens")
+    slots = outp(slots, max_tokens, torch.int64, "slots")
+    positions = outp(positions, max_tokens, torch.int32, "positions")
+    num_taken = outp(num_taken, 1, torch.int32, "num_taken")
+    _same_device(new_lens, cached_lens, block_table, free_blocks, query_start, seq_lens, slots, positions, num_taken)
+    d = SlotDesc()
+    d.num_reqs, d.block_size, d.max_blocks_per_seq = R, block_size, maxb
+    d.num_free, d.max_tokens, d.table_stride = free_blocks.numel(), max_tokens, stride
+    _launch("paged_slot_map", dev, stream, _ptr(new_lens), _ptr(cached_lens), _ptr(block_table), _ptr(free_blocks),
+            _ptr(query_start), _ptr(seq_lens), _ptr(slots), _ptr(positions), _ptr(num_taken), ctypes.byref(d))
+    return query_start, seq_lens, slots, positions, num_taken
+
+
+def _per_token_scales(kv_cache, k_scale, v_scale):
+    """True for [num_blocks, Hk, bs] scale tensors, False for one value each."""
+    _need_all(torch.float32, True, k_scale=k_scale, v_scale=v_scale)
+    NB, _, Hk, bs, _ = kv_cache.shape
+    if k_scale.dim() == 3:
+        _need(tuple(k_scale.shape) == (NB, Hk, bs) and tuple(v_scale.shape) == (NB, Hk, bs),
+              "per-token scales must be [num_blocks, num_kv_heads, block_size]")
+        return True
+    _need(k_scale.numel() == 1 and v_scale.numel() == 1, "per-tensor scales must have one element")
+    return False
+
+
+def _need_cache(kv_cache):
+    _need(kv_cache.dim() == 5 and kv_cache.shape[1] == 2, "kv_cache must be [num_blocks, 2, Hk, block_size, head_dim]")
+    _need_all(torch.uint8, True, kv_cache=kv_cache)
+
+
+def kv_append_fp8(k, v, kv_cache, slots, k_scale, v_scale, stream=None):
+    """Quantise new keys and values into the paged fp8 cache, in place.
+
+    k, v bf16 [T, Hk, D] (slices of a fused projection allowed); kv_cache uint8
+    [NB, 2, Hk, bs, D]; slots int64 [T], negative = skip the row; k_scale /
+    v_scale float32 with one element (read) or [NB, Hk, bs] (computed per token
+    and written). Returns kv_cache."""
+    _need_cache(kv_cache)
+    _need_all(torch.bfloat16, False, k=k, v=v)
+    _need_all(torch.int64, True, slots=slots)
+    NB, _, Hk, bs, D = kv_cache.shape
+    T = slots.numel()
+    _need(tuple(k.shape) == (T, Hk, D) and tuple(v.shape) == (T, Hk, D),
+          "k and v must be [num_tokens, num_kv_heads, head_dim] with a row per slot")
+    _need(T == 0 or (k.stride(2) == 1 and v.stride(2) == 1), "k and v must be contiguous along head_dim")
+    per_token = _per_token_scales(kv_cache, k_scale, v_scale)
+    _same_device(k, v, kv_cache, slots, k_scale, v_scale)
+    d = AppendDesc()
+    d.num_tokens, d.num_kv_heads, d.head_dim, d.block_size, d.num_blocks = T, Hk, D, bs, NB
+    d.kv_scale_per_token = 1 if per_token else 0
+    d.k_stride_tok, d.k_stride_head = _dim_stride(k, 0), _dim_stride(k, 1)
+    d.v_stride_tok, d.v_stride_head = _dim_stride(v, 0), _dim_stride(v, 1)
+    _launch("kv_append_fp8", k.device, stream, _ptr(k), _ptr(v), _ptr(kv_cache), _ptr(slots), _ptr(k_scale),
+            _ptr(v_scale), ctypes.byref(d))
+    return kv_cache
+
+
+def _dim_stride(t, i):
+    """Stride of dimension i for a descriptor, where 0 means contiguous: a
+    dimension of one element has no stride; an expanded one is refused."""
+    if t.shape[i] <= 1:
+        return 0
+    _need(t.stride(i) > 0, "expanded tensors are not supported")
+    return t.stride(i)
+
+
+def chunk_desc(q, kv_cache, block_table, query_group, per_token, softmax_scale=None):
+    """Descriptor of pa_chunk_fp8 for q bf16 [T, Hq, D]."""
+    _need_cache(kv_cache)
+    _need_all(torch.bfloat16, False, q=q)
+    _need_all(torch.int32, False, block_table=block_table)
+    T, Hq, D = q.shape
+    NB, _, Hk, bs, D2 = kv_cache.shape
+    _need(D2 == D and Hq == Hk * query_group, "q must be [num_tokens, num_kv_heads*query_group, head_dim]")
+    _need(T == 0 or q.stride(2) == 1, "q must be contiguous along head_dim")
+    maxb, stride = _rows(block_table)
+    d = ChunkDesc()
+    d.num_reqs, d.num_tokens, d.num_kv_heads, d.query_group = block_table.shape[0], T, Hk, query_group
+    d.head_dim, d.block_size, d.num_blocks, d.max_blocks_per_seq = D, bs, NB, maxb
+    d.kv_scale_per_token = 1 if per_token else 0
+    d.softmax_scale = 0.0 if softmax_scale is None else float(softmax_scale)
+    d.q_stride_tok, d.q_stride_head = _dim_stride(q, 0), _dim_stride(q, 1)
+    d.table_stride = stride
+    return d
+
+
+def pa_chunk_fp8_workspace_size(desc: ChunkDesc) -> int:
+    return int(load_library().pa_chunk_fp8_workspace_size(ctypes.byref(desc)))
+
+
+def pa_chunk_fp8(q, kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, query_group: int, out=None,
+                 workspace=None, softmax_scale=None, stream=None, desc=None):
+    """Attention of a chunk of new tokens per request over the paged fp8 cache.
+
+    q bf16 [T, Hq, D]; kv_cache uint8 [NB, 2, Hk, bs, D] (the new tokens are in
+    it, see kv_append_fp8); block_table int32 [R, max_blocks]; query_start int32
+    [R+1]; seq_lens int32 [R] counting the new tokens; k_scale / v_scale float32
+    with one element or [NB, Hk, bs]. Returns out bf16 [T, Hq, D]; rows outside
+    every request's range are not written. `desc` (from chunk_desc for these
+    tensors) and `workspace` may be kept between calls."""
+    per_token = _per_token_scales(kv_cache, k_scale, v_scale)
+    want = chunk_desc(q, kv_cache, block_table, query_group, per_token, softmax_scale)
+    if desc is None:
+        desc = want
+    else:
+        if softmax_scale is None:
+            want.softmax_scale = desc.softmax_scale
+        _need(bytes(desc) == bytes(want), "desc does not describe these tensors")
+    _need_all(torch.int32, True, query_start=query_start, seq_lens=seq_lens)
+    _need(query_start.numel() == desc.num_reqs + 1 and seq_lens.numel() == desc.num_reqs,
+          "query_start must have one entry more than requests, seq_lens one per request")
+    if out is None:
+        out = torch.empty(tuple(q.shape), dtype=torch.bfloat16, device=q.device)
+    else:
+        _need_all(torch.bfloat16, True, out=out)
+        _need(out.shape == q.shape, "out must have the shape of q")
+    if workspace is None:
+        workspace = alloc_workspace(pa_chunk_fp8_workspace_size(desc), q.device)
+    _same_device(q, kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, out, workspace)
+    _launch("pa_chunk_fp8", q.device, stream, _ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(query_start),
+            _ptr(seq_lens), _ptr(k_scale), _ptr(v_scale), _ptr(out), ctypes.byref(desc), _ptr(workspace),
+            workspace.numel() * workspace.element_size())
+    return out

@@ -156,6 +156,42 @@ int idx_check(const uint8_t* q, const uint8_t* pages, const int32_t* bt, const i
   return QPA_OK;
 }
 
+// ------------------------------------------------------------------ serving step
+bool block_size_ok(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128 || bs == 256; }
+
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an && bn && x < y + bn && y < x + an;
+}
+
+bool slot_shape_ok(const qpa_slot_desc* d) {
+  if (d->num_reqs < 0 || d->num_reqs > 16384 || !block_size_ok(d->block_size) || d->max_blocks_per_seq < 1) return false;
+  if (d->num_free < 0 || d->max_tokens < 0 || d->reserved != 0) return false;
+  if (d->table_stride != 0 && d->table_stride < d->max_blocks_per_seq) return false;
+  if ((long long)d->max_blocks_per_seq * d->block_size > 0x7fffffffLL) return false;
+  return true;
+}
+
+bool append_shape_ok(const qpa_append_desc* d) {
+  if (d->num_tokens < 0 || d->num_kv_heads < 1 || (d->head_dim != 64 && d->head_dim != 128)) return false;
+  if (!block_size_ok(d->block_size) || d->num_blocks < 1) return false;
+  if (d->kv_scale_per_token != 0 && d->kv_scale_per_token != 1) return false;
+  return true;
+}
+
+bool chunk_shape_ok(const qpa_chunk_desc* d) {
+  if (d->num_reqs < 0 || d->num_tokens < 0 || d->num_kv_heads < 1 || d->query_group < 1 || d->query_group > 64)
+    return false;
+  if ((d->head_dim != 64 && d->head_dim != 128) || !block_size_ok(d->block_size)) return false;
+  if (d->num_blocks < 1 || d->max_blocks_per_seq < 1) return false;
+  if (d->kv_scale_per_token != 0 && d->kv_scale_per_token != 1) return false;
+  if (d->table_stride != 0 && d->table_stride < d->max_blocks_per_seq) return false;
+  if ((long long)d->max_blocks_per_seq * d->block_size > 0x7fffffffLL) return false;
+  // the pages' rows are addressed by 32-bit tensor-map coordinates
+  if ((long long)2 * d->num_kv_heads * d->block_size > 0x7fffffffLL) return false;
+  return true;
+}
+
 }  // namespace
 }  // namespace qpa
 
@@ -172,6 +208,7 @@ const char* qpa_status_string(int s) {
     case QPA_ERR_WORKSPACE: return "workspace too small";
     case QPA_ERR_PARTITIONS: return "num_partitions must be >= 1";
     case QPA_ERR_CUDA: return "CUDA launch error";
+    case QPA_ERR_OVERLAP: return "an output overlaps an input";
     default: return "unknown status";
   }
 }
@@ -452,6 +489,135 @@ int nvfp4_index_score(const uint8_t* q, const uint8_t* kv_pages, const int32_t* 
   a.num_sms = num_sms_current();
   if (a.num_sms <= 0) return QPA_ERR_CUDA;
   return launch_idx_score(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QPA_OK : QPA_ERR_CUDA;
+}
+
+int paged_slot_map(const int32_t* new_lens, const int32_t* cached_lens, int32_t* block_table,
+                   const int32_t* free_blocks, int32_t* query_start, int32_t* seq_lens, int64_t* slots,
+                   int32_t* positions, int32_t* num_taken, const qpa_slot_desc* d, void* stream) {
+  if (!d) return QPA_ERR_NULL;
+  if (!slot_shape_ok(d)) return QPA_ERR_SHAPE;
+  const bool reqs = d->num_reqs > 0;
+  if (!query_start || !num_taken || (reqs && (!new_lens || !cached_lens || !block_table || !seq_lens)))
+    return QPA_ERR_NULL;
+  if ((d->max_tokens && (!slots || !positions)) || (d->num_free && !free_blocks)) return QPA_ERR_NULL;
+  const void* words[] = {new_lens, cached_lens, block_table, free_blocks, query_start, seq_lens, positions, num_taken};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return QPA_ERR_ALIGN;
+  if (!aligned(slots, 8)) return QPA_ERR_ALIGN;
+  SlotMapLaunch a;
+  a.table_stride = d->table_stride ? d->table_stride : d->max_blocks_per_seq;
+  // every CTA of the kernel reads the inputs, so an output written by one of
+  // them must not lie in what another still reads
+  const size_t nb = size_t(d->num_reqs) * 4, nt = size_t(d->max_tokens);
+  const size_t tb = reqs ? (size_t(d->num_reqs - 1) * a.table_stride + d->max_blocks_per_seq) * 4 : 0;
+  struct Span { const void* p; size_t n; };
+  const Span in[] = {{new_lens, nb}, {cached_lens, nb}, {free_blocks, size_t(d->num_free) * 4}, {block_table, tb}};
+  const Span outs[] = {{block_table, tb}, {query_start, nb + 4}, {seq_lens, nb}, {slots, nt * 8}, {positions, nt * 4},
+                       {num_taken, 4}};
+  for (int o = 0; o < 6; ++o) {
+    for (int i = 0; i < (o == 0 ? 3 : 4); ++i)
+      if (overlap(outs[o].p, outs[o].n, in[i].p, in[i].n)) return QPA_ERR_OVERLAP;
+    for (int i = 1; i < o; ++i)
+      if (overlap(outs[o].p, outs[o].n, outs[i].p, outs[i].n)) return QPA_ERR_OVERLAP;
+  }
+  a.new_lens = new_lens;
+  a.cached_lens = cached_lens;
+  a.block_table = block_table;
+  a.free_blocks = free_blocks;
+  a.query_start = query_start;
+  a.seq_lens = seq_lens;
+  a.slots = slots;
+  a.positions = positions;
+  a.num_taken = num_taken;
+  a.num_reqs = d->num_reqs;
+  a.block_size = d->block_size;
+  a.max_blocks = d->max_blocks_per_seq;
+  a.num_free = d->num_free;
+  a.max_tokens = d->max_tokens;
+  a.num_sms = num_sms_current();
+  if (a.num_sms <= 0) return QPA_ERR_CUDA;
+  return launch_slot_map(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QPA_OK : QPA_ERR_CUDA;
+}
+
+int kv_append_fp8(const void* k, const void* v, uint8_t* kv_cache, const int64_t* slots, float* k_scale,
+                  float* v_scale, const qpa_append_desc* d, void* stream) {
+  if (!d) return QPA_ERR_NULL;
+  if (!append_shape_ok(d)) return QPA_ERR_SHAPE;
+  if (d->num_tokens == 0) return QPA_OK;
+  if (!k || !v || !kv_cache || !slots || !k_scale || !v_scale) return QPA_ERR_NULL;
+  AppendLaunch a;
+  const long long row = (long long)d->num_kv_heads * d->head_dim;
+  a.k_stride_tok = d->k_stride_tok ? d->k_stride_tok : row;
+  a.v_stride_tok = d->v_stride_tok ? d->v_stride_tok : row;
+  a.k_stride_head = d->k_stride_head ? d->k_stride_head : d->head_dim;
+  a.v_stride_head = d->v_stride_head ? d->v_stride_head : d->head_dim;
+  for (long long s : {a.k_stride_tok, a.v_stride_tok, a.k_stride_head, a.v_stride_head})
+    if (s < 0 || s % 8) return QPA_ERR_ALIGN;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_cache, 16) || !aligned(slots, 8) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4))
+    return QPA_ERR_ALIGN;
+  a.k = k;
+  a.v = v;
+  a.kv = kv_cache;
+  a.slots = slots;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.num_tokens = d->num_tokens;
+  a.num_kv_heads = d->num_kv_heads;
+  a.head_dim = d->head_dim;
+  a.block_size = d->block_size;
+  a.num_blocks = d->num_blocks;
+  a.per_token = d->kv_scale_per_token;
+  a.num_sms = num_sms_current();
+  if (a.num_sms <= 0) return QPA_ERR_CUDA;
+  return launch_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QPA_OK : QPA_ERR_CUDA;
+}
+
+size_t pa_chunk_fp8_workspace_size(const qpa_chunk_desc* d) {
+  if (!d || !chunk_shape_ok(d)) return 0;
+  return chunk_workspace_bytes(d->num_tokens, d->query_group, d->head_dim);
+}
+
+int pa_chunk_fp8(const void* q, const uint8_t* kv_cache, const int32_t* block_table, const int32_t* query_start,
+                 const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* out,
+                 const qpa_chunk_desc* d, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!d) return QPA_ERR_NULL;
+  if (!chunk_shape_ok(d)) return QPA_ERR_SHAPE;
+  if (d->num_reqs == 0 || d->num_tokens == 0) return QPA_OK;
+  if (!q || !kv_cache || !block_table || !query_start || !seq_lens || !k_scale || !v_scale || !out || !workspace)
+    return QPA_ERR_NULL;
+  ChunkLaunch a;
+  a.q_stride_head = d->q_stride_head ? d->q_stride_head : d->head_dim;
+  a.q_stride_tok = d->q_stride_tok ? d->q_stride_tok : (long long)d->num_kv_heads * d->query_group * d->head_dim;
+  a.table_stride = d->table_stride ? d->table_stride : d->max_blocks_per_seq;
+  if (a.q_stride_head < 0 || a.q_stride_tok < 0 || (a.q_stride_head % 8) || (a.q_stride_tok % 8)) return QPA_ERR_ALIGN;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return QPA_ERR_ALIGN;
+  if (!aligned(block_table, 4) || !aligned(query_start, 4) || !aligned(seq_lens, 4)) return QPA_ERR_ALIGN;
+  const size_t sa = d->kv_scale_per_token ? 16 : 4;
+  if (!aligned(k_scale, sa) || !aligned(v_scale, sa)) return QPA_ERR_ALIGN;
+  if (workspace_bytes < chunk_workspace_bytes(d->num_tokens, d->query_group, d->head_dim)) return QPA_ERR_WORKSPACE;
+  a.q = q;
+  a.kv = kv_cache;
+  a.block_table = block_table;
+  a.query_start = query_start;
+  a.seq_lens = seq_lens;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.out = out;
+  a.workspace = workspace;
+  a.num_reqs = d->num_reqs;
+  a.num_tokens = d->num_tokens;
+  a.num_kv_heads = d->num_kv_heads;
+  a.qg = d->query_group;
+  a.head_dim = d->head_dim;
+  a.block_size = d->block_size;
+  a.num_blocks = d->num_blocks;
+  a.max_blocks = d->max_blocks_per_seq;
+  a.per_token = d->kv_scale_per_token;
+  a.softmax_scale = d->softmax_scale != 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)d->head_dim);
+  a.num_sms = num_sms_current();
+  if (a.num_sms <= 0) return QPA_ERR_CUDA;
+  return launch_chunk(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QPA_OK : QPA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -110,6 +110,52 @@ struct IdxLaunch {
   int num_sms;
 };
 
+// paged_slot_map
+struct SlotMapLaunch {
+  const int32_t* new_lens;
+  const int32_t* cached_lens;
+  int32_t* block_table;
+  const int32_t* free_blocks;
+  int32_t* query_start;
+  int32_t* seq_lens;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* num_taken;
+  long long table_stride;   // elements
+  int num_reqs, block_size, max_blocks, num_free, max_tokens;
+  int num_sms;
+};
+
+// kv_append_fp8
+struct AppendLaunch {
+  const void* k;
+  const void* v;
+  uint8_t* kv;
+  const int64_t* slots;
+  float* k_scale;
+  float* v_scale;
+  long long k_stride_tok, k_stride_head, v_stride_tok, v_stride_head;   // elements
+  int num_tokens, num_kv_heads, head_dim, block_size, num_blocks, per_token;
+  int num_sms;
+};
+
+// pa_chunk_fp8
+struct ChunkLaunch {
+  const void* q;
+  const uint8_t* kv;
+  const int32_t* block_table;
+  const int32_t* query_start;
+  const int32_t* seq_lens;
+  const float* k_scale;
+  const float* v_scale;
+  void* out;
+  void* workspace;
+  long long q_stride_tok, q_stride_head, table_stride;   // elements
+  int num_reqs, num_tokens, num_kv_heads, qg, head_dim, block_size, num_blocks, max_blocks, per_token;
+  float softmax_scale;
+  int num_sms;
+};
+
 __device__ __forceinline__ void store4(float* dst, float a, float b, float c, float d) {
   *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
 }
@@ -136,6 +182,11 @@ UqPlan uq_plan(int num_kv_heads, int query_group);
 cudaError_t launch_uq_partition(const UqLaunch& a, cudaStream_t stream);
 cudaError_t launch_uq_combine(const CombineLaunch& a, cudaStream_t stream);
 cudaError_t launch_idx_score(const IdxLaunch& a, cudaStream_t stream);
+cudaError_t launch_slot_map(const SlotMapLaunch& a, cudaStream_t stream);
+cudaError_t launch_append(const AppendLaunch& a, cudaStream_t stream);
+// Workspace bytes of a chunk launch (independent of the device).
+size_t chunk_workspace_bytes(int num_tokens, int query_group, int head_dim);
+cudaError_t launch_chunk(const ChunkLaunch& a, cudaStream_t stream);
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
