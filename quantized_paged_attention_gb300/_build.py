@@ -1,6 +1,6 @@
 """Builds libqpa.so in-tree with nvcc for sm_103a (no CMake, no torch
-extension machinery): each .cu file is compiled in parallel with -dc, then
-nvcc device-links and links the shared library."""
+extension machinery): each .cu file is compiled in parallel (with -dc, but for
+the files of WHOLE), then nvcc device-links and links the shared library."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -15,8 +15,11 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqpa.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-rdc=true",
+FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
+# compiled whole (no relocatable device code): the compiler ignores register
+# budgets per warp group (setmaxnreg) in code that other units may call
+WHOLE = {"pa_chunk.cu"}
 
 
 def _nvcc() -> str:
@@ -50,7 +53,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [nvcc, *ARCH, *FLAGS, *extra_flags, "-dc", src, "-o", obj]
+        mode = ["-c"] if os.path.basename(src) in WHOLE else ["-rdc=true", "-dc"]
+        cmd = [nvcc, *ARCH, *FLAGS, *extra_flags, *mode, src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")

@@ -1,0 +1,84 @@
+// The work list of pa_chunk_fp8, shared by the kernel and a host test.
+//
+// An item is bt = 256 / G whole tokens of one request and KV head; a unit is
+// one 128-key tile of an item. The units in order: heads, then requests, then
+// items, then key tiles. How many a request has is known in closed form, so
+// nobody has to list them.
+#pragma once
+#ifndef __CUDACC__
+#include <algorithm>
+#define QPA_HD
+namespace qpa { namespace chunk { using std::max; using std::min; } }
+#else
+#define QPA_HD __host__ __device__
+#endif
+
+namespace qpa {
+namespace chunk {
+
+constexpr int TILE = 128;            // keys per unit, rows per row tile
+
+// sum_{i < n} floor((a i + b) / m) for a, b >= 0 (the lattice points under a
+// line, by a Euclid-like reduction)
+QPA_HD inline long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    if (a >= m) {
+      s += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      s += n * (b / m);
+      b %= m;
+    }
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// One request as the schedule sees it: first query row, rows, cached tokens
+// (the rows' own included), items.
+struct Req {
+  int q0, ql, L, nt;
+  // key tiles of item j: those its last row sees, at least one
+  QPA_HD int tiles(int j, int bt) const {
+    const int last = min((j + 1) * bt, ql) - 1;
+    return max(L - ql + last, 0) / TILE + 1;
+  }
+  // units of items 0 .. j-1 (j < nt: all of them have bt tokens)
+  QPA_HD long long before(int j, int bt) const {
+    const long long d = (long long)L - ql;
+    // items whose last row sees nothing, d + (i + 1) bt - 1 < 0: one unit each
+    const int i0 = d + bt - 1 >= 0 ? 0 : (int)min((long long)j, (-d) / bt);
+    return j + floor_sum(j - i0, TILE, bt, d + (long long)(i0 + 1) * bt - 1);
+  }
+  QPA_HD long long units(int bt) const { return nt ? before(nt - 1, bt) + tiles(nt - 1, bt) : 0; }
+  // the item that holds unit off (0 <= off < units)
+  QPA_HD int find(long long off, int bt) const {
+    int lo = 0, hi = nt;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before(mid, bt) <= off) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+};
+
+QPA_HD inline Req make_req(int start, int next, int len, int num_tokens, int max_len, int bt) {
+  Req q;
+  q.q0 = max(0, min(start, num_tokens));
+  q.ql = max(0, max(0, min(next, num_tokens)) - q.q0);
+  q.L = max(0, min(len, max_len));
+  q.nt = q.ql / bt + (q.ql % bt != 0);
+  return q;
+}
+
+}  // namespace chunk
+}  // namespace qpa

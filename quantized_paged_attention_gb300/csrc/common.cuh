@@ -11,7 +11,13 @@ namespace qpa {
 // id (the library's only device-side state). 0 = no error.
 enum : int { KERR_NONE = 0, KERR_TIMEOUT_FULL = 1, KERR_TIMEOUT_EMPTY = 2, KERR_BAD_BLOCK = 3, KERR_SCHEDULE = 4,
              KERR_RANGE = 5, KERR_CAPACITY = 6 };
+#ifdef QPA_WHOLE_UNIT
+// a unit compiled without relocatable device code cannot share the word: it
+// has its own, which qpa_kernel_error() reads too
+static __device__ int g_kernel_error = 0;
+#else
 extern __device__ int g_kernel_error;
+#endif
 
 // Any wait gives up after this many nanoseconds and reports an error rather
 // than spinning forever.
@@ -91,6 +97,18 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
       " [%0], [%1, {%2, %3, %4}], [%5], %6;"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
+}
+// The same without a cache-policy hint (data that other CTAs read again).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+}
+// Contiguous copy global -> shared (both addresses and the size multiples of
+// 16 bytes), completion counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 // Asynchronous 16-byte copy global -> shared (L1 bypass) with an L2
 // cache-policy hint, and its group bookkeeping.
@@ -186,6 +204,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+
+// Register budget of the executing warpgroup (every warp of it executes this).
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // ---------------------------------------------------------------- conversions
 // Low / high 16 bits of x hold two e4m3fn bytes; returns them as f16x2

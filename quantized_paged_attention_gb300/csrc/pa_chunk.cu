@@ -1,87 +1,943 @@
 // pa_chunk_fp8: attention of a chunk of new tokens per request over the fp8
-// paged cache. One warp per (query row, head): the lanes split head_dim, one
-// pass over the visible tokens with the running maximum and sum of a softmax.
+// paged cache, on the 5th-generation tensor core.
+//
+// Mathematics: softmax(scale q k^T + causal) v with one pass over the keys, a
+// running maximum m and sum l per row: p = 2^(s c - m), O += p v, and O, l are
+// rescaled only when the maximum has grown by more than 2^8 since m was taken
+// (p <= 256 then, and O / l does not depend on m).
+//
+//  * Item: 256 query rows of one KV head, i.e. 256 / G whole tokens with their
+//    G heads (rows of a group share their keys), as two tiles of 128 rows.
+//    Unit: one 128-token key tile of an item. The units of all items (heads,
+//    then requests, then tokens) are cut into equal contiguous ranges, one per
+//    CTA, whatever the batch looks like. An item that crosses a cut leaves
+//    float32 partials (m, l, O / l) in the workspace, and the combine kernel
+//    merges them in order (no atomics: the result is the same every time).
+//    A CTA needs no plan from memory: the units of a request are a sum of
+//    floors of an arithmetic progression, in closed form, so a scan over the
+//    requests and one search find its range.
+//  * QK: S = Q K^T as kind::f8f6f4. K enters as the cache's e4m3 bytes; a query
+//    row, scaled by a power of two to a largest |q| in [128, 256), enters as
+//    the sum of 2 e4m3 terms into the same accumulator (8 significant bits:
+//    exact for a bf16 of magnitude >= 2^-2, else within 2^-10). Two fp8 passes
+//    cost what one bf16 pass does, and K needs no conversion.
+//  * PV: O += P V as kind::f16. P goes from the softmax registers to tensor
+//    memory (over the S it came from), V is converted e4m3 -> f16 (exact) once
+//    per tile by four warps. f16 keeps 11 bits of p, where two e4m3 terms would
+//    keep 8 and cost the softmax warps 2.5 instructions per element; the
+//    conversion is 0.4.
+//  * Roles: 2 x 4 softmax warps (a thread owns one row: no exchange between
+//    lanes), one per row tile, so that the tensor core works for one while the
+//    other computes; 4 warps that convert V and build the next item's query
+//    operand; an MMA warp; a warp that walks the schedule and issues the TMA
+//    copies (one box per page of the tile, one page per lane).
+//  * Tokens past the sequence's end are zeroed in V and masked in S; a NaN code
+//    in V is taken out of the product and put back only into the rows that see
+//    its token, so it cannot leak through 0 * NaN.
+// Every wait has a time limit; a timeout raises the error word and all roles
+// leave through the common teardown.
+#define QPA_WHOLE_UNIT
 #include "qpa.h"
 #include "common.cuh"
 #include "qpa_internal.h"
+#include "tc.cuh"
+#include "chunk_schedule.h"
 
 namespace qpa {
 
-namespace {
+namespace chunk {
+constexpr int ROWS = 256;            // query rows per item (two tiles)
+constexpr int MAX_GRID = 160;        // CTAs at most (bounds the workspace)
+constexpr int THREADS = 512;
+constexpr int W_CONV = 8, W_MMA = 12, W_LOAD = 13;
+constexpr int NK = 3, NV = 2, NW = 2;   // stages of K, V bytes, V f16
+constexpr int IR = 4;                // item ring
+constexpr float kNoMax = -1e30f;     // running maximum of a row that has seen no token
+constexpr float kLazy = 8.f;         // growth of the maximum (log2) that rescales
 
-template <int HD>
-__global__ void __launch_bounds__(256) chunk_simple_kernel(const ChunkLaunch p, const int log2_bs) {
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const int Hq = p.num_kv_heads * p.qg;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(row / Hq), hq = (int)(row % Hq);
-  if (t >= p.num_tokens) return;
-  // the request that owns row t: the last one starting at or before it
-  int lo = 0, hi = p.num_reqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.query_start[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const int q0 = max(0, p.query_start[lo]), q1 = min(p.num_tokens, p.query_start[lo + 1]);
-  if (t < q0 || t >= q1) return;
-  const int L = max(0, min(p.seq_lens[lo], p.max_blocks << log2_bs));
-  const int see = min(L, L - (q1 - q0) + (t - q0) + 1);
-  const int h = hq / p.qg, bs = p.block_size;
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + t * p.q_stride_tok + hq * p.q_stride_head + lane * E;
-  float qv[E], o[E], m = -INFINITY, l = 0.f;
-  const float c = p.softmax_scale * (p.per_token ? 1.f : *p.k_scale);
-  for (int e = 0; e < E; ++e) {
-    qv[e] = __uint_as_float((uint32_t)q[e] << 16);
-    o[e] = 0.f;
-  }
-  for (int tok = 0; tok < see; ++tok) {
-    int b = p.block_table[lo * p.table_stride + (tok >> log2_bs)];
-    if (b < 0 || b >= p.num_blocks) {
-      if (lane == 0) atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
-      b = 0;
-    }
-    const long long off = tok & (bs - 1);
-    const long long kr = ((long long)b * 2 * p.num_kv_heads + h) * bs + off;
-    const uint8_t* kp = p.kv + kr * HD + lane * E;
-    const uint8_t* vp = kp + (long long)p.num_kv_heads * bs * HD;
-    uint32_t kw = 0, vw = 0;
-    for (int e = 0; e < E; ++e) {
-      kw |= (uint32_t)kp[e] << (8 * e);
-      vw |= (uint32_t)vp[e] << (8 * e);
-    }
-    const uint32_t k2[2] = {e4m3x2_lo_to_f16x2(kw), e4m3x2_hi_to_f16x2(kw)};
-    const uint32_t v2[2] = {e4m3x2_lo_to_f16x2(vw), e4m3x2_hi_to_f16x2(vw)};
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s = fmaf(qv[e], (e & 1) ? f16_hi_to_f32(k2[e / 2]) : f16_lo_to_f32(k2[e / 2]), s);
-    for (int w = 16; w >= 1; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    const long long sr = ((long long)b * p.num_kv_heads + h) * bs + off;
-    s *= c * (p.per_token ? p.k_scale[sr] : 1.f);
-    const float vs = p.per_token ? p.v_scale[sr] : 1.f;
-    const float mn = fmaxf(m, s), al = expf(m - mn), w = expf(s - mn);
-    m = mn;
-    l = l * al + w;
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * al + w * vs * ((e & 1) ? f16_hi_to_f32(v2[e / 2]) : f16_lo_to_f32(v2[e / 2]));
-  }
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * HD + lane * E;
-  const float f = see > 0 ? (p.per_token ? 1.f : *p.v_scale) / l : 0.f;
-  for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16(see > 0 ? o[e] * f : 0.f);
+template <int D>
+struct Smem {
+  static constexpr int qTerm = TILE * D, qBytes = 4 * qTerm;      // [tile][term][128 rows][D]
+  static constexpr int kBytes = TILE * D, wBytes = 2 * TILE * D;
+  static constexpr int qOff = 0;
+  static constexpr int kOff = qOff + qBytes;
+  static constexpr int vOff = kOff + NK * kBytes;
+  static constexpr int wOff = vOff + NV * kBytes;
+  static constexpr int nanOff = wOff + NW * wBytes;               // [NW][128][D / 32] NaN dims of a token
+  static constexpr int crowOff = nanOff + NW * TILE * (D / 8);    // [2][256] logit multiplier of a row
+  static constexpr int krawOff = crowOff + 2 * ROWS * 4;          // [NK][128] per-token scales as copied
+  static constexpr int vrawOff = krawOff + NK * TILE * 4;
+  static constexpr int kscOff = vrawOff + NV * TILE * 4;          // [NW][128] for the softmax
+  static constexpr int vscOff = kscOff + NW * TILE * 4;
+  static constexpr int iringOff = vscOff + NW * TILE * 4;         // [IR] 64 bytes
+  static constexpr int qinfoOff = iringOff + IR * 64;             // [2] 64 bytes
+  static constexpr int flagOff = qinfoOff + 2 * 64;               // [NW][4 warps] NaN seen
+  static constexpr int evOff = flagOff + NW * 16;                 // [NW] exponent of the V scales (16 bytes)
+  static constexpr int schedOff = evOff + 16;                     // schedule scratch
+  static constexpr int barOff = schedOff + 256;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + 2 * IR + 4 + 1 + 6 + 1;
+  static constexpr int miscOff = barOff + NBAR * 8;
+  static constexpr int total = miscOff + 16 + 1024;
+  static_assert(total <= 227 * 1024, "shared memory");
+};
+
+struct Params {
+  const uint16_t* q;
+  const int32_t* block_table;
+  const int32_t* query_start;
+  const int32_t* seq_lens;
+  const float* k_scale;
+  const float* v_scale;
+  __nv_bfloat16* out;
+  float* part_o;           // [slots][part_rows][D]
+  float2* part_ml;         // [slots][part_rows]
+  int4* meta;              // [grid][2]
+  long long q_stride_tok, q_stride_head, table_stride;
+  int num_reqs, num_tokens, num_kv_heads, qg, log2_bs, num_blocks, max_len, part_rows;
+  float softmax_scale;
+};
+
+__device__ __forceinline__ Req load_req(const Params& p, int r, int bt) {
+  return make_req(__ldg(p.query_start + r), __ldg(p.query_start + r + 1), __ldg(p.seq_lens + r), p.num_tokens, p.max_len, bt);
 }
 
+// What the roles need of an item (the part of it in this CTA's range).
+struct Item {
+  int req, head, tok0, ntok;   // request, KV head, first query row, rows (tokens)
+  int lim0, L, t0, t1;         // last key that row tok0 sees, length, key tiles [t0, t1)
+  int e0, e1, slot, last;      // end of the key tiles per row tile; partial slot or -1; no more items
+};
+__device__ __forceinline__ Item lds_item(uint32_t a) {
+  const int4 x = lds_i4(a), y = lds_i4(a + 16), z = lds_i4(a + 32);
+  return Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+}
+__device__ __forceinline__ void sts_item(uint32_t a, const Item& i) {
+  sts_i4(a, make_int4(i.req, i.head, i.tok0, i.ntok));
+  sts_i4(a + 16, make_int4(i.lim0, i.L, i.t0, i.t1));
+  sts_i4(a + 32, make_int4(i.e0, i.e1, i.slot, i.last));
+}
+
+__device__ __forceinline__ void ffma2(float& a, float& b, float c, float m) {   // (a, b) = (a, b) * c + m
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %2}; mov.b64 z, {%3, %3}; "
+      "fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x; }" : "+f"(a), "+f"(b) : "f"(c), "f"(m));
+}
+__device__ __forceinline__ void fadd2(float& a, float& b, float c, float d) {
+  asm("{ .reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "+f"(a), "+f"(b) : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void fmul2(float& a, float& b, float c, float d) {
+  asm("{ .reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "+f"(a), "+f"(b) : "f"(c), "f"(d));
+}
+}  // namespace chunk
+
+using namespace chunk;
+
+template <int D, bool PT>
+__global__ void __launch_bounds__(THREADS, 1)
+pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ Params p) {
+  using S = Smem<D>;
+  constexpr uint32_t SWZ = D == 128 ? kSwizzle128B : kSwizzle64B;
+  constexpr uint32_t SBO = 8 * D;                  // 8 rows of D bytes
+  constexpr uint32_t IDESC_QK = idesc_e4m3(128, 128, false, false);
+  constexpr uint32_t IDESC_PV = idesc_f16(128, D, false, true);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;      // swizzle atoms need 1024-byte alignment
+  uint8_t* sm = smem_raw + (sb - raw);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::barOff);
+  uint64_t* kfull = bar;               // [NK] K tile copied
+  uint64_t* kempty = kfull + NK;       // [NK] K tile read (MMA commit; its scales: 4 warps)
+  uint64_t* vfull = kempty + NK;       // [NV] V bytes copied
+  uint64_t* vempty = vfull + NV;       // [NV] V bytes read (4 warps)
+  uint64_t* wfull = vempty + NV;       // [NW] V f16 written (4 warps)
+  uint64_t* wempty = wfull + NW;       // [NW] V f16 read (MMA commit)
+  uint64_t* ifull = wempty + NW;       // [IR] item published
+  uint64_t* iempty = ifull + IR;       // [IR] item read (4 warps)
+  uint64_t* qfull = iempty + IR;       // [2] query operand built, item passed on (4 warps)
+  uint64_t* qread = qfull + 2;         // [2] item read (8 softmax warps, MMA)
+  uint64_t* qfree = qread + 2;         // query operand read (MMA commit)
+  uint64_t* sfull = qfree + 1;         // [2] S of a row tile ready (MMA commit)
+  uint64_t* pfull = sfull + 2;         // [2] P written (4 warps)
+  uint64_t* ofull = pfull + 2;         // [2] O of an item ready (MMA commit)
+  uint64_t* done = ofull + 2;          // all MMAs finished
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::miscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::miscOff + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NK; ++i) { mbar_init(&kfull[i], 1); mbar_init(&kempty[i], PT ? 5 : 1); }
+    for (int i = 0; i < NV; ++i) { mbar_init(&vfull[i], 1); mbar_init(&vempty[i], 4); }
+    for (int i = 0; i < NW; ++i) { mbar_init(&wfull[i], 4); mbar_init(&wempty[i], 1); }
+    for (int i = 0; i < IR; ++i) { mbar_init(&ifull[i], 1); mbar_init(&iempty[i], 4); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qfull[i], 4);
+      mbar_init(&qread[i], 9);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 4);
+      mbar_init(&ofull[i], 1);
+    }
+    mbar_init(qfree, 1);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) tmem_alloc(tmem_slot, 512);
+  if (warp == W_LOAD && lane == 0) prefetch_tmap(&kv_map);
+
+  // ---- schedule: this CTA's range [u0, u1) of the units, its first request
+  const int bt = ROWS / p.qg;                      // tokens per item
+  long long* sched = reinterpret_cast<long long*>(sm + S::schedOff);   // [16] warp sums, then the start
+  long long W;
+  long long u0, u1;
+  {
+    const int per = (p.num_reqs + THREADS - 1) / THREADS;
+    const int r0 = threadIdx.x * per, r1 = min(p.num_reqs, r0 + per);
+    long long mine = 0;
+    for (int r = r0; r < r1; ++r) mine += load_req(p, r, bt).units(bt);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) sched[warp] = incl;
+    __syncthreads();
+    W = 0;
+    long long base = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) base += sched[w];
+      W += sched[w];
+    }
+    const long long U = W * p.num_kv_heads;
+    u0 = U * blockIdx.x / gridDim.x;
+    u1 = U * (blockIdx.x + 1) / gridDim.x;
+    if (u0 < u1) {
+      long long off = u0 - u0 / W * W - (base + incl - mine);
+      if (off >= 0 && off < mine) {
+        int r = r0;
+        while (true) {                             // ends: off lies below this thread's sum
+          const long long n = load_req(p, r, bt).units(bt);
+          if (off < n || r + 1 >= r1) break;
+          off -= n;
+          ++r;
+        }
+        sched[16] = r;
+        sched[17] = off;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < W_CONV) {
+    // ======================================================== softmax warps
+    reg_inc<192>();
+    const int a = warp >> 2;                       // row tile
+    const int row = a * TILE + (threadIdx.x & 127);
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = tl + a * 128, to = tl + 256 + a * D;
+    const float vscale = PT ? 1.f : __ldg(p.v_scale);
+    const int G = p.qg;
+    int sc = 0, oc = 0, n = 0;                     // S tiles, items of this row tile; key tiles of the CTA
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int qb = k & 1;
+      if (!warp_wait(&qfull[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+      const Item it = lds_item(sb + S::qinfoOff + 64 * qb);
+      const float c = ldsf(sb + S::crowOff + 4 * (qb * ROWS + row));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qread[qb]);
+      if (it.last) break;
+      const int end = a ? it.e1 : it.e0;
+      const int tok = row / G;
+      const bool valid = tok < it.ntok;
+      const int lim = valid ? it.lim0 + tok : -1;
+      float m = kNoMax, l = 0.f;
+      uint32_t nan[D / 32];
+      int ev = -126;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) nan[i] = 0;
+      for (int t = it.t0; t < end; ++t, ++sc) {
+        const int nn = n + t - it.t0, wb = nn % NW;
+        if (!warp_wait(&sfull[a], sc & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        tc_fence_after();
+        float s[4][32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, s[j]);
+        tmem_wait_ld();
+        // the converting warps are a tile ahead: their scales and NaN marks
+        if (!warp_wait(&wfull[wb], (nn / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        if constexpr (PT) {
+#pragma unroll
+          for (int i = 0; i < 128; i += 4) {
+            const float4 ks = lds_f4(sb + S::kscOff + 4 * (wb * TILE + i));
+            fmul2(s[i / 32][i % 32], s[i / 32][i % 32 + 1], ks.x, ks.y);
+            fmul2(s[i / 32][i % 32 + 2], s[i / 32][i % 32 + 3], ks.z, ks.w);
+          }
+        }
+        const int vis = lim - t * TILE;            // keys 0 .. vis of the tile are seen
+        const bool masked = __any_sync(0xffffffffu, vis < TILE - 1);
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i / 32][i % 32] = i <= vis ? s[i / 32][i % 32] : -INFINITY;
+        }
+        float mx4[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mx4[j] = s[j][0];
+#pragma unroll
+          for (int i = 1; i < 32; ++i) mx4[j] = fmaxf(mx4[j], s[j][i]);
+        }
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+        int en = ev;
+        if constexpr (PT) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(en) : "r"(sb + S::evOff + 4 * wb));
+        if (t == it.t0) {
+          m = fmaxf(mx, kNoMax);
+        } else {
+          const bool grow = mx > m + kLazy;
+          if (__any_sync(0xffffffffu, grow) || (PT && en != ev)) {
+            const float al = grow ? ex2(m - mx) : 1.f;
+            if (grow) m = mx;
+            l *= al;
+            // (ev only grows: the factor is at most 1)
+            const float f = PT ? al * ex2((float)(ev - en)) : al;
+#pragma unroll 1
+            for (int j = 0; j < D; j += 32) {
+              float o[32];
+              tmem_ld32(to + j, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              tmem_st32(to + j, reinterpret_cast<const uint32_t*>(o));
+            }
+          }
+        }
+        ev = en;
+        float la[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pw[64];
+        const float nm = -m;
+#pragma unroll
+        for (int i = 0; i < 128; i += 4) {
+          float* x = &s[i / 32][i % 32];
+          ffma2(x[0], x[1], c, nm);
+          ffma2(x[2], x[3], c, nm);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[u] = ex2(x[u]);
+          fadd2(la[0], la[1], x[0], x[1]);
+          fadd2(la[2], la[3], x[2], x[3]);
+          if constexpr (PT) {
+            const float4 vs = lds_f4(sb + S::vscOff + 4 * (wb * TILE + i));
+            fmul2(x[0], x[1], vs.x, vs.y);
+            fmul2(x[2], x[3], vs.z, vs.w);
+            if (masked) {                          // 0 times a scale that is not finite
+#pragma unroll
+              for (int u = 0; u < 4; ++u) x[u] = i + u <= vis ? x[u] : 0.f;
+            }
+          }
+          pw[i / 2] = f32x2_to_f16x2(x[0], x[1]);
+          pw[i / 2 + 1] = f32x2_to_f16x2(x[2], x[3]);
+        }
+        l += (la[0] + la[1]) + (la[2] + la[3]);
+        tmem_st32(ts, pw);
+        tmem_st32(ts + 32, pw + 32);
+        tmem_wait_st();
+        // NaN codes of V in this tile (none, as a rule)
+        const int4 nf = lds_i4(sb + S::flagOff + 16 * wb);
+        if ((nf.x | nf.y | nf.z | nf.w) != 0) {
+          const int f4[4] = {nf.x, nf.y, nf.z, nf.w};
+#pragma unroll 1
+          for (int tk = 0; tk < TILE; ++tk) {
+            if (f4[tk >> 5] == 0 || tk > vis) continue;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) nan[i] |= lds32(sb + S::nanOff + ((wb * TILE + tk) * (D / 32) + i) * 4);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[a]);
+      }
+      if (!ok) break;
+      n += it.t1 - it.t0;
+
+      // ---- the item's result
+      const bool any = it.t0 < end;
+      if (any) {
+        if (!warp_wait(&ofull[a], oc & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+        ++oc;
+        tc_fence_after();
+      }
+      const bool none = lim < 0 || l == 0.f;
+      const float rl = none ? 0.f : __frcp_rn(l);
+      const float sv = PT ? ex2((float)ev) : vscale;
+      const int head = it.head * G + row - tok * G;
+      __nv_bfloat16* orow = p.out + ((long long)(it.tok0 + tok) * (p.num_kv_heads * G) + head) * D;
+      float* prow = p.part_o + ((long long)it.slot * p.part_rows + row) * D;
+      if (it.slot >= 0 && valid) p.part_ml[(long long)it.slot * p.part_rows + row] = make_float2(none ? -INFINITY : m, l);
+      if (any) {
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          float o[32];
+          tmem_ld32(to + 32 * j, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            o[i] = none ? 0.f : o[i] * rl * sv;
+            if ((nan[j] >> i) & 1u) o[i] = __uint_as_float(0x7fffffffu);
+          }
+          if (valid) {
+            if (it.slot < 0) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                uint4 v;
+                __nv_bfloat162 b0 = __floats2bfloat162_rn(o[i], o[i + 1]), b1 = __floats2bfloat162_rn(o[i + 2], o[i + 3]);
+                __nv_bfloat162 b2 = __floats2bfloat162_rn(o[i + 4], o[i + 5]), b3 = __floats2bfloat162_rn(o[i + 6], o[i + 7]);
+                v.x = *reinterpret_cast<uint32_t*>(&b0);
+                v.y = *reinterpret_cast<uint32_t*>(&b1);
+                v.z = *reinterpret_cast<uint32_t*>(&b2);
+                v.w = *reinterpret_cast<uint32_t*>(&b3);
+                *reinterpret_cast<uint4*>(orow + 32 * j + i) = v;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) store4(prow + 32 * j + i, o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+          }
+        }
+      }
+    }
+  } else if (warp < W_MMA) {
+    // ======================================================== converting warps
+    reg_dec<80>();
+    const int cw = warp - W_CONV;
+    const int G = p.qg;
+    const float base = p.softmax_scale * (PT ? 1.f : __ldg(p.k_scale)) * kLog2e;
+    const uint32_t neg = base < 0.f ? 0x80000000u : 0u;
+    int n = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int qb = k & 1;
+      if (!warp_wait(&ifull[k % IR], (k / IR) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+      const Item it = lds_item(sb + S::iringOff + 64 * (k % IR));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[k % IR]);
+      if (k >= 2 && !warp_wait(&qread[qb], ((k >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
+      if (k >= 1 && !warp_wait(qfree, (k - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
+      if (!it.last) {
+        // ---- query operand: LPR lanes per row, 8 dims each
+        constexpr int LPR = D / 8, RPW = 32 / LPR;
+        const int part = lane % LPR;
+        const int rows = it.ntok * G;
+        const int rlim = rows > TILE ? ROWS : TILE;
+        constexpr int UN = 4;
+        for (int rr = cw * RPW + lane / LPR; rr < rlim; rr += UN * 4 * RPW) {
+          uint4 xv[UN];
+#pragma unroll
+          for (int u = 0; u < UN; ++u) {
+            const int row = rr + u * 4 * RPW;
+            xv[u] = make_uint4(0, 0, 0, 0);
+            if (row < rows) {
+              const int tok = row / G;
+              xv[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (it.tok0 + tok) * p.q_stride_tok +
+                                                           (long long)(it.head * G + row - tok * G) * p.q_stride_head) + part);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < UN; ++u) {
+            const int row = rr + u * 4 * RPW;
+            const uint32_t w[4] = {xv[u].x, xv[u].y, xv[u].z, xv[u].w};
+            float y[8], mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              y[2 * i] = __uint_as_float(w[i] << 16);
+              y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+              mx = fmaxf(mx, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+            }
+#pragma unroll
+            for (int o = LPR / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // 2^(7 - floor(log2 max)), and its inverse for the logits; rows below
+            // 2^-119 keep fewer bits (their logits vanish)
+            const int e = max((int)(__float_as_uint(mx) >> 23), 8);
+            const bool inf = e >= 255;
+            const float f = __uint_as_float(((uint32_t)(inf ? 127 : 261 - e) << 23) | neg);
+            if (part == 0) {
+              float cm = fabsf(base) * __uint_as_float((uint32_t)(inf ? 127 : e - 7) << 23);
+              // a masked score must stay -inf when multiplied; an infinite query gives a NaN row
+              if (cm == 0.f) cm = 1.17549435e-38f;
+              if (inf) cm = __uint_as_float(0x7fffffffu);
+              stsf(sb + S::crowOff + 4 * (qb * ROWS + row), cm);
+            }
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float z[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) z[j] = y[4 * i + j] * f;
+              const uint32_t h0 = f32x2_to_e4m3x2(z[0], z[1]), h1 = f32x2_to_e4m3x2(z[2], z[3]);
+              const uint32_t g0 = e4m3x2_lo_to_f16x2(h0), g1 = e4m3x2_lo_to_f16x2(h1);
+              hi[i] = prmt(h0, h1, 0x5410u);
+              lo[i] = prmt(f32x2_to_e4m3x2(z[0] - f16_lo_to_f32(g0), z[1] - f16_hi_to_f32(g0)),
+                           f32x2_to_e4m3x2(z[2] - f16_lo_to_f32(g1), z[3] - f16_hi_to_f32(g1)), 0x5410u);
+            }
+            const int tr = row & 127;
+            const uint32_t swz = D == 128 ? (tr & 7) : ((tr >> 1) & 3);
+            const uint32_t dst = sb + S::qOff + (row >> 7) * 2 * S::qTerm + tr * D + (((part >> 1) ^ swz) << 4) + (part & 1) * 8;
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + S::qTerm), "r"(lo[0]), "r"(lo[1]) : "memory");
+          }
+        }
+        fence_proxy_async();
+      }
+      if (cw == 0 && lane == 0) sts_item(sb + S::qinfoOff + 64 * qb, it);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qfull[qb]);
+      if (it.last) break;
+
+      // ---- V of the item's key tiles: e4m3 -> f16, [dims / 64][token][64 dims],
+      // 128-byte swizzle (the MN-major operand of the PV product)
+      int ev = -126;
+      for (int t = it.t0; t < it.t1; ++t, ++n) {
+        const int vb = n % NV, wb = n % NW;
+        const int live = it.L - t * TILE;            // tokens of the tile that exist
+        if (!warp_wait(&vfull[vb], (n / NV) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        if (n >= NW && !warp_wait(&wempty[wb], (n / NW - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
+        if constexpr (PT) {
+          const int kb = n % NK;
+          if (!warp_wait(&kfull[kb], (n / NK) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+          float vm = 0.f, vown = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int tk = 32 * i + lane;
+            const float x = tk < live ? ldsf(sb + S::vrawOff + 4 * (vb * TILE + tk)) : 0.f;
+            const float ax = fabsf(x);
+            if (ax < INFINITY) vm = fmaxf(vm, ax);
+            if (i == cw) vown = x;
+          }
+          vm = warp_max(vm);
+          // 2^ev above the largest scale so far: |v scale| 2^-ev < 1 (4 at the very top)
+          ev = max(ev, min((int)(__float_as_uint(vm) >> 23) - 126, 126));
+          const int tk = 32 * cw + lane;
+          const float kx = tk < live ? ldsf(sb + S::krawOff + 4 * (kb * TILE + tk)) : 0.f;
+          stsf(sb + S::kscOff + 4 * (wb * TILE + tk), kx);
+          stsf(sb + S::vscOff + 4 * (wb * TILE + tk), vown * ex2((float)-ev));
+          if (cw == 0 && lane == 0) asm volatile("st.shared.s32 [%0], %1;" ::"r"(sb + S::evOff + 4 * wb), "r"(ev) : "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kempty[kb]);
+        }
+        constexpr int CPR = D / 16, TPI = 32 / CPR, NI = 32 / TPI;   // 16-byte chunks per token, tokens per step
+        const int ch = lane % CPR, tr = lane / CPR;
+        const uint32_t src = sb + S::vOff + vb * S::kBytes, dst = sb + S::wOff + wb * S::wBytes;
+        uint32_t bad = 0;
+        uint4 x[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int tk = 32 * cw + TPI * i + tr;
+          const uint32_t swz = D == 128 ? (tk & 7) : ((tk >> 1) & 3);
+          x[i] = lds128(src + tk * D + ((ch ^ swz) << 4));
+          if (tk >= live) x[i] = make_uint4(0, 0, 0, 0);
+          const uint32_t y = (((x[i].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].y & 0x7f7f7f7fu) + 0x01010101u) |
+                              ((x[i].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+          bad |= y;
+        }
+        const bool anybad = __any_sync(0xffffffffu, bad != 0);
+        if (lane == 0) asm volatile("st.shared.s32 [%0], %1;" ::"r"(sb + S::flagOff + 16 * wb + 4 * cw), "r"((int)anybad) : "memory");
+        if (anybad) {
+          // mark the NaN dims of every token of this warp, and take them out
+          const uint32_t nb = S::nanOff + (wb * TILE + 32 * cw) * (D / 8);
+          uint32_t* nm = reinterpret_cast<uint32_t*>(sm + nb);
+          for (int i = lane; i < 32 * (D / 32); i += 32) nm[i] = 0;
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, bits = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t b = ((w4[j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // NaN bytes
+              bits |= (((b >> 7) & 1u) | ((b >> 14) & 2u) | ((b >> 21) & 4u) | ((b >> 28) & 8u)) << (4 * j);
+              w4[j] &= ~((b >> 7) * 0xffu);
+            }
+            x[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            if (bits) atomicOr(&nm[(TPI * i + tr) * (D / 32) + ch / 2], bits << (16 * (ch & 1)));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int tk = 32 * cw + TPI * i + tr;
+          const uint32_t rowa = dst + (D == 128 ? (ch >> 2) * (TILE * 128) : 0) + (tk >> 3) * 1024 + (tk & 7) * 128;
+          const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t f[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[2 * j] = e4m3x2_lo_to_f16x2(w4[j]);
+            f[2 * j + 1] = e4m3x2_hi_to_f16x2(w4[j]);
+          }
+          // the two 16-byte halves in an order that differs between the atoms, so
+          // that 8 lanes of a store touch 8 different bank groups
+          const bool sw = D == 128 && (ch >> 2);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int ee = sw ? 1 - e : e;
+            const uint32_t addr = rowa + ((((ch & 3) * 2 + ee) ^ (tk & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(ee ? f[4] : f[0]), "r"(ee ? f[5] : f[1]),
+                         "r"(ee ? f[6] : f[2]), "r"(ee ? f[7] : f[3]) : "memory");
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&wfull[wb]);
+          mbar_arrive(&vempty[vb]);
+        }
+      }
+    }
+  } else {
+    reg_dec<48>();
+    if (warp == W_MMA) {
+      // ====================================================== MMA warp
+      if (lane == 0) {
+        int n = 0, pc[2] = {0, 0};
+        bool ok = true;
+        const uint32_t qa = sb + S::qOff;
+        auto qk = [&](int a, int kb) {
+          // two query terms into one accumulator
+          const uint32_t ka = sb + S::kOff + kb * S::kBytes;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              mma_e4m3(tmem + a * 128, umma_desc(qa + (2 * a + j) * S::qTerm + 32 * i, 16, SBO, SWZ),
+                       umma_desc(ka + 32 * i, 16, SBO, SWZ), IDESC_QK, j | i);
+          umma_commit(&sfull[a]);
+        };
+        auto kwait = [&](int nn) -> bool {
+          return role_wait(&kfull[nn % NK], (nn / NK) & 1, abort_flag, KERR_TIMEOUT_FULL);
+        };
+        for (int k = 0; ok; ++k) {
+          const int qb = k & 1;
+          if (!role_wait(&qfull[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+          const Item it = lds_item(sb + S::qinfoOff + 64 * qb);
+          mbar_arrive(&qread[qb]);
+          if (it.last) break;
+          const int end[2] = {it.e0, it.e1};
+          if (!kwait(n)) break;
+          tc_fence_after();
+          if (it.t0 < end[0]) qk(0, n % NK);
+          if (it.t0 < end[1]) qk(1, n % NK);
+          umma_commit(&kempty[n % NK]);
+          if (it.t0 + 1 == it.t1) umma_commit(qfree);
+          for (int t = it.t0; t < it.t1; ++t, ++n) {
+            const int wb = n % NW;
+            if (!role_wait(&wfull[wb], (n / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+            bool kready = false;
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+              if (t < end[a]) {
+                if (!role_wait(&pfull[a], pc[a] & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+                ++pc[a];
+                tc_fence_after();
+                const uint32_t va = sb + S::wOff + wb * S::wBytes;
+#pragma unroll
+                for (int i = 0; i < TILE / 16; ++i)
+                  mma_f16_ts(tmem + 256 + a * D, tmem + a * 128 + 8 * i,
+                             umma_desc(va + 2048 * i, TILE * 128, 1024, kSwizzle128B), IDESC_PV, (t > it.t0) | (i > 0));
+                if (t == end[a] - 1) umma_commit(&ofull[a]);
+              }
+              if (t + 1 < end[a]) {
+                if (!kready) {
+                  if (!kwait(n + 1)) { ok = false; break; }
+                  kready = true;
+                  tc_fence_after();
+                }
+                qk(a, (n + 1) % NK);
+              }
+            }
+            if (!ok) break;
+            umma_commit(&wempty[wb]);
+            if (t + 1 < it.t1) {
+              umma_commit(&kempty[(n + 1) % NK]);
+              if (t + 2 == it.t1) umma_commit(qfree);
+            }
+          }
+        }
+        // every issued MMA must finish before the tensor memory is released
+        umma_commit(done);
+        if (!mbar_try_wait(done, 0)) {
+          const unsigned long long t0 = globaltimer();
+          while (!mbar_try_wait(done, 0)) {
+            if (globaltimer() - t0 > kWaitLimitNs) {
+              atomicExch(&g_kernel_error, (int)KERR_TIMEOUT_FULL);
+              break;
+            }
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == W_LOAD) {
+      // ====================================================== schedule and copies
+      const int bs = 1 << p.log2_bs;
+      const int bsr = min(bs, TILE);                 // rows of a copy
+      const int ppt = TILE / bsr;                    // pages per key tile
+      const int Hk = p.num_kv_heads;
+      int k = 0, n = 0, kn = 0, vn = 0;              // items, key tiles, K and V copies issued
+      bool ok = true;
+      long long left = u1 - u0;
+      // for the combine: the item that starts here and is cut (head, row, tokens,
+      // slot); whether the first item began earlier, whether it ends here, no items
+      int4 m_start = make_int4(0, 0, 0, -1), m_cont = make_int4(0, 0, left <= 0, 0);;
+      int h = 0, r = 0, j = 0, t = 0;
+      Req rq = {0, 0, 0, 0};
+      if (left > 0) {
+        h = (int)(u0 / W);
+        r = (int)sched[16];
+        const long long off = sched[17];
+        rq = load_req(p, r, bt);
+        j = rq.find(off, bt);
+        t = (int)(off - rq.before(j, bt));
+      }
+      while (ok) {
+        Item it;
+        it.last = left <= 0;
+        if (!it.last) {
+          const int nk = rq.tiles(j, bt);
+          it.req = r;
+          it.head = h;
+          it.tok0 = rq.q0 + j * bt;
+          it.ntok = min(bt, rq.ql - j * bt);
+          it.lim0 = rq.L - rq.ql + j * bt;
+          it.L = rq.L;
+          it.t0 = t;
+          it.t1 = (int)min((long long)nk, t + left);
+          const int rows = it.ntok * p.qg;
+          const int n0 = max(it.lim0 + (min(rows, TILE) - 1) / p.qg, 0) / TILE + 1;
+          it.e0 = min(it.t1, n0);
+          it.e1 = rows > TILE ? it.t1 : it.t0;
+          const bool starts = t == 0, ends = it.t1 == nk;
+          // slot 2 b: the CTA's first item, slot 2 b + 1: its last (if another)
+          it.slot = starts && ends ? -1 : 2 * (int)blockIdx.x + (k > 0);
+          if (starts && !ends) m_start = make_int4(h, it.tok0, it.ntok, it.slot);
+          if (!starts) m_cont = make_int4(1, ends, 0, 0);
+        }
+        if (k >= IR && !warp_wait(&iempty[k % IR], (k / IR - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
+        if (lane == 0) {
+          sts_item(sb + S::iringOff + 64 * (k % IR), it);
+          mbar_arrive(&ifull[k % IR]);
+        }
+        if (it.last) break;
+        ++k;
+        left -= it.t1 - it.t0;
+
+        const int32_t* tab = p.block_table + it.req * p.table_stride;
+        const int npages = (it.L + bs - 1) >> p.log2_bs;
+        // the item's block ids, 32 at a time and the next 32 in flight
+        int win = (it.t0 * TILE) >> p.log2_bs;
+        auto entry = [&](int e) -> int { return e < npages ? __ldg(tab + e) : 0; };
+        int cur = entry(win + lane), nxt = entry(win + 32 + lane);
+        for (t = it.t0; t < it.t1; ++t, ++n) {
+          const int kb = n % NK, vb = n % NV;
+          const int e0 = (t * TILE) >> p.log2_bs;    // first page of the tile
+          if (e0 >= win + 32) {
+            cur = nxt;
+            win += 32;
+            nxt = entry(win + 32 + lane);
+          }
+          const int np = max(0, min(ppt, npages - e0));
+          int blk = __shfl_sync(0xffffffffu, cur, (e0 - win + lane) & 31);
+          if (lane < np && (blk < 0 || blk >= p.num_blocks)) {
+            atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
+            blk = 0;
+          }
+          const int y0 = bs > TILE ? (t & 1) * TILE : 0;   // 256-token pages: half a page
+          const uint32_t pb = bsr * D, tx = np * (pb + (PT ? bsr * 4 : 0));
+          if (n >= NK && !warp_wait(&kempty[kb], (n / NK - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
+          if (lane == 0) {
+            if (np) mbar_arrive_expect_tx(&kfull[kb], tx);
+            else mbar_arrive(&kfull[kb]);
+          }
+          __syncwarp();
+          if (lane < np) {
+            tma_load_3d(sb + S::kOff + kb * S::kBytes + lane * pb, &kv_map, 0, h * bs + y0, blk, &kfull[kb]);
+            if constexpr (PT)
+              bulk_load(sb + S::krawOff + 4 * (kb * TILE + lane * bsr), p.k_scale + ((long long)blk * Hk + h) * bs + y0,
+                        bsr * 4, &kfull[kb]);
+          }
+          kn = n + 1;
+          if (n >= NV && !warp_wait(&vempty[vb], (n / NV - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
+          if (lane == 0) {
+            if (np) mbar_arrive_expect_tx(&vfull[vb], tx);
+            else mbar_arrive(&vfull[vb]);
+          }
+          __syncwarp();
+          if (lane < np) {
+            tma_load_3d(sb + S::vOff + vb * S::kBytes + lane * pb, &kv_map, 0, (Hk + h) * bs + y0, blk, &vfull[vb]);
+            if constexpr (PT)
+              bulk_load(sb + S::vrawOff + 4 * (vb * TILE + lane * bsr), p.v_scale + ((long long)blk * Hk + h) * bs + y0,
+                        bsr * 4, &vfull[vb]);
+          }
+          vn = n + 1;
+        }
+        if (!ok) break;
+        // ---- next item: token range, request, head
+        t = 0;
+        if (left > 0 && ++j >= rq.nt) {
+          j = 0;
+          do {                                       // left > 0: a request with units follows
+            if (++r >= p.num_reqs) {
+              r = 0;
+              ++h;
+            }
+            rq = load_req(p, r, bt);
+          } while (rq.nt == 0 && h < Hk);
+          if (h >= Hk) left = 0;                     // (not reached while the inputs stay as they were)
+        }
+      }
+      if (lane == 0) {
+        p.meta[2 * blockIdx.x] = m_start;
+        p.meta[2 * blockIdx.x + 1] = m_cont;
+      }
+      // the copies in flight must land before the CTA exits (only after an abort
+      // are there any)
+      if (*abort_flag && lane == 0) {
+        const unsigned long long t0 = globaltimer();
+        for (int i = max(0, kn - NK); i < kn; ++i)
+          while (!mbar_try_wait(&kfull[i % NK], (i / NK) & 1) && globaltimer() - t0 < kWaitLimitNs) {}
+        for (int i = max(0, vn - NV); i < vn; ++i)
+          while (!mbar_try_wait(&vfull[i % NV], (i / NV) & 1) && globaltimer() - t0 < kWaitLimitNs) {}
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of the items that cross a cut: block (c, y) looks at the item that
+// starts in CTA c and does not end there, rows 32 y .. 32 y + 31. Its pieces are
+// the starting CTA's last slot and the first slots of the CTAs behind it.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p, const int grid) {
+  const int c = blockIdx.x;
+  const int4 ms = p.meta[2 * c];
+  if (ms.w < 0) return;
+  constexpr int TPR = D / 4, RPB = 256 / TPR;        // threads per row (4 dims each), rows per pass
+  const int col = threadIdx.x % TPR;
+  const int rows = ms.z * p.qg;
+  for (int row = blockIdx.y * 32 + threadIdx.x / TPR; row < min(rows, (int)blockIdx.y * 32 + 32); row += RPB) {
+    float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    auto piece = [&](int slot) {
+      const float2 ml = p.part_ml[(long long)slot * p.part_rows + row];
+      if (ml.y == 0.f) return;                       // the row saw no key of it, O is not written
+      const float4 x = *reinterpret_cast<const float4*>(p.part_o + ((long long)slot * p.part_rows + row) * D + 4 * col);
+      const float mn = fmaxf(M, ml.x);
+      const float a0 = ex2(M - mn), w = ml.y * ex2(ml.x - mn);
+      M = mn;
+      l = l * a0 + w;
+      o[0] = o[0] * a0 + w * x.x;
+      o[1] = o[1] * a0 + w * x.y;
+      o[2] = o[2] * a0 + w * x.z;
+      o[3] = o[3] * a0 + w * x.w;
+    };
+    piece(ms.w);
+    for (int d = c + 1; d < grid; ++d) {
+      const int4 mc = p.meta[2 * d + 1];
+      if (mc.z) continue;                            // a CTA without units
+      if (!mc.x) break;
+      piece(2 * d);
+      if (mc.y) break;
+    }
+    const float rl = l == 0.f ? 0.f : 1.f / l;
+    const int tok = row / p.qg;
+    __nv_bfloat16* dst = p.out + ((long long)(ms.y + tok) * (p.num_kv_heads * p.qg) + ms.x * p.qg + row - tok * p.qg) * D;
+    store4(dst + 4 * col, o[0] * rl, o[1] * rl, o[2] * rl, o[3] * rl);
+  }
+}
+
+namespace {
+struct Layout {
+  size_t ml, meta, total;
+  int rows;
+};
+Layout chunk_layout(int num_tokens, int qg, int D) {
+  Layout L;
+  L.rows = (int)std::min<long long>(ROWS, (long long)num_tokens * qg);
+  const size_t slots = 2 * MAX_GRID;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  L.ml = up(slots * L.rows * D * sizeof(float));
+  L.meta = L.ml + up(slots * L.rows * sizeof(float2));
+  L.total = L.meta + up(slots * sizeof(int4));
+  return L;
+}
 }  // namespace
 
-size_t chunk_workspace_bytes(int, int, int) { return 256; }
+cudaError_t take_chunk_error(int* v) {
+  const int z = 0;
+  const cudaError_t e = cudaMemcpyFromSymbol(v, g_kernel_error, sizeof(int));
+  return e == cudaSuccess && *v ? cudaMemcpyToSymbol(g_kernel_error, &z, sizeof(int)) : e;
+}
+
+size_t chunk_workspace_bytes(int num_tokens, int query_group, int head_dim) {
+  return chunk_layout(num_tokens, query_group, head_dim).total;
+}
 
 cudaError_t launch_chunk(const ChunkLaunch& a, cudaStream_t stream) {
-  int log2_bs = 0;
-  while ((1 << log2_bs) < a.block_size) ++log2_bs;
-  const long long rows = (long long)a.num_tokens * a.num_kv_heads * a.qg;
-  const long long grid = (rows + 7) / 8;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (a.head_dim == 64) chunk_simple_kernel<64><<<(unsigned)grid, 256, 0, stream>>>(a, log2_bs);
-  else chunk_simple_kernel<128><<<(unsigned)grid, 256, 0, stream>>>(a, log2_bs);
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return cudaErrorNotSupported;
+  const int D = a.head_dim, bs = a.block_size;
+  CUtensorMap map;
+  const cuuint64_t page_rows = (cuuint64_t)2 * a.num_kv_heads * bs;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, page_rows, (cuuint64_t)a.num_blocks};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, page_rows * D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)std::min(bs, TILE), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(a.kv), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const Layout L = chunk_layout(a.num_tokens, a.qg, D);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  Params p;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.block_table = a.block_table;
+  p.query_start = a.query_start;
+  p.seq_lens = a.seq_lens;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + L.ml);
+  p.meta = reinterpret_cast<int4*>(ws + L.meta);
+  p.q_stride_tok = a.q_stride_tok;
+  p.q_stride_head = a.q_stride_head;
+  p.table_stride = a.table_stride;
+  p.num_reqs = a.num_reqs;
+  p.num_tokens = a.num_tokens;
+  p.num_kv_heads = a.num_kv_heads;
+  p.qg = a.qg;
+  p.log2_bs = 0;
+  while ((1 << p.log2_bs) < bs) ++p.log2_bs;
+  p.num_blocks = a.num_blocks;
+  p.max_len = a.max_blocks * bs;
+  p.part_rows = L.rows;
+  p.softmax_scale = a.softmax_scale;
+  const int grid = std::min(a.num_sms, MAX_GRID);
+  cudaError_t e = cudaSuccess;
+  auto launch = [&](auto kernel, int smem) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) kernel<<<grid, THREADS, smem, stream>>>(map, p);
+  };
+  if (D == 64) a.per_token ? launch(pa_chunk_kernel<64, true>, Smem<64>::total) : launch(pa_chunk_kernel<64, false>, Smem<64>::total);
+  else a.per_token ? launch(pa_chunk_kernel<128, true>, Smem<128>::total) : launch(pa_chunk_kernel<128, false>, Smem<128>::total);
+  if (e != cudaSuccess) return e;
+  const dim3 cg(grid, (L.rows + 31) / 32);
+  if (D == 64) chunk_combine_kernel<64><<<cg, 256, 0, stream>>>(p, grid);
+  else chunk_combine_kernel<128><<<cg, 256, 0, stream>>>(p, grid);
   return cudaGetLastError();
 }
 

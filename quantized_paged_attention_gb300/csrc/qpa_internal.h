@@ -186,6 +186,8 @@ cudaError_t launch_slot_map(const SlotMapLaunch& a, cudaStream_t stream);
 cudaError_t launch_append(const AppendLaunch& a, cudaStream_t stream);
 // Workspace bytes of a chunk launch (independent of the device).
 size_t chunk_workspace_bytes(int num_tokens, int query_group, int head_dim);
+// Reads and clears the chunk kernel's own error word of the current device.
+cudaError_t take_chunk_error(int* v);
 cudaError_t launch_chunk(const ChunkLaunch& a, cudaStream_t stream);
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
