@@ -424,70 +424,83 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       const Item it = lds_item(sb + S::iringOff + 64 * (k % IR));
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[k % IR]);
+      // ---- query operand: LPR lanes per row, 8 dims each; batches of UN loads,
+      // two batches in flight, the first two issued before the operand is free
+      constexpr int LPR = D / 8, RPW = 32 / LPR, UN = 4, BATCH = UN * 4 * RPW;   // rows per batch
+      const int part = lane % LPR;
+      const int rows = it.last ? 0 : it.ntok * G;
+      const int nb = it.last ? 0 : (rows > TILE ? ROWS : TILE) / BATCH;
+      auto load = [&](int b, uint4 (&x)[UN]) {
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          const int row = b * BATCH + (u * 4 + cw) * RPW + lane / LPR;
+          x[u] = make_uint4(0, 0, 0, 0);
+          if (row < rows) {
+            const int tok = row / G;
+            x[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (it.tok0 + tok) * p.q_stride_tok +
+                                                        (long long)(it.head * G + row - tok * G) * p.q_stride_head) + part);
+          }
+        }
+      };
+      auto build = [&](int b, const uint4 (&x)[UN]) {
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          const int row = b * BATCH + (u * 4 + cw) * RPW + lane / LPR;
+          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          float y[8], mx = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[2 * i] = __uint_as_float(w[i] << 16);
+            y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            mx = fmaxf(mx, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+          }
+#pragma unroll
+          for (int o = LPR / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          // 2^(7 - floor(log2 max)), and its inverse for the logits; rows below
+          // 2^-119 keep fewer bits (their logits vanish)
+          const int e = max((int)(__float_as_uint(mx) >> 23), 8);
+          const bool inf = e >= 255;
+          const float f = __uint_as_float(((uint32_t)(inf ? 127 : 261 - e) << 23) | neg);
+          if (part == 0) {
+            float cm = fabsf(base) * __uint_as_float((uint32_t)(inf ? 127 : e - 7) << 23);
+            // a masked score must stay -inf when multiplied; an infinite query gives a NaN row
+            if (cm == 0.f) cm = 1.17549435e-38f;
+            if (inf) cm = __uint_as_float(0x7fffffffu);
+            stsf(sb + S::crowOff + 4 * (qb * ROWS + row), cm);
+          }
+          // the scaled value in f16 (exact from 2^-14 up, 8 bits of 11; within
+          // 2^-25 below), its e4m3, and the e4m3 of what is left
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t z0 = f32x2_to_f16x2(y[4 * i] * f, y[4 * i + 1] * f);
+            const uint32_t z1 = f32x2_to_f16x2(y[4 * i + 2] * f, y[4 * i + 3] * f);
+            const uint32_t h0 = f16x2_to_e4m3x2(z0), h1 = f16x2_to_e4m3x2(z1);
+            hi[i] = prmt(h0, h1, 0x5410u);
+            lo[i] = prmt(f16x2_to_e4m3x2(hsub2(z0, e4m3x2_lo_to_f16x2(h0))),
+                         f16x2_to_e4m3x2(hsub2(z1, e4m3x2_lo_to_f16x2(h1))), 0x5410u);
+          }
+          const int tr = row & 127;
+          const uint32_t swz = D == 128 ? (tr & 7) : ((tr >> 1) & 3);
+          const uint32_t dst = sb + S::qOff + (row >> 7) * 2 * S::qTerm + tr * D + (((part >> 1) ^ swz) << 4) + (part & 1) * 8;
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + S::qTerm), "r"(lo[0]), "r"(lo[1]) : "memory");
+        }
+      };
+      uint4 x0[UN], x1[UN];
+      if (nb) {
+        load(0, x0);
+        load(1, x1);
+      }
       if (k >= 2 && !warp_wait(&qread[qb], ((k >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       if (k >= 1 && !warp_wait(qfree, (k - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       if (!it.last) {
-        // ---- query operand: LPR lanes per row, 8 dims each
-        constexpr int LPR = D / 8, RPW = 32 / LPR;
-        const int part = lane % LPR;
-        const int rows = it.ntok * G;
-        const int rlim = rows > TILE ? ROWS : TILE;
-        constexpr int UN = 4;
-        for (int rr = cw * RPW + lane / LPR; rr < rlim; rr += UN * 4 * RPW) {
-          uint4 xv[UN];
-#pragma unroll
-          for (int u = 0; u < UN; ++u) {
-            const int row = rr + u * 4 * RPW;
-            xv[u] = make_uint4(0, 0, 0, 0);
-            if (row < rows) {
-              const int tok = row / G;
-              xv[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (it.tok0 + tok) * p.q_stride_tok +
-                                                           (long long)(it.head * G + row - tok * G) * p.q_stride_head) + part);
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < UN; ++u) {
-            const int row = rr + u * 4 * RPW;
-            const uint32_t w[4] = {xv[u].x, xv[u].y, xv[u].z, xv[u].w};
-            float y[8], mx = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              y[2 * i] = __uint_as_float(w[i] << 16);
-              y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-              mx = fmaxf(mx, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
-            }
-#pragma unroll
-            for (int o = LPR / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            // 2^(7 - floor(log2 max)), and its inverse for the logits; rows below
-            // 2^-119 keep fewer bits (their logits vanish)
-            const int e = max((int)(__float_as_uint(mx) >> 23), 8);
-            const bool inf = e >= 255;
-            const float f = __uint_as_float(((uint32_t)(inf ? 127 : 261 - e) << 23) | neg);
-            if (part == 0) {
-              float cm = fabsf(base) * __uint_as_float((uint32_t)(inf ? 127 : e - 7) << 23);
-              // a masked score must stay -inf when multiplied; an infinite query gives a NaN row
-              if (cm == 0.f) cm = 1.17549435e-38f;
-              if (inf) cm = __uint_as_float(0x7fffffffu);
-              stsf(sb + S::crowOff + 4 * (qb * ROWS + row), cm);
-            }
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float z[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) z[j] = y[4 * i + j] * f;
-              const uint32_t h0 = f32x2_to_e4m3x2(z[0], z[1]), h1 = f32x2_to_e4m3x2(z[2], z[3]);
-              const uint32_t g0 = e4m3x2_lo_to_f16x2(h0), g1 = e4m3x2_lo_to_f16x2(h1);
-              hi[i] = prmt(h0, h1, 0x5410u);
-              lo[i] = prmt(f32x2_to_e4m3x2(z[0] - f16_lo_to_f32(g0), z[1] - f16_hi_to_f32(g0)),
-                           f32x2_to_e4m3x2(z[2] - f16_lo_to_f32(g1), z[3] - f16_hi_to_f32(g1)), 0x5410u);
-            }
-            const int tr = row & 127;
-            const uint32_t swz = D == 128 ? (tr & 7) : ((tr >> 1) & 3);
-            const uint32_t dst = sb + S::qOff + (row >> 7) * 2 * S::qTerm + tr * D + (((part >> 1) ^ swz) << 4) + (part & 1) * 8;
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + S::qTerm), "r"(lo[0]), "r"(lo[1]) : "memory");
-          }
+#pragma unroll 1
+        for (int b = 0; b < nb; b += 2) {
+          build(b, x0);
+          if (b + 2 < nb) load(b + 2, x0);
+          build(b + 1, x1);
+          if (b + 2 < nb) load(b + 3, x1);
         }
         fence_proxy_async();
       }
@@ -597,71 +610,80 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
     reg_dec<48>();
     if (warp == W_MMA) {
       // ====================================================== MMA warp
-      if (lane == 0) {
-        int n = 0, pc[2] = {0, 0};
-        bool ok = true;
-        const uint32_t qa = sb + S::qOff;
-        auto qk = [&](int a, int kb) {
-          // two query terms into one accumulator
-          const uint32_t ka = sb + S::kOff + kb * S::kBytes;
+      // the whole warp walks and waits, one elected lane issues
+      int n = 0, pc[2] = {0, 0};
+      bool ok = true;
+      constexpr uint32_t HI = desc_hi(SBO, SWZ), HI_V = desc_hi(1024, kSwizzle128B);
+      const uint32_t q_lo = desc_lo(sb + S::qOff, 16), k_lo = desc_lo(sb + S::kOff, 16), v_lo = desc_lo(sb + S::wOff, TILE * 128);
+      // two query terms into one accumulator
+      auto qk = [&](int a, int kb) {
+        const uint32_t ql = q_lo + a * (2 * S::qTerm / 16), kl = k_lo + kb * (S::kBytes / 16);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              mma_e4m3(tmem + a * 128, umma_desc(qa + (2 * a + j) * S::qTerm + 32 * i, 16, SBO, SWZ),
-                       umma_desc(ka + 32 * i, 16, SBO, SWZ), IDESC_QK, j | i);
-          umma_commit(&sfull[a]);
-        };
-        auto kwait = [&](int nn) -> bool {
-          return role_wait(&kfull[nn % NK], (nn / NK) & 1, abort_flag, KERR_TIMEOUT_FULL);
-        };
-        for (int k = 0; ok; ++k) {
-          const int qb = k & 1;
-          if (!role_wait(&qfull[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
-          const Item it = lds_item(sb + S::qinfoOff + 64 * qb);
-          mbar_arrive(&qread[qb]);
-          if (it.last) break;
-          const int end[2] = {it.e0, it.e1};
-          if (!kwait(n)) break;
-          tc_fence_after();
-          if (it.t0 < end[0]) qk(0, n % NK);
-          if (it.t0 < end[1]) qk(1, n % NK);
+          for (int i = 0; i < D / 32; ++i)
+            mma_e4m3_ss(tmem + a * 128, ql + j * (S::qTerm / 16) + 2 * i, HI, kl + 2 * i, HI, IDESC_QK, j | i);
+        umma_commit(&sfull[a]);
+      };
+      auto kwait = [&](int nn) -> bool { return warp_wait(&kfull[nn % NK], (nn / NK) & 1, abort_flag, KERR_TIMEOUT_FULL); };
+      for (int k = 0; ok; ++k) {
+        const int qb = k & 1;
+        if (!warp_wait(&qfull[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+        const Item it = lds_item(sb + S::qinfoOff + 64 * qb);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qread[qb]);
+        if (it.last) break;
+        if (!kwait(n)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (it.t0 < it.e0) qk(0, n % NK);
+          if (it.t0 < it.e1) qk(1, n % NK);
           umma_commit(&kempty[n % NK]);
           if (it.t0 + 1 == it.t1) umma_commit(qfree);
-          for (int t = it.t0; t < it.t1; ++t, ++n) {
-            const int wb = n % NW;
-            if (!role_wait(&wfull[wb], (n / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-            bool kready = false;
+        }
+        __syncwarp();
+        for (int t = it.t0; t < it.t1; ++t, ++n) {
+          const int wb = n % NW;
+          if (!warp_wait(&wfull[wb], (n / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+          bool kready = false;
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              if (t < end[a]) {
-                if (!role_wait(&pfull[a], pc[a] & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-                ++pc[a];
-                tc_fence_after();
-                const uint32_t va = sb + S::wOff + wb * S::wBytes;
+          for (int a = 0; a < 2; ++a) {
+            const int end = a ? it.e1 : it.e0;
+            if (t >= end) continue;
+            if (!warp_wait(&pfull[a], pc[a] & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+            ++pc[a];
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t vl = v_lo + wb * (S::wBytes / 16);
 #pragma unroll
-                for (int i = 0; i < TILE / 16; ++i)
-                  mma_f16_ts(tmem + 256 + a * D, tmem + a * 128 + 8 * i,
-                             umma_desc(va + 2048 * i, TILE * 128, 1024, kSwizzle128B), IDESC_PV, (t > it.t0) | (i > 0));
-                if (t == end[a] - 1) umma_commit(&ofull[a]);
-              }
-              if (t + 1 < end[a]) {
-                if (!kready) {
-                  if (!kwait(n + 1)) { ok = false; break; }
-                  kready = true;
-                  tc_fence_after();
-                }
-                qk(a, (n + 1) % NK);
-              }
+              for (int i = 0; i < TILE / 16; ++i)
+                mma_f16_ts(tmem + 256 + a * D, tmem + a * 128 + 8 * i, vl + 128 * i, HI_V, IDESC_PV,
+                           i > 0 ? 1u : (uint32_t)(t > it.t0));
+              if (t == end - 1) umma_commit(&ofull[a]);
             }
-            if (!ok) break;
+            __syncwarp();
+            if (t + 1 < end) {
+              if (!kready) {
+                if (!kwait(n + 1)) { ok = false; break; }
+                kready = true;
+                tc_fence_after();
+              }
+              if (elect_one()) qk(a, (n + 1) % NK);
+              __syncwarp();
+            }
+          }
+          if (!ok) break;
+          if (elect_one()) {
             umma_commit(&wempty[wb]);
             if (t + 1 < it.t1) {
               umma_commit(&kempty[(n + 1) % NK]);
               if (t + 2 == it.t1) umma_commit(qfree);
             }
           }
+          __syncwarp();
         }
+      }
+      if (elect_one()) {
         // every issued MMA must finish before the tensor memory is released
         umma_commit(done);
         if (!mbar_try_wait(done, 0)) {

@@ -56,13 +56,32 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
 // Instruction descriptor for kind::f16 with f16 A and B and an f32 accumulator
 // (the type fields are 0, as for e4m3 in kind::f8f6f4).
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool a_mn, bool b_mn) { return idesc_e4m3(m, n, a_mn, b_mn); }
+// The same two products with descriptors as 32-bit halves (umma_desc split): the
+// high half does not depend on the address, so a step along an operand is one
+// 32-bit addition of its bytes / 16 to the low half.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16); }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swz) { return (sbo >> 4) | (1u << 14) | (swz << 29); }
+__device__ __forceinline__ void mma_e4m3_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %6, 0; mov.b64 a, {%1, %2}; mov.b64 b, {%3, %4}; "
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p; }"
+      ::"r"(d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem], f16 operands, issued by one thread. A: lane =
 // row, a 32-bit column holds elements 2c (low half) and 2c + 1.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                           uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+      "{ .reg .pred p; .reg .b64 b; setp.ne.b32 p, %5, 0; mov.b64 b, {%2, %3}; "
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }"
+      ::"r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
+}
+// One lane of a converged warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(ok));
+  return ok != 0;
 }
 // Arrive once on the mbarrier when every MMA issued so far by this thread
 // has completed.
