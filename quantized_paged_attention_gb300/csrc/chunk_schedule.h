@@ -19,27 +19,33 @@ namespace chunk {
 constexpr int TILE = 128;            // keys per unit, rows per row tile
 
 // sum_{i < n} floor((a i + b) / m) for a, b >= 0 (the lattice points under a
-// line, by a Euclid-like reduction)
-QPA_HD inline long long floor_sum(long long n, long long m, long long a, long long b) {
+// line, by a Euclid-like reduction). T: 32 bits where a n + b and m fit (the
+// divisions are most of the work), else 64.
+template <typename T>
+QPA_HD inline long long floor_sum_t(T n, T m, T a, T b) {
   long long s = 0;
   while (n > 0) {
     if (a >= m) {
-      s += n * (n - 1) / 2 * (a / m);
+      s += (long long)n * (n - 1) / 2 * (a / m);
       a %= m;
     }
     if (b >= m) {
-      s += n * (b / m);
+      s += (long long)n * (b / m);
       b %= m;
     }
-    const long long y = a * n + b;
+    const T y = a * n + b;
     if (y < m) break;
     n = y / m;
     b = y % m;
-    const long long t = m;
+    const T t = m;
     m = a;
     a = t;
   }
   return s;
+}
+QPA_HD inline long long floor_sum(long long n, long long m, long long a, long long b) {
+  if (a * n + b <= 0x7fffffffLL) return floor_sum_t<unsigned>((unsigned)n, (unsigned)m, (unsigned)a, (unsigned)b);
+  return floor_sum_t<long long>(n, m, a, b);
 }
 
 // One request as the schedule sees it: first query row, rows, cached tokens
@@ -59,16 +65,9 @@ struct Req {
     return j + floor_sum(j - i0, TILE, bt, d + (long long)(i0 + 1) * bt - 1);
   }
   QPA_HD long long units(int bt) const { return nt ? before(nt - 1, bt) + tiles(nt - 1, bt) : 0; }
-  // the item that holds unit off (0 <= off < units)
-  QPA_HD int find(long long off, int bt) const {
-    int lo = 0, hi = nt;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (before(mid, bt) <= off) lo = mid;
-      else hi = mid;
-    }
-    return lo;
-  }
+  // One step of the search for the item that holds unit off, which lies in
+  // [lo, hi): whether probe i of 32 splits it at or before off, and where that is
+  QPA_HD static int split(int lo, int hi, int i) { return lo + (int)((long long)(hi - lo) * (i + 1) / 33); }
 };
 
 QPA_HD inline Req make_req(int start, int next, int len, int num_tokens, int max_len, int bt) {

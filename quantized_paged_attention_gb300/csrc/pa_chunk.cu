@@ -49,7 +49,7 @@ namespace chunk {
 constexpr int ROWS = 256;            // query rows per item (two tiles)
 constexpr int MAX_GRID = 160;        // CTAs at most (bounds the workspace)
 constexpr int THREADS = 512;
-constexpr int W_CONV = 8, W_MMA = 12, W_LOAD = 13;
+constexpr int W_CONV = 8, W_MMA = 12, W_LOAD = 13, W_PREF = 14;
 constexpr int NK = 3, NV = 2, NW = 2;   // stages of K, V bytes, V f16
 constexpr int IR = 4;                // item ring
 constexpr float kNoMax = -1e30f;     // running maximum of a row that has seen no token
@@ -153,7 +153,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
   uint64_t* wfull = vempty + NV;       // [NW] V f16 written (4 warps)
   uint64_t* wempty = wfull + NW;       // [NW] V f16 read (MMA commit)
   uint64_t* ifull = wempty + NW;       // [IR] item published
-  uint64_t* iempty = ifull + IR;       // [IR] item read (4 warps)
+  uint64_t* iempty = ifull + IR;       // [IR] item read (4 converting warps, prefetch warp)
   uint64_t* qfull = iempty + IR;       // [2] query operand built, item passed on (4 warps)
   uint64_t* qread = qfull + 2;         // [2] item read (8 softmax warps, MMA)
   uint64_t* qfree = qread + 2;         // query operand read (MMA commit)
@@ -169,7 +169,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
     for (int i = 0; i < NK; ++i) { mbar_init(&kfull[i], 1); mbar_init(&kempty[i], PT ? 5 : 1); }
     for (int i = 0; i < NV; ++i) { mbar_init(&vfull[i], 1); mbar_init(&vempty[i], 4); }
     for (int i = 0; i < NW; ++i) { mbar_init(&wfull[i], 4); mbar_init(&wempty[i], 1); }
-    for (int i = 0; i < IR; ++i) { mbar_init(&ifull[i], 1); mbar_init(&iempty[i], 4); }
+    for (int i = 0; i < IR; ++i) { mbar_init(&ifull[i], 1); mbar_init(&iempty[i], 5); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 4);
       mbar_init(&qread[i], 9);
@@ -187,6 +187,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
 
   // ---- schedule: this CTA's range [u0, u1) of the units, its first request
   const int bt = ROWS / p.qg;                      // tokens per item
+  const uint32_t gm = (65535u + p.qg) / p.qg;      // row / G = row * gm >> 16 for row < 256
   long long* sched = reinterpret_cast<long long*>(sm + S::schedOff);   // [16] warp sums, then the start
   long long W;
   long long u0, u1;
@@ -235,7 +236,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
 
   if (warp < W_CONV) {
     // ======================================================== softmax warps
-    reg_inc<192>();
+    reg_inc<184>();
     const int a = warp >> 2;                       // row tile
     const int row = a * TILE + (threadIdx.x & 127);
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -253,7 +254,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       if (lane == 0) mbar_arrive(&qread[qb]);
       if (it.last) break;
       const int end = a ? it.e1 : it.e0;
-      const int tok = row / G;
+      const int tok = (int)(row * gm >> 16);
       const bool valid = tok < it.ntok;
       const int lim = valid ? it.lim0 + tok : -1;
       float m = kNoMax, l = 0.f;
@@ -436,7 +437,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
           const int row = b * BATCH + (u * 4 + cw) * RPW + lane / LPR;
           x[u] = make_uint4(0, 0, 0, 0);
           if (row < rows) {
-            const int tok = row / G;
+            const int tok = (int)(row * gm >> 16);
             x[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (it.tok0 + tok) * p.q_stride_tok +
                                                         (long long)(it.head * G + row - tok * G) * p.q_stride_head) + part);
           }
@@ -607,7 +608,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       }
     }
   } else {
-    reg_dec<48>();
+    reg_dec<64>();
     if (warp == W_MMA) {
       // ====================================================== MMA warp
       // the whole warp walks and waits, one elected lane issues
@@ -716,7 +717,15 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
         r = (int)sched[16];
         const long long off = sched[17];
         rq = load_req(p, r, bt);
-        j = rq.find(off, bt);
+        int lo = 0, hi = rq.nt;                      // the item that holds unit off of the request
+        while (hi - lo > 1) {
+          const int probe = Req::split(lo, hi, lane);
+          const int below = __popc(__ballot_sync(0xffffffffu, rq.before(probe, bt) <= off));
+          const int l = __shfl_sync(0xffffffffu, probe, max(below - 1, 0)), h2 = __shfl_sync(0xffffffffu, probe, below & 31);
+          lo = below > 0 ? l : lo;
+          hi = below < 32 ? h2 : hi;
+        }
+        j = lo;
         t = (int)(off - rq.before(j, bt));
       }
       while (ok) {
@@ -829,6 +838,26 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
           while (!mbar_try_wait(&vfull[i % NV], (i / NV) & 1) && globaltimer() - t0 < kWaitLimitNs) {}
       }
       __syncwarp();
+    } else if (warp == W_PREF) {
+      // ====================================================== query rows to L2
+      // An item is published some key tiles before its query operand is built;
+      // from DRAM the 64 KB of rows, 16 KB in flight, took 10 us, all of it with
+      // the tensor core idle.
+      for (int k = 0;; ++k) {
+        if (!warp_wait(&ifull[k % IR], (k / IR) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+        const Item it = lds_item(sb + S::iringOff + 64 * (k % IR));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&iempty[k % IR]);
+        if (it.last) break;
+        constexpr int LPR = D / 64;                  // 128-byte lines per row (16-byte aligned rows may touch one more)
+        const int rows = it.ntok * p.qg;
+        for (int i = lane; i < rows * LPR; i += 32) {
+          const int row = i / LPR, tok = (int)(row * gm >> 16);
+          const uint16_t* src = p.q + (it.tok0 + tok) * p.q_stride_tok +
+                                (long long)(it.head * p.qg + row - tok * p.qg) * p.q_stride_head + (i % LPR) * 64;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+        }
+      }
     }
   }
 
