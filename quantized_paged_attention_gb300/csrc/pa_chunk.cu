@@ -416,7 +416,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
     const int cw = warp - W_CONV;
     const int G = p.qg;
     const float base = p.softmax_scale * (PT ? 1.f : __ldg(p.k_scale)) * kLog2e;
-    const uint32_t neg = base < 0.f ? 0x80000000u : 0u;
+    const uint32_t neg = base < 0.f ? 0x8000u : 0u;
     int n = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -425,70 +425,78 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       const Item it = lds_item(sb + S::iringOff + 64 * (k % IR));
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[k % IR]);
-      // ---- query operand: LPR lanes per row, 8 dims each; batches of UN loads,
-      // two batches in flight, the first two issued before the operand is free
-      constexpr int LPR = D / 8, RPW = 32 / LPR, UN = 4, BATCH = UN * 4 * RPW;   // rows per batch
+      // ---- query operand: LPR lanes per row, 32 dims each; a step is RPS rows of
+      // the four warps, two steps in flight, the first two issued before the
+      // operand's space is free. (8 dims per lane, with four times the shuffles
+      // and a chain per row, took 10 us per item.)
+      constexpr int LPR = D / 32, RPW = 32 / LPR, RPS = 4 * RPW;
       const int part = lane % LPR;
       const int rows = it.last ? 0 : it.ntok * G;
-      const int nb = it.last ? 0 : (rows > TILE ? ROWS : TILE) / BATCH;
-      auto load = [&](int b, uint4 (&x)[UN]) {
+      const int nb = it.last ? 0 : (rows > TILE ? ROWS : TILE) / RPS;
+      auto load = [&](int b, uint4 (&x)[4]) {
+        const int row = b * RPS + cw * RPW + lane / LPR;
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-          const int row = b * BATCH + (u * 4 + cw) * RPW + lane / LPR;
-          x[u] = make_uint4(0, 0, 0, 0);
-          if (row < rows) {
-            const int tok = (int)(row * gm >> 16);
-            x[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (it.tok0 + tok) * p.q_stride_tok +
-                                                        (long long)(it.head * G + row - tok * G) * p.q_stride_head) + part);
-          }
+        for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
+        if (row < rows) {
+          const int tok = (int)(row * gm >> 16);
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (it.tok0 + tok) * p.q_stride_tok +
+                                                            (long long)(it.head * G + row - tok * G) * p.q_stride_head) + 4 * part;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = __ldg(src + i);
         }
       };
-      auto build = [&](int b, const uint4 (&x)[UN]) {
+      auto build = [&](int b, const uint4 (&x)[4]) {
+        const int row = b * RPS + cw * RPW + lane / LPR;
+        const uint32_t w[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
+                                x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
+        // largest |q| by its bits (NaN counts as above infinity)
+        uint32_t mx = 0;
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-          const int row = b * BATCH + (u * 4 + cw) * RPW + lane / LPR;
-          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-          float y[8], mx = 0.f;
+        for (int i = 0; i < 16; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(mx) : "r"(w[i] & 0x7fff7fffu));
+        mx = max(mx & 0xffffu, mx >> 16);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            y[2 * i] = __uint_as_float(w[i] << 16);
-            y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            mx = fmaxf(mx, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+        for (int o = LPR / 2; o >= 1; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        // 2^(7 - floor(log2 max)) and its inverse for the logits; rows below
+        // 2^-119 keep fewer bits (their logits vanish)
+        const uint32_t e = max(mx >> 7, 8u);
+        const bool inf = e >= 255;
+        if (part == 0) {
+          float cm = fabsf(base) * __uint_as_float((inf ? 127u : e - 7) << 23);
+          // a masked score must stay -inf when multiplied; a query that is not finite gives a NaN row
+          if (cm == 0.f) cm = 1.17549435e-38f;
+          if (inf) cm = __uint_as_float(0x7fffffffu);
+          stsf(sb + S::crowOff + 4 * (qb * ROWS + row), cm);
+        }
+        const uint32_t f1 = ((inf ? 127u : 261 - e) << 7) | neg;
+        const uint32_t f2 = f1 | (f1 << 16);
+        const int tr = row & 127;
+        const uint32_t swz = D == 128 ? (tr & 7) : ((tr >> 1) & 3);
+        const uint32_t dst = sb + S::qOff + (row >> 7) * 2 * S::qTerm + tr * D;
+        // the scaled value in f16 (exact from 2^-17 up: 8 bits of 11, within
+        // 2^-25 below), its e4m3, and the e4m3 of what is left
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t z[2], h[2], g[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t y;
+              asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w[8 * i + 2 * j + u]), "r"(f2));
+              z[u] = f32x2_to_f16x2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+              h[u] = f16x2_to_e4m3x2(z[u]);
+              g[u] = f16x2_to_e4m3x2(hsub2(z[u], e4m3x2_lo_to_f16x2(h[u])));
+            }
+            hi[j] = prmt(h[0], h[1], 0x5410u);
+            lo[j] = prmt(g[0], g[1], 0x5410u);
           }
-#pragma unroll
-          for (int o = LPR / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          // 2^(7 - floor(log2 max)), and its inverse for the logits; rows below
-          // 2^-119 keep fewer bits (their logits vanish)
-          const int e = max((int)(__float_as_uint(mx) >> 23), 8);
-          const bool inf = e >= 255;
-          const float f = __uint_as_float(((uint32_t)(inf ? 127 : 261 - e) << 23) | neg);
-          if (part == 0) {
-            float cm = fabsf(base) * __uint_as_float((uint32_t)(inf ? 127 : e - 7) << 23);
-            // a masked score must stay -inf when multiplied; an infinite query gives a NaN row
-            if (cm == 0.f) cm = 1.17549435e-38f;
-            if (inf) cm = __uint_as_float(0x7fffffffu);
-            stsf(sb + S::crowOff + 4 * (qb * ROWS + row), cm);
-          }
-          // the scaled value in f16 (exact from 2^-14 up, 8 bits of 11; within
-          // 2^-25 below), its e4m3, and the e4m3 of what is left
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t z0 = f32x2_to_f16x2(y[4 * i] * f, y[4 * i + 1] * f);
-            const uint32_t z1 = f32x2_to_f16x2(y[4 * i + 2] * f, y[4 * i + 3] * f);
-            const uint32_t h0 = f16x2_to_e4m3x2(z0), h1 = f16x2_to_e4m3x2(z1);
-            hi[i] = prmt(h0, h1, 0x5410u);
-            lo[i] = prmt(f16x2_to_e4m3x2(hsub2(z0, e4m3x2_lo_to_f16x2(h0))),
-                         f16x2_to_e4m3x2(hsub2(z1, e4m3x2_lo_to_f16x2(h1))), 0x5410u);
-          }
-          const int tr = row & 127;
-          const uint32_t swz = D == 128 ? (tr & 7) : ((tr >> 1) & 3);
-          const uint32_t dst = sb + S::qOff + (row >> 7) * 2 * S::qTerm + tr * D + (((part >> 1) ^ swz) << 4) + (part & 1) * 8;
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + S::qTerm), "r"(lo[0]), "r"(lo[1]) : "memory");
+          const uint32_t at = dst + (((2 * part + i) ^ swz) << 4);
+          sts_i4(at, make_int4(hi[0], hi[1], hi[2], hi[3]));
+          sts_i4(at + S::qTerm, make_int4(lo[0], lo[1], lo[2], lo[3]));
         }
       };
-      uint4 x0[UN], x1[UN];
+      uint4 x0[4], x1[4];
       if (nb) {
         load(0, x0);
         load(1, x1);
