@@ -12,6 +12,11 @@ namespace qpa { namespace chunk { using std::max; using std::min; } }
 #else
 #define QPA_HD __host__ __device__
 #endif
+#ifdef __CUDACC__
+#define QPA_HD_CALL __host__ __device__ __noinline__   // cold code, once per kernel
+#else
+#define QPA_HD_CALL
+#endif
 
 namespace qpa {
 namespace chunk {
@@ -43,7 +48,7 @@ QPA_HD inline long long floor_sum_t(T n, T m, T a, T b) {
   }
   return s;
 }
-QPA_HD inline long long floor_sum(long long n, long long m, long long a, long long b) {
+QPA_HD_CALL inline long long floor_sum(long long n, long long m, long long a, long long b) {
   if (a * n + b <= 0x7fffffffLL) return floor_sum_t<unsigned>((unsigned)n, (unsigned)m, (unsigned)a, (unsigned)b);
   return floor_sum_t<long long>(n, m, a, b);
 }
@@ -58,10 +63,10 @@ struct Req {
     return max(L - ql + last, 0) / TILE + 1;
   }
   // units of items 0 .. j-1 (j < nt: all of them have bt tokens)
-  QPA_HD long long before(int j, int bt) const {
-    const long long d = (long long)L - ql;
+  QPA_HD_CALL long long before(int j, int bt) const {
+    const int d = L - ql;
     // items whose last row sees nothing, d + (i + 1) bt - 1 < 0: one unit each
-    const int i0 = d + bt - 1 >= 0 ? 0 : (int)min((long long)j, (-d) / bt);
+    const int i0 = d >= 1 - bt ? 0 : min(j, -d / bt);
     return j + floor_sum(j - i0, TILE, bt, d + (long long)(i0 + 1) * bt - 1);
   }
   QPA_HD long long units(int bt) const { return nt ? before(nt - 1, bt) + tiles(nt - 1, bt) : 0; }

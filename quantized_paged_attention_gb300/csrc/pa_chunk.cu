@@ -51,6 +51,7 @@ constexpr int MAX_GRID = 160;        // CTAs at most (bounds the workspace)
 constexpr int THREADS = 512;
 constexpr int W_CONV = 8, W_MMA = 12, W_LOAD = 13, W_PREF = 14;
 constexpr int NK = 3, NV = 2, NW = 2;   // stages of K, V bytes, V f16
+constexpr int NC = 4;                // stages of the per-token scales for the softmax
 constexpr int IR = 4;                // item ring
 constexpr float kNoMax = -1e30f;     // running maximum of a row that has seen no token
 constexpr float kLazy = 8.f;         // growth of the maximum (log2) that rescales
@@ -67,15 +68,15 @@ struct Smem {
   static constexpr int crowOff = nanOff + NW * TILE * (D / 8);    // [2][256] logit multiplier of a row
   static constexpr int krawOff = crowOff + 2 * ROWS * 4;          // [NK][128] per-token scales as copied
   static constexpr int vrawOff = krawOff + NK * TILE * 4;
-  static constexpr int kscOff = vrawOff + NV * TILE * 4;          // [NW][128] for the softmax
-  static constexpr int vscOff = kscOff + NW * TILE * 4;
-  static constexpr int iringOff = vscOff + NW * TILE * 4;         // [IR] 64 bytes
+  static constexpr int kscOff = vrawOff + NV * TILE * 4;          // [NC][128] for the softmax
+  static constexpr int vscOff = kscOff + NC * TILE * 4;
+  static constexpr int iringOff = vscOff + NC * TILE * 4;         // [IR] 64 bytes
   static constexpr int qinfoOff = iringOff + IR * 64;             // [2] 64 bytes
   static constexpr int flagOff = qinfoOff + 2 * 64;               // [NW][4 warps] NaN seen
-  static constexpr int evOff = flagOff + NW * 16;                 // [NW] exponent of the V scales (16 bytes)
+  static constexpr int evOff = flagOff + NW * 16;                 // [NC] exponent of the V scales (16 bytes)
   static constexpr int schedOff = evOff + 16;                     // schedule scratch
   static constexpr int barOff = schedOff + 256;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + 2 * IR + 4 + 1 + 6 + 1;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 4 + 1 + 6 + 1;
   static constexpr int miscOff = barOff + NBAR * 8;
   static constexpr int total = miscOff + 16 + 1024;
   static_assert(total <= 227 * 1024, "shared memory");
@@ -152,7 +153,8 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
   uint64_t* vempty = vfull + NV;       // [NV] V bytes read (4 warps)
   uint64_t* wfull = vempty + NV;       // [NW] V f16 written (4 warps)
   uint64_t* wempty = wfull + NW;       // [NW] V f16 read (MMA commit)
-  uint64_t* ifull = wempty + NW;       // [IR] item published
+  uint64_t* cfull = wempty + NW;       // [NC] scales written (4 warps, per-token scales only)
+  uint64_t* ifull = cfull + NC;        // [IR] item published
   uint64_t* iempty = ifull + IR;       // [IR] item read (4 converting warps, prefetch warp)
   uint64_t* qfull = iempty + IR;       // [2] query operand built, item passed on (4 warps)
   uint64_t* qread = qfull + 2;         // [2] item read (8 softmax warps, MMA)
@@ -169,6 +171,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
     for (int i = 0; i < NK; ++i) { mbar_init(&kfull[i], 1); mbar_init(&kempty[i], PT ? 5 : 1); }
     for (int i = 0; i < NV; ++i) { mbar_init(&vfull[i], 1); mbar_init(&vempty[i], 4); }
     for (int i = 0; i < NW; ++i) { mbar_init(&wfull[i], 4); mbar_init(&wempty[i], 1); }
+    for (int i = 0; i < NC; ++i) mbar_init(&cfull[i], 4);
     for (int i = 0; i < IR; ++i) { mbar_init(&ifull[i], 1); mbar_init(&iempty[i], 5); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 4);
@@ -195,6 +198,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
     const int per = (p.num_reqs + THREADS - 1) / THREADS;
     const int r0 = threadIdx.x * per, r1 = min(p.num_reqs, r0 + per);
     long long mine = 0;
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) mine += load_req(p, r, bt).units(bt);
     long long incl = mine;
 #pragma unroll
@@ -212,10 +216,10 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       W += sched[w];
     }
     const long long U = W * p.num_kv_heads;
-    u0 = U * blockIdx.x / gridDim.x;
-    u1 = U * (blockIdx.x + 1) / gridDim.x;
+    u0 = div_nonneg(U * blockIdx.x, gridDim.x);
+    u1 = div_nonneg(U * (blockIdx.x + 1), gridDim.x);
     if (u0 < u1) {
-      long long off = u0 - u0 / W * W - (base + incl - mine);
+      long long off = u0 - div_nonneg(u0, W) * W - (base + incl - mine);
       if (off >= 0 && off < mine) {
         int r = r0;
         while (true) {                             // ends: off lies below this thread's sum
@@ -263,19 +267,18 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) nan[i] = 0;
       for (int t = it.t0; t < end; ++t, ++sc) {
-        const int nn = n + t - it.t0, wb = nn % NW;
+        const int nn = n + t - it.t0, wb = nn % NW, cb = nn % NC;
         if (!warp_wait(&sfull[a], sc & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
         tc_fence_after();
         float s[4][32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, s[j]);
         tmem_wait_ld();
-        // the converting warps are a tile ahead: their scales and NaN marks
-        if (!warp_wait(&wfull[wb], (nn / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
         if constexpr (PT) {
+          if (!warp_wait(&cfull[cb], (nn / NC) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
 #pragma unroll
           for (int i = 0; i < 128; i += 4) {
-            const float4 ks = lds_f4(sb + S::kscOff + 4 * (wb * TILE + i));
+            const float4 ks = lds_f4(sb + S::kscOff + 4 * (cb * TILE + i));
             fmul2(s[i / 32][i % 32], s[i / 32][i % 32 + 1], ks.x, ks.y);
             fmul2(s[i / 32][i % 32 + 2], s[i / 32][i % 32 + 3], ks.z, ks.w);
           }
@@ -295,7 +298,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
         }
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
         int en = ev;
-        if constexpr (PT) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(en) : "r"(sb + S::evOff + 4 * wb));
+        if constexpr (PT) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(en) : "r"(sb + S::evOff + 4 * cb));
         if (t == it.t0) {
           m = fmaxf(mx, kNoMax);
         } else {
@@ -331,7 +334,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
           fadd2(la[0], la[1], x[0], x[1]);
           fadd2(la[2], la[3], x[2], x[3]);
           if constexpr (PT) {
-            const float4 vs = lds_f4(sb + S::vscOff + 4 * (wb * TILE + i));
+            const float4 vs = lds_f4(sb + S::vscOff + 4 * (cb * TILE + i));
             fmul2(x[0], x[1], vs.x, vs.y);
             fmul2(x[2], x[3], vs.z, vs.w);
             if (masked) {                          // 0 times a scale that is not finite
@@ -346,7 +349,10 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
         tmem_st32(ts, pw);
         tmem_st32(ts + 32, pw + 32);
         tmem_wait_st();
-        // NaN codes of V in this tile (none, as a rule)
+        // NaN codes of V in this tile (none, as a rule). The product needs the
+        // converted V anyway; waiting for it any earlier puts the conversion
+        // between the products of two tiles
+        if (!warp_wait(&wfull[wb], (nn / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
         const int4 nf = lds_i4(sb + S::flagOff + 16 * wb);
         if ((nf.x | nf.y | nf.z | nf.w) != 0) {
           const int f4[4] = {nf.x, nf.y, nf.z, nf.w};
@@ -379,15 +385,23 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       float* prow = p.part_o + ((long long)it.slot * p.part_rows + row) * D;
       if (it.slot >= 0 && valid) p.part_ml[(long long)it.slot * p.part_rows + row] = make_float2(none ? -INFINITY : m, l);
       if (any) {
+        bool anynan = false;
 #pragma unroll
+        for (int j = 0; j < D / 32; ++j) anynan = anynan || nan[j] != 0;
+        anynan = __any_sync(0xffffffffu, anynan);
+#pragma unroll 1
         for (int j = 0; j < D / 32; ++j) {
           float o[32];
           tmem_ld32(to + 32 * j, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            o[i] = none ? 0.f : o[i] * rl * sv;
-            if ((nan[j] >> i) & 1u) o[i] = __uint_as_float(0x7fffffffu);
+          for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * rl * sv;
+          if (anynan) {
+            uint32_t w = nan[0];
+#pragma unroll
+            for (int i = 1; i < D / 32; ++i) w = j == i ? nan[i] : w;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = ((w >> i) & 1u) ? __uint_as_float(0x7fffffffu) : o[i];
           }
           if (valid) {
             if (it.slot < 0) {
@@ -505,11 +519,15 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       if (k >= 1 && !warp_wait(qfree, (k - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       if (!it.last) {
 #pragma unroll 1
-        for (int b = 0; b < nb; b += 2) {
-          build(b, x0);
-          if (b + 2 < nb) load(b + 2, x0);
-          build(b + 1, x1);
-          if (b + 2 < nb) load(b + 3, x1);
+        for (int b = 0; b < nb; ++b) {
+          uint4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = x0[i];
+            x0[i] = x1[i];
+          }
+          if (b + 2 < nb) load(b + 2, x1);
+          build(b, x);
         }
         fence_proxy_async();
       }
@@ -522,11 +540,12 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       // 128-byte swizzle (the MN-major operand of the PV product)
       int ev = -126;
       for (int t = it.t0; t < it.t1; ++t, ++n) {
-        const int vb = n % NV, wb = n % NW;
+        const int vb = n % NV, wb = n % NW, cb = n % NC;
         const int live = it.L - t * TILE;            // tokens of the tile that exist
         if (!warp_wait(&vfull[vb], (n / NV) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-        if (n >= NW && !warp_wait(&wempty[wb], (n / NW - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
         if constexpr (PT) {
+          // scales first, ahead of the wait for room for V: the scores need them.
+          // (Room here: the last tile waited for the product three tiles back.)
           const int kb = n % NK;
           if (!warp_wait(&kfull[kb], (n / NK) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
           float vm = 0.f, vown = 0.f;
@@ -543,12 +562,16 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
           ev = max(ev, min((int)(__float_as_uint(vm) >> 23) - 126, 126));
           const int tk = 32 * cw + lane;
           const float kx = tk < live ? ldsf(sb + S::krawOff + 4 * (kb * TILE + tk)) : 0.f;
-          stsf(sb + S::kscOff + 4 * (wb * TILE + tk), kx);
-          stsf(sb + S::vscOff + 4 * (wb * TILE + tk), vown * ex2((float)-ev));
-          if (cw == 0 && lane == 0) asm volatile("st.shared.s32 [%0], %1;" ::"r"(sb + S::evOff + 4 * wb), "r"(ev) : "memory");
+          stsf(sb + S::kscOff + 4 * (cb * TILE + tk), kx);
+          stsf(sb + S::vscOff + 4 * (cb * TILE + tk), vown * ex2((float)-ev));
+          if (cw == 0 && lane == 0) asm volatile("st.shared.s32 [%0], %1;" ::"r"(sb + S::evOff + 4 * cb), "r"(ev) : "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&kempty[kb]);
+          if (lane == 0) {
+            mbar_arrive(&cfull[cb]);
+            mbar_arrive(&kempty[kb]);
+          }
         }
+        if (n >= NW && !warp_wait(&wempty[wb], (n / NW - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
         constexpr int CPR = D / 16, TPI = 32 / CPR, NI = 32 / TPI;   // 16-byte chunks per token, tokens per step
         const int ch = lane % CPR, tr = lane / CPR;
         const uint32_t src = sb + S::vOff + vb * S::kBytes, dst = sb + S::wOff + wb * S::wBytes;
@@ -721,7 +744,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       int h = 0, r = 0, j = 0, t = 0;
       Req rq = {0, 0, 0, 0};
       if (left > 0) {
-        h = (int)(u0 / W);
+        h = (int)div_nonneg(u0, W);
         r = (int)sched[16];
         const long long off = sched[17];
         rq = load_req(p, r, bt);
