@@ -68,15 +68,14 @@ struct Smem {
   static constexpr int crowOff = nanOff + NW * TILE * (D / 8);    // [2][256] logit multiplier of a row
   static constexpr int krawOff = crowOff + 2 * ROWS * 4;          // [NK][128] per-token scales as copied
   static constexpr int vrawOff = krawOff + NK * TILE * 4;
-  static constexpr int kscOff = vrawOff + NV * TILE * 4;          // [NC][128] for the softmax
-  static constexpr int vscOff = kscOff + NC * TILE * 4;
-  static constexpr int iringOff = vscOff + NC * TILE * 4;         // [IR] 64 bytes
+  static constexpr int kscOff = vrawOff + NV * TILE * 4;          // [NC][128] K scales for the softmax
+  static constexpr int iringOff = kscOff + NC * TILE * 4;         // [IR] 64 bytes
   static constexpr int qinfoOff = iringOff + IR * 64;             // [2] 64 bytes
   static constexpr int flagOff = qinfoOff + 2 * 64;               // [NW][4 warps] NaN seen
   static constexpr int evOff = flagOff + NW * 16;                 // [NC] exponent of the V scales (16 bytes)
   static constexpr int schedOff = evOff + 16;                     // schedule scratch
   static constexpr int barOff = schedOff + 256;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 4 + 1 + 6 + 1;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 6 + 2 + 10 + 1;
   static constexpr int miscOff = barOff + NBAR * 8;
   static constexpr int total = miscOff + 16 + 1024;
   static_assert(total <= 227 * 1024, "shared memory");
@@ -140,6 +139,11 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
   using S = Smem<D>;
   constexpr uint32_t SWZ = D == 128 ? kSwizzle128B : kSwizzle64B;
   constexpr uint32_t SBO = 8 * D;                  // 8 rows of D bytes
+  // Tensor memory: S of the two row tiles (128 columns each), O (D each). With
+  // head_dim 64 there are 128 columns left for P, so the next S is computed
+  // while the softmax still works; with 128 P overwrites its S.
+  constexpr bool SEP = D == 64;
+  constexpr uint32_t T_O = 256, T_P = SEP ? 384 : 0, P_STEP = SEP ? 64 : 128;
   constexpr uint32_t IDESC_QK = idesc_e4m3(128, 128, false, false);
   constexpr uint32_t IDESC_PV = idesc_f16(128, D, false, true);
   extern __shared__ uint8_t smem_raw[];
@@ -156,12 +160,15 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
   uint64_t* cfull = wempty + NW;       // [NC] scales written (4 warps, per-token scales only)
   uint64_t* ifull = cfull + NC;        // [IR] item published
   uint64_t* iempty = ifull + IR;       // [IR] item read (4 converting warps, prefetch warp)
-  uint64_t* qfull = iempty + IR;       // [2] query operand built, item passed on (4 warps)
-  uint64_t* qread = qfull + 2;         // [2] item read (8 softmax warps, MMA)
-  uint64_t* qfree = qread + 2;         // query operand read (MMA commit)
-  uint64_t* sfull = qfree + 1;         // [2] S of a row tile ready (MMA commit)
-  uint64_t* pfull = sfull + 2;         // [2] P written (4 warps)
-  uint64_t* ofull = pfull + 2;         // [2] O of an item ready (MMA commit)
+  uint64_t* qfull = iempty + IR;       // [2] item passed on, row tile 0's query operand built (4 warps)
+  uint64_t* qfull1 = qfull + 2;        // [2] row tile 1's query operand built (4 warps)
+  uint64_t* qread = qfull1 + 2;        // [2] item read (8 softmax warps, MMA)
+  uint64_t* qfree = qread + 2;         // [2] a row tile's query operand read (MMA commit)
+  uint64_t* sfull = qfree + 2;         // [2] S of a row tile ready (MMA commit)
+  uint64_t* sfree = sfull + 2;         // [2] S read (4 warps; SEP)
+  uint64_t* pfull = sfree + 2;         // [2] P written (4 warps)
+  uint64_t* pfree = pfull + 2;         // [2] P read, O complete so far (MMA commit; SEP)
+  uint64_t* ofull = pfree + 2;         // [2] O of an item ready (MMA commit)
   uint64_t* done = ofull + 2;          // all MMAs finished
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::miscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::miscOff + 4);
@@ -175,12 +182,15 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
     for (int i = 0; i < IR; ++i) { mbar_init(&ifull[i], 1); mbar_init(&iempty[i], 5); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 4);
+      mbar_init(&qfull1[i], 4);
       mbar_init(&qread[i], 9);
+      mbar_init(&qfree[i], 1);
       mbar_init(&sfull[i], 1);
+      mbar_init(&sfree[i], 4);
       mbar_init(&pfull[i], 4);
+      mbar_init(&pfree[i], 1);
       mbar_init(&ofull[i], 1);
     }
-    mbar_init(qfree, 1);
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -244,7 +254,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
     const int a = warp >> 2;                       // row tile
     const int row = a * TILE + (threadIdx.x & 127);
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = tl + a * 128, to = tl + 256 + a * D;
+    const uint32_t ts = tl + a * 128, to = tl + T_O + a * D, tp = tl + T_P + a * P_STEP;
     const float vscale = PT ? 1.f : __ldg(p.v_scale);
     const int G = p.qg;
     int sc = 0, oc = 0, n = 0;                     // S tiles, items of this row tile; key tiles of the CTA
@@ -253,6 +263,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       const int qb = k & 1;
       if (!warp_wait(&qfull[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
       const Item it = lds_item(sb + S::qinfoOff + 64 * qb);
+      if (a && !warp_wait(&qfull1[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
       const float c = ldsf(sb + S::crowOff + 4 * (qb * ROWS + row));
       __syncwarp();
       if (lane == 0) mbar_arrive(&qread[qb]);
@@ -274,6 +285,11 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, s[j]);
         tmem_wait_ld();
+        if constexpr (SEP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[a]);
+        }
         if constexpr (PT) {
           if (!warp_wait(&cfull[cb], (nn / NC) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
 #pragma unroll
@@ -309,6 +325,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
             l *= al;
             // (ev only grows: the factor is at most 1)
             const float f = PT ? al * ex2((float)(ev - en)) : al;
+            // (without SEP the S at hand came after the last product)
+            if (SEP && !warp_wait(&pfree[a], (sc & 1) ^ 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+            if (SEP) tc_fence_after();
 #pragma unroll 1
             for (int j = 0; j < D; j += 32) {
               float o[32];
@@ -333,21 +352,16 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
           for (int u = 0; u < 4; ++u) x[u] = ex2(x[u]);
           fadd2(la[0], la[1], x[0], x[1]);
           fadd2(la[2], la[3], x[2], x[3]);
-          if constexpr (PT) {
-            const float4 vs = lds_f4(sb + S::vscOff + 4 * (cb * TILE + i));
-            fmul2(x[0], x[1], vs.x, vs.y);
-            fmul2(x[2], x[3], vs.z, vs.w);
-            if (masked) {                          // 0 times a scale that is not finite
-#pragma unroll
-              for (int u = 0; u < 4; ++u) x[u] = i + u <= vis ? x[u] : 0.f;
-            }
-          }
           pw[i / 2] = f32x2_to_f16x2(x[0], x[1]);
           pw[i / 2 + 1] = f32x2_to_f16x2(x[2], x[3]);
         }
         l += (la[0] + la[1]) + (la[2] + la[3]);
-        tmem_st32(ts, pw);
-        tmem_st32(ts + 32, pw + 32);
+        if (SEP && sc > 0) {                       // the last product has read P
+          if (!warp_wait(&pfree[a], (sc & 1) ^ 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+          tc_fence_after();
+        }
+        tmem_st32(tp, pw);
+        tmem_st32(tp + 32, pw + 32);
         tmem_wait_st();
         // NaN codes of V in this tile (none, as a rule). The product needs the
         // converted V anyway; waiting for it any earlier puts the conversion
@@ -446,7 +460,8 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       constexpr int LPR = D / 32, RPW = 32 / LPR, RPS = 4 * RPW;
       const int part = lane % LPR;
       const int rows = it.last ? 0 : it.ntok * G;
-      const int nb = it.last ? 0 : (rows > TILE ? ROWS : TILE) / RPS;
+      constexpr int NB = TILE / RPS;                   // steps per row tile
+      const int nb = it.last ? 0 : (rows > TILE ? 2 : 1) * NB;
       auto load = [&](int b, uint4 (&x)[4]) {
         const int row = b * RPS + cw * RPW + lane / LPR;
 #pragma unroll
@@ -516,10 +531,11 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
         load(1, x1);
       }
       if (k >= 2 && !warp_wait(&qread[qb], ((k >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
-      if (k >= 1 && !warp_wait(qfree, (k - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
-      if (!it.last) {
+      // row tile 0, then 1: the products of 0 start while 1 is built
 #pragma unroll 1
-        for (int b = 0; b < nb; ++b) {
+      for (int b = 0; b < 2 * NB && ok; ++b) {
+        if (b % NB == 0 && k >= 1 && !warp_wait(&qfree[b / NB], (k - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) ok = false;
+        if (b < nb) {
           uint4 x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -529,12 +545,14 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
           if (b + 2 < nb) load(b + 2, x1);
           build(b, x);
         }
-        fence_proxy_async();
+        if (b % NB == NB - 1) {
+          fence_proxy_async();
+          if (b < NB && cw == 0 && lane == 0) sts_item(sb + S::qinfoOff + 64 * qb, it);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b < NB ? &qfull[qb] : &qfull1[qb]);
+        }
       }
-      if (cw == 0 && lane == 0) sts_item(sb + S::qinfoOff + 64 * qb, it);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&qfull[qb]);
-      if (it.last) break;
+      if (it.last || !ok) break;
 
       // ---- V of the item's key tiles: e4m3 -> f16, [dims / 64][token][64 dims],
       // 128-byte swizzle (the MN-major operand of the PV product)
@@ -543,27 +561,29 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
         const int vb = n % NV, wb = n % NW, cb = n % NC;
         const int live = it.L - t * TILE;            // tokens of the tile that exist
         if (!warp_wait(&vfull[vb], (n / NV) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        float vown = 1.f;
         if constexpr (PT) {
           // scales first, ahead of the wait for room for V: the scores need them.
           // (Room here: the last tile waited for the product three tiles back.)
           const int kb = n % NK;
           if (!warp_wait(&kfull[kb], (n / NK) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-          float vm = 0.f, vown = 0.f;
+          float vm = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int tk = 32 * i + lane;
             const float x = tk < live ? ldsf(sb + S::vrawOff + 4 * (vb * TILE + tk)) : 0.f;
             const float ax = fabsf(x);
             if (ax < INFINITY) vm = fmaxf(vm, ax);
-            if (i == cw) vown = x;
+            if (i == cw) vown = x;                   // token 32 cw + lane
           }
           vm = warp_max(vm);
-          // 2^ev above the largest scale so far: |v scale| 2^-ev < 1 (4 at the very top)
+          // 2^ev above the largest scale so far: |v scale| 2^-ev < 1 (4 at the very
+          // top). V enters as f16(v scale 2^-ev); when ev grows, O shrinks
           ev = max(ev, min((int)(__float_as_uint(vm) >> 23) - 126, 126));
           const int tk = 32 * cw + lane;
           const float kx = tk < live ? ldsf(sb + S::krawOff + 4 * (kb * TILE + tk)) : 0.f;
           stsf(sb + S::kscOff + 4 * (cb * TILE + tk), kx);
-          stsf(sb + S::vscOff + 4 * (cb * TILE + tk), vown * ex2((float)-ev));
+          vown *= ex2((float)-ev);
           if (cw == 0 && lane == 0) asm volatile("st.shared.s32 [%0], %1;" ::"r"(sb + S::evOff + 4 * cb), "r"(ev) : "memory");
           __syncwarp();
           if (lane == 0) {
@@ -587,7 +607,10 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
                               ((x[i].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
           bad |= y;
         }
-        const bool anybad = __any_sync(0xffffffffu, bad != 0);
+        // per token: a scale that is not finite makes every dim NaN
+        const bool nf = PT && !(fabsf(vown) < INFINITY);
+        const uint32_t vs16 = nf ? 0u : f32x2_to_f16x2(vown, vown);
+        const bool anybad = __any_sync(0xffffffffu, bad != 0 || nf);
         if (lane == 0) asm volatile("st.shared.s32 [%0], %1;" ::"r"(sb + S::flagOff + 16 * wb + 4 * cw), "r"((int)anybad) : "memory");
         if (anybad) {
           // mark the NaN dims of every token of this warp, and take them out
@@ -595,6 +618,8 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
           uint32_t* nm = reinterpret_cast<uint32_t*>(sm + nb);
           for (int i = lane; i < 32 * (D / 32); i += 32) nm[i] = 0;
           __syncwarp();
+          if (nf)
+            for (int i = 0; i < D / 32; ++i) atomicOr(&nm[lane * (D / 32) + i], 0xffffffffu);
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
             uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, bits = 0;
@@ -618,6 +643,11 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
           for (int j = 0; j < 4; ++j) {
             f[2 * j] = e4m3x2_lo_to_f16x2(w4[j]);
             f[2 * j + 1] = e4m3x2_hi_to_f16x2(w4[j]);
+          }
+          if constexpr (PT) {
+            const uint32_t sc2 = __shfl_sync(0xffffffffu, vs16, TPI * i + tr);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = hmul2(f[j], sc2);
           }
           // the two 16-byte halves in an order that differs between the atoms, so
           // that 8 lanes of a store touch 8 different bank groups
@@ -658,6 +688,19 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
         umma_commit(&sfull[a]);
       };
       auto kwait = [&](int nn) -> bool { return warp_wait(&kfull[nn % NK], (nn / NK) & 1, abort_flag, KERR_TIMEOUT_FULL); };
+      int qc[2] = {0, 0};                            // S tiles issued per row tile
+      // S of row tile a, key tile nn (the item's last one for it: last)
+      auto issue_qk = [&](int a, int nn, bool last) -> bool {
+        if (SEP && qc[a] > 0 && !warp_wait(&sfree[a], (qc[a] - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
+        ++qc[a];
+        tc_fence_after();
+        if (elect_one()) {
+          qk(a, nn % NK);
+          if (last) umma_commit(&qfree[a]);
+        }
+        __syncwarp();
+        return true;
+      };
       for (int k = 0; ok; ++k) {
         const int qb = k & 1;
         if (!warp_wait(&qfull[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
@@ -666,51 +709,61 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
         if (lane == 0) mbar_arrive(&qread[qb]);
         if (it.last) break;
         if (!kwait(n)) break;
-        tc_fence_after();
+        if (it.t0 < it.e0) {
+          if (!issue_qk(0, n, it.t0 + 1 == it.e0)) break;
+        }
+        if (!warp_wait(&qfull1[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+        if (it.t0 < it.e1) {
+          if (!issue_qk(1, n, it.t0 + 1 == it.e1)) break;
+        }
         if (elect_one()) {
-          if (it.t0 < it.e0) qk(0, n % NK);
-          if (it.t0 < it.e1) qk(1, n % NK);
           umma_commit(&kempty[n % NK]);
-          if (it.t0 + 1 == it.t1) umma_commit(qfree);
+          // a row tile without key tiles here never reads its operand
+          if (it.t0 >= it.e0) umma_commit(&qfree[0]);
+          if (it.t0 >= it.e1) umma_commit(&qfree[1]);
         }
         __syncwarp();
         for (int t = it.t0; t < it.t1; ++t, ++n) {
           const int wb = n % NW;
-          if (!warp_wait(&wfull[wb], (n / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
           bool kready = false;
+          // S of the next key tile: with room for P beside S right away, else
+          // behind the product that reads P
+          auto next_qk = [&](int a) -> bool {
+            const int end = a ? it.e1 : it.e0;
+            if (t + 1 >= end) return true;
+            if (!kready && !kwait(n + 1)) return false;
+            kready = true;
+            return issue_qk(a, n + 1, t + 2 == end);
+          };
+          if (SEP) {
+            if (!next_qk(0) || !next_qk(1)) { ok = false; break; }
+            if (t + 1 < it.t1 && elect_one()) umma_commit(&kempty[(n + 1) % NK]);
+            __syncwarp();
+          }
+          if (!warp_wait(&wfull[wb], (n / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
             const int end = a ? it.e1 : it.e0;
-            if (t >= end) continue;
-            if (!warp_wait(&pfull[a], pc[a] & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+            if (t >= end || !ok) continue;
+            if (!warp_wait(&pfull[a], pc[a] & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; continue; }
             ++pc[a];
             tc_fence_after();
             if (elect_one()) {
               const uint32_t vl = v_lo + wb * (S::wBytes / 16);
 #pragma unroll
               for (int i = 0; i < TILE / 16; ++i)
-                mma_f16_ts(tmem + 256 + a * D, tmem + a * 128 + 8 * i, vl + 128 * i, HI_V, IDESC_PV,
+                mma_f16_ts(tmem + T_O + a * D, tmem + T_P + a * P_STEP + 8 * i, vl + 128 * i, HI_V, IDESC_PV,
                            i > 0 ? 1u : (uint32_t)(t > it.t0));
+              if (SEP) umma_commit(&pfree[a]);
               if (t == end - 1) umma_commit(&ofull[a]);
             }
             __syncwarp();
-            if (t + 1 < end) {
-              if (!kready) {
-                if (!kwait(n + 1)) { ok = false; break; }
-                kready = true;
-                tc_fence_after();
-              }
-              if (elect_one()) qk(a, (n + 1) % NK);
-              __syncwarp();
-            }
+            if (!SEP && !next_qk(a)) ok = false;
           }
           if (!ok) break;
           if (elect_one()) {
             umma_commit(&wempty[wb]);
-            if (t + 1 < it.t1) {
-              umma_commit(&kempty[(n + 1) % NK]);
-              if (t + 2 == it.t1) umma_commit(qfree);
-            }
+            if (!SEP && t + 1 < it.t1) umma_commit(&kempty[(n + 1) % NK]);
           }
           __syncwarp();
         }

@@ -5,6 +5,8 @@ Slots, tables, lengths and e4m3 codes have to be equal. The tolerance of the
 attention, per element, with A = sum_t p_t |v_t| from the oracle:
     2^-8 |ref|                      the output's rounding to bf16
   + 2^-11 A                         the probabilities' rounding to f16
+  + 2^-10 A                         per-token scales: the V scale's rounding to f16 and
+                                    that of the scaled V, 2^-11 each
   + 2 (dq + da) A                   a logit error e changes p by e^(+-e): dq from the
                                     query's residue (2^-18 of the row's largest |q| per
                                     dim), da from float32 sums of D products, the scale
@@ -266,7 +268,8 @@ class Chunk:
         qmax = np.abs(decode_bf16(self.q_bits)).max(axis=-1, keepdims=True)
         dq = scale * 2.0 ** -18 * qmax * k1
         da = scale * qmax * k1 * (D + 4) * 2.0 ** -24 + 2.0 ** -22
-        return (2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -18) * bound + 2 * (dq + da) * bound
+        pv = 2.0 ** -11 + (2.0 ** -10 if self.per_token else 0.0) + 2.0 ** -18
+        return (2.0 ** -8 * np.abs(ref) + pv * bound + 2 * (dq + da) * bound
                 + int(self.lens.max(initial=0)) * 2.0 ** -24 * vmax)
 
 
