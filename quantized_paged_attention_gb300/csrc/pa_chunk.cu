@@ -32,8 +32,8 @@
 //    operand; an MMA warp; a warp that walks the schedule and issues the TMA
 //    copies (one box per page of the tile, one page per lane).
 //  * Tokens past the sequence's end are zeroed in V and masked in S; a NaN code
-//    in V is taken out of the product and put back only into the rows that see
-//    its token, so it cannot leak through 0 * NaN.
+//    in V is taken out of the product, and at the item's end put back into the
+//    rows that see its token, so it cannot leak through 0 * NaN.
 // Every wait has a time limit; a timeout raises the error word and all roles
 // leave through the common teardown.
 #define QPA_WHOLE_UNIT
@@ -64,18 +64,17 @@ struct Smem {
   static constexpr int kOff = qOff + qBytes;
   static constexpr int vOff = kOff + NK * kBytes;
   static constexpr int wOff = vOff + NV * kBytes;
-  static constexpr int nanOff = wOff + NW * wBytes;               // [NW][128][D / 32] NaN dims of a token
-  static constexpr int crowOff = nanOff + NW * TILE * (D / 8);    // [2][256] logit multiplier of a row
+  static constexpr int crowOff = wOff + NW * wBytes;              // [2][256] logit multiplier of a row
   static constexpr int krawOff = crowOff + 2 * ROWS * 4;          // [NK][128] per-token scales as copied
   static constexpr int vrawOff = krawOff + NK * TILE * 4;
   static constexpr int kscOff = vrawOff + NV * TILE * 4;          // [NC][128] K scales for the softmax
   static constexpr int iringOff = kscOff + NC * TILE * 4;         // [IR] 64 bytes
   static constexpr int qinfoOff = iringOff + IR * 64;             // [2] 64 bytes
-  static constexpr int flagOff = qinfoOff + 2 * 64;               // [NW][4 warps] NaN seen
-  static constexpr int evOff = flagOff + NW * 16;                 // [NC] exponent of the V scales (16 bytes)
+  static constexpr int flagOff = qinfoOff + 2 * 64;               // [4] V of an item holds a NaN
+  static constexpr int evOff = flagOff + 16;                 // [NC] exponent of the V scales (16 bytes)
   static constexpr int schedOff = evOff + 16;                     // schedule scratch
   static constexpr int barOff = schedOff + 256;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 6 + 2 + 10 + 1;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 6 + 2 + 12 + 1;
   static constexpr int miscOff = barOff + NBAR * 8;
   static constexpr int total = miscOff + 16 + 1024;
   static_assert(total <= 227 * 1024, "shared memory");
@@ -133,9 +132,33 @@ __device__ __forceinline__ void fmul2(float& a, float& b, float c, float d) {
 
 using namespace chunk;
 
+// A warp's rows against the NaN of V among tokens [a, b): mask gets the dims in
+// which a token that the lane's row sees (index at most lim) holds a NaN code,
+// all of them where its V scale is not finite. Reads the pages again: about a
+// byte per clock and warp, for broken inputs only.
+template <int D, bool PT>
+__device__ __noinline__ void find_nans(const Params& p, const uint8_t* kv, const Item& it, int a, int b, int lim, int lane,
+                                       uint32_t (&mask)[D / 32]) {
+  const int bs = 1 << p.log2_bs, last = min(b, it.L);
+  for (int t = a; t < last; ++t) {
+    int blk = __ldg(p.block_table + it.req * p.table_stride + (t >> p.log2_bs));
+    if (blk < 0 || blk >= p.num_blocks) blk = 0;
+    const long long off = t & (bs - 1);
+    const uint8_t* v = kv + ((((long long)blk * 2 + 1) * p.num_kv_heads + it.head) * bs + off) * D;
+    bool all = false;
+    if constexpr (PT)
+      all = !(fabsf(__ldg(p.v_scale + ((long long)blk * p.num_kv_heads + it.head) * bs + off)) < INFINITY);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t w = __ballot_sync(0xffffffffu, all || (__ldg(v + 32 * i + lane) & 0x7f) == 0x7f);
+      if (t <= lim) mask[i] |= w;
+    }
+  }
+}
+
 template <int D, bool PT>
 __global__ void __launch_bounds__(THREADS, 1)
-pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ Params p) {
+pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, const __grid_constant__ Params p) {
   using S = Smem<D>;
   constexpr uint32_t SWZ = D == 128 ? kSwizzle128B : kSwizzle64B;
   constexpr uint32_t SBO = 8 * D;                  // 8 rows of D bytes
@@ -166,8 +189,8 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
   uint64_t* qfree = qread + 2;         // [2] a row tile's query operand read (MMA commit)
   uint64_t* sfull = qfree + 2;         // [2] S of a row tile ready (MMA commit)
   uint64_t* sfree = sfull + 2;         // [2] S read (4 warps; SEP)
-  uint64_t* pfull = sfree + 2;         // [2] P written (4 warps)
-  uint64_t* pfree = pfull + 2;         // [2] P read, O complete so far (MMA commit; SEP)
+  uint64_t* pfull = sfree + 2;         // [2][2 halves] P written (4 warps)
+  uint64_t* pfree = pfull + 4;         // [2] P read, O complete so far (MMA commit; SEP)
   uint64_t* ofull = pfree + 2;         // [2] O of an item ready (MMA commit)
   uint64_t* done = ofull + 2;          // all MMAs finished
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::miscOff);
@@ -188,6 +211,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       mbar_init(&sfull[i], 1);
       mbar_init(&sfree[i], 4);
       mbar_init(&pfull[i], 4);
+      mbar_init(&pfull[2 + i], 4);
       mbar_init(&pfree[i], 1);
       mbar_init(&ofull[i], 1);
     }
@@ -273,12 +297,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       const bool valid = tok < it.ntok;
       const int lim = valid ? it.lim0 + tok : -1;
       float m = kNoMax, l = 0.f;
-      uint32_t nan[D / 32];
       int ev = -126;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) nan[i] = 0;
       for (int t = it.t0; t < end; ++t, ++sc) {
-        const int nn = n + t - it.t0, wb = nn % NW, cb = nn % NC;
+        const int nn = n + t - it.t0, cb = nn % NC;
         if (!warp_wait(&sfull[a], sc & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
         tc_fence_after();
         float s[4][32];
@@ -341,45 +362,36 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
         }
         ev = en;
         float la[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pw[64];
         const float nm = -m;
+        // P in two halves: the product with the first 64 keys runs while the
+        // exponentials of the others are still computed
 #pragma unroll
-        for (int i = 0; i < 128; i += 4) {
-          float* x = &s[i / 32][i % 32];
-          ffma2(x[0], x[1], c, nm);
-          ffma2(x[2], x[3], c, nm);
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pw[32];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) x[u] = ex2(x[u]);
-          fadd2(la[0], la[1], x[0], x[1]);
-          fadd2(la[2], la[3], x[2], x[3]);
-          pw[i / 2] = f32x2_to_f16x2(x[0], x[1]);
-          pw[i / 2 + 1] = f32x2_to_f16x2(x[2], x[3]);
-        }
-        l += (la[0] + la[1]) + (la[2] + la[3]);
-        if (SEP && sc > 0) {                       // the last product has read P
-          if (!warp_wait(&pfree[a], (sc & 1) ^ 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-          tc_fence_after();
-        }
-        tmem_st32(tp, pw);
-        tmem_st32(tp + 32, pw + 32);
-        tmem_wait_st();
-        // NaN codes of V in this tile (none, as a rule). The product needs the
-        // converted V anyway; waiting for it any earlier puts the conversion
-        // between the products of two tiles
-        if (!warp_wait(&wfull[wb], (nn / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-        const int4 nf = lds_i4(sb + S::flagOff + 16 * wb);
-        if ((nf.x | nf.y | nf.z | nf.w) != 0) {
-          const int f4[4] = {nf.x, nf.y, nf.z, nf.w};
-#pragma unroll 1
-          for (int tk = 0; tk < TILE; ++tk) {
-            if (f4[tk >> 5] == 0 || tk > vis) continue;
+          for (int i = 0; i < 64; i += 4) {
+            float* x = &s[2 * hf + i / 32][i % 32];
+            ffma2(x[0], x[1], c, nm);
+            ffma2(x[2], x[3], c, nm);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) nan[i] |= lds32(sb + S::nanOff + ((wb * TILE + tk) * (D / 32) + i) * 4);
+            for (int u = 0; u < 4; ++u) x[u] = ex2(x[u]);
+            fadd2(la[0], la[1], x[0], x[1]);
+            fadd2(la[2], la[3], x[2], x[3]);
+            pw[i / 2] = f32x2_to_f16x2(x[0], x[1]);
+            pw[i / 2 + 1] = f32x2_to_f16x2(x[2], x[3]);
           }
+          if (SEP && hf == 0 && sc > 0) {            // the last product has read P
+            if (!warp_wait(&pfree[a], (sc & 1) ^ 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+            tc_fence_after();
+          }
+          tmem_st32(tp + 32 * hf, pw);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pfull[2 * a + hf]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[a]);
+        if (!ok) break;
+        l += (la[0] + la[1]) + (la[2] + la[3]);
       }
       if (!ok) break;
       n += it.t1 - it.t0;
@@ -399,10 +411,13 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
       float* prow = p.part_o + ((long long)it.slot * p.part_rows + row) * D;
       if (it.slot >= 0 && valid) p.part_ml[(long long)it.slot * p.part_rows + row] = make_float2(none ? -INFINITY : m, l);
       if (any) {
-        bool anynan = false;
+        // NaN codes in the item's V (none, as a rule) were taken out of the
+        // products: look for them again and put NaN into the rows that see them
+        uint32_t nan[D / 32];
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) anynan = anynan || nan[j] != 0;
-        anynan = __any_sync(0xffffffffu, anynan);
+        for (int i = 0; i < D / 32; ++i) nan[i] = 0;
+        const bool anynan = lds32(sb + S::flagOff + 4 * (k & 3)) != 0;
+        if (anynan) find_nans<D, PT>(p, kv, it, it.t0 * TILE, end * TILE, lim, lane, nan);
 #pragma unroll 1
         for (int j = 0; j < D / 32; ++j) {
           float o[32];
@@ -531,6 +546,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
         load(1, x1);
       }
       if (k >= 2 && !warp_wait(&qread[qb], ((k >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
+      if (cw == 0 && lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + S::flagOff + 4 * (k & 3)), "r"(0u) : "memory");
       // row tile 0, then 1: the products of 0 start while 1 is built
 #pragma unroll 1
       for (int b = 0; b < 2 * NB && ok; ++b) {
@@ -611,27 +627,15 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
         const bool nf = PT && !(fabsf(vown) < INFINITY);
         const uint32_t vs16 = nf ? 0u : f32x2_to_f16x2(vown, vown);
         const bool anybad = __any_sync(0xffffffffu, bad != 0 || nf);
-        if (lane == 0) asm volatile("st.shared.s32 [%0], %1;" ::"r"(sb + S::flagOff + 16 * wb + 4 * cw), "r"((int)anybad) : "memory");
-        if (anybad) {
-          // mark the NaN dims of every token of this warp, and take them out
-          const uint32_t nb = S::nanOff + (wb * TILE + 32 * cw) * (D / 8);
-          uint32_t* nm = reinterpret_cast<uint32_t*>(sm + nb);
-          for (int i = lane; i < 32 * (D / 32); i += 32) nm[i] = 0;
-          __syncwarp();
-          if (nf)
-            for (int i = 0; i < D / 32; ++i) atomicOr(&nm[lane * (D / 32) + i], 0xffffffffu);
+        if (anybad) {                                // 0 times NaN must not reach a row that does not see the token
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
-            uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, bits = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t b = ((w4[j] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // NaN bytes
-              bits |= (((b >> 7) & 1u) | ((b >> 14) & 2u) | ((b >> 21) & 4u) | ((b >> 28) & 8u)) << (4 * j);
-              w4[j] &= ~((b >> 7) * 0xffu);
-            }
-            x[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-            if (bits) atomicOr(&nm[(TPI * i + tr) * (D / 32) + ch / 2], bits << (16 * (ch & 1)));
+            auto clean = [](uint32_t w) -> uint32_t {
+              return w & ~(((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu);
+            };
+            x[i] = make_uint4(clean(x[i].x), clean(x[i].y), clean(x[i].z), clean(x[i].w));
           }
+          if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + S::flagOff + 4 * (k & 3)), "r"(1u) : "memory");
         }
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -745,19 +749,25 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constan
           for (int a = 0; a < 2; ++a) {
             const int end = a ? it.e1 : it.e0;
             if (t >= end || !ok) continue;
-            if (!warp_wait(&pfull[a], pc[a] & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; continue; }
-            ++pc[a];
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t vl = v_lo + wb * (S::wBytes / 16);
+            const uint32_t vl = v_lo + wb * (S::wBytes / 16);
 #pragma unroll
-              for (int i = 0; i < TILE / 16; ++i)
-                mma_f16_ts(tmem + T_O + a * D, tmem + T_P + a * P_STEP + 8 * i, vl + 128 * i, HI_V, IDESC_PV,
-                           i > 0 ? 1u : (uint32_t)(t > it.t0));
-              if (SEP) umma_commit(&pfree[a]);
-              if (t == end - 1) umma_commit(&ofull[a]);
+            for (int hf = 0; hf < 2; ++hf) {
+              if (!ok || !warp_wait(&pfull[2 * a + hf], pc[a] & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; continue; }
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int i = 4 * hf; i < 4 * hf + 4; ++i)
+                  mma_f16_ts(tmem + T_O + a * D, tmem + T_P + a * P_STEP + 8 * i, vl + 128 * i, HI_V, IDESC_PV,
+                             i > 0 ? 1u : (uint32_t)(t > it.t0));
+                if (hf) {
+                  if (SEP) umma_commit(&pfree[a]);
+                  if (t == end - 1) umma_commit(&ofull[a]);
+                }
+              }
+              __syncwarp();
             }
-            __syncwarp();
+            ++pc[a];
+            if (!ok) continue;
             if (!SEP && !next_qk(a)) ok = false;
           }
           if (!ok) break;
@@ -1065,7 +1075,7 @@ cudaError_t launch_chunk(const ChunkLaunch& a, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   auto launch = [&](auto kernel, int smem) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) kernel<<<grid, THREADS, smem, stream>>>(map, p);
+    if (e == cudaSuccess) kernel<<<grid, THREADS, smem, stream>>>(map, a.kv, p);
   };
   if (D == 64) a.per_token ? launch(pa_chunk_kernel<64, true>, Smem<64>::total) : launch(pa_chunk_kernel<64, false>, Smem<64>::total);
   else a.per_token ? launch(pa_chunk_kernel<128, true>, Smem<128>::total) : launch(pa_chunk_kernel<128, false>, Smem<128>::total);
