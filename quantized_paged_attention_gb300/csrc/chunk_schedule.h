@@ -1,9 +1,10 @@
 // The work list of pa_chunk_fp8, shared by the kernel and a host test.
 //
-// An item is bt = 256 / G whole tokens of one request and KV head; a unit is
-// one 128-key tile of an item. The units in order: heads, then requests, then
-// items, then key tiles. How many a request has is known in closed form, so
-// nobody has to list them.
+// An item is bt = 256 / G whole tokens of one request and KV head; it costs a
+// unit per 128-key tile and ITEM_COST units to begin (its query operand, the
+// first tile's way through the pipeline, its result). The units in order:
+// heads, then requests, then items, then the beginning and the key tiles. How
+// many a request has is known in closed form, so nobody has to list them.
 #pragma once
 #ifndef __CUDACC__
 #include <algorithm>
@@ -22,6 +23,7 @@ namespace qpa {
 namespace chunk {
 
 constexpr int TILE = 128;            // keys per unit, rows per row tile
+constexpr int ITEM_COST = 3;
 
 // sum_{i < n} floor((a i + b) / m) for a, b >= 0 (the lattice points under a
 // line, by a Euclid-like reduction). T: 32 bits where a n + b and m fit (the
@@ -67,9 +69,11 @@ struct Req {
     const int d = L - ql;
     // items whose last row sees nothing, d + (i + 1) bt - 1 < 0: one unit each
     const int i0 = d >= 1 - bt ? 0 : min(j, -d / bt);
-    return j + floor_sum(j - i0, TILE, bt, d + (long long)(i0 + 1) * bt - 1);
+    return (long long)j * (1 + ITEM_COST) + floor_sum(j - i0, TILE, bt, d + (long long)(i0 + 1) * bt - 1);
   }
-  QPA_HD long long units(int bt) const { return nt ? before(nt - 1, bt) + tiles(nt - 1, bt) : 0; }
+  QPA_HD long long units(int bt) const { return nt ? before(nt - 1, bt) + tiles(nt - 1, bt) + ITEM_COST : 0; }
+  // first key tile at offset o into an item's units
+  QPA_HD static int tile_at(long long o) { return o > ITEM_COST ? (int)(o - ITEM_COST) : 0; }
   // One step of the search for the item that holds unit off, which lies in
   // [lo, hi): whether probe i of 32 splits it at or before off, and where that is
   QPA_HD static int split(int lo, int hi, int i) { return lo + (int)((long long)(hi - lo) * (i + 1) / 33); }

@@ -49,7 +49,7 @@ namespace chunk {
 constexpr int ROWS = 256;            // query rows per item (two tiles)
 constexpr int MAX_GRID = 160;        // CTAs at most (bounds the workspace)
 constexpr int THREADS = 512;
-constexpr int W_CONV = 8, W_MMA = 12, W_LOAD = 13, W_PREF = 14;
+constexpr int W_CONV = 8, W_MMA = 12, W_MMA1 = 13, W_LOAD = 14, W_PREF = 15;
 constexpr int NK = 3, NV = 2, NW = 2;   // stages of K, V bytes, V f16
 constexpr int NC = 4;                // stages of the per-token scales for the softmax
 constexpr int IR = 4;                // item ring
@@ -74,7 +74,7 @@ struct Smem {
   static constexpr int evOff = flagOff + 16;                 // [NC] exponent of the V scales (16 bytes)
   static constexpr int schedOff = evOff + 16;                     // schedule scratch
   static constexpr int barOff = schedOff + 256;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 6 + 2 + 12 + 1;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 6 + 2 + 12 + 2;
   static constexpr int miscOff = barOff + NBAR * 8;
   static constexpr int total = miscOff + 16 + 1024;
   static_assert(total <= 227 * 1024, "shared memory");
@@ -175,38 +175,38 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
   uint8_t* sm = smem_raw + (sb - raw);
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + S::barOff);
   uint64_t* kfull = bar;               // [NK] K tile copied
-  uint64_t* kempty = kfull + NK;       // [NK] K tile read (MMA commit; its scales: 4 warps)
+  uint64_t* kempty = kfull + NK;       // [NK] K tile read (both MMA warps; its scales: 4 warps)
   uint64_t* vfull = kempty + NK;       // [NV] V bytes copied
   uint64_t* vempty = vfull + NV;       // [NV] V bytes read (4 warps)
   uint64_t* wfull = vempty + NV;       // [NW] V f16 written (4 warps)
-  uint64_t* wempty = wfull + NW;       // [NW] V f16 read (MMA commit)
+  uint64_t* wempty = wfull + NW;       // [NW] V f16 read (both MMA warps)
   uint64_t* cfull = wempty + NW;       // [NC] scales written (4 warps, per-token scales only)
   uint64_t* ifull = cfull + NC;        // [IR] item published
   uint64_t* iempty = ifull + IR;       // [IR] item read (4 converting warps, prefetch warp)
   uint64_t* qfull = iempty + IR;       // [2] item passed on, row tile 0's query operand built (4 warps)
   uint64_t* qfull1 = qfull + 2;        // [2] row tile 1's query operand built (4 warps)
-  uint64_t* qread = qfull1 + 2;        // [2] item read (8 softmax warps, MMA)
+  uint64_t* qread = qfull1 + 2;        // [2] item read (8 softmax warps, 2 MMA warps)
   uint64_t* qfree = qread + 2;         // [2] a row tile's query operand read (MMA commit)
   uint64_t* sfull = qfree + 2;         // [2] S of a row tile ready (MMA commit)
   uint64_t* sfree = sfull + 2;         // [2] S read (4 warps; SEP)
   uint64_t* pfull = sfree + 2;         // [2][2 halves] P written (4 warps)
   uint64_t* pfree = pfull + 4;         // [2] P read, O complete so far (MMA commit; SEP)
   uint64_t* ofull = pfree + 2;         // [2] O of an item ready (MMA commit)
-  uint64_t* done = ofull + 2;          // all MMAs finished
+  uint64_t* done = ofull + 2;          // [2] all MMAs of a row tile finished
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::miscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::miscOff + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NK; ++i) { mbar_init(&kfull[i], 1); mbar_init(&kempty[i], PT ? 5 : 1); }
+    for (int i = 0; i < NK; ++i) { mbar_init(&kfull[i], 1); mbar_init(&kempty[i], PT ? 6 : 2); }
     for (int i = 0; i < NV; ++i) { mbar_init(&vfull[i], 1); mbar_init(&vempty[i], 4); }
-    for (int i = 0; i < NW; ++i) { mbar_init(&wfull[i], 4); mbar_init(&wempty[i], 1); }
+    for (int i = 0; i < NW; ++i) { mbar_init(&wfull[i], 4); mbar_init(&wempty[i], 2); }
     for (int i = 0; i < NC; ++i) mbar_init(&cfull[i], 4);
     for (int i = 0; i < IR; ++i) { mbar_init(&ifull[i], 1); mbar_init(&iempty[i], 5); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 4);
       mbar_init(&qfull1[i], 4);
-      mbar_init(&qread[i], 9);
+      mbar_init(&qread[i], SEP ? 10 : 9);
       mbar_init(&qfree[i], 1);
       mbar_init(&sfull[i], 1);
       mbar_init(&sfree[i], 4);
@@ -214,8 +214,8 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       mbar_init(&pfull[2 + i], 4);
       mbar_init(&pfree[i], 1);
       mbar_init(&ofull[i], 1);
+      mbar_init(&done[i], 1);
     }
-    mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -460,6 +460,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
     const int G = p.qg;
     const float base = p.softmax_scale * (PT ? 1.f : __ldg(p.k_scale)) * kLog2e;
     const uint32_t neg = base < 0.f ? 0x8000u : 0u;
+    const uint64_t pol = policy_evict_first();       // a query row is read once
     int n = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -468,106 +469,105 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       const Item it = lds_item(sb + S::iringOff + 64 * (k % IR));
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[k % IR]);
-      // ---- query operand: LPR lanes per row, 32 dims each; a step is RPS rows of
-      // the four warps, two steps in flight, the first two issued before the
-      // operand's space is free. (8 dims per lane, with four times the shuffles
-      // and a chain per row, took 10 us per item.)
-      constexpr int LPR = D / 32, RPW = 32 / LPR, RPS = 4 * RPW;
+      // ---- query operand, in place: 16 dims of a row are 32 bytes of bf16 and 16
+      // bytes in each term. A lane copies their halves (cp.async) to where its 16
+      // bytes of the first and the second term belong and turns them into those,
+      // so a row tile's copies are all in flight at once without a register and
+      // no lane meets another's bytes. (Loads through registers, 16 KB in flight,
+      // took 10 us per item with the tensor core idle.)
+      constexpr int LPR = D / 16, RPW = 32 / LPR, RPS = 4 * RPW, NB = TILE / RPS;   // lanes per row, rows per step, steps
       const int part = lane % LPR;
       const int rows = it.last ? 0 : it.ntok * G;
-      constexpr int NB = TILE / RPS;                   // steps per row tile
-      const int nb = it.last ? 0 : (rows > TILE ? 2 : 1) * NB;
-      auto load = [&](int b, uint4 (&x)[4]) {
-        const int row = b * RPS + cw * RPW + lane / LPR;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
-        if (row < rows) {
-          const int tok = (int)(row * gm >> 16);
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (it.tok0 + tok) * p.q_stride_tok +
-                                                            (long long)(it.head * G + row - tok * G) * p.q_stride_head) + 4 * part;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = __ldg(src + i);
-        }
+      auto spot = [&](int a, int b) -> uint32_t {
+        const int tr = b * RPS + cw * RPW + lane / LPR;
+        return sb + S::qOff + a * 2 * S::qTerm + tr * D + ((part ^ (D == 128 ? (tr & 7) : ((tr >> 1) & 3))) << 4);
       };
-      auto build = [&](int b, const uint4 (&x)[4]) {
-        const int row = b * RPS + cw * RPW + lane / LPR;
-        const uint32_t w[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
-                                x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
-        // largest |q| by its bits (NaN counts as above infinity)
-        uint32_t mx = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(mx) : "r"(w[i] & 0x7fff7fffu));
-        mx = max(mx & 0xffffu, mx >> 16);
-#pragma unroll
-        for (int o = LPR / 2; o >= 1; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        // 2^(7 - floor(log2 max)) and its inverse for the logits; rows below
-        // 2^-119 keep fewer bits (their logits vanish)
-        const uint32_t e = max(mx >> 7, 8u);
-        const bool inf = e >= 255;
-        if (part == 0) {
-          float cm = fabsf(base) * __uint_as_float((inf ? 127u : e - 7) << 23);
-          // a masked score must stay -inf when multiplied; a query that is not finite gives a NaN row
-          if (cm == 0.f) cm = 1.17549435e-38f;
-          if (inf) cm = __uint_as_float(0x7fffffffu);
-          stsf(sb + S::crowOff + 4 * (qb * ROWS + row), cm);
+      auto fetch = [&](int a) {
+#pragma unroll 1
+        for (int b = 0; b < NB; ++b) {
+          const int row = a * TILE + b * RPS + cw * RPW + lane / LPR;
+          const int tok = (int)(row * gm >> 16);
+          const bool in = row < rows;
+          const uint16_t* src = p.q;
+          if (in)
+            src += (it.tok0 + tok) * p.q_stride_tok + (long long)(it.head * G + row - tok * G) * p.q_stride_head + 16 * part;
+          const uint32_t at = spot(a, b);
+          cp_async16_zfill(at, src, in, pol);        // rows past the item's are zero
+          cp_async16_zfill(at + S::qTerm, in ? src + 8 : src, in, pol);
         }
-        const uint32_t f1 = ((inf ? 127u : 261 - e) << 7) | neg;
-        const uint32_t f2 = f1 | (f1 << 16);
-        const int tr = row & 127;
-        const uint32_t swz = D == 128 ? (tr & 7) : ((tr >> 1) & 3);
-        const uint32_t dst = sb + S::qOff + (row >> 7) * 2 * S::qTerm + tr * D;
-        // the scaled value in f16 (exact from 2^-17 up: 8 bits of 11, within
-        // 2^-25 below), its e4m3, and the e4m3 of what is left
+        cp_async_commit();
+      };
+      auto build = [&](int a) {
+#pragma unroll 2
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t at = spot(a, b);
+          const uint4 x0 = lds128(at), x1 = lds128(at + S::qTerm);
+          const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+          // largest |q| by its bits (NaN counts as above infinity)
+          uint32_t mx = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < 8; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(mx) : "r"(w[i] & 0x7fff7fffu));
+          mx = max(mx & 0xffffu, mx >> 16);
+#pragma unroll
+          for (int o = LPR / 2; o >= 1; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          // 2^(7 - floor(log2 max)) and its inverse for the logits; rows below
+          // 2^-119 keep fewer bits (their logits vanish)
+          const uint32_t e = max(mx >> 7, 8u);
+          const bool inf = e >= 255;
+          if (part == 0) {
+            float cm = fabsf(base) * __uint_as_float((inf ? 127u : e - 7) << 23);
+            // a masked score must stay -inf when multiplied; a query that is not finite gives a NaN row
+            if (cm == 0.f) cm = 1.17549435e-38f;
+            if (inf) cm = __uint_as_float(0x7fffffffu);
+            stsf(sb + S::crowOff + 4 * (qb * ROWS + a * TILE + b * RPS + cw * RPW + lane / LPR), cm);
+          }
+          const uint32_t f1 = ((inf ? 127u : 261 - e) << 7) | neg;
+          const uint32_t f2 = f1 | (f1 << 16);
+          // the scaled value in f16 (exact from 2^-17 up: 8 bits of 11, within
+          // 2^-25 below), its e4m3, and the e4m3 of what is left
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t z[2], h[2], g[2];
+            uint32_t h[2], g[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               uint32_t y;
-              asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w[8 * i + 2 * j + u]), "r"(f2));
-              z[u] = f32x2_to_f16x2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
-              h[u] = f16x2_to_e4m3x2(z[u]);
-              g[u] = f16x2_to_e4m3x2(hsub2(z[u], e4m3x2_lo_to_f16x2(h[u])));
+              asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w[2 * j + u]), "r"(f2));
+              const uint32_t z = f32x2_to_f16x2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+              h[u] = f16x2_to_e4m3x2(z);
+              g[u] = f16x2_to_e4m3x2(hsub2(z, e4m3x2_lo_to_f16x2(h[u])));
             }
             hi[j] = prmt(h[0], h[1], 0x5410u);
             lo[j] = prmt(g[0], g[1], 0x5410u);
           }
-          const uint32_t at = dst + (((2 * part + i) ^ swz) << 4);
           sts_i4(at, make_int4(hi[0], hi[1], hi[2], hi[3]));
           sts_i4(at + S::qTerm, make_int4(lo[0], lo[1], lo[2], lo[3]));
         }
       };
-      uint4 x0[4], x1[4];
-      if (nb) {
-        load(0, x0);
-        load(1, x1);
-      }
       if (k >= 2 && !warp_wait(&qread[qb], ((k >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
-      if (cw == 0 && lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + S::flagOff + 4 * (k & 3)), "r"(0u) : "memory");
+      if (cw == 0 && lane == 0) {
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + S::flagOff + 4 * (k & 3)), "r"(0u) : "memory");
+        sts_item(sb + S::qinfoOff + 64 * qb, it);
+      }
+      const int na = it.last ? 0 : rows > TILE ? 2 : 1;
+#pragma unroll 1
+      for (int a = 0; a < 2 && ok; ++a) {
+        if (k >= 1 && !warp_wait(&qfree[a], (k - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
+        if (a < na) fetch(a);
+      }
       // row tile 0, then 1: the products of 0 start while 1 is built
 #pragma unroll 1
-      for (int b = 0; b < 2 * NB && ok; ++b) {
-        if (b % NB == 0 && k >= 1 && !warp_wait(&qfree[b / NB], (k - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) ok = false;
-        if (b < nb) {
-          uint4 x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = x0[i];
-            x0[i] = x1[i];
-          }
-          if (b + 2 < nb) load(b + 2, x1);
-          build(b, x);
-        }
-        if (b % NB == NB - 1) {
+      for (int a = 0; a < 2 && ok; ++a) {
+        if (a < na) {
+          if (a + 1 < na) cp_async_wait<1>();
+          else cp_async_wait<0>();
+          build(a);
           fence_proxy_async();
-          if (b < NB && cw == 0 && lane == 0) sts_item(sb + S::qinfoOff + 64 * qb, it);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b < NB ? &qfull[qb] : &qfull1[qb]);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(a == 0 ? &qfull[qb] : &qfull1[qb]);
       }
+      if (!ok) cp_async_wait_all();
       if (it.last || !ok) break;
 
       // ---- V of the item's key tiles: e4m3 -> f16, [dims / 64][token][64 dims],
@@ -674,37 +674,19 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
     }
   } else {
     reg_dec<64>();
-    if (warp == W_MMA) {
-      // ====================================================== MMA warp
-      // the whole warp walks and waits, one elected lane issues
-      int n = 0, pc[2] = {0, 0};
+    if (warp == W_MMA || (SEP && warp == W_MMA1)) {
+      // ====================================================== MMA warps
+      // SEP: one per row tile, neither tile's chain (S, softmax, P V) waits for
+      // the other's softmax. Otherwise one for both, in strict turns: two warps
+      // drift into step there, each tile's products behind the other's and both
+      // softmaxes at once (1024 new tokens over 65536: 883 us against 777). The
+      // whole warp walks and waits, one elected lane issues.
+      const int a_lo = SEP ? warp - W_MMA : 0, a_hi = SEP ? a_lo + 1 : 2;
+      int n = 0, pc[2] = {0, 0}, qc[2] = {0, 0};     // key tiles of the CTA, products and S tiles per row tile
       bool ok = true;
       constexpr uint32_t HI = desc_hi(SBO, SWZ), HI_V = desc_hi(1024, kSwizzle128B);
-      const uint32_t q_lo = desc_lo(sb + S::qOff, 16), k_lo = desc_lo(sb + S::kOff, 16), v_lo = desc_lo(sb + S::wOff, TILE * 128);
-      // two query terms into one accumulator
-      auto qk = [&](int a, int kb) {
-        const uint32_t ql = q_lo + a * (2 * S::qTerm / 16), kl = k_lo + kb * (S::kBytes / 16);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            mma_e4m3_ss(tmem + a * 128, ql + j * (S::qTerm / 16) + 2 * i, HI, kl + 2 * i, HI, IDESC_QK, j | i);
-        umma_commit(&sfull[a]);
-      };
-      auto kwait = [&](int nn) -> bool { return warp_wait(&kfull[nn % NK], (nn / NK) & 1, abort_flag, KERR_TIMEOUT_FULL); };
-      int qc[2] = {0, 0};                            // S tiles issued per row tile
-      // S of row tile a, key tile nn (the item's last one for it: last)
-      auto issue_qk = [&](int a, int nn, bool last) -> bool {
-        if (SEP && qc[a] > 0 && !warp_wait(&sfree[a], (qc[a] - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
-        ++qc[a];
-        tc_fence_after();
-        if (elect_one()) {
-          qk(a, nn % NK);
-          if (last) umma_commit(&qfree[a]);
-        }
-        __syncwarp();
-        return true;
-      };
+      const uint32_t q_lo = desc_lo(sb + S::qOff, 16), k_lo = desc_lo(sb + S::kOff, 16);
+      const uint32_t v_lo = desc_lo(sb + S::wOff, TILE * 128);
       for (int k = 0; ok; ++k) {
         const int qb = k & 1;
         if (!warp_wait(&qfull[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
@@ -712,78 +694,85 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         __syncwarp();
         if (lane == 0) mbar_arrive(&qread[qb]);
         if (it.last) break;
-        if (!kwait(n)) break;
-        if (it.t0 < it.e0) {
-          if (!issue_qk(0, n, it.t0 + 1 == it.e0)) break;
-        }
-        if (!warp_wait(&qfull1[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
-        if (it.t0 < it.e1) {
-          if (!issue_qk(1, n, it.t0 + 1 == it.e1)) break;
-        }
-        if (elect_one()) {
-          umma_commit(&kempty[n % NK]);
-          // a row tile without key tiles here never reads its operand
-          if (it.t0 >= it.e0) umma_commit(&qfree[0]);
-          if (it.t0 >= it.e1) umma_commit(&qfree[1]);
-        }
-        __syncwarp();
-        for (int t = it.t0; t < it.t1; ++t, ++n) {
-          const int wb = n % NW;
-          bool kready = false;
-          // S of the next key tile: with room for P beside S right away, else
-          // behind the product that reads P
-          auto next_qk = [&](int a) -> bool {
-            const int end = a ? it.e1 : it.e0;
-            if (t + 1 >= end) return true;
-            if (!kready && !kwait(n + 1)) return false;
-            kready = true;
-            return issue_qk(a, n + 1, t + 2 == end);
-          };
-          if (SEP) {
-            if (!next_qk(0) || !next_qk(1)) { ok = false; break; }
-            if (t + 1 < it.t1 && elect_one()) umma_commit(&kempty[(n + 1) % NK]);
-            __syncwarp();
+        // S of key tile t; past the row tile's end its stage is only passed on
+        // (after its copy: an earlier arrival would count for the stage's last use)
+        auto issue_qk = [&](int a, int t) -> bool {
+          if (t >= it.t1) return true;
+          const int end = a ? it.e1 : it.e0;
+          const int nn = n + t - it.t0, kb = nn % NK;
+          if (!warp_wait(&kfull[kb], (nn / NK) & 1, abort_flag, KERR_TIMEOUT_FULL)) return false;
+          if (t >= end) {
+            if (lane == 0) mbar_arrive(&kempty[kb]);
+            return true;
           }
-          if (!warp_wait(&wfull[wb], (n / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-#pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            const int end = a ? it.e1 : it.e0;
-            if (t >= end || !ok) continue;
-            const uint32_t vl = v_lo + wb * (S::wBytes / 16);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              if (!ok || !warp_wait(&pfull[2 * a + hf], pc[a] & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; continue; }
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int i = 4 * hf; i < 4 * hf + 4; ++i)
-                  mma_f16_ts(tmem + T_O + a * D, tmem + T_P + a * P_STEP + 8 * i, vl + 128 * i, HI_V, IDESC_PV,
-                             i > 0 ? 1u : (uint32_t)(t > it.t0));
-                if (hf) {
-                  if (SEP) umma_commit(&pfree[a]);
-                  if (t == end - 1) umma_commit(&ofull[a]);
-                }
-              }
-              __syncwarp();
-            }
-            ++pc[a];
-            if (!ok) continue;
-            if (!SEP && !next_qk(a)) ok = false;
-          }
-          if (!ok) break;
+          if (SEP && qc[a] > 0 && !warp_wait(&sfree[a], (qc[a] - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
+          ++qc[a];
+          tc_fence_after();
           if (elect_one()) {
-            umma_commit(&wempty[wb]);
-            if (!SEP && t + 1 < it.t1) umma_commit(&kempty[(n + 1) % NK]);
+            const uint32_t ql = q_lo + a * (2 * S::qTerm / 16), kl = k_lo + kb * (S::kBytes / 16);
+            // two query terms into one accumulator
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i)
+                mma_e4m3_ss(tmem + a * 128, ql + j * (S::qTerm / 16) + 2 * i, HI, kl + 2 * i, HI, IDESC_QK, j | i);
+            umma_commit(&sfull[a]);
+            umma_commit(&kempty[kb]);
+            if (t + 1 == end) umma_commit(&qfree[a]);
           }
           __syncwarp();
+          return true;
+        };
+#pragma unroll 1
+        for (int a = a_lo; a < a_hi && ok; ++a) {
+          if (a && !warp_wait(&qfull1[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) ok = false;
+          // a row tile without key tiles here never reads its operand
+          if (it.t0 >= (a ? it.e1 : it.e0) && lane == 0) mbar_arrive(&qfree[a]);
+          if (ok) ok = issue_qk(a, it.t0);
         }
+        for (int t = it.t0; t < it.t1 && ok; ++t) {
+          const int nn = n + t - it.t0, wb = nn % NW;
+#pragma unroll 1
+          for (int a = a_lo; a < a_hi && ok; ++a) {
+            const int end = a ? it.e1 : it.e0;
+            // with room for P beside S the next S goes ahead of the product, else
+            // behind it (P lies in S)
+            if (SEP && !issue_qk(a, t + 1)) { ok = false; break; }
+            if (!warp_wait(&wfull[wb], (nn / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+            if (t < end) {
+              const uint32_t vl = v_lo + wb * (S::wBytes / 16);
+              const uint32_t t_o = tmem + T_O + a * D, t_p = tmem + T_P + a * P_STEP;
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                if (!ok || !warp_wait(&pfull[2 * a + hf], pc[a] & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; continue; }
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                  for (int i = 4 * hf; i < 4 * hf + 4; ++i)
+                    mma_f16_ts(t_o, t_p + 8 * i, vl + 128 * i, HI_V, IDESC_PV, i > 0 ? 1u : (uint32_t)(t > it.t0));
+                  if (hf) {
+                    umma_commit(&wempty[wb]);
+                    if (SEP) umma_commit(&pfree[a]);
+                    if (t == end - 1) umma_commit(&ofull[a]);
+                  }
+                }
+                __syncwarp();
+              }
+              ++pc[a];
+            } else if (lane == 0) {
+              mbar_arrive(&wempty[wb]);
+            }
+            if (!SEP && ok) ok = issue_qk(a, t + 1);
+          }
+        }
+        n += it.t1 - it.t0;
       }
       if (elect_one()) {
         // every issued MMA must finish before the tensor memory is released
-        umma_commit(done);
-        if (!mbar_try_wait(done, 0)) {
+        umma_commit(&done[a_lo]);
+        if (!mbar_try_wait(&done[a_lo], 0)) {
           const unsigned long long t0 = globaltimer();
-          while (!mbar_try_wait(done, 0)) {
+          while (!mbar_try_wait(&done[a_lo], 0)) {
             if (globaltimer() - t0 > kWaitLimitNs) {
               atomicExch(&g_kernel_error, (int)KERR_TIMEOUT_FULL);
               break;
@@ -803,8 +792,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       long long left = u1 - u0;
       // for the combine: the item that starts here and is cut (head, row, tokens,
       // slot); whether the first item began earlier, whether it ends here, no items
-      int4 m_start = make_int4(0, 0, 0, -1), m_cont = make_int4(0, 0, left <= 0, 0);;
-      int h = 0, r = 0, j = 0, t = 0;
+      int4 m_start = make_int4(0, 0, 0, -1), m_cont = make_int4(0, 0, 1, 0);;
+      int h = 0, r = 0, j = 0;
+      long long o = 0;                               // units of item j that lie before the range
       Req rq = {0, 0, 0, 0};
       if (left > 0) {
         h = (int)div_nonneg(u0, W);
@@ -820,30 +810,47 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           hi = below < 32 ? h2 : hi;
         }
         j = lo;
-        t = (int)(off - rq.before(j, bt));
+        o = off - rq.before(j, bt);
       }
       while (ok) {
         Item it;
         it.last = left <= 0;
         if (!it.last) {
           const int nk = rq.tiles(j, bt);
+          const long long take = min(left, (long long)nk + ITEM_COST - o);
           it.req = r;
           it.head = h;
           it.tok0 = rq.q0 + j * bt;
           it.ntok = min(bt, rq.ql - j * bt);
           it.lim0 = rq.L - rq.ql + j * bt;
           it.L = rq.L;
-          it.t0 = t;
-          it.t1 = (int)min((long long)nk, t + left);
+          it.t0 = Req::tile_at(o);
+          it.t1 = Req::tile_at(o + take);
           const int rows = it.ntok * p.qg;
           const int n0 = max(it.lim0 + (min(rows, TILE) - 1) / p.qg, 0) / TILE + 1;
           it.e0 = min(it.t1, n0);
           it.e1 = rows > TILE ? it.t1 : it.t0;
-          const bool starts = t == 0, ends = it.t1 == nk;
+          const bool starts = it.t0 == 0, ends = it.t1 == nk;
           // slot 2 b: the CTA's first item, slot 2 b + 1: its last (if another)
           it.slot = starts && ends ? -1 : 2 * (int)blockIdx.x + (k > 0);
-          if (starts && !ends) m_start = make_int4(h, it.tok0, it.ntok, it.slot);
+          left -= take;
+          // ---- the next item: token range, request, head
+          o = 0;
+          if (left > 0 && ++j >= rq.nt) {
+            j = 0;
+            do {                                     // left > 0: a request with units follows
+              if (++r >= p.num_reqs) {
+                r = 0;
+                ++h;
+              }
+              rq = load_req(p, r, bt);
+            } while (rq.nt == 0 && h < Hk);
+            if (h >= Hk) left = 0;                   // (not reached while the inputs stay as they were)
+          }
+          if (it.t0 == it.t1) continue;              // cut before its first key tile: the next CTA's
+          if (starts && !ends) m_start = make_int4(it.head, it.tok0, it.ntok, it.slot);
           if (!starts) m_cont = make_int4(1, ends, 0, 0);
+          m_cont.z = 0;
         }
         if (k >= IR && !warp_wait(&iempty[k % IR], (k / IR - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
         if (lane == 0) {
@@ -852,7 +859,6 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         }
         if (it.last) break;
         ++k;
-        left -= it.t1 - it.t0;
 
         const int32_t* tab = p.block_table + it.req * p.table_stride;
         const int npages = (it.L + bs - 1) >> p.log2_bs;
@@ -860,7 +866,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         int win = (it.t0 * TILE) >> p.log2_bs;
         auto entry = [&](int e) -> int { return e < npages ? __ldg(tab + e) : 0; };
         int cur = entry(win + lane), nxt = entry(win + 32 + lane);
-        for (t = it.t0; t < it.t1; ++t, ++n) {
+        for (int t = it.t0; t < it.t1; ++t, ++n) {
           const int kb = n % NK, vb = n % NV;
           const int e0 = (t * TILE) >> p.log2_bs;    // first page of the tile
           if (e0 >= win + 32) {
@@ -883,9 +889,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           }
           __syncwarp();
           if (lane < np) {
-            tma_load_3d(sb + S::kOff + kb * S::kBytes + lane * pb, &kv_map, 0, h * bs + y0, blk, &kfull[kb]);
+            tma_load_3d(sb + S::kOff + kb * S::kBytes + lane * pb, &kv_map, 0, it.head * bs + y0, blk, &kfull[kb]);
             if constexpr (PT)
-              bulk_load(sb + S::krawOff + 4 * (kb * TILE + lane * bsr), p.k_scale + ((long long)blk * Hk + h) * bs + y0,
+              bulk_load(sb + S::krawOff + 4 * (kb * TILE + lane * bsr), p.k_scale + ((long long)blk * Hk + it.head) * bs + y0,
                         bsr * 4, &kfull[kb]);
           }
           kn = n + 1;
@@ -896,27 +902,14 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           }
           __syncwarp();
           if (lane < np) {
-            tma_load_3d(sb + S::vOff + vb * S::kBytes + lane * pb, &kv_map, 0, (Hk + h) * bs + y0, blk, &vfull[vb]);
+            tma_load_3d(sb + S::vOff + vb * S::kBytes + lane * pb, &kv_map, 0, (Hk + it.head) * bs + y0, blk, &vfull[vb]);
             if constexpr (PT)
-              bulk_load(sb + S::vrawOff + 4 * (vb * TILE + lane * bsr), p.v_scale + ((long long)blk * Hk + h) * bs + y0,
+              bulk_load(sb + S::vrawOff + 4 * (vb * TILE + lane * bsr), p.v_scale + ((long long)blk * Hk + it.head) * bs + y0,
                         bsr * 4, &vfull[vb]);
           }
           vn = n + 1;
         }
         if (!ok) break;
-        // ---- next item: token range, request, head
-        t = 0;
-        if (left > 0 && ++j >= rq.nt) {
-          j = 0;
-          do {                                       // left > 0: a request with units follows
-            if (++r >= p.num_reqs) {
-              r = 0;
-              ++h;
-            }
-            rq = load_req(p, r, bt);
-          } while (rq.nt == 0 && h < Hk);
-          if (h >= Hk) left = 0;                     // (not reached while the inputs stay as they were)
-        }
       }
       if (lane == 0) {
         p.meta[2 * blockIdx.x] = m_start;

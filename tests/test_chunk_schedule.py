@@ -3,12 +3,16 @@ compiles (chunk_schedule.h) against a plain enumeration, and the cut into
 equal ranges: every unit once, pieces of an item in consecutive ranges."""
 import os
 import random
+import re
 import subprocess
 
 import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "quantized_paged_attention_gb300", "csrc")
+
+with open(os.path.join(CSRC, "chunk_schedule.h")) as f:
+    COST = int(re.search(r"ITEM_COST = (\d+);", f.read()).group(1))
 
 MAIN = r"""
 #include "chunk_schedule.h"
@@ -36,8 +40,8 @@ int main() {
     bool found = true;
     for (int j = 0; j < r.nt; ++j) {
       printf(" %d %lld", r.tiles(j, bt), r.before(j, bt));
-      if (r.nt < 300 || j % 97 == 0) found = found && find(r, u, bt) == j && find(r, u + r.tiles(j, bt) - 1, bt) == j;
-      u += r.tiles(j, bt);
+      if (r.nt < 300 || j % 97 == 0) found = found && find(r, u, bt) == j && find(r, u + r.tiles(j, bt) + ITEM_COST - 1, bt) == j;
+      u += r.tiles(j, bt) + ITEM_COST;
     }
     printf(" %d\n", (int)found);
   }
@@ -86,9 +90,9 @@ def test_closed_forms(prog):
         q0, ql, LL, nt, units, *rest = map(int, line.split())
         assert q0 == max(0, min(a, T)) and ql == max(0, max(0, min(b, T)) - q0) and LL == max(0, min(L, M))
         tiles = _rows(bt, ql, LL)
-        assert nt == len(tiles) and units == sum(tiles) and rest[-1] == 1
+        assert nt == len(tiles) and units == sum(tiles) + COST * nt and rest[-1] == 1
         assert rest[:-1:2] == tiles
-        assert rest[1:-1:2] == [sum(tiles[:j]) for j in range(nt)] if nt < 200 else True
+        assert rest[1:-1:2] == [sum(tiles[:j]) + COST * j for j in range(nt)] if nt < 200 else True
 
 
 def test_ranges_cover_every_unit_once_and_pieces_are_found():
@@ -99,29 +103,37 @@ def test_ranges_cover_every_unit_once_and_pieces_are_found():
     for _ in range(300):
         grid = r.choice([1, 2, 5, 152])
         items = [r.randint(1, r.choice([1, 4, 60])) for _ in range(r.randint(1, 40))]
-        U = sum(items)
+        cost = r.choice([0, COST, 9])
+        U = sum(n + cost for n in items)
         first = [0]
         for n in items:
-            first.append(first[-1] + n)
-        pieces, start, cont = {}, {}, {}
+            first.append(first[-1] + n + cost)
+        pieces, start, cont, tiles = {}, {}, {}, [0] * len(items)
         for c in range(grid):
             u, u1 = U * c // grid, U * (c + 1) // grid
-            cont[c] = dict(empty=u >= u1, x=False, ends=False)
+            cont[c] = dict(empty=True, x=False, ends=False)
             k = 0
             while u < u1:
                 i = max(j for j in range(len(items)) if first[j] <= u)
                 e = min(first[i + 1], u1)
-                starts, ends = u == first[i], e == first[i + 1]
+                t0, t1 = max(0, u - first[i] - cost), max(0, e - first[i] - cost)
+                u = e
+                if t0 == t1:
+                    continue
+                tiles[i] += t1 - t0
+                starts, ends = t0 == 0, t1 == items[i]
                 if not (starts and ends):
                     slot = 2 * c + (k > 0)
                     assert slot not in pieces
-                    pieces[slot] = (i, u, e)
+                    pieces[slot] = (i, t0, t1)
                     if starts:
                         start[c] = (i, slot)
                     else:
                         assert k == 0
                         cont[c].update(x=True, ends=ends)
-                u, k = e, k + 1
+                cont[c]["empty"] = False
+                k += 1
+        assert tiles == items
         met = 0
         for c, (i, slot) in start.items():
             got = [pieces[slot]]
@@ -134,7 +146,7 @@ def test_ranges_cover_every_unit_once_and_pieces_are_found():
                 if cont[d]["ends"]:
                     break
             assert all(p[0] == i for p in got)
-            assert got[0][1] == first[i] and got[-1][2] == first[i + 1]
+            assert got[0][1] == 0 and got[-1][2] == items[i]
             assert all(x[2] == y[1] for x, y in zip(got, got[1:]))
             met += len(got)
         assert met == len(pieces)
