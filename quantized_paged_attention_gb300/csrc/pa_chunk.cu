@@ -681,7 +681,8 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       // drift into step there, each tile's products behind the other's and both
       // softmaxes at once (1024 new tokens over 65536: 883 us against 777). The
       // whole warp walks and waits, one elected lane issues.
-      const int a_lo = SEP ? warp - W_MMA : 0, a_hi = SEP ? a_lo + 1 : 2;
+      constexpr int NA = SEP ? 1 : 2;
+      const int a_lo = SEP ? warp - W_MMA : 0;
       int n = 0, pc[2] = {0, 0}, qc[2] = {0, 0};     // key tiles of the CTA, products and S tiles per row tile
       bool ok = true;
       constexpr uint32_t HI = desc_hi(SBO, SWZ), HI_V = desc_hi(1024, kSwizzle128B);
@@ -696,11 +697,11 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         if (it.last) break;
         // S of key tile t; past the row tile's end its stage is only passed on
         // (after its copy: an earlier arrival would count for the stage's last use)
-        auto issue_qk = [&](int a, int t) -> bool {
+        auto issue_qk = [&](int a, int t, bool kready) -> bool {
           if (t >= it.t1) return true;
           const int end = a ? it.e1 : it.e0;
           const int nn = n + t - it.t0, kb = nn % NK;
-          if (!warp_wait(&kfull[kb], (nn / NK) & 1, abort_flag, KERR_TIMEOUT_FULL)) return false;
+          if (!kready && !warp_wait(&kfull[kb], (nn / NK) & 1, abort_flag, KERR_TIMEOUT_FULL)) return false;
           if (t >= end) {
             if (lane == 0) mbar_arrive(&kempty[kb]);
             return true;
@@ -723,22 +724,29 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           __syncwarp();
           return true;
         };
-#pragma unroll 1
-        for (int a = a_lo; a < a_hi && ok; ++a) {
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+          const int a = SEP ? a_lo : i;
+          if (!ok) continue;
           if (a && !warp_wait(&qfull1[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) ok = false;
           // a row tile without key tiles here never reads its operand
           if (it.t0 >= (a ? it.e1 : it.e0) && lane == 0) mbar_arrive(&qfree[a]);
-          if (ok) ok = issue_qk(a, it.t0);
+          if (ok) ok = issue_qk(a, it.t0, false);
         }
         for (int t = it.t0; t < it.t1 && ok; ++t) {
           const int nn = n + t - it.t0, wb = nn % NW;
-#pragma unroll 1
-          for (int a = a_lo; a < a_hi && ok; ++a) {
+#pragma unroll
+          for (int i = 0; i < NA; ++i) {
+            const int a = SEP ? a_lo : i;
+            if (!ok) continue;
             const int end = a ? it.e1 : it.e0;
             // with room for P beside S the next S goes ahead of the product, else
             // behind it (P lies in S)
-            if (SEP && !issue_qk(a, t + 1)) { ok = false; break; }
-            if (!warp_wait(&wfull[wb], (nn / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+            if (SEP && !issue_qk(a, t + 1, false)) { ok = false; continue; }
+            if ((SEP || a == 0) && !warp_wait(&wfull[wb], (nn / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; continue; }
+            // K of the next tile, before P so that nothing is waited for between
+            // the product and the next S
+            if (!SEP && a == 0 && t + 1 < it.t1 && !warp_wait(&kfull[(nn + 1) % NK], ((nn + 1) / NK) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; continue; }
             if (t < end) {
               const uint32_t vl = v_lo + wb * (S::wBytes / 16);
               const uint32_t t_o = tmem + T_O + a * D, t_p = tmem + T_P + a * P_STEP;
@@ -762,7 +770,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
             } else if (lane == 0) {
               mbar_arrive(&wempty[wb]);
             }
-            if (!SEP && ok) ok = issue_qk(a, t + 1);
+            if (!SEP && ok) ok = issue_qk(a, t + 1, true);
           }
         }
         n += it.t1 - it.t0;
