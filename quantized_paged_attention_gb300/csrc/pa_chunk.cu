@@ -166,6 +166,13 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
   // head_dim 64 there are 128 columns left for P, so the next S is computed
   // while the softmax still works; with 128 P overwrites its S.
   constexpr bool SEP = D == 64;
+  // registers per thread: the sum over the four groups is what the block is
+  // launched with (4 x 128). Fewer for the softmax than it could use, since the
+  // other roles' spills cost more (head_dim 128, 1024 new tokens over 65536:
+  // 184/80/64 772 us, 200/64/48 818, 168/96/80 740, 160/112/80 1296; head_dim 64:
+  // 184/80/64 574 us, 176/96/64 558, 168/96/80 603)
+  constexpr int REG_SOFTMAX = D == 128 ? 168 : 176, REG_CONV = 96, REG_REST = D == 128 ? 80 : 64;
+  static_assert(2 * REG_SOFTMAX + REG_CONV + REG_REST <= 512, "register budget");
   constexpr uint32_t T_O = 256, T_P = SEP ? 384 : 0, P_STEP = SEP ? 64 : 128;
   constexpr uint32_t IDESC_QK = idesc_e4m3(128, 128, false, false);
   constexpr uint32_t IDESC_PV = idesc_f16(128, D, false, true);
@@ -274,7 +281,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
 
   if (warp < W_CONV) {
     // ======================================================== softmax warps
-    reg_inc<184>();
+    reg_inc<REG_SOFTMAX>();
     const int a = warp >> 2;                       // row tile
     const int row = a * TILE + (threadIdx.x & 127);
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -455,7 +462,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
     }
   } else if (warp < W_MMA) {
     // ======================================================== converting warps
-    reg_dec<80>();
+    reg_dec<REG_CONV>();
     const int cw = warp - W_CONV;
     const int G = p.qg;
     const float base = p.softmax_scale * (PT ? 1.f : __ldg(p.k_scale)) * kLog2e;
@@ -673,7 +680,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       }
     }
   } else {
-    reg_dec<64>();
+    reg_dec<REG_REST>();
     if (warp == W_MMA || (SEP && warp == W_MMA1)) {
       // ====================================================== MMA warps
       // SEP: one per row tile, neither tile's chain (S, softmax, P V) waits for
