@@ -417,39 +417,64 @@ def nvfp4_index_score(q_codes, pages, block_table, seq_lens, query_len: int, num
 
 
 # --------------------------------------------------------------------- serving step
-def _need(cond, msg):
-    if not cond:
-        raise ValueError(msg)
-
-
-def _need_all(dtype, dense, **ts):
-    """Each tensor: the dtype and, with dense, contiguous."""
-    for name, t in ts.items():
-        _need(t.dtype == dtype, f"{name} must be {dtype}, is {t.dtype}")
-        _need(not dense or t.is_contiguous(), f"{name} must be contiguous")
-
-
-def _same_device(*ts):
-    _need_cuda(*ts)
-    _need(len({t.device for t in ts if t is not None}) == 1, "all tensors must be on one device")
+# These calls take a few microseconds on the GPU, so their checks are written
+# out straight: a helper per property costs more than the kernel.
+def _fail(msg):
+    raise ValueError(msg)
 
 
 def _rows(block_table):
-    _need(block_table.dim() == 2, "block_table must be [num_reqs, max_blocks]")
+    """(max_blocks, row stride or 0) of an int32 block table with contiguous rows."""
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        _fail("block_table must be int32 [num_reqs, max_blocks]")
     R, maxb = block_table.shape
-    _need(R == 0 or maxb <= 1 or block_table.stride(1) == 1, "block_table must have contiguous rows")
-    _need(R <= 1 or block_table.stride(0) >= maxb, "block_table rows must not overlap")
-    return maxb, block_table.stride(0) if R > 1 else 0
+    if R > 0 and maxb > 1 and block_table.stride(1) != 1:
+        _fail("block_table must have contiguous rows")
+    if R <= 1:
+        return maxb, 0
+    stride = block_table.stride(0)
+    if stride < maxb:
+        _fail("block_table rows must not overlap")
+    return maxb, stride
 
 
-def _launch(fn, device, stream, *args):
+def _dim_stride(t, i):
+    """Stride of dimension i for a descriptor, where 0 means contiguous: a
+    dimension of one element has no stride; an expanded one is refused."""
+    if t.shape[i] <= 1:
+        return 0
+    s = t.stride(i)
+    if s <= 0:
+        _fail("expanded tensors are not supported")
+    return s
+
+
+def _launch(fn, index, stream, *args):
     """Call an entry point on `stream` (default: the device's current stream)
-    with the tensors' device current."""
-    with torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        _need(stream.device == device, "the stream must belong to the tensors' device")
-        _check(fn, getattr(load_library(), fn)(*args, ctypes.c_void_p(stream.cuda_stream)))
+    with device `index`, that of all the call's tensors, current."""
+    lib = _lib if _lib is not None else load_library()
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        if stream.device_index != index:
+            _fail("the stream must belong to the tensors' device")
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        st = getattr(lib, fn)(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            st = getattr(lib, fn)(*args, raw)
+    if st != QPA_OK:
+        raise QpaError(fn, st)
+
+
+def _device_of(*ts):
+    """Index of the CUDA device that holds every tensor."""
+    index = ts[0].get_device()
+    for t in ts:
+        if t.get_device() != index or index < 0:
+            _fail("qpa runs on CUDA tensors only (no CPU path), all of them on one device")
+    return index
 
 
 def paged_slot_map(new_lens, cached_lens, block_table, free_blocks, block_size: int, max_tokens: int,
@@ -462,50 +487,57 @@ def paged_slot_map(new_lens, cached_lens, block_table, free_blocks, block_size: 
     int32 [R], slots int64 [max_tokens], positions int32 [max_tokens],
     num_taken int32 [1]), written into the tensors passed for them if any
     (a captured graph keeps its own)."""
-    dev = new_lens.device
-    _need_all(torch.int32, True, new_lens=new_lens, cached_lens=cached_lens, free_blocks=free_blocks)
-    _need_all(torch.int32, False, block_table=block_table)
+    i32 = torch.int32
     R = new_lens.numel()
+    for t in (new_lens, cached_lens, free_blocks):
+        if t.dtype != i32 or not t.is_contiguous():
+            _fail("new_lens, cached_lens and free_blocks must be contiguous int32")
     maxb, stride = _rows(block_table)
-    _need(cached_lens.numel() == R and block_table.shape[0] == R,
-          "new_lens, cached_lens and block_table must have one entry per request")
-
-    def outp(t, n, dtype, name):
-        if t is None:
-            return torch.empty(n, dtype=dtype, device=dev)
-        _need_all(dtype, True, **{name: t})
-        _need(t.numel() == n, f"{name} must have {n} elements")
-        return t
-
-    query_start = outp(query_start, R + 1, torch.int32, "query_start")
-    seq_lens = outp(seq_lens, R, torch.int32, "seq_lens")
-    slots = outp(slots, max_tokens, torch.int64, "slots")
-    positions = outp(positions, max_tokens, torch.int32, "positions")
-    num_taken = outp(num_taken, 1, torch.int32, "num_taken")
-    _same_device(new_lens, cached_lens, block_table, free_blocks, query_start, seq_lens, slots, positions, num_taken)
-    d = SlotDesc()
-    d.num_reqs, d.block_size, d.max_blocks_per_seq = R, block_size, maxb
-    d.num_free, d.max_tokens, d.table_stride = free_blocks.numel(), max_tokens, stride
-    _launch("paged_slot_map", dev, stream, _ptr(new_lens), _ptr(cached_lens), _ptr(block_table), _ptr(free_blocks),
-            _ptr(query_start), _ptr(seq_lens), _ptr(slots), _ptr(positions), _ptr(num_taken), ctypes.byref(d))
+    if cached_lens.numel() != R or block_table.shape[0] != R:
+        _fail("new_lens, cached_lens and block_table must have one entry per request")
+    for t, n, dt in ((query_start, R + 1, i32), (seq_lens, R, i32), (slots, max_tokens, torch.int64),
+                     (positions, max_tokens, i32), (num_taken, 1, i32)):
+        if t is not None and (t.dtype != dt or t.numel() != n or not t.is_contiguous()):
+            _fail(f"an output has to be contiguous, {dt}, of {n} elements")
+    dev = new_lens.device
+    if query_start is None:
+        query_start = torch.empty(R + 1, dtype=i32, device=dev)
+    if seq_lens is None:
+        seq_lens = torch.empty(R, dtype=i32, device=dev)
+    if slots is None:
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(max_tokens, dtype=i32, device=dev)
+    if num_taken is None:
+        num_taken = torch.empty(1, dtype=i32, device=dev)
+    index = _device_of(new_lens, cached_lens, block_table, free_blocks, query_start, seq_lens, slots, positions,
+                       num_taken)
+    d = SlotDesc(R, block_size, maxb, free_blocks.numel(), max_tokens, 0, stride)
+    _launch("paged_slot_map", index, stream, new_lens.data_ptr(), cached_lens.data_ptr(), block_table.data_ptr(),
+            free_blocks.data_ptr(), query_start.data_ptr(), seq_lens.data_ptr(), slots.data_ptr(),
+            positions.data_ptr(), num_taken.data_ptr(), ctypes.byref(d))
     return query_start, seq_lens, slots, positions, num_taken
 
 
-def _per_token_scales(kv_cache, k_scale, v_scale):
+def _cache_shape(kv_cache):
+    if kv_cache.dtype != torch.uint8 or kv_cache.dim() != 5 or kv_cache.shape[1] != 2 or not kv_cache.is_contiguous():
+        _fail("kv_cache must be contiguous uint8 [num_blocks, 2, num_kv_heads, block_size, head_dim]")
+    NB, _, Hk, bs, D = kv_cache.shape
+    return NB, Hk, bs, D
+
+
+def _per_token_scales(NB, Hk, bs, k_scale, v_scale):
     """True for [num_blocks, Hk, bs] scale tensors, False for one value each."""
-    _need_all(torch.float32, True, k_scale=k_scale, v_scale=v_scale)
-    NB, _, Hk, bs, _ = kv_cache.shape
+    f32 = torch.float32
+    if k_scale.dtype != f32 or v_scale.dtype != f32 or not k_scale.is_contiguous() or not v_scale.is_contiguous():
+        _fail("k_scale and v_scale must be contiguous float32")
     if k_scale.dim() == 3:
-        _need(tuple(k_scale.shape) == (NB, Hk, bs) and tuple(v_scale.shape) == (NB, Hk, bs),
-              "per-token scales must be [num_blocks, num_kv_heads, block_size]")
+        if tuple(k_scale.shape) != (NB, Hk, bs) or tuple(v_scale.shape) != (NB, Hk, bs):
+            _fail("per-token scales must be [num_blocks, num_kv_heads, block_size]")
         return True
-    _need(k_scale.numel() == 1 and v_scale.numel() == 1, "per-tensor scales must have one element")
+    if k_scale.numel() != 1 or v_scale.numel() != 1:
+        _fail("per-tensor scales must have one element")
     return False
-
-
-def _need_cache(kv_cache):
-    _need(kv_cache.dim() == 5 and kv_cache.shape[1] == 2, "kv_cache must be [num_blocks, 2, Hk, block_size, head_dim]")
-    _need_all(torch.uint8, True, kv_cache=kv_cache)
 
 
 def kv_append_fp8(k, v, kv_cache, slots, k_scale, v_scale, stream=None):
@@ -515,53 +547,35 @@ def kv_append_fp8(k, v, kv_cache, slots, k_scale, v_scale, stream=None):
     [NB, 2, Hk, bs, D]; slots int64 [T], negative = skip the row; k_scale /
     v_scale float32 with one element (read) or [NB, Hk, bs] (computed per token
     and written). Returns kv_cache."""
-    _need_cache(kv_cache)
-    _need_all(torch.bfloat16, False, k=k, v=v)
-    _need_all(torch.int64, True, slots=slots)
-    NB, _, Hk, bs, D = kv_cache.shape
+    NB, Hk, bs, D = _cache_shape(kv_cache)
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or slots.dtype != torch.int64:
+        _fail("k and v must be bfloat16, slots int64")
     T = slots.numel()
-    _need(tuple(k.shape) == (T, Hk, D) and tuple(v.shape) == (T, Hk, D),
-          "k and v must be [num_tokens, num_kv_heads, head_dim] with a row per slot")
-    _need(T == 0 or (k.stride(2) == 1 and v.stride(2) == 1), "k and v must be contiguous along head_dim")
-    per_token = _per_token_scales(kv_cache, k_scale, v_scale)
-    _same_device(k, v, kv_cache, slots, k_scale, v_scale)
-    d = AppendDesc()
-    d.num_tokens, d.num_kv_heads, d.head_dim, d.block_size, d.num_blocks = T, Hk, D, bs, NB
-    d.kv_scale_per_token = 1 if per_token else 0
-    d.k_stride_tok, d.k_stride_head = _dim_stride(k, 0), _dim_stride(k, 1)
-    d.v_stride_tok, d.v_stride_head = _dim_stride(v, 0), _dim_stride(v, 1)
-    _launch("kv_append_fp8", k.device, stream, _ptr(k), _ptr(v), _ptr(kv_cache), _ptr(slots), _ptr(k_scale),
-            _ptr(v_scale), ctypes.byref(d))
+    if tuple(k.shape) != (T, Hk, D) or tuple(v.shape) != (T, Hk, D) or not slots.is_contiguous():
+        _fail("k and v must be [num_tokens, num_kv_heads, head_dim] with a row per (contiguous) slot")
+    if T and (k.stride(2) != 1 or v.stride(2) != 1):
+        _fail("k and v must be contiguous along head_dim")
+    per_token = _per_token_scales(NB, Hk, bs, k_scale, v_scale)
+    index = _device_of(k, v, kv_cache, slots, k_scale, v_scale)
+    d = AppendDesc(T, Hk, D, bs, NB, 1 if per_token else 0, _dim_stride(k, 0), _dim_stride(k, 1), _dim_stride(v, 0),
+                   _dim_stride(v, 1))
+    _launch("kv_append_fp8", index, stream, k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(), slots.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), ctypes.byref(d))
     return kv_cache
-
-
-def _dim_stride(t, i):
-    """Stride of dimension i for a descriptor, where 0 means contiguous: a
-    dimension of one element has no stride; an expanded one is refused."""
-    if t.shape[i] <= 1:
-        return 0
-    _need(t.stride(i) > 0, "expanded tensors are not supported")
-    return t.stride(i)
 
 
 def chunk_desc(q, kv_cache, block_table, query_group, per_token, softmax_scale=None):
     """Descriptor of pa_chunk_fp8 for q bf16 [T, Hq, D]."""
-    _need_cache(kv_cache)
-    _need_all(torch.bfloat16, False, q=q)
-    _need_all(torch.int32, False, block_table=block_table)
-    T, Hq, D = q.shape
-    NB, _, Hk, bs, D2 = kv_cache.shape
-    _need(D2 == D and Hq == Hk * query_group, "q must be [num_tokens, num_kv_heads*query_group, head_dim]")
-    _need(T == 0 or q.stride(2) == 1, "q must be contiguous along head_dim")
+    NB, Hk, bs, D = _cache_shape(kv_cache)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[1] != Hk * query_group or q.shape[2] != D:
+        _fail("q must be bfloat16 [num_tokens, num_kv_heads*query_group, head_dim]")
+    T = q.shape[0]
+    if T and q.stride(2) != 1:
+        _fail("q must be contiguous along head_dim")
     maxb, stride = _rows(block_table)
-    d = ChunkDesc()
-    d.num_reqs, d.num_tokens, d.num_kv_heads, d.query_group = block_table.shape[0], T, Hk, query_group
-    d.head_dim, d.block_size, d.num_blocks, d.max_blocks_per_seq = D, bs, NB, maxb
-    d.kv_scale_per_token = 1 if per_token else 0
-    d.softmax_scale = 0.0 if softmax_scale is None else float(softmax_scale)
-    d.q_stride_tok, d.q_stride_head = _dim_stride(q, 0), _dim_stride(q, 1)
-    d.table_stride = stride
-    return d
+    return ChunkDesc(block_table.shape[0], T, Hk, query_group, D, bs, NB, maxb, 1 if per_token else 0,
+                     0.0 if softmax_scale is None else float(softmax_scale), _dim_stride(q, 0), _dim_stride(q, 1),
+                     stride)
 
 
 def pa_chunk_fp8_workspace_size(desc: ChunkDesc) -> int:
@@ -578,26 +592,27 @@ def pa_chunk_fp8(q, kv_cache, block_table, query_start, seq_lens, k_scale, v_sca
     with one element or [NB, Hk, bs]. Returns out bf16 [T, Hq, D]; rows outside
     every request's range are not written. `desc` (from chunk_desc for these
     tensors) and `workspace` may be kept between calls."""
-    per_token = _per_token_scales(kv_cache, k_scale, v_scale)
+    NB, Hk, bs, _ = _cache_shape(kv_cache)
+    per_token = _per_token_scales(NB, Hk, bs, k_scale, v_scale)
+    if softmax_scale is None and desc is not None:
+        softmax_scale = desc.softmax_scale
     want = chunk_desc(q, kv_cache, block_table, query_group, per_token, softmax_scale)
-    if desc is None:
-        desc = want
-    else:
-        if softmax_scale is None:
-            want.softmax_scale = desc.softmax_scale
-        _need(bytes(desc) == bytes(want), "desc does not describe these tensors")
-    _need_all(torch.int32, True, query_start=query_start, seq_lens=seq_lens)
-    _need(query_start.numel() == desc.num_reqs + 1 and seq_lens.numel() == desc.num_reqs,
-          "query_start must have one entry more than requests, seq_lens one per request")
+    if desc is not None and bytes(desc) != bytes(want):
+        _fail("desc does not describe these tensors")
+    R = want.num_reqs
+    if query_start.dtype != torch.int32 or seq_lens.dtype != torch.int32 or not query_start.is_contiguous() or \
+            not seq_lens.is_contiguous() or query_start.numel() != R + 1 or seq_lens.numel() != R:
+        _fail("query_start must be contiguous int32 with one entry more than requests, seq_lens with one per request")
     if out is None:
-        out = torch.empty(tuple(q.shape), dtype=torch.bfloat16, device=q.device)
-    else:
-        _need_all(torch.bfloat16, True, out=out)
-        _need(out.shape == q.shape, "out must have the shape of q")
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
+        _fail("out must be contiguous bfloat16 of the shape of q")
     if workspace is None:
-        workspace = alloc_workspace(pa_chunk_fp8_workspace_size(desc), q.device)
-    _same_device(q, kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, out, workspace)
-    _launch("pa_chunk_fp8", q.device, stream, _ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(query_start),
-            _ptr(seq_lens), _ptr(k_scale), _ptr(v_scale), _ptr(out), ctypes.byref(desc), _ptr(workspace),
-            workspace.numel() * workspace.element_size())
+        workspace = alloc_workspace(pa_chunk_fp8_workspace_size(want), q.device)
+    elif not workspace.is_contiguous():
+        _fail("workspace must be contiguous")
+    index = _device_of(q, kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, out, workspace)
+    _launch("pa_chunk_fp8", index, stream, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
+            query_start.data_ptr(), seq_lens.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(),
+            ctypes.byref(want), workspace.data_ptr(), workspace.nbytes)
     return out
