@@ -24,6 +24,7 @@ namespace chunk {
 
 constexpr int TILE = 128;            // keys per unit, rows per row tile
 constexpr int ITEM_COST = 3;
+constexpr int MIN_UNITS = 4;         // per CTA: fewer CTAs take part rather than smaller ranges
 
 // sum_{i < n} floor((a i + b) / m) for a, b >= 0 (the lattice points under a
 // line, by a Euclid-like reduction). T: 32 bits where a n + b and m fit (the
@@ -86,6 +87,12 @@ QPA_HD inline Req make_req(int start, int next, int len, int num_tokens, int max
   q.L = max(0, min(len, max_len));
   q.nt = q.ql / bt + (q.ql % bt != 0);
   return q;
+}
+
+// CTAs that take part in U units
+QPA_HD inline int active_ctas(long long U, int grid) {
+  const long long n = (U + MIN_UNITS - 1) / MIN_UNITS;
+  return n < grid ? (int)n : grid;
 }
 
 }  // namespace chunk

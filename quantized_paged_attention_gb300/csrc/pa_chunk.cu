@@ -42,6 +42,7 @@
 #include "qpa_internal.h"
 #include "tc.cuh"
 #include "chunk_schedule.h"
+#include <climits>
 
 namespace qpa {
 
@@ -257,8 +258,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       W += sched[w];
     }
     const long long U = W * p.num_kv_heads;
-    u0 = div_nonneg(U * blockIdx.x, gridDim.x);
-    u1 = div_nonneg(U * (blockIdx.x + 1), gridDim.x);
+    const int nc = active_ctas(U, gridDim.x), bc = min((int)blockIdx.x, nc);
+    u0 = nc ? div_nonneg(U * bc, nc) : 0;
+    u1 = nc ? div_nonneg(U * min(bc + 1, nc), nc) : 0;
     if (u0 < u1) {
       long long off = u0 - div_nonneg(u0, W) * W - (base + incl - mine);
       if (off >= 0 && off < mine) {
@@ -302,7 +304,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       const int end = a ? it.e1 : it.e0;
       const int tok = (int)(row * gm >> 16);
       const bool valid = tok < it.ntok;
-      const int lim = valid ? it.lim0 + tok : -1;
+      // (rows of no token see everything: their scores are 0, and a key tile with
+      // masks costs more)
+      const int lim = valid ? it.lim0 + tok : INT_MAX;
       float m = kNoMax, l = 0.f;
       int ev = -126;
       for (int t = it.t0; t < end; ++t, ++sc) {
@@ -973,37 +977,73 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
 
 // Merge of the items that cross a cut: block (c, y) looks at the item that
 // starts in CTA c and does not end there, rows 32 y .. 32 y + 31. Its pieces are
-// the starting CTA's last slot and the first slots of the CTAs behind it.
+// the starting CTA's last slot and the first slots of the CTAs behind it, found
+// at once by a vote over all of them (following them one load after the other
+// took 15 us where 38 CTAs shared a short request).
 template <int D>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p, const int grid) {
   const int c = blockIdx.x;
   const int4 ms = p.meta[2 * c];
   if (ms.w < 0) return;
+  __shared__ int slots[MAX_GRID + 4];
+  __shared__ int stop, count;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) stop = grid;
+  __syncthreads();
+  const int d = c + 1 + tid;
+  int4 mc = make_int4(0, 0, 1, 0);
+  if (d < grid) mc = p.meta[2 * d + 1];
+  // the walk ends at the first CTA that has items and does not continue this one
+  // (not part of it) or ends it (the last part); CTAs without items are passed
+  if (d < grid && !mc.z && (!mc.x || mc.y)) atomicMin(&stop, d);
+  __syncthreads();
+  const bool mine = d < grid && !mc.z && mc.x && d <= stop;
+  __shared__ unsigned votes[8];
+  const unsigned vote = __ballot_sync(0xffffffffu, mine);
+  if (lane == 0) votes[tid >> 5] = vote;
+  __syncthreads();
+  if (mine) {
+    int at = 1 + __popc(vote & ((1u << lane) - 1u));
+    for (int w = 0; w < (tid >> 5); ++w) at += __popc(votes[w]);
+    slots[at] = 2 * d;
+  }
+  if (tid == 0) {
+    slots[0] = ms.w;
+    int n = 1;
+    for (int w = 0; w < 8; ++w) n += __popc(votes[w]);
+    count = n;
+  }
+  __syncthreads();
   constexpr int TPR = D / 4, RPB = 256 / TPR;        // threads per row (4 dims each), rows per pass
-  const int col = threadIdx.x % TPR;
+  const int col = tid % TPR, n = count;
   const int rows = ms.z * p.qg;
-  for (int row = blockIdx.y * 32 + threadIdx.x / TPR; row < min(rows, (int)blockIdx.y * 32 + 32); row += RPB) {
+  for (int row = blockIdx.y * 32 + tid / TPR; row < min(rows, (int)blockIdx.y * 32 + 32); row += RPB) {
     float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    auto piece = [&](int slot) {
-      const float2 ml = p.part_ml[(long long)slot * p.part_rows + row];
-      if (ml.y == 0.f) return;                       // the row saw no key of it, O is not written
-      const float4 x = *reinterpret_cast<const float4*>(p.part_o + ((long long)slot * p.part_rows + row) * D + 4 * col);
-      const float mn = fmaxf(M, ml.x);
-      const float a0 = ex2(M - mn), w = ml.y * ex2(ml.x - mn);
-      M = mn;
-      l = l * a0 + w;
-      o[0] = o[0] * a0 + w * x.x;
-      o[1] = o[1] * a0 + w * x.y;
-      o[2] = o[2] * a0 + w * x.z;
-      o[3] = o[3] * a0 + w * x.w;
-    };
-    piece(ms.w);
-    for (int d = c + 1; d < grid; ++d) {
-      const int4 mc = p.meta[2 * d + 1];
-      if (mc.z) continue;                            // a CTA without units
-      if (!mc.x) break;
-      piece(2 * d);
-      if (mc.y) break;
+#pragma unroll 1
+    for (int i = 0; i < n; i += 4) {                 // four pieces' loads at once
+      float2 ml[4];
+      float4 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        ml[u] = make_float2(-INFINITY, 0.f);
+        if (i + u < n) {
+          const long long at = (long long)slots[i + u] * p.part_rows + row;
+          ml[u] = p.part_ml[at];
+          x[u] = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * col);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (ml[u].y == 0.f) continue;                // the row saw no key of it, O is not written
+        const float mn = fmaxf(M, ml[u].x);
+        const float a0 = ex2(M - mn), w = ml[u].y * ex2(ml[u].x - mn);
+        M = mn;
+        l = l * a0 + w;
+        o[0] = o[0] * a0 + w * x[u].x;
+        o[1] = o[1] * a0 + w * x[u].y;
+        o[2] = o[2] * a0 + w * x[u].z;
+        o[3] = o[3] * a0 + w * x[u].w;
+      }
     }
     const float rl = l == 0.f ? 0.f : 1.f / l;
     const int tok = row / p.qg;

@@ -109,8 +109,9 @@ def test_ranges_cover_every_unit_once_and_pieces_are_found():
         for n in items:
             first.append(first[-1] + n + cost)
         pieces, start, cont, tiles = {}, {}, {}, [0] * len(items)
+        active = min(grid, -(-U // r.choice([1, 4])))
         for c in range(grid):
-            u, u1 = U * c // grid, U * (c + 1) // grid
+            u, u1 = U * min(c, active) // active, U * min(c + 1, active) // active
             cont[c] = dict(empty=True, x=False, ends=False)
             k = 0
             while u < u1:
