@@ -75,10 +75,11 @@ struct Smem {
   static constexpr int evOff = flagOff + 16;                 // [NC] exponent of the V scales (16 bytes)
   static constexpr int schedOff = evOff + 16;                     // schedule scratch
   static constexpr int barOff = schedOff + 256;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 6 + 2 + 12 + 2;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 6 + 2 + 12 + 2 + 2;
   static constexpr int miscOff = barOff + NBAR * 8;
   static constexpr int total = miscOff + 16 + 1024;
   static_assert(total <= 227 * 1024, "shared memory");
+  static_assert(NW == 2 && wBytes == TILE * D * 2, "a V buffer holds a row tile of the result");
 };
 
 struct Params {
@@ -172,7 +173,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
   // other roles' spills cost more (head_dim 128, 1024 new tokens over 65536:
   // 184/80/64 772 us, 200/64/48 818, 168/96/80 740, 160/112/80 1296; head_dim 64:
   // 184/80/64 574 us, 176/96/64 558, 168/96/80 603)
-  constexpr int REG_SOFTMAX = D == 128 ? 168 : 176, REG_CONV = 96, REG_REST = D == 128 ? 80 : 64;
+  constexpr int REG_SOFTMAX = D == 128 ? 168 : 176, REG_CONV = D == 128 ? 104 : 96, REG_REST = D == 128 ? 72 : 64;
   static_assert(2 * REG_SOFTMAX + REG_CONV + REG_REST <= 512, "register budget");
   constexpr uint32_t T_O = 256, T_P = SEP ? 384 : 0, P_STEP = SEP ? 64 : 128;
   constexpr uint32_t IDESC_QK = idesc_e4m3(128, 128, false, false);
@@ -201,6 +202,8 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
   uint64_t* pfree = pfull + 4;         // [2] P read, O complete so far (MMA commit; SEP)
   uint64_t* ofull = pfree + 2;         // [2] O of an item ready (MMA commit)
   uint64_t* done = ofull + 2;          // [2] all MMAs of a row tile finished
+  uint64_t* efree = done + 2;          // [2] results of an item out of the V buffers (8 softmax warps); two, since a
+                                       // row tile without work in an item may be one item ahead of the other
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::miscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::miscOff + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -223,6 +226,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       mbar_init(&pfree[i], 1);
       mbar_init(&ofull[i], 1);
       mbar_init(&done[i], 1);
+      mbar_init(&efree[i], 8);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -295,22 +299,26 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
     for (int k = 0; ok; ++k) {
       const int qb = k & 1;
       if (!warp_wait(&qfull[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
-      const Item it = lds_item(sb + S::qinfoOff + 64 * qb);
-      if (a && !warp_wait(&qfull1[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
-      const float c = ldsf(sb + S::crowOff + 4 * (qb * ROWS + row));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&qread[qb]);
-      if (it.last) break;
-      const int end = a ? it.e1 : it.e0;
-      const int tok = (int)(row * gm >> 16);
-      const bool valid = tok < it.ntok;
-      // (rows of no token see everything: their scores are 0, and a key tile with
-      // masks costs more)
-      const int lim = valid ? it.lim0 + tok : INT_MAX;
+      // (the item is read again for its result: what the key tiles do not need
+      // would hold registers through them)
+      int t0, end, lim;
+      float c;
+      {
+        const Item it = lds_item(sb + S::qinfoOff + 64 * qb);
+        if (a && !warp_wait(&qfull1[qb], (k >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+        if (it.last) break;
+        c = ldsf(sb + S::crowOff + 4 * (qb * ROWS + row));
+        t0 = it.t0;
+        end = a ? it.e1 : it.e0;
+        // (rows of no token see everything: their scores are 0, and a key tile with
+        // masks costs more)
+        const int tok = (int)(row * gm >> 16);
+        lim = tok < it.ntok ? it.lim0 + tok : INT_MAX;
+      }
       float m = kNoMax, l = 0.f;
       int ev = -126;
-      for (int t = it.t0; t < end; ++t, ++sc) {
-        const int nn = n + t - it.t0, cb = nn % NC;
+      for (int t = t0; t < end; ++t, ++sc) {
+        const int nn = n + t - t0, cb = nn % NC;
         if (!warp_wait(&sfull[a], sc & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
         tc_fence_after();
         float s[4][32];
@@ -347,7 +355,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
         int en = ev;
         if constexpr (PT) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(en) : "r"(sb + S::evOff + 4 * cb));
-        if (t == it.t0) {
+        if (t == t0) {
           m = fmaxf(mx, kNoMax);
         } else {
           const bool grow = mx > m + kLazy;
@@ -405,7 +413,12 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         l += (la[0] + la[1]) + (la[2] + la[3]);
       }
       if (!ok) break;
+      const Item it = lds_item(sb + S::qinfoOff + 64 * qb);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qread[qb]);
       n += it.t1 - it.t0;
+      const int tok = (int)(row * gm >> 16);
+      const bool valid = tok < it.ntok;
 
       // ---- the item's result
       const bool any = it.t0 < end;
@@ -414,11 +427,17 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         ++oc;
         tc_fence_after();
       }
+      // The result leaves through the V buffers (a row tile's rows fit one): a
+      // lane holds a row, and 32 rows' 16 bytes a store kept the load-store unit
+      // from the warps that build the next item's operand (3 us of 5 there). They
+      // are free once both row tiles' last products are done, until the first V
+      // of the next item, which waits for efree.
+      const uint32_t stg = sb + S::wOff + a * S::wBytes + (warp & 3) * 32 * 2 * D;
+      const int used = (n + 1 - a) / 2;              // times V buffer a was filled
+      if (used > 0 && !warp_wait(&wempty[a], (used - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       const bool none = lim < 0 || l == 0.f;
       const float rl = none ? 0.f : __frcp_rn(l);
       const float sv = PT ? ex2((float)ev) : vscale;
-      const int head = it.head * G + row - tok * G;
-      __nv_bfloat16* orow = p.out + ((long long)(it.tok0 + tok) * (p.num_kv_heads * G) + head) * D;
       float* prow = p.part_o + ((long long)it.slot * p.part_rows + row) * D;
       if (it.slot >= 0 && valid) p.part_ml[(long long)it.slot * p.part_rows + row] = make_float2(none ? -INFINITY : m, l);
       if (any) {
@@ -443,26 +462,37 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = ((w >> i) & 1u) ? __uint_as_float(0x7fffffffu) : o[i];
           }
-          if (valid) {
-            if (it.slot < 0) {
+          if (it.slot < 0) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                uint4 v;
-                __nv_bfloat162 b0 = __floats2bfloat162_rn(o[i], o[i + 1]), b1 = __floats2bfloat162_rn(o[i + 2], o[i + 3]);
-                __nv_bfloat162 b2 = __floats2bfloat162_rn(o[i + 4], o[i + 5]), b3 = __floats2bfloat162_rn(o[i + 6], o[i + 7]);
-                v.x = *reinterpret_cast<uint32_t*>(&b0);
-                v.y = *reinterpret_cast<uint32_t*>(&b1);
-                v.z = *reinterpret_cast<uint32_t*>(&b2);
-                v.w = *reinterpret_cast<uint32_t*>(&b3);
-                *reinterpret_cast<uint4*>(orow + 32 * j + i) = v;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) store4(prow + 32 * j + i, o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 32; i += 8) {
+              __nv_bfloat162 b0 = __floats2bfloat162_rn(o[i], o[i + 1]), b1 = __floats2bfloat162_rn(o[i + 2], o[i + 3]);
+              __nv_bfloat162 b2 = __floats2bfloat162_rn(o[i + 4], o[i + 5]), b3 = __floats2bfloat162_rn(o[i + 6], o[i + 7]);
+              sts_i4(stg + lane * (2 * D) + (((4 * j + i / 8) ^ (lane & 7)) << 4),
+                     make_int4(*reinterpret_cast<int*>(&b0), *reinterpret_cast<int*>(&b1), *reinterpret_cast<int*>(&b2),
+                               *reinterpret_cast<int*>(&b3)));
             }
+          } else if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) store4(prow + 32 * j + i, o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        if (it.slot < 0) {
+          // whole rows out, the warp's 32 of them a few at a time
+          __syncwarp();
+          constexpr int CPR = D / 8, RPI = 32 / CPR;
+          const int ch = lane % CPR;
+#pragma unroll 4
+          for (int i = lane / CPR; i < 32; i += RPI) {
+            const int r = a * TILE + (warp & 3) * 32 + i, rt = (int)(r * gm >> 16);
+            const int4 v = lds_i4(stg + i * (2 * D) + ((ch ^ (i & 7)) << 4));
+            if (rt < it.ntok)
+              *reinterpret_cast<int4*>(p.out + ((long long)(it.tok0 + rt) * (p.num_kv_heads * G) + it.head * G + r - rt * G) * D +
+                                       8 * ch) = v;
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&efree[qb]);
     }
   } else if (warp < W_MMA) {
     // ======================================================== converting warps
@@ -509,7 +539,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         cp_async_commit();
       };
       auto build = [&](int a) {
-#pragma unroll 2
+#pragma unroll 4
         for (int b = 0; b < NB; ++b) {
           const uint32_t at = spot(a, b);
           const uint4 x0 = lds128(at), x1 = lds128(at + S::qTerm);
@@ -580,6 +610,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       }
       if (!ok) cp_async_wait_all();
       if (it.last || !ok) break;
+      if (k >= 1 && !warp_wait(&efree[qb ^ 1], ((k - 1) >> 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
 
       // ---- V of the item's key tiles: e4m3 -> f16, [dims / 64][token][64 dims],
       // 128-byte swizzle (the MN-major operand of the PV product)
