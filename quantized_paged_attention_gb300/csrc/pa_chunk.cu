@@ -122,6 +122,11 @@ __device__ __forceinline__ void ffma2(float& a, float& b, float c, float m) {   
   asm("{ .reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %2}; mov.b64 z, {%3, %3}; "
       "fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x; }" : "+f"(a), "+f"(b) : "f"(c), "f"(m));
 }
+__device__ __forceinline__ float fmax3(float a, float b, float c) {   // NaN ignored, as fmaxf
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void fadd2(float& a, float& b, float c, float d) {
   asm("{ .reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
       : "+f"(a), "+f"(b) : "f"(c), "f"(d));
@@ -332,11 +337,18 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         }
         if constexpr (PT) {
           if (!warp_wait(&cfull[cb], (nn / NC) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+          // (the loads of 32 keys at once: one at a time, their latency was a
+          // third of the tile's time)
 #pragma unroll
-          for (int i = 0; i < 128; i += 4) {
-            const float4 ks = lds_f4(sb + S::kscOff + 4 * (cb * TILE + i));
-            fmul2(s[i / 32][i % 32], s[i / 32][i % 32 + 1], ks.x, ks.y);
-            fmul2(s[i / 32][i % 32 + 2], s[i / 32][i % 32 + 3], ks.z, ks.w);
+          for (int j = 0; j < 4; ++j) {
+            float4 ks[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ks[i] = lds_f4(sb + S::kscOff + 4 * (cb * TILE + 32 * j + 4 * i));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              fmul2(s[j][4 * i], s[j][4 * i + 1], ks[i].x, ks[i].y);
+              fmul2(s[j][4 * i + 2], s[j][4 * i + 3], ks[i].z, ks[i].w);
+            }
           }
         }
         const int vis = lim - t * TILE;            // keys 0 .. vis of the tile are seen
@@ -348,9 +360,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         float mx4[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          mx4[j] = s[j][0];
+          mx4[j] = fmaxf(s[j][0], s[j][1]);
 #pragma unroll
-          for (int i = 1; i < 32; ++i) mx4[j] = fmaxf(mx4[j], s[j][i]);
+          for (int i = 2; i < 32; i += 2) mx4[j] = fmax3(mx4[j], s[j][i], s[j][i + 1]);
         }
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
         int en = ev;
