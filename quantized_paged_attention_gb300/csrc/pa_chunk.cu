@@ -175,10 +175,11 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
   constexpr bool SEP = D == 64;
   // registers per thread: the sum over the four groups is what the block is
   // launched with (4 x 128). Fewer for the softmax than it could use, since the
-  // other roles' spills cost more (head_dim 128, 1024 new tokens over 65536:
-  // 184/80/64 772 us, 200/64/48 818, 168/96/80 740, 160/112/80 1296; head_dim 64:
-  // 184/80/64 574 us, 176/96/64 558, 168/96/80 603)
-  constexpr int REG_SOFTMAX = D == 128 ? 168 : 176, REG_CONV = D == 128 ? 104 : 96, REG_REST = D == 128 ? 72 : 64;
+  // other roles' spills cost more. Measured, softmax/conversion/rest: head_dim 128,
+  // 8192-token prompt 176/88/72 961 us, 168/96/80 913, 168/104/72 900, and with
+  // 160/112/80 1357; head_dim 64, per-token scales 168/96/80 574 us, 176/96/64 572,
+  // 192/72/56 557.
+  constexpr int REG_SOFTMAX = D == 128 ? 168 : 192, REG_CONV = D == 128 ? 104 : 72, REG_REST = D == 128 ? 72 : 56;
   static_assert(2 * REG_SOFTMAX + REG_CONV + REG_REST <= 512, "register budget");
   constexpr uint32_t T_O = 256, T_P = SEP ? 384 : 0, P_STEP = SEP ? 64 : 128;
   constexpr uint32_t IDESC_QK = idesc_e4m3(128, 128, false, false);
@@ -324,21 +325,45 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       int ev = -126;
       for (int t = t0; t < end; ++t, ++sc) {
         const int nn = n + t - t0, cb = nn % NC;
+        float s[4][32];
+        // Per-token scales: with head_dim 64, where the softmax warps are what
+        // bounds, the keys' scales are loaded while S is awaited, into the registers
+        // that S times them takes then (6 requests of 200 to 1500 new tokens: 703 us
+        // with the loads after S, 572 so; head_dim 128, where S is late: 996 and 1130)
+        if constexpr (PT && SEP) {
+          if (!warp_wait(&cfull[cb], (nn / NC) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+#pragma unroll
+          for (int i = 0; i < 128; i += 4) {
+            const float4 ks = lds_f4(sb + S::kscOff + 4 * (cb * TILE + i));
+            s[i / 32][i % 32] = ks.x;
+            s[i / 32][i % 32 + 1] = ks.y;
+            s[i / 32][i % 32 + 2] = ks.z;
+            s[i / 32][i % 32 + 3] = ks.w;
+          }
+        }
         if (!warp_wait(&sfull[a], sc & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
         tc_fence_after();
-        float s[4][32];
+        if constexpr (PT && SEP) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, s[j]);
-        tmem_wait_ld();
+          for (int j = 0; j < 4; ++j) {
+            float x[32];
+            tmem_ld32(ts + 32 * j, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) fmul2(s[j][i], s[j][i + 1], x[i], x[i + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, s[j]);
+          tmem_wait_ld();
+        }
         if constexpr (SEP) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sfree[a]);
         }
-        if constexpr (PT) {
+        if constexpr (PT && !SEP) {
           if (!warp_wait(&cfull[cb], (nn / NC) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-          // (the loads of 32 keys at once: one at a time, their latency was a
-          // third of the tile's time)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float4 ks[8];
