@@ -103,11 +103,13 @@ __device__ __forceinline__ uint32_t quant4(uint32_t a, uint32_t b, const Scale& 
 // A token's 2 Hk head vectors take 2 Hk TPR threads (in rounds, if more than the
 // block has); a block holds as many tokens side by side as fit. A thread keeps
 // its place (K or V, head, 16 dims) and steps through the tokens, UN of them at
-// once so that their slots and then their 32 bytes are in flight together.
+// once so that their slots and then their 32 bytes are in flight together. Two
+// tokens and 4 blocks per SM, one wave: 16384 tokens x 8 heads x 128 23.5 us (39
+// with per-token scales); 4 tokens and 2 blocks 24.5 (43), 6 blocks 31 (43).
 template <int HD, bool PT>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendLaunch p, const int log2_bs, const int side) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendLaunch p, const int log2_bs, const int side) {
   constexpr int TPR = HD / 16;                 // threads per head vector
-  constexpr int UN = 4;
+  constexpr int UN = 2;
   const int Hk = p.num_kv_heads, bs = p.block_size;
   const int tpt = 2 * Hk * TPR;                // threads per token
   const long long slots = (long long)p.num_blocks * bs;
@@ -185,7 +187,7 @@ cudaError_t launch_append(const AppendLaunch& a, cudaStream_t stream) {
   const int tpt = 2 * a.num_kv_heads * (a.head_dim / 16);
   const int side = std::max(1, kThreads / tpt);
   const long long want = ((long long)a.num_tokens + side - 1) / side;
-  const int grid = (int)std::min(want, (long long)a.num_sms * 6);
+  const int grid = (int)std::min(want, (long long)a.num_sms * 4);
   auto launch = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(a, log2_bs, side); };
   if (a.head_dim == 64) a.per_token ? launch(append_kernel<64, true>) : launch(append_kernel<64, false>);
   else a.per_token ? launch(append_kernel<128, true>) : launch(append_kernel<128, false>);

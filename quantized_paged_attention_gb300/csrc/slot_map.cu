@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const SlotMapLaunch 
   }
   __syncthreads();
   const uint32_t total = carry_t, need = carry_b;
-  const int gtid = blockIdx.x * kThreads + tid, gsize = gridDim.x * kThreads;
+  const uint32_t gtid = blockIdx.x * kThreads + tid, gsize = gridDim.x * kThreads;
   if (blockIdx.x == 0) {
     for (int r = tid; r <= B; r += kThreads) p.query_start[r] = (int)start[r];
     if (tid == 0) *p.num_taken = (int)need;
@@ -101,23 +101,24 @@ __global__ void __launch_bounds__(kThreads) slot_map_kernel(const SlotMapLaunch 
 
   int err = KERR_NONE;
   // ---- table entries of the taken blocks
-  const int have = (int)min(need, (uint32_t)p.num_free);
-  for (int k = gtid; k < have; k += gsize) {
-    const int r = find(base, B, (uint32_t)k);
-    const uint32_t e = blocks((uint32_t)max(0, __ldg(p.cached_lens + r))) + ((uint32_t)k - base[r]);
+  // (counts up to INT32_MAX, steps below 2^18: 32 unsigned bits hold the sums)
+  const uint32_t have = min(need, (uint32_t)p.num_free);
+  for (uint32_t k = gtid; k < have; k += gsize) {
+    const int r = find(base, B, k);
+    const uint32_t e = blocks((uint32_t)max(0, __ldg(p.cached_lens + r))) + (k - base[r]);
     if (e < (uint32_t)p.max_blocks) p.block_table[r * p.table_stride + e] = __ldg(p.free_blocks + k);
     else err = KERR_CAPACITY;
   }
   if (need > (uint32_t)p.num_free) err = KERR_CAPACITY;
 
   // ---- slots and positions
-  for (int i = gtid; i < p.max_tokens; i += gsize) {
+  for (uint32_t i = gtid; i < (uint32_t)p.max_tokens; i += gsize) {
     long long slot = -1;
     uint32_t pos = 0;
-    if ((uint32_t)i < total) {
-      const int r = find(start, B, (uint32_t)i);
+    if (i < total) {
+      const int r = find(start, B, i);
       const uint32_t c = (uint32_t)max(0, __ldg(p.cached_lens + r));
-      pos = sat_add(c, (uint32_t)i - start[r]);
+      pos = sat_add(c, i - start[r]);
       const uint32_t e = pos >> log2_bs, held = blocks(c);
       int32_t blk = -1;
       bool room = e < (uint32_t)p.max_blocks;
