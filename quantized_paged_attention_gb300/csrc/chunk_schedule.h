@@ -56,6 +56,23 @@ QPA_HD_CALL inline long long floor_sum(long long n, long long m, long long a, lo
   return floor_sum_t<long long>(n, m, a, b);
 }
 
+// sum_{i < n} floor((bt i + b) / TILE) for b >= 0. Group sizes are powers of two
+// as a rule, so bt is one too and no division is left: with bt <= TILE, q = TILE
+// / bt and c = floor(b / bt) the terms are floor((c + i) / q), a difference of
+// F(x) = sum_{y < x} floor(y / q) = q k (k - 1) / 2 + k (x - q k), k = floor(x / q).
+// (The general reduction took 1.7 us of a launch.)
+QPA_HD inline long long tile_sum(int n, int bt, long long b) {
+  if (n <= 0) return 0;
+  if ((bt & (bt - 1)) != 0) return floor_sum(n, TILE, bt, b);
+  if (bt > TILE) return (b / TILE) * n + (long long)(bt / TILE) * n * (n - 1) / 2;   // constants: shifts
+  int lb = 0;
+  while ((1 << lb) < bt) ++lb;
+  const int lq = 7 - lb;
+  static_assert(TILE == 128, "2^7");
+  const long long c = b >> lb, x = c + n, kc = c >> lq, kx = x >> lq;
+  return (((kx * (kx - 1)) << lq) >> 1) + kx * (x - (kx << lq)) - (((kc * (kc - 1)) << lq) >> 1) - kc * (c - (kc << lq));
+}
+
 // One request as the schedule sees it: first query row, rows, cached tokens
 // (the rows' own included), items.
 struct Req {
@@ -70,7 +87,7 @@ struct Req {
     const int d = L - ql;
     // items whose last row sees nothing, d + (i + 1) bt - 1 < 0: one unit each
     const int i0 = d >= 1 - bt ? 0 : min(j, -d / bt);
-    return (long long)j * (1 + ITEM_COST) + floor_sum(j - i0, TILE, bt, d + (long long)(i0 + 1) * bt - 1);
+    return (long long)j * (1 + ITEM_COST) + tile_sum(j - i0, bt, d + (long long)(i0 + 1) * bt - 1);
   }
   QPA_HD long long units(int bt) const { return nt ? before(nt - 1, bt) + tiles(nt - 1, bt) + ITEM_COST : 0; }
   // first key tile at offset o into an item's units
