@@ -250,8 +250,12 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
     const int per = (p.num_reqs + THREADS - 1) / THREADS;
     const int r0 = threadIdx.x * per, r1 = min(p.num_reqs, r0 + per);
     long long mine = 0;
+    Req only = {0, 0, 0, 0};                       // the thread's request, if it has one
 #pragma unroll 1
-    for (int r = r0; r < r1; ++r) mine += load_req(p, r, bt).units(bt);
+    for (int r = r0; r < r1; ++r) {
+      only = load_req(p, r, bt);
+      mine += only.units(bt);
+    }
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -275,14 +279,20 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       long long off = u0 - div_nonneg(u0, W) * W - (base + incl - mine);
       if (off >= 0 && off < mine) {
         int r = r0;
-        while (true) {                             // ends: off lies below this thread's sum
-          const long long n = load_req(p, r, bt).units(bt);
-          if (off < n || r + 1 >= r1) break;
-          off -= n;
-          ++r;
+        Req q = only;
+        if (per > 1) {
+#pragma unroll 1
+          while (true) {                           // ends: off lies below this thread's sum
+            q = load_req(p, r, bt);
+            const long long n = q.units(bt);
+            if (off < n || r + 1 >= r1) break;
+            off -= n;
+            ++r;
+          }
         }
         sched[16] = r;
         sched[17] = off;
+        sts_i4(sb + S::schedOff + 18 * 8, make_int4(q.q0, q.ql, q.L, q.nt));
       }
     }
   }
@@ -561,7 +571,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         return sb + S::qOff + a * 2 * S::qTerm + tr * D + ((part ^ (D == 128 ? (tr & 7) : ((tr >> 1) & 3))) << 4);
       };
       auto fetch = [&](int a) {
-#pragma unroll 1
+#pragma unroll 4
         for (int b = 0; b < NB; ++b) {
           const int row = a * TILE + b * RPS + cw * RPW + lane / LPR;
           const int tok = (int)(row * gm >> 16);
@@ -887,7 +897,8 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         h = (int)div_nonneg(u0, W);
         r = (int)sched[16];
         const long long off = sched[17];
-        rq = load_req(p, r, bt);
+        const int4 q = lds_i4(sb + S::schedOff + 18 * 8);
+        rq = Req{q.x, q.y, q.z, q.w};
         int lo = 0, hi = rq.nt;                      // the item that holds unit off of the request
         while (hi - lo > 1) {
           const int probe = Req::split(lo, hi, lane);
@@ -1187,7 +1198,11 @@ cudaError_t launch_chunk(const ChunkLaunch& a, cudaStream_t stream) {
   p.max_len = a.max_blocks * bs;
   p.part_rows = L.rows;
   p.softmax_scale = a.softmax_scale;
-  const int grid = std::min(a.num_sms, MAX_GRID);
+  // no more CTAs than the most units that these sizes can have would employ
+  const int bt = ROWS / a.qg;
+  const long long items = (long long)a.num_tokens / bt + std::min(a.num_reqs, a.num_tokens);
+  const long long most = std::min(items * a.num_kv_heads, 1LL << 20) * ((p.max_len - 1) / TILE + 1 + ITEM_COST);
+  const int grid = active_ctas(most, std::min(a.num_sms, MAX_GRID));
   cudaError_t e = cudaSuccess;
   auto launch = [&](auto kernel, int smem) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
