@@ -416,13 +416,13 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
             if (SEP && !warp_wait(&pfree[a], (sc & 1) ^ 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
             if (SEP) tc_fence_after();
 #pragma unroll 1
-            for (int j = 0; j < D; j += 32) {
-              float o[32];
-              tmem_ld32(to + j, o);
+            for (int j = 0; j < D; j += 16) {        // (the scores hold 128 registers)
+              float o[16];
+              tmem_ld16(to + j, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= f;
-              tmem_st32(to + j, reinterpret_cast<const uint32_t*>(o));
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tmem_st16(to + j, reinterpret_cast<const uint32_t*>(o));
             }
           }
         }
