@@ -7,15 +7,15 @@
 // (p <= 256 then, and O / l does not depend on m).
 //
 //  * Item: 256 query rows of one KV head, i.e. 256 / G whole tokens with their
-//    G heads (rows of a group share their keys), as two tiles of 128 rows.
-//    Unit: one 128-token key tile of an item. The units of all items (heads,
-//    then requests, then tokens) are cut into equal contiguous ranges, one per
-//    CTA, whatever the batch looks like. An item that crosses a cut leaves
-//    float32 partials (m, l, O / l) in the workspace, and the combine kernel
-//    merges them in order (no atomics: the result is the same every time).
-//    A CTA needs no plan from memory: the units of a request are a sum of
-//    floors of an arithmetic progression, in closed form, so a scan over the
-//    requests and one search find its range.
+//    G heads (rows of a group share their keys), as two tiles of 128 rows,
+//    walked in key tiles of 128. An item costs a unit per key tile and some to
+//    begin; the units of all items (heads, then requests, then tokens) are cut
+//    into equal contiguous ranges, one per CTA, whatever the batch looks like. An
+//    item that crosses a cut leaves float32 partials (m, l, O / l) in the
+//    workspace, and the combine kernel merges them in order (no atomics: the
+//    result is the same every time). A CTA needs no plan from memory: the units of
+//    a request are a sum of floors of an arithmetic progression, in closed form,
+//    so a scan over the requests and one search find its range.
 //  * QK: S = Q K^T as kind::f8f6f4. K enters as the cache's e4m3 bytes; a query
 //    row, scaled by a power of two to a largest |q| in [128, 256), enters as
 //    the sum of 2 e4m3 terms into the same accumulator (8 significant bits:
@@ -29,11 +29,25 @@
 //  * Roles: 2 x 4 softmax warps (a thread owns one row: no exchange between
 //    lanes), one per row tile, so that the tensor core works for one while the
 //    other computes; 4 warps that convert V and build the next item's query
-//    operand; an MMA warp; a warp that walks the schedule and issues the TMA
-//    copies (one box per page of the tile, one page per lane).
+//    operand; an MMA warp (head_dim 64: two); a warp that walks the schedule and
+//    issues the TMA copies (one box per page of the tile, one page per lane); a
+//    warp that brings the next items' query rows to L2.
 //  * Tokens past the sequence's end are zeroed in V and masked in S; a NaN code
 //    in V is taken out of the product, and at the item's end put back into the
 //    rows that see its token, so it cannot leak through 0 * NaN.
+// Bound: a key tile's products take the tensor core 2048 clocks (head_dim 128),
+// the two row tiles' turns come every 3200: per row tile S, the softmax's
+// maximum, its exponentials (512 clocks of the special function unit, twice) and
+// P V follow one another, and only the other row tile's chain overlaps them.
+// Tensor memory is full (S and O of both), so a third chain does not fit.
+// Measured (GB300): 1024 new tokens over 65536, 8 x 4 heads of 128, 1.50 PFLOP/s,
+// 78 % of the measured bf16 rate; a prompt of 8192, 8 x 8 heads, 1.22 PFLOP/s (the
+// rest is its items' beginnings); 64 single tokens over 1024..16384 3.1 TB/s.
+// Tried and slower: both row tiles' pipelines on alternate key tiles of an item
+// that has 128 rows at most, and its next S in the idle row tile's buffer (the
+// registers cost every other case 10 to 18 % and such items gained nothing: their
+// V waits for the conversion); an eighth or a quarter of the exponentials as
+// polynomials on the FMA pipe (+7 %, +12 %); P in stores of 16 columns.
 // Every wait has a time limit; a timeout raises the error word and all roles
 // leave through the common teardown.
 #define QPA_WHOLE_UNIT
@@ -71,8 +85,8 @@ struct Smem {
   static constexpr int kscOff = vrawOff + NV * TILE * 4;          // [NC][128] K scales for the softmax
   static constexpr int iringOff = kscOff + NC * TILE * 4;         // [IR] 64 bytes
   static constexpr int qinfoOff = iringOff + IR * 64;             // [2] 64 bytes
-  static constexpr int flagOff = qinfoOff + 2 * 64;               // [4] V of an item holds a NaN
-  static constexpr int evOff = flagOff + 16;                 // [NC] exponent of the V scales (16 bytes)
+  static constexpr int flagOff = qinfoOff + 2 * 64;               // [4 items][4 warps] V holds a NaN
+  static constexpr int evOff = flagOff + 64;                      // [NC] exponent of the V scales (16 bytes)
   static constexpr int schedOff = evOff + 16;                     // schedule scratch
   static constexpr int barOff = schedOff + 256;
   static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 6 + 2 + 12 + 2 + 2;
@@ -139,22 +153,22 @@ __device__ __forceinline__ void fmul2(float& a, float& b, float c, float d) {
 
 using namespace chunk;
 
-// A warp's rows against the NaN of V among tokens [a, b): mask gets the dims in
+// A warp's rows against the NaN of V among tokens [a, last): mask gets the dims in
 // which a token that the lane's row sees (index at most lim) holds a NaN code,
 // all of them where its V scale is not finite. Reads the pages again: about a
 // byte per clock and warp, for broken inputs only.
 template <int D, bool PT>
-__device__ __noinline__ void find_nans(const Params& p, const uint8_t* kv, const Item& it, int a, int b, int lim, int lane,
+__device__ __noinline__ void find_nans(const Params& p, const uint8_t* kv, int req, int head, int a, int last, int lim, int lane,
                                        uint32_t (&mask)[D / 32]) {
-  const int bs = 1 << p.log2_bs, last = min(b, it.L);
+  const int bs = 1 << p.log2_bs;
   for (int t = a; t < last; ++t) {
-    int blk = __ldg(p.block_table + it.req * p.table_stride + (t >> p.log2_bs));
+    int blk = __ldg(p.block_table + req * p.table_stride + (t >> p.log2_bs));
     if (blk < 0 || blk >= p.num_blocks) blk = 0;
     const long long off = t & (bs - 1);
-    const uint8_t* v = kv + ((((long long)blk * 2 + 1) * p.num_kv_heads + it.head) * bs + off) * D;
+    const uint8_t* v = kv + ((((long long)blk * 2 + 1) * p.num_kv_heads + head) * bs + off) * D;
     bool all = false;
     if constexpr (PT)
-      all = !(fabsf(__ldg(p.v_scale + ((long long)blk * p.num_kv_heads + it.head) * bs + off)) < INFINITY);
+      all = !(fabsf(__ldg(p.v_scale + ((long long)blk * p.num_kv_heads + head) * bs + off)) < INFINITY);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const uint32_t w = __ballot_sync(0xffffffffu, all || (__ldg(v + 32 * i + lane) & 0x7f) == 0x7f);
@@ -493,8 +507,11 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         uint32_t nan[D / 32];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) nan[i] = 0;
-        const bool anynan = lds32(sb + S::flagOff + 4 * (k & 3)) != 0;
-        if (anynan) find_nans<D, PT>(p, kv, it, it.t0 * TILE, end * TILE, lim, lane, nan);
+        // (the converting warps' marks, each before its last V of the item)
+        if (!warp_wait(&wfull[(n - 1) % NW], ((n - 1) / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+        const int4 marks = lds_i4(sb + S::flagOff + 16 * (k & 3));
+        const bool anynan = (marks.x | marks.y | marks.z | marks.w) != 0;
+        if (anynan) find_nans<D, PT>(p, kv, it.req, it.head, it.t0 * TILE, min(end * TILE, it.L), lim, lane, nan);
 #pragma unroll 1
         for (int j = 0; j < D / 32; ++j) {
           float o[32];
@@ -633,9 +650,10 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         }
       };
       if (k >= 2 && !warp_wait(&qread[qb], ((k >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
-      if (cw == 0 && lane == 0) {
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + S::flagOff + 4 * (k & 3)), "r"(0u) : "memory");
-        sts_item(sb + S::qinfoOff + 64 * qb, it);
+      if (lane == 0) {
+        // (a mark of this warp's own: the warps are not in step)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + S::flagOff + 16 * (k & 3) + 4 * cw), "r"(0u) : "memory");
+        if (cw == 0) sts_item(sb + S::qinfoOff + 64 * qb, it);
       }
       const int na = it.last ? 0 : rows > TILE ? 2 : 1;
 #pragma unroll 1
@@ -724,7 +742,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
             };
             x[i] = make_uint4(clean(x[i].x), clean(x[i].y), clean(x[i].z), clean(x[i].w));
           }
-          if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + S::flagOff + 4 * (k & 3)), "r"(1u) : "memory");
+          if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + S::flagOff + 16 * (k & 3) + 4 * cw), "r"(1u) : "memory");
         }
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -889,7 +907,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       long long left = u1 - u0;
       // for the combine: the item that starts here and is cut (head, row, tokens,
       // slot); whether the first item began earlier, whether it ends here, no items
-      int4 m_start = make_int4(0, 0, 0, -1), m_cont = make_int4(0, 0, 1, 0);;
+      int4 m_start = make_int4(0, 0, 0, -1), m_cont = make_int4(0, 0, 1, 0);
       int h = 0, r = 0, j = 0;
       long long o = 0;                               // units of item j that lie before the range
       Req rq = {0, 0, 0, 0};

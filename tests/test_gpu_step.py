@@ -155,7 +155,8 @@ def _check_append(k_bits, v_bits, cache, slots, ks, vs, fused=False, err=0):
 
 @pytest.mark.parametrize("per_token", [False, True])
 @pytest.mark.parametrize("T,Hk,D,bs,fused", [(1, 1, 64, 16, False), (1, 1, 128, 16, True), (7, 3, 128, 32, True),
-                                             (33, 8, 64, 64, False), (130, 5, 128, 128, False), (301, 2, 64, 256, True)])
+                                             (33, 8, 64, 64, False), (130, 5, 128, 128, False), (301, 2, 64, 256, True),
+                                             (9, 20, 128, 16, False), (5, 70, 64, 16, True)])
 def test_append_codes_and_scales(T, Hk, D, bs, fused, per_token):
     r = synth.rng(T * 7 + Hk + D)
     k, v = (synth.round_to_bf16_bits(r.standard_normal((T, Hk, D)) * np.exp(r.uniform(-4, 4, (T, Hk, 1))))
@@ -312,6 +313,9 @@ CASES = [
     ([(260, 261)], 1, 1, 64, 64, True, 2),
     ([(70, 900), (1, 2000), (0, 0)], 2, 4, 128, 256, True, 0),
     ([(50, 50), (3, 1100)], 3, 5, 64, 16, True, 4),
+    ([(30, 200), (15, 15)], 1, 33, 64, 128, False, 0),
+    ([(1, 20000)], 1, 4, 128, 64, False, 0),               # one item over many CTAs
+    ([(1, 9000), (40, 12000)], 1, 4, 64, 16, True, 0),
 ]
 
 
@@ -475,6 +479,39 @@ def test_chunk_two_streams_at_once_and_graph_replay():
     want = qpa.pa_chunk_fp8(**t1)
     _clean()
     assert torch.equal(o3, want)
+
+
+def test_pages_past_4_gib():
+    """Blocks at the end of a cache of more than 2^32 bytes: append there, then
+    attend over them, beside blocks at its start."""
+    Hk, bs, D = 8, 16, 128
+    NB = (1 << 32) // (2 * Hk * bs * D) + 5000
+    r = synth.rng(31)
+    blocks = np.array([NB - 1, 3, NB - 77, NB // 2 + 9, 0, NB - 4999])
+    T = 90
+    k, v, q = (synth.round_to_bf16_bits(r.standard_normal((T, h, D))) for h in (Hk, Hk, Hk))
+    pos = np.arange(T)
+    slots = (blocks[pos // bs] * bs + pos % bs).astype(np.int64)
+    for per_token in (False, True):
+        cache = torch.empty(NB, 2, Hk, bs, D, dtype=torch.uint8, device=dev())
+        n = (NB, Hk, bs) if per_token else (1,)
+        ks, vs = torch.full(n, 0.01, device=dev()), torch.full(n, 0.02, device=dev())
+        qpa.kv_append_fp8(bf16_tensor(k, dev()), bf16_tensor(v, dev()), cache, torch.from_numpy(slots).to(dev()), ks, vs)
+        out = qpa.pa_chunk_fp8(bf16_tensor(q, dev()), cache, _i32(blocks[None]), _i32([0, T]), _i32([T]), ks, vs, 1)
+        _clean()
+        # the oracle on the six blocks, numbered 0..5
+        small = np.zeros((6, 2, Hk, bs, D), np.uint8)
+        sk, sv = (np.full((6, Hk, bs) if per_token else (1,), x, np.float32) for x in (0.01, 0.02))
+        small, sk, sv = oracle.kv_append_fp8(k, v, small, pos, sk, sv)
+        idx = torch.from_numpy(blocks).to(dev())
+        live = np.ones((6, 2, Hk, bs, D), bool)
+        live[5, :, :, T - 80:] = False                  # slots that nothing wrote
+        assert np.array_equal(cache[idx].cpu().numpy()[live], small[live])
+        c = Chunk.__new__(Chunk)
+        c.G, c.scale, c.per_token, c.bs = 1, None, per_token, bs
+        c.q_bits, c.cache, c.table, c.start, c.lens, c.ks, c.vs = q, small, np.arange(6)[None], [0, T], np.array([T]), sk, sv
+        _compare(c, out)
+        del cache
 
 
 # ------------------------------------------------------------------ together
