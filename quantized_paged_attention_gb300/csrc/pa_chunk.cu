@@ -40,9 +40,10 @@
 // maximum, its exponentials (512 clocks of the special function unit, twice) and
 // P V follow one another, and only the other row tile's chain overlaps them.
 // Tensor memory is full (S and O of both), so a third chain does not fit.
-// Measured (GB300): 1024 new tokens over 65536, 8 x 4 heads of 128, 1.50 PFLOP/s,
-// 78 % of the measured bf16 rate; a prompt of 8192, 8 x 8 heads, 1.22 PFLOP/s (the
-// rest is its items' beginnings); 64 single tokens over 1024..16384 3.1 TB/s.
+// Measured (GB300): 1024 new tokens over 65536, 8 x 4 heads of 128, 732 us, 1.51
+// PFLOP/s, 79 % of the measured bf16 rate; a prompt of 8192, 8 x 8 heads, 871 us,
+// 1.26 PFLOP/s (5 us between items); 64 single tokens over 1024..16384 323 us,
+// 3.3 TB/s; head_dim 64, 1024 over 65536 551 us, 1.0 PFLOP/s.
 // Tried and slower: both row tiles' pipelines on alternate key tiles of an item
 // that has 128 rows at most, and its next S in the idle row tile's buffer (the
 // registers cost every other case 10 to 18 % and such items gained nothing: their

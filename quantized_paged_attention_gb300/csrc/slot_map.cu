@@ -10,7 +10,9 @@
 // (2 * 4 bytes per request out of L2) instead of waiting for another CTA or a
 // first kernel: the call is latency-bound, its bytes are 20 per token at most.
 // A new token's block comes from the free list directly, never through the
-// table entry that another CTA may be writing.
+// table entry that another CTA may be writing. Replayed back to back it takes 6.3
+// us for 256 requests or 103 k tokens alike, 2 us more than the least a kernel
+// takes so: the lengths' round trip and the searches.
 #include "qpa.h"
 #include "common.cuh"
 #include "qpa_internal.h"
