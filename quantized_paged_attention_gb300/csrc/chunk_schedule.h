@@ -23,7 +23,7 @@ namespace qpa {
 namespace chunk {
 
 constexpr int TILE = 128;            // keys per unit, rows per row tile
-constexpr int ITEM_COST = 3;
+constexpr int ITEM_COST = 4;
 constexpr int MIN_UNITS = 4;         // per CTA: fewer CTAs take part rather than smaller ranges
 
 // sum_{i < n} floor((a i + b) / m) for a, b >= 0 (the lattice points under a
