@@ -513,40 +513,46 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         const int4 marks = lds_i4(sb + S::flagOff + 16 * (k & 3));
         const bool anynan = (marks.x | marks.y | marks.z | marks.w) != 0;
         if (anynan) find_nans<D, PT>(p, kv, it.req, it.head, it.t0 * TILE, min(end * TILE, it.L), lim, lane, nan);
+        // columns at a time: 16 keep the code small (per-token scales, head_dim 128: 931
+        // us, 1040 with 32); head_dim 64 has registers for 32 (551 us, 590 with 16)
+        constexpr int EC = D == 128 ? 16 : 32;
 #pragma unroll 1
-        for (int j = 0; j < D / 32; ++j) {
-          float o[32];
-          tmem_ld32(to + 32 * j, o);
+        for (int j = 0; j < D / EC; ++j) {
+          float o[EC];
+          if constexpr (EC == 16) tmem_ld16(to + EC * j, o);
+          else tmem_ld32(to + EC * j, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * rl * sv;
+          for (int i = 0; i < EC; ++i) o[i] = none ? 0.f : o[i] * rl * sv;
           if (anynan) {
             uint32_t w = nan[0];
 #pragma unroll
-            for (int i = 1; i < D / 32; ++i) w = j == i ? nan[i] : w;
+            for (int i = 1; i < D / 32; ++i) w = j * EC / 32 == i ? nan[i] : w;
+            w >>= EC * j % 32;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = ((w >> i) & 1u) ? __uint_as_float(0x7fffffffu) : o[i];
+            for (int i = 0; i < EC; ++i) o[i] = ((w >> i) & 1u) ? __uint_as_float(0x7fffffffu) : o[i];
           }
           if (it.slot < 0) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
+            for (int i = 0; i < EC; i += 8) {
               __nv_bfloat162 b0 = __floats2bfloat162_rn(o[i], o[i + 1]), b1 = __floats2bfloat162_rn(o[i + 2], o[i + 3]);
               __nv_bfloat162 b2 = __floats2bfloat162_rn(o[i + 4], o[i + 5]), b3 = __floats2bfloat162_rn(o[i + 6], o[i + 7]);
-              sts_i4(stg + lane * (2 * D) + (((4 * j + i / 8) ^ (lane & 7)) << 4),
+              sts_i4(stg + lane * (2 * D) + (((EC / 8 * j + i / 8) ^ (lane & 7)) << 4),
                      make_int4(*reinterpret_cast<int*>(&b0), *reinterpret_cast<int*>(&b1), *reinterpret_cast<int*>(&b2),
                                *reinterpret_cast<int*>(&b3)));
             }
           } else if (valid) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) store4(prow + 32 * j + i, o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < EC; i += 4) store4(prow + EC * j + i, o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
         if (it.slot < 0) {
-          // whole rows out, the warp's 32 of them a few at a time
+          // whole rows out, the warp's 32 of them a few at a time (little unrolled,
+          // as all that runs once per item)
           __syncwarp();
           constexpr int CPR = D / 8, RPI = 32 / CPR;
           const int ch = lane % CPR;
-#pragma unroll 4
+#pragma unroll 2
           for (int i = lane / CPR; i < 32; i += RPI) {
             const int r = a * TILE + (warp & 3) * 32 + i, rt = (int)(r * gm >> 16);
             const int4 v = lds_i4(stg + i * (2 * D) + ((ch ^ (i & 7)) << 4));
@@ -589,7 +595,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         return sb + S::qOff + a * 2 * S::qTerm + tr * D + ((part ^ (D == 128 ? (tr & 7) : ((tr >> 1) & 3))) << 4);
       };
       auto fetch = [&](int a) {
-#pragma unroll 4
+#pragma unroll 1
         for (int b = 0; b < NB; ++b) {
           const int row = a * TILE + b * RPS + cw * RPW + lane / LPR;
           const int tok = (int)(row * gm >> 16);
@@ -603,8 +609,10 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         }
         cp_async_commit();
       };
+      // (not unrolled, nor the copies: they run once per item, out of a cold
+      // instruction cache; unrolled by 4 the 8192-token prompt took 849 us, not 815)
       auto build = [&](int a) {
-#pragma unroll 4
+#pragma unroll 1
         for (int b = 0; b < NB; ++b) {
           const uint32_t at = spot(a, b);
           const uint4 x0 = lds128(at), x1 = lds128(at + S::qTerm);
