@@ -1,21 +1,27 @@
 // kv_append_fp8: new keys and values quantised to e4m3 and put into the pages.
 //
 // A unit is the head vector of one (row, K or V, head): head_dim / 16 threads
-// take 16 elements each (32 bytes in, 16 bytes out). The call moves
-// 4 + 2 bytes per element pair: 16384 tokens x 8 heads x 128 in 22 us, 4.5 TB/s,
-// bound half by them and half by the conversions (ALU 55 % busy).
+// take 16 elements each (32 bytes in, 16 bytes out). Bound: 4 bytes in and 2 out
+// per element pair. Measured (GB300): 16384 tokens x 8 heads x 128 in 20 us, 5.1
+// TB/s (25 us after other work has filled L2), 22.5 us with per-token scales;
+// 5003 tokens x 8 heads x 64 with per-token scales 9 us, half of it the launch.
 //
-// Rounding. The code is the nearest e4m3 value of the exact quotient x / s.
-// A float32 quotient rounded again can land on the wrong side of a midpoint
-// between two codes, so the midpoint is compared without a quotient: with
-// floor cell [f, f + u) of |x / s| and midpoint m = f + u/2 (at most 5
-// significant bits), the sign of fma(-m, |s|, |x|) is the exact sign of
-// |x| - m |s|: above 0 the code is the upper one, below 0 the lower one, and 0
-// is a tie that goes to the even code. The cell comes from the rounded
-// quotient; where that rounds up onto a cell's border f the comparison still
-// gives f. The common case needs none of this: x times 1/s taken a little too
-// small and a little too large rounds (in hardware) to the same code unless a
-// midpoint lies between the two, and only then the comparison runs.
+// Rounding. The code is the nearest e4m3 value of the exact quotient x / s, a tie
+// going to the even code. Midpoints between codes have a significand m of 5 bits
+// at most, x has 8. With q = x hi + x lo, hi + lo = 1/s to 2^-40, a quotient that
+// is a midpoint comes out as that midpoint, and one that is 2^-18 of it away or
+// more stays on its side. One in between, x = m s (1 - d) with 0 < |d| < 2^-18,
+// could end on the wrong side. But all of them have the same d for a given s:
+// s (1 - d) = x / m, and two such quotients of 8 and 5 bits are equal or 2^-13
+// apart. So hi is moved by 2^-20 towards d's side, once per scale, and the
+// conversion needs no test: two packed multiplies and one conversion per pair.
+//  * Per tensor, the 16 odd m are tried by 16 lanes: the bf16 nearest to m s
+//    tells whether there is such a quotient, and the sign of d.
+//  * Per token, s = amax / 448 rounded: if there is one, then d is that rounding,
+//    the sign of amax - 448 s.
+// (Converting with 1/s moved down and up, and comparing m s with x where the codes
+// differed, took 39 us for 16384 tokens x 8 heads x 128 with per-token scales,
+// whose ties are frequent: 448 = 7 * 64, and one significand in 7 divides by 7.)
 #include "qpa.h"
 #include "common.cuh"
 #include "qpa_internal.h"
@@ -50,63 +56,73 @@ __device__ __noinline__ uint32_t e4m3_exact(float x, float s) {
 }
 
 struct Scale {
-  float s, inv, lo, hi;   // the scale; 1/s, and 1/s moved down and up past every error of x * (1/s)
+  float s, hi, lo;         // the scale; hi + lo = 1/s, hi moved past near midpoints
   bool fast;
 };
 
-__device__ __forceinline__ Scale make_scale(float s) {
+// `side`: the sign of d above, so that x / s lies below (> 0) or above (< 0) its
+// near midpoints, or 0: no such quotient, or exact ones
+__device__ __forceinline__ Scale make_scale(float s, float side) {
   Scale c;
   c.s = s;
-  const float a = fabsf(s);
-  c.fast = a > 7.8886e-31f && a < 1.2676e30f;   // 2^-100 .. 2^100: neither 1/s nor x/s near 448 leaves the normals
-  const float inv = __frcp_rn(s);
-  c.inv = inv;
-  // a power of two: its reciprocal and the quotient are exact, nothing is ambiguous
-  const bool pow2 = (__float_as_uint(s) & 0x007fffffu) == 0u;
-  // |fl(x fl(1/s)) / (x/s) - 1| < 2^-22.9; the factors move it by 2^-21
-  c.lo = pow2 ? inv : inv * (1.f - 4.76837158e-7f);
-  c.hi = pow2 ? inv : inv * (1.f + 4.76837158e-7f);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));     // within 2^-23
+  const float h = r * (1.f - 2.38418579e-7f);               // 2^-22: below 1/s, so that lo has the sign of hi
+  c.lo = fmaf(-s, h, 1.f) * h;                              // (and is not 0: infinity times it stays infinite)
+  c.hi = h * (side > 0.f ? 1.f - 9.53674316e-7f : side < 0.f ? 1.f + 9.53674316e-7f : 1.f);
+  c.fast = fabsf(s) > 7.8886e-31f && fabsf(s) < 1.2676e30f;   // 2^-100 .. 2^100: nothing above leaves the normals
   return c;
+}
+
+// The side of a scale's near midpoints, in every lane of a warp.
+__device__ __forceinline__ float side_of(float s, int lane) {
+  const float as = fabsf(s), m = (float)(2 * (lane & 15) + 1), v = m * as;
+  const float x = __bfloat162float(__float2bfloat16_rn(v));
+  const float d = fabsf(v - x) <= v * 3.81469727e-6f ? fmaf(m, as, -x) : 0.f;   // 2^-18 (rounding of v: 2^-24)
+  const unsigned below = __ballot_sync(0xffffffffu, d > 0.f), above = __ballot_sync(0xffffffffu, d < 0.f);
+  return below ? 1.f : above ? -1.f : 0.f;
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// A value that rounds (in hardware) to the code of x / s: the midpoint of the
-// cell that holds |x / s|, moved towards the quotient's side of it, or not at a
-// tie. The cell comes from x * (1/s): off by an ulp it can be the neighbour's
-// only where the quotient is next to the border between them, and either cell's
-// comparison gives that border.
-__device__ __forceinline__ float side_of_midpoint(float x, const Scale& c) {
-  const float a = fabsf(x * c.inv);
-  const float q = a > 480.f ? 480.f : a;             // (NaN stays)
-  const float base = q < 0.015625f ? 0.015625f : 0.f;   // subnormal codes: as e4m3_exact
-  const float m = __uint_as_float((__float_as_uint(q + base) & 0xfff00000u) | 0x00080000u) - base;
-  const float r = fmaf(-m, fabsf(c.s), fabsf(x));
-  const float v = r > 0.f ? m * 1.0009765625f : r < 0.f ? m * 0.9990234375f : r == 0.f ? m : r;
-  return __uint_as_float((__float_as_uint(v) & 0x7fffffffu) | ((__float_as_uint(x) ^ __float_as_uint(c.s)) & 0x80000000u));
+// (a, b) * hi + (a, b) * lo
+__device__ __forceinline__ uint32_t quant2(float a, float b, const Scale& c) {
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %2}; mov.b64 z, {%3, %3}; "
+      "mul.rn.f32x2 z, x, z; fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x; }" : "+f"(a), "+f"(b) : "f"(c.hi), "f"(c.lo));
+  return f32x2_to_e4m3x2(a, b);
 }
 
 // 4 codes of the bf16 pairs a, b
+template <bool FAST>
 __device__ __forceinline__ uint32_t quant4(uint32_t a, uint32_t b, const Scale& c) {
   const float x0 = bf_lo(a), x1 = bf_hi(a), x2 = bf_lo(b), x3 = bf_hi(b);
-  const uint32_t lo = prmt(f32x2_to_e4m3x2(x0 * c.lo, x1 * c.lo), f32x2_to_e4m3x2(x2 * c.lo, x3 * c.lo), 0x5410u);
-  const uint32_t hi = prmt(f32x2_to_e4m3x2(x0 * c.hi, x1 * c.hi), f32x2_to_e4m3x2(x2 * c.hi, x3 * c.hi), 0x5410u);
-  if (lo == hi && c.fast) return lo;
-  // (with per-token scales a vector whose largest element has a multiple of 7 as
-  // significand, 448 being 7 * 64, meets a tie in every 16th element)
-  if (c.fast)
-    return prmt(f32x2_to_e4m3x2(side_of_midpoint(x0, c), side_of_midpoint(x1, c)),
-                f32x2_to_e4m3x2(side_of_midpoint(x2, c), side_of_midpoint(x3, c)), 0x5410u);
+  if (FAST || c.fast) return prmt(quant2(x0, x1, c), quant2(x2, x3, c), 0x5410u);
   return e4m3_exact(x0, c.s) | (e4m3_exact(x1, c.s) << 8) | (e4m3_exact(x2, c.s) << 16) | (e4m3_exact(x3, c.s) << 24);
+}
+
+// max(m, |w|) of bf16 pairs, a NaN ignored
+__device__ __forceinline__ void amax2(uint32_t& m, uint32_t w) {
+  asm("{ .reg .b32 t; abs.bf16x2 t, %1; max.bf16x2 %0, %0, t; }" : "+r"(m) : "r"(w));
+}
+
+// amax / 448 rounded to nearest, at least 2^-126 (infinity as the largest bf16)
+__device__ __forceinline__ Scale token_scale(float m) {
+  m = fminf(m, 3.38953139e38f);
+  // 1/448 as two floats; the quotient of 8 bits by 7 is no closer than 1/7 of a
+  // unit to where the rounding would turn, and this sum is within 2^-20 units
+  float s = fmaf(m, 0.00223214295692741870880126953125f, m * -9.97845626e-11f);
+  if (m < 8.2718e-25f) s = fmaxf(__fdiv_rn(m, 448.f), 1.17549435e-38f);    // 2^-80: the second part leaves the normals
+  return make_scale(s, s > 1.17549435e-38f ? fmaf(448.f, s, -m) : 0.f);
 }
 
 // A token's 2 Hk head vectors take 2 Hk TPR threads (in rounds, if more than the
 // block has); a block holds as many tokens side by side as fit. A thread keeps
 // its place (K or V, head, 16 dims) and steps through the tokens, UN of them at
 // once so that their slots and then their 32 bytes are in flight together. Two
-// tokens and 4 blocks per SM, one wave: 16384 tokens x 8 heads x 128 23.5 us (39
-// with per-token scales); 4 tokens and 2 blocks 24.5 (43), 6 blocks 31 (43).
+// tokens and 4 blocks per SM, one wave: 16384 tokens x 8 heads x 128 20 us (22.5
+// with per-token scales); 5 blocks 26 (24.5), 1 token and 6 blocks 24.5 (24.5), 4
+// tokens and 3 blocks 20.4 (22.4).
 template <int HD, bool PT>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendLaunch p, const int log2_bs, const int side) {
   constexpr int TPR = HD / 16;                 // threads per head vector
@@ -118,8 +134,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendLaunch 
   const int round = kThreads / TPR * TPR;      // threads of a round (tpt > kThreads: one token)
   Scale fixed_k, fixed_v;
   if constexpr (!PT) {
-    fixed_k = make_scale(__ldg(p.k_scale));
-    fixed_v = make_scale(__ldg(p.v_scale));
+    const float sk = __ldg(p.k_scale), sv = __ldg(p.v_scale);
+    fixed_k = make_scale(sk, side_of(sk, threadIdx.x & 31));
+    fixed_v = make_scale(sv, side_of(sv, threadIdx.x & 31));
   }
   const int step = gridDim.x * side;
   for (int i0 = 0; i0 < tpt; i0 += round) {
@@ -157,19 +174,20 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendLaunch 
         const uint32_t w[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
         Scale c = fixed;
         if constexpr (PT) {
-          float m = 0.f;                       // fmaxf ignores NaN
+          uint32_t m2 = 0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(bf_lo(w[j])), fabsf(bf_hi(w[j]))));
+          for (int j = 0; j < 8; ++j) amax2(m2, w[j]);
+          float m = fmaxf(bf_lo(m2), bf_hi(m2));
 #pragma unroll
           for (int o = TPR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          c = make_scale(fmaxf(__fdiv_rn(fminf(m, 3.38953139e38f), 448.f), 1.17549435e-38f));
+          c = token_scale(m);
         }
         if (slot[u] < 0) continue;
         uint4 o;
-        o.x = quant4(w[0], w[1], c);
-        o.y = quant4(w[2], w[3], c);
-        o.z = quant4(w[4], w[5], c);
-        o.w = quant4(w[6], w[7], c);
+        o.x = quant4<PT>(w[0], w[1], c);
+        o.y = quant4<PT>(w[2], w[3], c);
+        o.z = quant4<PT>(w[4], w[5], c);
+        o.w = quant4<PT>(w[6], w[7], c);
         const long long blk = slot[u] >> log2_bs;
         const int off = (int)(slot[u] & (bs - 1));
         reinterpret_cast<uint4*>(p.kv + (((blk * 2 + kv) * Hk + h) * bs + off) * HD)[part] = o;

@@ -182,6 +182,30 @@ def test_append_every_bf16_value(scale):
     _check_append(bits, bits[::-1].copy(), cache, np.arange(256, dtype=np.int64), s, s)
 
 
+@pytest.mark.parametrize("scale", [np.nextafter(np.float32(1), np.float32(2)), np.nextafter(np.float32(1), np.float32(0)),
+                                   np.nextafter(np.float32(0.75), np.float32(1)), 130 / 448, 250 / 448,
+                                   -np.nextafter(np.float32(131 / 21), np.float32(9)), 2.0 ** 99, 2.0 ** -99])
+def test_append_scales_beside_ties(scale):
+    """Scales a unit away from those that make ties, where x / scale falls within
+    2^-24 of a midpoint between two codes."""
+    test_append_every_bf16_value(scale)
+
+
+@pytest.mark.parametrize("lead", [2.0 ** -126, 2.0 ** -81, 2.0 ** -79, 1.0, 2.0 ** 127])
+def test_append_per_token_every_largest_significand(lead):
+    """Vectors of every significand of the largest element, their elements all
+    significands of the 11 binades below it, both signs."""
+    sig = np.arange(128, 256) / 128
+    top = sig * lead
+    x = np.stack([np.concatenate([[t], s * lead * 2.0 ** -k]) for t in top for k in range(12) for s in (sig[:127], -sig[1:])])
+    x[np.abs(x) > np.abs(x[:, :1])] = 0
+    bits = synth.round_to_bf16_bits(x).reshape(-1, 8, 128)
+    T = len(bits)
+    cache = np.zeros((T // 16, 2, 8, 16, 128), np.uint8)
+    z = np.zeros((T // 16, 8, 16), np.float32)
+    _check_append(bits, bits[::-1].copy(), cache, np.arange(T, dtype=np.int64), z, z)
+
+
 def test_append_per_token_extremes():
     """Zero vectors, subnormal ones, infinities and NaN beside finite values."""
     x = np.zeros((6, 1, 64), np.float32)
