@@ -350,7 +350,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       int ev = -126;
       for (int t = t0; t < end; ++t, ++sc) {
         const int nn = n + t - t0, cb = nn % NC;
-        float s[4][32];
+        float s[4][32], mx4[4];
         // Per-token scales: with head_dim 64, where the softmax warps are what
         // bounds, the keys' scales are loaded while S is awaited, into the registers
         // that S times them takes then (6 requests of 200 to 1500 new tokens: 703 us
@@ -379,7 +379,10 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, s[j]);
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (PT) tmem_ld32(ts + 32 * j, s[j]);
+            else tmem_ld32_max(ts + 32 * j, s[j], mx4[j]);
+          }
           tmem_wait_ld();
         }
         if constexpr (SEP) {
@@ -407,12 +410,13 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
 #pragma unroll
           for (int i = 0; i < 128; ++i) s[i / 32][i % 32] = i <= vis ? s[i / 32][i % 32] : -INFINITY;
         }
-        float mx4[4];
+        if (PT || masked) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          mx4[j] = fmaxf(s[j][0], s[j][1]);
+          for (int j = 0; j < 4; ++j) {
+            mx4[j] = fmaxf(s[j][0], s[j][1]);
 #pragma unroll
-          for (int i = 2; i < 32; i += 2) mx4[j] = fmax3(mx4[j], s[j][i], s[j][i + 1]);
+            for (int i = 2; i < 32; i += 2) mx4[j] = fmax3(mx4[j], s[j][i], s[j][i + 1]);
+          }
         }
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
         int en = ev;
