@@ -191,10 +191,14 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
   // registers per thread: the sum over the four groups is what the block is
   // launched with (4 x 128). Fewer for the softmax than it could use, since the
   // other roles' spills cost more. Measured, softmax/conversion/rest: head_dim 128,
-  // 8192-token prompt 176/88/72 961 us, 168/96/80 913, 168/104/72 900, and with
-  // 160/112/80 1357; head_dim 64, per-token scales 168/96/80 574 us, 176/96/64 572,
-  // 192/72/56 557.
-  constexpr int REG_SOFTMAX = D == 128 ? 168 : 192, REG_CONV = D == 128 ? 104 : 72, REG_REST = D == 128 ? 72 : 56;
+  // 8192-token prompt 168/88/88 794 us, 168/104/72 799, 176/88/72 807, 176/72/88
+  // 812 (64 single tokens, which one row tile computes, 318, 318, 300, 304); with
+  // per-token scales, 1024 over 65536, 184/64/80 860, 192/64/64 882, 184/72/72 898;
+  // head_dim 64, the same 184/88/56 502, 192/72/56 515, with per-token scales
+  // prompts 192/72/56 499, 184/80/64 519.
+  constexpr int REG_SOFTMAX = D == 128 ? (PT ? 184 : 168) : (PT ? 192 : 184);
+  constexpr int REG_CONV = D == 128 ? (PT ? 64 : 88) : (PT ? 72 : 88);
+  constexpr int REG_REST = D == 128 ? (PT ? 80 : 88) : 56;
   static_assert(2 * REG_SOFTMAX + REG_CONV + REG_REST <= 512, "register budget");
   constexpr uint32_t T_O = 256, T_P = SEP ? 384 : 0, P_STEP = SEP ? 64 : 128;
   constexpr uint32_t IDESC_QK = idesc_e4m3(128, 128, false, false);
@@ -731,57 +735,64 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         constexpr int CPR = D / 16, TPI = 32 / CPR, NI = 32 / TPI;   // 16-byte chunks per token, tokens per step
         const int ch = lane % CPR, tr = lane / CPR;
         const uint32_t src = sb + S::vOff + vb * S::kBytes, dst = sb + S::wOff + wb * S::wBytes;
-        uint32_t bad = 0;
-        uint4 x[NI];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int tk = 32 * cw + TPI * i + tr;
-          const uint32_t swz = D == 128 ? (tk & 7) : ((tk >> 1) & 3);
-          x[i] = lds128(src + tk * D + ((ch ^ swz) << 4));
-          if (tk >= live) x[i] = make_uint4(0, 0, 0, 0);
-          const uint32_t y = (((x[i].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].y & 0x7f7f7f7fu) + 0x01010101u) |
-                              ((x[i].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
-          bad |= y;
-        }
         // per token: a scale that is not finite makes every dim NaN
         const bool nf = PT && !(fabsf(vown) < INFINITY);
         const uint32_t vs16 = nf ? 0u : f32x2_to_f16x2(vown, vown);
-        const bool anybad = __any_sync(0xffffffffu, bad != 0 || nf);
-        if (anybad) {                                // 0 times NaN must not reach a row that does not see the token
+        // a few steps at a time: fewer registers than all at once (per-token scales: 932
+        // us for 1024 over 65536 with all 8, 912 with 4; head_dim 64 502 with 1 of 4, 531
+        // with all, but without scales 517 with all, 538 with 2)
+        constexpr int NH = D == 128 ? 2 : PT ? 1 : NI;
+#pragma unroll 1
+        for (int i0 = 0; i0 < NI; i0 += NH) {
+          uint32_t bad = 0;
+          uint4 x[NH];
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            auto clean = [](uint32_t w) -> uint32_t {
-              return w & ~(((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu);
-            };
-            x[i] = make_uint4(clean(x[i].x), clean(x[i].y), clean(x[i].z), clean(x[i].w));
+          for (int i = 0; i < NH; ++i) {
+            const int tk = 32 * cw + TPI * (i0 + i) + tr;
+            const uint32_t swz = D == 128 ? (tk & 7) : ((tk >> 1) & 3);
+            x[i] = lds128(src + tk * D + ((ch ^ swz) << 4));
+            if (tk >= live) x[i] = make_uint4(0, 0, 0, 0);
+            const uint32_t y = (((x[i].x & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].y & 0x7f7f7f7fu) + 0x01010101u) |
+                                ((x[i].z & 0x7f7f7f7fu) + 0x01010101u) | ((x[i].w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+            bad |= y;
           }
-          if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + S::flagOff + 16 * (k & 3) + 4 * cw), "r"(1u) : "memory");
-        }
+          const bool anybad = __any_sync(0xffffffffu, bad != 0 || nf);
+          if (anybad) {                                // 0 times NaN must not reach a row that does not see the token
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int tk = 32 * cw + TPI * i + tr;
-          const uint32_t rowa = dst + (D == 128 ? (ch >> 2) * (TILE * 128) : 0) + (tk >> 3) * 1024 + (tk & 7) * 128;
-          const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          uint32_t f[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[2 * j] = e4m3x2_lo_to_f16x2(w4[j]);
-            f[2 * j + 1] = e4m3x2_hi_to_f16x2(w4[j]);
+            for (int i = 0; i < NH; ++i) {
+              auto clean = [](uint32_t w) -> uint32_t {
+                return w & ~(((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu);
+              };
+              x[i] = make_uint4(clean(x[i].x), clean(x[i].y), clean(x[i].z), clean(x[i].w));
+            }
+            if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + S::flagOff + 16 * (k & 3) + 4 * cw), "r"(1u) : "memory");
           }
-          if constexpr (PT) {
-            const uint32_t sc2 = __shfl_sync(0xffffffffu, vs16, TPI * i + tr);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = hmul2(f[j], sc2);
-          }
-          // the two 16-byte halves in an order that differs between the atoms, so
-          // that 8 lanes of a store touch 8 different bank groups
-          const bool sw = D == 128 && (ch >> 2);
+          for (int i = 0; i < NH; ++i) {
+            const int tk = 32 * cw + TPI * (i0 + i) + tr;
+            const uint32_t rowa = dst + (D == 128 ? (ch >> 2) * (TILE * 128) : 0) + (tk >> 3) * 1024 + (tk & 7) * 128;
+            const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t f[8];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int ee = sw ? 1 - e : e;
-            const uint32_t addr = rowa + ((((ch & 3) * 2 + ee) ^ (tk & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(ee ? f[4] : f[0]), "r"(ee ? f[5] : f[1]),
-                         "r"(ee ? f[6] : f[2]), "r"(ee ? f[7] : f[3]) : "memory");
+            for (int j = 0; j < 4; ++j) {
+              f[2 * j] = e4m3x2_lo_to_f16x2(w4[j]);
+              f[2 * j + 1] = e4m3x2_hi_to_f16x2(w4[j]);
+            }
+            if constexpr (PT) {
+              const uint32_t sc2 = __shfl_sync(0xffffffffu, vs16, TPI * (i0 + i) + tr);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) f[j] = hmul2(f[j], sc2);
+            }
+            // the two 16-byte halves in an order that differs between the atoms, so
+            // that 8 lanes of a store touch 8 different bank groups
+            const bool sw = D == 128 && (ch >> 2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int ee = sw ? 1 - e : e;
+              const uint32_t addr = rowa + ((((ch & 3) * 2 + ee) ^ (tk & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(ee ? f[4] : f[0]), "r"(ee ? f[5] : f[1]),
+                           "r"(ee ? f[6] : f[2]), "r"(ee ? f[7] : f[3]) : "memory");
+            }
           }
         }
         fence_proxy_async();
