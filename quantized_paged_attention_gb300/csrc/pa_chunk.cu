@@ -193,7 +193,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
   // other roles' spills cost more. Measured, softmax/conversion/rest: head_dim 128,
   // 8192-token prompt 168/88/88 794 us, 168/104/72 799, 176/88/72 807, 176/72/88
   // 812 (64 single tokens, which one row tile computes, 318, 318, 300, 304); with
-  // per-token scales, 1024 over 65536, 184/64/80 860, 192/64/64 882, 184/72/72 898;
+  // per-token scales, 1024 over 65536, 184/64/80 810, 192/64/64 825, 176/80/80 827;
   // head_dim 64, the same 184/88/56 502, 192/72/56 515, with per-token scales
   // prompts 192/72/56 499, 184/80/64 519.
   constexpr int REG_SOFTMAX = D == 128 ? (PT ? 184 : 168) : (PT ? 192 : 184);
@@ -355,11 +355,10 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       for (int t = t0; t < end; ++t, ++sc) {
         const int nn = n + t - t0, cb = nn % NC;
         float s[4][32], mx4[4];
-        // Per-token scales: with head_dim 64, where the softmax warps are what
-        // bounds, the keys' scales are loaded while S is awaited, into the registers
-        // that S times them takes then (6 requests of 200 to 1500 new tokens: 703 us
-        // with the loads after S, 572 so; head_dim 128, where S is late: 996 and 1130)
-        if constexpr (PT && SEP) {
+        // Per-token scales: the keys' scales are loaded while S is awaited, into the
+        // registers that S times them takes then (loaded after S: 1024 over 65536 861
+        // us, 812 so; head_dim 64, prompts 525, 498)
+        if constexpr (PT) {
           if (!warp_wait(&cfull[cb], (nn / NC) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
 #pragma unroll
           for (int i = 0; i < 128; i += 4) {
@@ -372,7 +371,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         }
         if (!warp_wait(&sfull[a], sc & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
         tc_fence_after();
-        if constexpr (PT && SEP) {
+        if constexpr (PT) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float x[32];
@@ -383,30 +382,13 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (PT) tmem_ld32(ts + 32 * j, s[j]);
-            else tmem_ld32_max(ts + 32 * j, s[j], mx4[j]);
-          }
+          for (int j = 0; j < 4; ++j) tmem_ld32_max(ts + 32 * j, s[j], mx4[j]);
           tmem_wait_ld();
         }
         if constexpr (SEP) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sfree[a]);
-        }
-        if constexpr (PT && !SEP) {
-          if (!warp_wait(&cfull[cb], (nn / NC) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float4 ks[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ks[i] = lds_f4(sb + S::kscOff + 4 * (cb * TILE + 32 * j + 4 * i));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              fmul2(s[j][4 * i], s[j][4 * i + 1], ks[i].x, ks[i].y);
-              fmul2(s[j][4 * i + 2], s[j][4 * i + 3], ks[i].z, ks[i].w);
-            }
-          }
         }
         const int vis = lim - t * TILE;            // keys 0 .. vis of the tile are seen
         const bool masked = __any_sync(0xffffffffu, vis < TILE - 1);
