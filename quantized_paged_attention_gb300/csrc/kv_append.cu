@@ -18,7 +18,7 @@
 //  * Per tensor, the 16 odd m are tried by 16 lanes: the bf16 nearest to m s
 //    tells whether there is such a quotient, and the sign of d.
 //  * Per token, s = amax / 448 rounded: if there is one, then d is that rounding,
-//    the sign of amax - 448 s.
+//    with the sign of 448 s - amax.
 // (Converting with 1/s moved down and up, and comparing m s with x where the codes
 // differed, took 39 us for 16384 tokens x 8 heads x 128 with per-token scales,
 // whose ties are frequent: 448 = 7 * 64, and one significand in 7 divides by 7.)
@@ -33,7 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 
 // The code of x / s by the exact comparison, for any s (s = 0 and NaN follow
-// IEEE division); scales outside [2^-100, 2^100] come here.
+// IEEE division); scales per tensor outside (2^-100, 2^100) come here.
 __device__ __noinline__ uint32_t e4m3_exact(float x, float s) {
   const uint32_t sign = ((__float_as_uint(x) ^ __float_as_uint(s)) >> 24) & 0x80u;
   float ax = fabsf(x), as = fabsf(s);

@@ -36,19 +36,24 @@
 //    in V is taken out of the product, and at the item's end put back into the
 //    rows that see its token, so it cannot leak through 0 * NaN.
 // Bound: a key tile's products take the tensor core 2048 clocks (head_dim 128),
-// the two row tiles' turns come every 3200: per row tile S, the softmax's
-// maximum, its exponentials (512 clocks of the special function unit, twice) and
-// P V follow one another, and only the other row tile's chain overlaps them.
-// Tensor memory is full (S and O of both), so a third chain does not fit.
-// Measured (GB300): 1024 new tokens over 65536, 8 x 4 heads of 128, 732 us, 1.51
-// PFLOP/s, 79 % of the measured bf16 rate; a prompt of 8192, 8 x 8 heads, 871 us,
-// 1.26 PFLOP/s (5 us between items); 64 single tokens over 1024..16384 323 us,
-// 3.3 TB/s; head_dim 64, 1024 over 65536 551 us, 1.0 PFLOP/s.
+// the two row tiles' turns come every 3100: per row tile S, the softmax (its
+// maximum comes with the load of S from tensor memory, its exponentials take the
+// special function unit 512 clocks, twice) and P V follow one another, and only
+// the other row tile's chain overlaps them. Tensor memory is full (S and O of
+// both), so a third chain does not fit. Per-token scales add 1024 clocks of shared
+// memory reads per key tile, a scale per score of each of 8 warps.
+// Measured (GB300): 1024 new tokens over 65536, 8 x 4 heads of 128, 709 us, 1.56
+// PFLOP/s, 81 % of the measured bf16 rate, with per-token scales 810; a prompt of
+// 8192, 8 x 8 heads, 796 us, 1.38 PFLOP/s (5 us between items); 64 single tokens
+// over 1024..16384 318 us, 3.5 TB/s; head_dim 64, 1024 over 65536 500 us, 1.1
+// PFLOP/s, with per-token scales 740.
 // Tried and slower: both row tiles' pipelines on alternate key tiles of an item
 // that has 128 rows at most, and its next S in the idle row tile's buffer (the
 // registers cost every other case 10 to 18 % and such items gained nothing: their
 // V waits for the conversion); an eighth or a quarter of the exponentials as
-// polynomials on the FMA pipe (+7 %, +12 %); P in stores of 16 columns.
+// polynomials on the FMA pipe (+7 %, +12 %); P in stores of 16 columns; with
+// per-token scales S in the layout where a thread holds a quarter of 4 rows and
+// needs a quarter of the scales (+16 %, +33 %: its tensor memory accesses).
 // Every wait has a time limit; a timeout raises the error word and all roles
 // leave through the common teardown.
 #define QPA_WHOLE_UNIT
