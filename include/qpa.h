@@ -490,6 +490,7 @@ int paged_slot_map(const int32_t* new_lens, const int32_t* cached_lens, int32_t*
  * the descriptor (elements, multiples of 8; slices of a fused QKV projection
  * can be passed directly); kv_cache uint8 [num_blocks][2][num_kv_heads]
  * [block_size][head_dim]; slots int64 [num_tokens] (as paged_slot_map writes).
+ * kv_cache and written scales may overlap nothing else (QPA_ERR_OVERLAP).
  * Supported: head_dim 64 or 128, block_size 16/32/64/128/256.
  * Alignment: k, v and kv_cache 16 bytes, slots 8, scales 4 bytes.
  * ====================================================================== */
@@ -542,6 +543,8 @@ int kv_append_fp8(const void* k, const void* v, uint8_t* kv_cache, const int64_t
  * initialisation; calls that may overlap need a workspace each.
  * Supported: head_dim 64 or 128, query_group 1..64, block_size
  * 16/32/64/128/256. Alignment: q, kv_cache, out 16 bytes; per-token scales 16.
+ * out and workspace may overlap neither each other nor an input
+ * (QPA_ERR_OVERLAP: out is not q).
  * Errors as pa_decode_fp8; an invalid block id reads block 0 and raises error
  * word 3.
  * ====================================================================== */

@@ -164,6 +164,26 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   return an && bn && x < y + bn && y < x + an;
 }
 
+struct Span {
+  const void* p;
+  size_t n;
+};
+// no output may lie in an input or in another output
+template <int NO, int NI>
+bool overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
+  for (int o = 0; o < NO; ++o) {
+    for (const Span& i : ins)
+      if (overlap(outs[o].p, outs[o].n, i.p, i.n)) return true;
+    for (int x = 0; x < o; ++x)
+      if (overlap(outs[o].p, outs[o].n, outs[x].p, outs[x].n)) return true;
+  }
+  return false;
+}
+// bytes from the first to behind the last bf16 of [tokens][heads][dim]
+size_t extent(long long tokens, long long heads, int dim, long long stride_tok, long long stride_head) {
+  return (size_t(tokens - 1) * stride_tok + size_t(heads - 1) * stride_head + dim) * 2;
+}
+
 bool slot_shape_ok(const qpa_slot_desc* d) {
   if (d->num_reqs < 0 || d->num_reqs > 16384 || !block_size_ok(d->block_size) || d->max_blocks_per_seq < 1) return false;
   if (d->num_free < 0 || d->max_tokens < 0 || d->reserved != 0) return false;
@@ -512,16 +532,10 @@ int paged_slot_map(const int32_t* new_lens, const int32_t* cached_lens, int32_t*
   // them must not lie in what another still reads
   const size_t nb = size_t(d->num_reqs) * 4, nt = size_t(d->max_tokens);
   const size_t tb = reqs ? (size_t(d->num_reqs - 1) * a.table_stride + d->max_blocks_per_seq) * 4 : 0;
-  struct Span { const void* p; size_t n; };
-  const Span in[] = {{new_lens, nb}, {cached_lens, nb}, {free_blocks, size_t(d->num_free) * 4}, {block_table, tb}};
+  const Span in[] = {{new_lens, nb}, {cached_lens, nb}, {free_blocks, size_t(d->num_free) * 4}};
   const Span outs[] = {{block_table, tb}, {query_start, nb + 4}, {seq_lens, nb}, {slots, nt * 8}, {positions, nt * 4},
                        {num_taken, 4}};
-  for (int o = 0; o < 6; ++o) {
-    for (int i = 0; i < (o == 0 ? 3 : 4); ++i)
-      if (overlap(outs[o].p, outs[o].n, in[i].p, in[i].n)) return QPA_ERR_OVERLAP;
-    for (int i = 1; i < o; ++i)
-      if (overlap(outs[o].p, outs[o].n, outs[i].p, outs[i].n)) return QPA_ERR_OVERLAP;
-  }
+  if (overlap(outs, in)) return QPA_ERR_OVERLAP;
   a.new_lens = new_lens;
   a.cached_lens = cached_lens;
   a.block_table = block_table;
@@ -558,6 +572,13 @@ int kv_append_fp8(const void* k, const void* v, uint8_t* kv_cache, const int64_t
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_cache, 16) || !aligned(slots, 8) || !aligned(k_scale, 4) ||
       !aligned(v_scale, 4))
     return QPA_ERR_ALIGN;
+  const size_t scales = size_t(d->num_blocks) * d->num_kv_heads * d->block_size;
+  const size_t ks_in = d->kv_scale_per_token ? 0 : 4, ks_out = d->kv_scale_per_token ? scales * 4 : 0;
+  const Span in[] = {{k, extent(d->num_tokens, d->num_kv_heads, d->head_dim, a.k_stride_tok, a.k_stride_head)},
+                     {v, extent(d->num_tokens, d->num_kv_heads, d->head_dim, a.v_stride_tok, a.v_stride_head)},
+                     {slots, size_t(d->num_tokens) * 8}, {k_scale, ks_in}, {v_scale, ks_in}};
+  const Span outs[] = {{kv_cache, scales * 2 * d->head_dim}, {k_scale, ks_out}, {v_scale, ks_out}};
+  if (overlap(outs, in)) return QPA_ERR_OVERLAP;
   a.k = k;
   a.v = v;
   a.kv = kv_cache;
@@ -597,7 +618,17 @@ int pa_chunk_fp8(const void* q, const uint8_t* kv_cache, const int32_t* block_ta
   if (!aligned(block_table, 4) || !aligned(query_start, 4) || !aligned(seq_lens, 4)) return QPA_ERR_ALIGN;
   const size_t sa = d->kv_scale_per_token ? 16 : 4;
   if (!aligned(k_scale, sa) || !aligned(v_scale, sa)) return QPA_ERR_ALIGN;
-  if (workspace_bytes < chunk_workspace_bytes(d->num_tokens, d->query_group, d->head_dim)) return QPA_ERR_WORKSPACE;
+  const size_t ws = chunk_workspace_bytes(d->num_tokens, d->query_group, d->head_dim);
+  if (workspace_bytes < ws) return QPA_ERR_WORKSPACE;
+  const long long heads = (long long)d->num_kv_heads * d->query_group;
+  const size_t scales = size_t(d->num_blocks) * d->num_kv_heads * d->block_size, sn = d->kv_scale_per_token ? scales * 4 : 4;
+  const Span in[] = {{q, extent(d->num_tokens, heads, d->head_dim, a.q_stride_tok, a.q_stride_head)},
+                     {kv_cache, scales * 2 * d->head_dim},
+                     {block_table, (size_t(d->num_reqs - 1) * a.table_stride + d->max_blocks_per_seq) * 4},
+                     {query_start, size_t(d->num_reqs) * 4 + 4}, {seq_lens, size_t(d->num_reqs) * 4},
+                     {k_scale, sn}, {v_scale, sn}};
+  const Span outs[] = {{out, size_t(d->num_tokens) * heads * d->head_dim * 2}, {workspace, ws}};
+  if (overlap(outs, in)) return QPA_ERR_OVERLAP;
   a.q = q;
   a.kv = kv_cache;
   a.block_table = block_table;

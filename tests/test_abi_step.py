@@ -79,6 +79,16 @@ def test_append_refusals(qpa):
     assert _append(qpa, {i: NULL for i in range(6)}, num_tokens=0) == 0
 
 
+def test_append_overlaps(qpa):
+    row, cache = 2 * 128 * 2, 4 * 2 * 2 * 16 * 128                # bytes of a token's heads, of the cache
+    assert _append(qpa, {0: at(2, cache - 16)}) == -7             # k begins in the cache's end
+    assert _append(qpa, {1: at(2, -3 * row + 16)}) == -7          # v ends in its beginning
+    assert _append(qpa, {1: at(2, -5 * row + 16)}, v_stride_tok=2 * row // 2) == -7   # strided: 2 x 2 rows + 1
+    assert _append(qpa, {3: at(2, 64)}) == -7
+    assert _append(qpa, {4: at(2, cache - 4)}) == -7
+    assert _append(qpa, {5: at(4, 4 * 2 * 16 * 4 - 4)}, kv_scale_per_token=1) == -7   # written scales over each other
+
+
 def _chunk_desc(qpa, **kw):
     return _set(qpa.ChunkDesc(), kw, num_reqs=2, num_tokens=5, num_kv_heads=2, query_group=4, head_dim=128,
                 block_size=16, num_blocks=4, max_blocks_per_seq=4)
@@ -108,6 +118,16 @@ def test_chunk_refusals(qpa):
     n = qpa.pa_chunk_fp8_workspace_size(_chunk_desc(qpa))
     assert n > 0 and _chunk(qpa, ws_bytes=n - 1) == -4
     assert _chunk(qpa, num_reqs=0) == 0 and _chunk(qpa, {i: NULL for i in range(9)}, num_tokens=0) == 0
+
+
+def test_chunk_overlaps(qpa):
+    out = 5 * 8 * 128 * 2
+    ws = qpa.pa_chunk_fp8_workspace_size(_chunk_desc(qpa))
+    assert _chunk(qpa, {7: at(0)}) == -7                          # in place
+    assert _chunk(qpa, {7: at(0, -out + 16)}) == -7
+    assert _chunk(qpa, {8: at(0, -ws + 256)}, ws_bytes=ws) == -7 and _chunk(qpa, {7: at(8, 256)}) == -7
+    assert _chunk(qpa, {7: at(1, 4 * 2 * 2 * 16 * 128 - 16)}) == -7
+    assert _chunk(qpa, {3: at(7, 8)}) == -7 and _chunk(qpa, {4: at(8, 4)}) == -7 and _chunk(qpa, {6: at(7, 4)}) == -7
 
 
 def test_descriptor_layouts(qpa):
