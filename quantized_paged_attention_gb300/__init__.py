@@ -468,6 +468,15 @@ def _launch(fn, index, stream, *args):
         raise QpaError(fn, st)
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for a launch on `stream`, from that stream's own pool: another
+    stream's may still be in use there by work queued before."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _device_of(*ts):
     """Index of the CUDA device that holds every tensor."""
     index = ts[0].get_device()
@@ -501,15 +510,15 @@ def paged_slot_map(new_lens, cached_lens, block_table, free_blocks, block_size: 
             _fail(f"an output has to be contiguous, {dt}, of {n} elements")
     dev = new_lens.device
     if query_start is None:
-        query_start = torch.empty(R + 1, dtype=i32, device=dev)
+        query_start = _empty(R + 1, i32, dev, stream)
     if seq_lens is None:
-        seq_lens = torch.empty(R, dtype=i32, device=dev)
+        seq_lens = _empty(R, i32, dev, stream)
     if slots is None:
-        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        slots = _empty(max_tokens, torch.int64, dev, stream)
     if positions is None:
-        positions = torch.empty(max_tokens, dtype=i32, device=dev)
+        positions = _empty(max_tokens, i32, dev, stream)
     if num_taken is None:
-        num_taken = torch.empty(1, dtype=i32, device=dev)
+        num_taken = _empty(1, i32, dev, stream)
     index = _device_of(new_lens, cached_lens, block_table, free_blocks, query_start, seq_lens, slots, positions,
                        num_taken)
     d = SlotDesc(R, block_size, maxb, free_blocks.numel(), max_tokens, 0, stride)
@@ -604,11 +613,11 @@ def pa_chunk_fp8(q, kv_cache, block_table, query_start, seq_lens, k_scale, v_sca
             not seq_lens.is_contiguous() or query_start.numel() != R + 1 or seq_lens.numel() != R:
         _fail("query_start must be contiguous int32 with one entry more than requests, seq_lens with one per request")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
     elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
         _fail("out must be contiguous bfloat16 of the shape of q")
     if workspace is None:
-        workspace = alloc_workspace(pa_chunk_fp8_workspace_size(want), q.device)
+        workspace = _empty(max(pa_chunk_fp8_workspace_size(want), 256), torch.uint8, q.device, stream)
     elif not workspace.is_contiguous():
         _fail("workspace must be contiguous")
     index = _device_of(q, kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, out, workspace)

@@ -505,6 +505,30 @@ def test_chunk_two_streams_at_once_and_graph_replay():
     assert torch.equal(o3, want)
 
 
+def test_memory_of_a_call_on_another_stream():
+    """Outputs and workspace that the binding allocates belong to the stream of
+    the call: a block that the current stream has freed, with a write to it still
+    queued there, is not handed out."""
+    c = Chunk(9, [(200, 900), (1, 5000)], 2, 8)
+    t = c.tensors()
+    want = qpa.pa_chunk_fp8(**t).clone()
+    new, free, table = _i32([3, 2]), _i32(range(8)), _i32(np.zeros((2, 4)))
+    side = torch.cuda.Stream()
+    n = qpa.pa_chunk_fp8_workspace_size(qpa.chunk_desc(t["q"], t["kv_cache"], t["block_table"], c.G, False))
+    freed = [torch.empty(k, dtype=torch.uint8, device=dev()) for k in (n, want.nbytes, 12, 8, 40, 20, 4)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                      # some tens of ms before the writes
+    for x in freed:
+        x.fill_(255)
+    del freed, x
+    got = qpa.pa_chunk_fp8(**t, stream=side)
+    got2 = qpa.paged_slot_map(new, new, table, free, 16, 5, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert got2[0].tolist() == [0, 3, 5] and got2[1].tolist() == [6, 4] and got2[3].tolist() == [3, 4, 5, 2, 3]
+    _clean()
+
+
 def test_pages_past_4_gib():
     """Blocks at the end of a cache of more than 2^32 bytes: append there, then
     attend over them, beside blocks at its start."""
