@@ -191,6 +191,19 @@ def test_append_scales_beside_ties(scale):
     test_append_every_bf16_value(scale)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.0, np.inf, -np.inf, np.nan])
+def test_append_scales_that_are_no_scales(scale):
+    """Division as IEEE has it: by 0 saturated infinities (NaN for 0 / 0), by
+    infinity zeros, by NaN NaN."""
+    bits = np.array([0, 0x8000, 0x3F80, 0xC000, 0x7F80, 0xFF80, 0x7FC0, 1] * 8, np.uint16).reshape(1, 1, 64)
+    with np.errstate(all="ignore"):
+        want = oracle.e4m3_nearest(decode_bf16(bits[0, 0]) / np.float64(scale), 1.0)
+    s = np.array([scale], np.float32)
+    got, _, _ = _append(bits, bits, np.zeros((1, 2, 1, 16, 64), np.uint8), np.zeros(1, np.int64), s, s)
+    assert np.array_equal(got[0, 0, 0, 0], want) and np.array_equal(got[0, 1, 0, 0], want)
+    _clean()
+
+
 @pytest.mark.parametrize("lead", [2.0 ** -126, 2.0 ** -81, 2.0 ** -79, 1.0, 2.0 ** 127])
 def test_append_per_token_every_largest_significand(lead):
     """Vectors of every significand of the largest element, their elements all
