@@ -604,10 +604,12 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         }
         cp_async_commit();
       };
-      // (not unrolled, nor the copies: they run once per item, out of a cold
-      // instruction cache; unrolled by 4 the 8192-token prompt took 849 us, not 815)
+      // (hardly unrolled, nor the copies: they run once per item, out of a cold
+      // instruction cache. By 4 the 8192-token prompt took 849 us, by 1 815; later 797
+      // by 1 and 785 by 2, two steps' chains at once; with per-token scales, whose
+      // budget of registers is smaller, a prompt of 4096 302 by 1 and 332 by 2)
       auto build = [&](int a) {
-#pragma unroll 1
+#pragma unroll (PT ? 1 : 2)
         for (int b = 0; b < NB; ++b) {
           const uint32_t at = spot(a, b);
           const uint4 x0 = lds128(at), x1 = lds128(at + S::qTerm);
