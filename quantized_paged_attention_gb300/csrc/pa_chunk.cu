@@ -44,16 +44,19 @@
 // memory reads per key tile, a scale per score of each of 8 warps.
 // Measured (GB300): 1024 new tokens over 65536, 8 x 4 heads of 128, 709 us, 1.56
 // PFLOP/s, 81 % of the measured bf16 rate, with per-token scales 810; a prompt of
-// 8192, 8 x 8 heads, 796 us, 1.38 PFLOP/s (5 us between items); 64 single tokens
+// 8192, 8 x 8 heads, 785 us, 1.40 PFLOP/s (5 us between items); 64 single tokens
 // over 1024..16384 318 us, 3.5 TB/s; head_dim 64, 1024 over 65536 500 us, 1.1
-// PFLOP/s, with per-token scales 740.
+// PFLOP/s, with per-token scales 740. Between items: the query rows' copies 2.5 us,
+// row tile 0's operand 2, its S and softmax 1.
 // Tried and slower: both row tiles' pipelines on alternate key tiles of an item
 // that has 128 rows at most, and its next S in the idle row tile's buffer (the
 // registers cost every other case 10 to 18 % and such items gained nothing: their
 // V waits for the conversion); an eighth or a quarter of the exponentials as
 // polynomials on the FMA pipe (+7 %, +12 %); P in stores of 16 columns; with
 // per-token scales S in the layout where a thread holds a quarter of 4 rows and
-// needs a quarter of the scales (+16 %, +33 %: its tensor memory accesses).
+// needs a quarter of the scales (+16 %, +33 %: its tensor memory accesses); V of
+// an item's first key tile before row tile 1's operand, with that tile's first S
+// behind the first product (prompt +8 %, long context +7 %) or before it (+3 %, +1 %).
 // Every wait has a time limit; a timeout raises the error word and all roles
 // leave through the common teardown.
 #define QPA_WHOLE_UNIT
