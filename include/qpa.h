@@ -525,7 +525,9 @@ int kv_append_fp8(const void* k, const void* v, uint8_t* kv_cache, const int64_t
  * row does not see have no influence on it, NaN codes included.
  * Precision: each query row, scaled by a power of two, enters the tensor core
  * as 2 e4m3 terms (exact down to 2^-10 of the row's largest |q|, within 2^-18
- * of it below), K and V exactly; the probabilities enter as f16; per-token V
+ * of it below), K and V exactly; the probabilities enter as f16, scaled so that
+ * one keeps its 11 bits down to 2^-21 of the row's largest and is within 2^-32 of
+ * it below; per-token V
  * scales, over a power of two above the largest of the request's so far, and
  * the V scaled by them are rounded to f16; sums and softmax statistics are
  * float32. The output is bf16 only: probabilities of 11 bits would leave the

@@ -2,9 +2,11 @@
 // paged cache, on the 5th-generation tensor core.
 //
 // Mathematics: softmax(scale q k^T + causal) v with one pass over the keys, a
-// running maximum m and sum l per row: p = 2^(s c - m), O += p v, and O, l are
+// reference m and a sum l per row: p = 2^(s c - m), O += p v, and O, l are
 // rescaled only when the maximum has grown by more than 2^8 since m was taken
-// (p <= 256 then, and O / l does not depend on m).
+// (O / l does not depend on m). m lies 2^7 below the maximum, so that p, up to
+// 2^15, uses f16's range: the sum of many small weights is lost only where each is
+// below 2^-32 of the largest.
 //
 //  * Item: 256 query rows of one KV head, i.e. 256 / G whole tokens with their
 //    G heads (rows of a group share their keys), as two tiles of 128 rows,
@@ -77,7 +79,8 @@ constexpr int W_CONV = 8, W_MMA = 12, W_MMA1 = 13, W_LOAD = 14, W_PREF = 15;
 constexpr int NK = 3, NV = 2, NW = 2;   // stages of K, V bytes, V f16
 constexpr int NC = 4;                // stages of the per-token scales for the softmax
 constexpr int IR = 4;                // item ring
-constexpr float kNoMax = -1e30f;     // running maximum of a row that has seen no token
+constexpr float kNoMax = -1e30f;     // reference of a row that has seen no token
+constexpr float kRoom = 7.f;         // the reference lies so far (log2) below the maximum
 constexpr float kLazy = 8.f;         // growth of the maximum (log2) that rescales
 
 template <int D>
@@ -415,13 +418,14 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
         int en = ev;
         if constexpr (PT) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(en) : "r"(sb + S::evOff + 4 * cb));
+        const float mr = mx - kRoom;
         if (t == t0) {
-          m = fmaxf(mx, kNoMax);
+          m = fmaxf(mr, kNoMax);
         } else {
-          const bool grow = mx > m + kLazy;
+          const bool grow = mr > m + kLazy;
           if (__any_sync(0xffffffffu, grow) || (PT && en != ev)) {
-            const float al = grow ? ex2(m - mx) : 1.f;
-            if (grow) m = mx;
+            const float al = grow ? ex2(m - mr) : 1.f;
+            if (grow) m = mr;
             l *= al;
             // (ev only grows: the factor is at most 1)
             const float f = PT ? al * ex2((float)(ev - en)) : al;

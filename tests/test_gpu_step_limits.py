@@ -1,0 +1,119 @@
+"""GPU tests of the serving-step entry points at the limits of what they take:
+rows that see no token beside queries that are not finite, weights and scales far
+apart, logits far from 0, every significand of a scale, calls from two threads,
+two errors at once.
+
+The attention's tolerance, per element, with A = sum_t p_t |v_t| and M the
+largest p_t times V scale, times the largest code, all over the tokens that the
+row sees:
+    2^-8 |ref| + 2^-11 A + 2^-18 A  the bf16 output, p in f16, float32 sums and the
+                                    merge of split rows
+  + 2^-10 A                         per-token scales: the V scale's rounding to f16
+                                    and that of the scaled V, 2^-11 each
+  + 2 (dq + da) A                   a logit error e changes p by e^(+-e): dq from the
+                                    query's residue (2^-17 of the row's largest |q|
+                                    per dim), da from float32 sums of D products, the
+                                    scale product and the exponential (2^-24 each step)
+  + L 2^-32 M                       p below f16's normals has an error of 2^-25 against
+                                    a largest one of at least 2^7 (doubled with
+                                    per-token scales, by the V scale's power of two)
+"""
+import ctypes
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_paged_attention_gb300 as qpa
+import synth
+from _gpu import dev
+from oracle.formats import decode_bf16, decode_e4m3fn
+from test_gpu_step import Chunk, _check_append, _clean, _i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def _reference(c):
+    """(ref, tolerance), float64; rows of no request NaN."""
+    q = decode_bf16(c.q_bits)
+    T, Hq, D = q.shape
+    Hk = c.cache.shape[2]
+    scale = D ** -0.5 if c.scale is None else c.scale
+    ref, tol = np.full((T, Hq, D), np.nan), np.full((T, Hq, D), np.nan)
+    for r, L in enumerate(int(x) for x in c.lens):
+        a, b = int(c.start[r]), int(c.start[r + 1])
+        pos = np.arange(L)
+        blk, off = c.table[r, pos // c.bs].astype(np.int64), pos % c.bs
+        seen = pos[None, :] <= (L - (b - a) + np.arange(b - a))[:, None]          # [rows, L]
+        for h in range(Hk):
+            ks, vs = ((x[blk, h, off].astype(np.float64) if c.per_token else np.full(L, float(x[0])))
+                      for x in (c.ks, c.vs))
+            k, code = (decode_e4m3fn(c.cache[blk, i, h, off]) for i in (0, 1))
+            k, v = k * ks[:, None], code * vs[:, None]
+            for g in range(h * c.G, (h + 1) * c.G):
+                with np.errstate(all="ignore"):
+                    s = np.where(seen, scale * (q[a:b, g] @ k.T), -np.inf)
+                    p = np.exp(s - np.where(seen.any(axis=1), s.max(axis=1, initial=-np.inf), 0.0)[:, None])
+                    p /= np.maximum(p.sum(axis=1, keepdims=True), 1e-300)
+                # (0 times what a row does not see is 0)
+                for i in range(b - a):
+                    n = int(seen[i].sum())
+                    w = p[i, :n]
+                    ref[a + i, g] = w @ v[:n]
+                    A = w @ np.abs(v[:n])
+                    M = (w * np.abs(vs[:n])).max(initial=0.0) * np.nan_to_num(np.abs(code[:n])).max(initial=0.0)
+                    qk = np.abs(q[a + i, g]).max() * np.abs(k[:n]).sum(axis=1).max(initial=0.0) * abs(scale)
+                    e = 2.0 ** -17 * qk + (D + 4) * 2.0 ** -24 * qk + 2.0 ** -22
+                    pv = 2.0 ** -11 + 2.0 ** -18 + (2.0 ** -10 if c.per_token else 0.0)
+                    tol[a + i, g] = (2.0 ** -8 * np.abs(ref[a + i, g]) + (pv + 2 * e) * A
+                                     + n * (2.0 ** -31 if c.per_token else 2.0 ** -32) * M)
+    return ref, tol
+
+
+def _run(c):
+    t = c.tensors()
+    out = qpa.pa_chunk_fp8(**t)
+    _clean()
+    return out.double().cpu().numpy()
+
+
+def _check(c):
+    got = _run(c)
+    ref, tol = _reference(c)
+    nan = np.isnan(ref)
+    assert np.array_equal(np.isnan(got), nan), "NaN pattern differs"
+    err, lim = np.abs(got - ref)[~nan], tol[~nan]
+    assert np.all(err <= lim), f"worst {np.max(err / np.maximum(lim, 1e-300)):.3g} of the tolerance"
+
+
+def _place(c, r, pos):
+    return c.table[r, pos // c.bs].astype(np.int64), pos % c.bs
+
+
+VARIANTS = [(128, False), (64, False), (128, True), (64, True)]
+
+
+@pytest.mark.parametrize("D,per_token", VARIANTS)
+@pytest.mark.parametrize("drop", [13.3, 24.5, 25.01, 27.3])
+def test_many_small_probabilities(D, per_token, drop):
+    """A token of weight 1 and V = 0 in every page, the others 2^-drop of it: the
+    result is the sum of those, whatever f16 makes of each."""
+    L = 65536
+    c = Chunk(42, [(1, L)], 1, 1, D, 256, per_token)
+    c.cache[:, 0] = 0
+    c.cache[:, 1] = 0x38                                # 1
+    c.cache[:, 0, 0, 0, 0] = 0x38
+    c.cache[:, 1, 0, 0] = 0
+    c.ks[:], c.vs[:] = 0.25, 0.5
+    q = np.zeros((1, 1, D))
+    q[..., 0] = 1
+    c.q_bits = synth.round_to_bf16_bits(q)
+    c.scale = float(drop * np.log(2) / 0.25)
+    _check(c)
