@@ -503,7 +503,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       const float rl = none ? 0.f : __frcp_rn(l);
       const float sv = PT ? ex2((float)ev) : vscale;
       float* prow = p.part_o + ((long long)it.slot * p.part_rows + row) * D;
-      if (it.slot >= 0 && valid) p.part_ml[(long long)it.slot * p.part_rows + row] = make_float2(none ? -INFINITY : m, l);
+      // (l of a row that sees no token is NaN if its query is not finite)
+      if (it.slot >= 0 && valid)
+        p.part_ml[(long long)it.slot * p.part_rows + row] = none ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
       if (any) {
         // NaN codes in the item's V (none, as a rule) were taken out of the
         // products: look for them again and put NaN into the rows that see them

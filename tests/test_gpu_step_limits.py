@@ -101,6 +101,24 @@ VARIANTS = [(128, False), (64, False), (128, True), (64, True)]
 
 
 @pytest.mark.parametrize("D,per_token", VARIANTS)
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_rows_without_a_token_and_bad_queries(D, per_token, bad):
+    """A row that sees no token gives 0 whatever its query holds, in an item that
+    the schedule cuts (280 rows over 260 tokens, 2 heads: head 1's first item lies
+    in two CTAs) as in one that it does not."""
+    c = Chunk(41, [(280, 260)], 2, 1, D, 16, per_token)
+    q = decode_bf16(c.q_bits)
+    q[3, :, 5] = q[19, 1, 0] = bad
+    c.q_bits = synth.round_to_bf16_bits(q)
+    out = _run(c)
+    assert np.all(out[:20] == 0)
+    q[3, :, 5] = q[19, 1, 0] = 0
+    c.q_bits = synth.round_to_bf16_bits(q)
+    ref, tol = _reference(c)
+    assert np.all(np.abs(out - ref) <= tol)
+
+
+@pytest.mark.parametrize("D,per_token", VARIANTS)
 @pytest.mark.parametrize("drop", [13.3, 24.5, 25.01, 27.3])
 def test_many_small_probabilities(D, per_token, drop):
     """A token of weight 1 and V = 0 in every page, the others 2^-drop of it: the
