@@ -527,9 +527,11 @@ int kv_append_fp8(const void* k, const void* v, uint8_t* kv_cache, const int64_t
  * as 2 e4m3 terms (exact down to 2^-10 of the row's largest |q|, within 2^-18
  * of it below), K and V exactly; the probabilities enter as f16, scaled so that
  * one keeps its 11 bits down to 2^-21 of the row's largest and is within 2^-32 of
- * it below; per-token V
- * scales, over a power of two above the largest of the request's so far, and
- * the V scaled by them are rounded to f16; sums and softmax statistics are
+ * it below. Per-token V scales, and V scaled by them, are rounded to f16 without
+ * their powers of two, which the probabilities take: those then keep 11 bits, and
+ * the absolute error, against the row's largest probability times V scale (down to
+ * 2^-13 of it, with an error of 2^-24 below, where scales of 128 tokens differ by
+ * up to 2^8). Sums and softmax statistics are
  * float32. The output is bf16 only: probabilities of 11 bits would leave the
  * rest of a float32 output without meaning. A per-token V scale that is not
  * finite makes the rows that see its token NaN; logits beyond float32 are

@@ -28,6 +28,12 @@
 //    per tile by four warps. f16 keeps 11 bits of p, where two e4m3 terms would
 //    keep 8 and cost the softmax warps 2.5 instructions per element; the
 //    conversion is 0.4.
+//  * Per-token V scales: V enters as f16(scale 2^-e) times its codes, and the power of
+//    two 2^e goes into P, of which a row keeps a reference of its own: what f16 drops is
+//    small against the row's largest p times scale, whatever the tokens' scales are that it
+//    does not see or hardly weighs. A key tile has one e where its scales (but 0) lie
+//    within 2^7 or so; otherwise each token has its own and the tile takes the long way
+//    (apart_tile).
 //  * Roles: 2 x 4 softmax warps (a thread owns one row: no exchange between
 //    lanes), one per row tile, so that the tensor core works for one while the
 //    other computes; 4 warps that convert V and build the next item's query
@@ -82,6 +88,8 @@ constexpr int IR = 4;                // item ring
 constexpr float kNoMax = -1e30f;     // reference of a row that has seen no token
 constexpr float kRoom = 7.f;         // the reference lies so far (log2) below the maximum
 constexpr float kLazy = 8.f;         // growth of the maximum (log2) that rescales
+constexpr int kSpread = 7;           // V scales of a tile this far apart (log2) share a power of two
+constexpr float kFar = 64.f;         // a row's reference so far (log2) above a tile's: P would vanish where p counts
 
 template <int D>
 struct Smem {
@@ -95,15 +103,17 @@ struct Smem {
   static constexpr int krawOff = crowOff + 2 * ROWS * 4;          // [NK][128] per-token scales as copied
   static constexpr int vrawOff = krawOff + NK * TILE * 4;
   static constexpr int kscOff = vrawOff + NV * TILE * 4;          // [NC][128] K scales for the softmax
-  static constexpr int iringOff = kscOff + NC * TILE * 4;         // [IR] 64 bytes
+  static constexpr int vexpOff = kscOff + NC * TILE * 4;          // [NC][128] power of two out of each token's V
+  static constexpr int iringOff = vexpOff + NC * TILE * 4;        // [IR] 64 bytes
   static constexpr int qinfoOff = iringOff + IR * 64;             // [2] 64 bytes
   static constexpr int flagOff = qinfoOff + 2 * 64;               // [4 items][4 warps] V holds a NaN
-  static constexpr int evOff = flagOff + 64;                      // [NC] exponent of the V scales (16 bytes)
-  static constexpr int schedOff = evOff + 16;                     // schedule scratch
+  static constexpr int evOff = flagOff + 64;                      // [NC] the tile's power of two, NaN: the tokens' own
+  static constexpr int schedOff = evOff + 4 * NC;                 // schedule scratch
   static constexpr int barOff = schedOff + 256;
   static constexpr int NBAR = 2 * NK + 2 * NV + 2 * NW + NC + 2 * IR + 6 + 2 + 12 + 2 + 2;
   static constexpr int miscOff = barOff + NBAR * 8;
   static constexpr int total = miscOff + 16 + 1024;
+  static_assert(schedOff % 16 == 0, "sts_item");
   static_assert(total <= 227 * 1024, "shared memory");
   static_assert(NW == 2 && wBytes == TILE * D * 2, "a V buffer holds a row tile of the result");
 };
@@ -187,6 +197,109 @@ __device__ __noinline__ void find_nans(const Params& p, const uint8_t* kv, int r
       if (t <= lim) mask[i] |= w;
     }
   }
+}
+
+// O of the warp's rows in tensor memory times f (16 columns: the scores hold 128 registers)
+template <int D>
+__device__ __forceinline__ void rescale_o(uint32_t to, float f) {
+#pragma unroll 1
+  for (int j = 0; j < D; j += 16) {
+    float o[16];
+    tmem_ld16(to + j, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] *= f;
+    tmem_st16(to + j, reinterpret_cast<const uint32_t*>(o));
+  }
+}
+
+// A softmax warp's work on a key tile whose V scales are too far apart for one power
+// of two, or lie so far below what the row has in O that its weights would vanish
+// in P: P with each token's own power of two, l by itself. Small code that loads the
+// scores three times, since it may not cost the common tiles registers or room in the
+// instruction cache (written out, or with the scores in registers, 4 to 12 %). 1024
+// over 65536 with such scales in every tile 3570 us, 816 in none.
+struct Apart {
+  float c, m, l, x, e;         // m, l and x go in and out
+  uint32_t ksc, vexp;          // the tile's K scales and powers of two in shared memory
+  uint32_t ts, to, tp;         // S, O and P of the warp's rows in tensor memory
+  uint64_t *sfull, *sfree, *pfree, *pfull;   // sfree and pfree null: S is not handed back, P is free
+  int sparity, vis;            // keys 0 .. vis of the tile are seen
+  bool first;
+  int lane;
+  volatile int* abort_flag;
+};
+template <int D>
+__device__ __forceinline__ bool apart_tile(Apart& w) {
+  if (!warp_wait(w.sfull, w.sparity, w.abort_flag, KERR_TIMEOUT_FULL)) return false;
+  tc_fence_after();
+  // Three passes over the scores, in one body: the maximum for m, then l and the largest
+  // P for x, then P (in place of S where there is no room beside it: its columns lie
+  // at or before those of the scores read so far)
+  float mx = -INFINITY, g = -INFINITY, l = 0.f;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+#pragma unroll 1
+    for (int j = 0; j < TILE; j += 16) {
+      float y[16];
+      uint32_t pw[8];
+      __syncwarp();
+      tmem_ld16(w.ts + j, y);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 ks = lds_f4(w.ksc + 4 * (j + i));
+        float4 et = make_float4(w.e, w.e, w.e, w.e);
+        if (!(w.e == w.e)) et = lds_f4(w.vexp + 4 * (j + i));
+        fmul2(y[i], y[i + 1], ks.x, ks.y);
+        fmul2(y[i + 2], y[i + 3], ks.z, ks.w);
+        const float ep[4] = {et.x, et.y, et.z, et.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float& p = y[i + u];
+          if (j + i + u > w.vis) p = -INFINITY;
+          mx = fmaxf(mx, p);
+          p = fmaf(p, w.c, -w.m);
+          l += ex2(p);
+          p += ep[u];
+          g = fmaxf(g, p);
+          p = ex2(p - w.x);
+        }
+        pw[i / 2] = f32x2_to_f16x2(y[i], y[i + 1]);
+        pw[i / 2 + 1] = f32x2_to_f16x2(y[i + 2], y[i + 3]);
+      }
+      if (pass == 2) {
+        tmem_st8(w.tp + j / 2, pw);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (w.lane == 0) {
+          if (j == TILE - 16 && w.sfree) mbar_arrive(w.sfree);
+          if ((j & 48) == 48) mbar_arrive(w.pfull + j / 64);
+        }
+      }
+    }
+    if (pass == 0) {
+      mx *= w.c;
+      if (mx - w.m > kRoom + kLazy) {
+        const float mr = fmaxf(floorf(mx) - kRoom, kNoMax), d = mr - w.m;
+        w.l *= ex2(-d);
+        w.x -= d;
+        w.m = mr;
+      }
+      g = -INFINITY;
+      l = 0.f;
+    } else if (pass == 1) {
+      w.l += l;
+      const float x = g - w.x > kRoom + kLazy ? fmaxf(floorf(g) - kRoom, kNoMax) : w.x;
+      if (w.pfree && !warp_wait(w.pfree, w.sparity ^ 1, w.abort_flag, KERR_TIMEOUT_FULL)) return false;
+      tc_fence_after();
+      __syncwarp();
+      if (!w.first && __any_sync(0xffffffffu, x != w.x)) rescale_o<D>(w.to, ex2(w.x - x));
+      w.x = x;
+    }
+  }
+  return true;
 }
 
 template <int D, bool PT>
@@ -362,15 +475,26 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         lim = tok < it.ntok ? it.lim0 + tok : INT_MAX;
       }
       float m = kNoMax, l = 0.f;
-      int ev = -126;
-      for (int t = t0; t < end; ++t, ++sc) {
+      // Per-token scales: P holds 2^(s c + e - m - x) with the tile's (or token's) power
+      // of two e out of V, x the row's reference of O against m, so that what a row
+      // keeps goes by p times the V scale, of the tokens that it sees. m and x are whole
+      // numbers: their sums are exact
+      float x = kNoMax;
+      bool apart = false;                            // (per-token scales) left for a tile that apart_tile takes
+      int t = t0;
+    tiles:
+      for (; t < end; ++t, ++sc) {
         const int nn = n + t - t0, cb = nn % NC;
         float s[4][32], mx4[4];
+        float e = 0.f;                               // (per-token scales) the tile's power of two out of V
         // Per-token scales: the keys' scales are loaded while S is awaited, into the
         // registers that S times them takes then (loaded after S: 1024 over 65536 861
         // us, 812 so; head_dim 64, prompts 525, 498)
         if constexpr (PT) {
           if (!warp_wait(&cfull[cb], (nn / NC) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+          // (the check stands ahead of S: no scores to keep through the long way)
+          e = ldsf(sb + S::evOff + 4 * cb);
+          if ((apart = __any_sync(0xffffffffu, !(x - e <= kFar)))) break;   // (NaN too)
 #pragma unroll
           for (int i = 0; i < 128; i += 4) {
             const float4 ks = lds_f4(sb + S::kscOff + 4 * (cb * TILE + i));
@@ -416,36 +540,48 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           }
         }
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
-        int en = ev;
-        if constexpr (PT) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(en) : "r"(sb + S::evOff + 4 * cb));
-        const float mr = mx - kRoom;
-        if (t == t0) {
-          m = fmaxf(mr, kNoMax);
-        } else {
-          const bool grow = mr > m + kLazy;
-          if (__any_sync(0xffffffffu, grow) || (PT && en != ev)) {
-            const float al = grow ? ex2(m - mr) : 1.f;
-            if (grow) m = mr;
-            l *= al;
-            // (ev only grows: the factor is at most 1)
-            const float f = PT ? al * ex2((float)(ev - en)) : al;
-            // (without SEP the S at hand came after the last product)
-            if (SEP && !warp_wait(&pfree[a], (sc & 1) ^ 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-            if (SEP) tc_fence_after();
-#pragma unroll 1
-            for (int j = 0; j < D; j += 16) {        // (the scores hold 128 registers)
-              float o[16];
-              tmem_ld16(to + j, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= f;
-              tmem_st16(to + j, reinterpret_cast<const uint32_t*>(o));
+        float nm;                                    // P = 2^(s c + nm)
+        if constexpr (PT) {
+          const float most = kRoom + kLazy + fminf(x - e, 0.f);
+          if (__any_sync(0xffffffffu, t == t0 || mx - m > most)) {
+            if (mx - m > kRoom + kLazy) {
+              const float mr = fmaxf(floorf(mx) - kRoom, kNoMax), d = mr - m;
+              l *= ex2(-d);
+              x -= d;
+              m = mr;
+            }
+            const float g = mx - m + e;              // largest P, but for x
+            const bool grow = g - x > kRoom + kLazy;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float xr = grow ? fmaxf(floorf(g) - kRoom, kNoMax) : x, f = ex2(x - xr);
+              x = xr;
+              if (t != t0) {
+                // (without SEP the S at hand came after the last product)
+                if (SEP && !warp_wait(&pfree[a], (sc & 1) ^ 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+                if (SEP) tc_fence_after();
+                rescale_o<D>(to, f);
+              }
             }
           }
+          nm = e - x - m;
+        } else {
+          const float mr = mx - kRoom;
+          if (t == t0) {
+            m = fmaxf(mr, kNoMax);
+          } else {
+            const bool grow = mr > m + kLazy;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float al = grow ? ex2(m - mr) : 1.f;
+              if (grow) m = mr;
+              l *= al;
+              if (SEP && !warp_wait(&pfree[a], (sc & 1) ^ 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+              if (SEP) tc_fence_after();
+              rescale_o<D>(to, al);
+            }
+          }
+          nm = -m;
         }
-        ev = en;
         float la[4] = {0.f, 0.f, 0.f, 0.f};
-        const float nm = -m;
         // P in two halves: the product with the first 64 keys runs while the
         // exponentials of the others are still computed
 #pragma unroll
@@ -453,15 +589,15 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           uint32_t pw[32];
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
-            float* x = &s[2 * hf + i / 32][i % 32];
-            ffma2(x[0], x[1], c, nm);
-            ffma2(x[2], x[3], c, nm);
+            float* y = &s[2 * hf + i / 32][i % 32];
+            ffma2(y[0], y[1], c, nm);
+            ffma2(y[2], y[3], c, nm);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) x[u] = ex2(x[u]);
-            fadd2(la[0], la[1], x[0], x[1]);
-            fadd2(la[2], la[3], x[2], x[3]);
-            pw[i / 2] = f32x2_to_f16x2(x[0], x[1]);
-            pw[i / 2 + 1] = f32x2_to_f16x2(x[2], x[3]);
+            for (int u = 0; u < 4; ++u) y[u] = ex2(y[u]);
+            fadd2(la[0], la[1], y[0], y[1]);
+            fadd2(la[2], la[3], y[2], y[3]);
+            pw[i / 2] = f32x2_to_f16x2(y[0], y[1]);
+            pw[i / 2 + 1] = f32x2_to_f16x2(y[2], y[3]);
           }
           if (SEP && hf == 0 && sc > 0) {            // the last product has read P
             if (!warp_wait(&pfree[a], (sc & 1) ^ 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
@@ -474,7 +610,28 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           if (lane == 0) mbar_arrive(&pfull[2 * a + hf]);
         }
         if (!ok) break;
-        l += (la[0] + la[1]) + (la[2] + la[3]);
+        const float sum = (la[0] + la[1]) + (la[2] + la[3]);
+        l += PT ? sum * ex2(x - e) : sum;
+      }
+      if (PT && apart) {
+        // (outside the loop, and from a 0 that the compiler does not know: what it
+        // prepares for this ahead of the tiles costs them registers)
+        apart = false;
+        int z;
+        asm volatile("mov.u32 %0, 0;" : "=r"(z));
+        const int cb = (n + t - t0 + z) % NC;
+        const uint32_t sz = sb + 4 * (cb * TILE), tz = tl + z;
+        uint64_t* bz = sfull + a + z;
+        Apart w{c, m, l, x, ldsf(sb + S::evOff + 4 * cb), sz + S::kscOff, sz + S::vexpOff, tz + a * 128, tz + T_O + a * D,
+                tz + T_P + a * P_STEP, bz, SEP ? bz + 2 : nullptr, SEP && sc > 0 ? bz + (pfree - sfull) : nullptr,
+                bz + a + (pfull - sfull), sc & 1, lim - t * TILE, t == t0, lane, abort_flag};
+        ok = apart_tile<D>(w);
+        m = w.m;
+        l = w.l;
+        x = w.x;
+        ++t;
+        ++sc;
+        if (ok) goto tiles;
       }
       if (!ok) break;
       const Item it = lds_item(sb + S::qinfoOff + 64 * qb);
@@ -500,8 +657,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       const int used = (n + 1 - a) / 2;              // times V buffer a was filled
       if (used > 0 && !warp_wait(&wempty[a], (used - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       const bool none = lim < 0 || l == 0.f;
-      const float rl = none ? 0.f : __frcp_rn(l);
-      const float sv = PT ? ex2((float)ev) : vscale;
+      // (per-token scales: 2^(x - 7), in two factors since it may leave the normals)
+      const float xh = floorf(0.5f * (x - 7.f)), sv = PT ? ex2(x - 7.f - xh) : vscale;
+      const float rl = none ? 0.f : PT ? __frcp_rn(l) * ex2(xh) : __frcp_rn(l);
       float* prow = p.part_o + ((long long)it.slot * p.part_rows + row) * D;
       // (l of a row that sees no token is NaN if its query is not finite)
       if (it.slot >= 0 && valid)
@@ -694,7 +852,6 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
 
       // ---- V of the item's key tiles: e4m3 -> f16, [dims / 64][token][64 dims],
       // 128-byte swizzle (the MN-major operand of the PV product)
-      int ev = -126;
       for (int t = it.t0; t < it.t1; ++t, ++n) {
         const int vb = n % NV, wb = n % NW, cb = n % NC;
         const int live = it.L - t * TILE;            // tokens of the tile that exist
@@ -705,24 +862,37 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           // (Room here: the last tile waited for the product three tiles back.)
           const int kb = n % NK;
           if (!warp_wait(&kfull[kb], (n / NK) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-          float vm = 0.f;
+          uint32_t ax[4], hi = 0;                    // |scale|, its largest (finite), as bits
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int tk = 32 * i + lane;
             const float x = tk < live ? ldsf(sb + S::vrawOff + 4 * (vb * TILE + tk)) : 0.f;
-            const float ax = fabsf(x);
-            if (ax < INFINITY) vm = fmaxf(vm, ax);
+            ax[i] = __float_as_uint(x) & 0x7fffffffu;
+            if (ax[i] >= 0x7f800000u) ax[i] = 0;
+            hi = max(hi, ax[i]);
             if (i == cw) vown = x;                   // token 32 cw + lane
           }
-          vm = warp_max(vm);
-          // 2^ev above the largest scale so far: |v scale| 2^-ev < 1 (4 at the very
-          // top). V enters as f16(v scale 2^-ev); when ev grows, O shrinks
-          ev = max(ev, min((int)(__float_as_uint(vm) >> 23) - 126, 126));
+          // V enters as f16(v scale 2^(7-e)), below 2^7 (times 448: f16's range) for a
+          // power of two 2^e above the scale, which goes into p: one for the tile if none of
+          // its scales (but 0) lies 2^kSpread further below, each token's own otherwise
+          hi = __reduce_max_sync(0xffffffffu, hi);
+          auto pow2 = [](uint32_t x) { return max((int)(x >> 23) - 126, -119); };
+          int e = pow2(hi);
+          const uint32_t low = (uint32_t)(e + 126 - kSpread) << 23;   // 2^(e - 1 - kSpread)
+          bool far = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) far = far || ax[i] - 1u < low - 1u;
+          const bool several = __any_sync(0xffffffffu, far && e > kSpread - 126);
           const int tk = 32 * cw + lane;
           const float kx = tk < live ? ldsf(sb + S::krawOff + 4 * (kb * TILE + tk)) : 0.f;
           stsf(sb + S::kscOff + 4 * (cb * TILE + tk), kx);
-          vown *= ex2((float)-ev);
-          if (cw == 0 && lane == 0) asm volatile("st.shared.s32 [%0], %1;" ::"r"(sb + S::evOff + 4 * cb), "r"(ev) : "memory");
+          if (cw == 0 && lane == 0) stsf(sb + S::evOff + 4 * cb, several ? __uint_as_float(0x7fffffffu) : (float)e);
+          if (several) {
+            const uint32_t own = __float_as_uint(vown) & 0x7fffffffu;
+            e = pow2(own < 0x7f800000u ? own : 0u);
+            stsf(sb + S::vexpOff + 4 * (cb * TILE + tk), (float)e);
+          }
+          vown *= __uint_as_float((uint32_t)(134 - e) << 23);   // 2^(7 - e)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&cfull[cb]);

@@ -15,8 +15,11 @@ row sees:
                                     per dim), da from float32 sums of D products, the
                                     scale product and the exponential (2^-24 each step)
   + L 2^-32 M                       p below f16's normals has an error of 2^-25 against
-                                    a largest one of at least 2^7 (doubled with
-                                    per-token scales, by the V scale's power of two)
+                                    a largest one of at least 2^7
+  + L 2^-24 M                       instead, per-token scales: the reference of p times
+                                    the scale is at most 2^8 above what the row sees (a
+                                    bit to a power of two, `spread` = 7 bits between the
+                                    scales of a tile that share one)
 """
 import ctypes
 import threading
@@ -40,7 +43,7 @@ def _lib():
     __graft_entry__.build()
 
 
-def _reference(c):
+def _reference(c, spread=7):
     """(ref, tolerance), float64; rows of no request NaN."""
     q = decode_bf16(c.q_bits)
     T, Hq, D = q.shape
@@ -73,7 +76,7 @@ def _reference(c):
                     e = 2.0 ** -17 * qk + (D + 4) * 2.0 ** -24 * qk + 2.0 ** -22
                     pv = 2.0 ** -11 + 2.0 ** -18 + (2.0 ** -10 if c.per_token else 0.0)
                     tol[a + i, g] = (2.0 ** -8 * np.abs(ref[a + i, g]) + (pv + 2 * e) * A
-                                     + n * (2.0 ** -31 if c.per_token else 2.0 ** -32) * M)
+                                     + n * (2.0 ** (spread - 31) if c.per_token else 2.0 ** -32) * M)
     return ref, tol
 
 
@@ -84,9 +87,9 @@ def _run(c):
     return out.double().cpu().numpy()
 
 
-def _check(c):
+def _check(c, spread=7):
     got = _run(c)
-    ref, tol = _reference(c)
+    ref, tol = _reference(c, spread)
     nan = np.isnan(ref)
     assert np.array_equal(np.isnan(got), nan), "NaN pattern differs"
     err, lim = np.abs(got - ref)[~nan], tol[~nan]
@@ -134,4 +137,91 @@ def test_many_small_probabilities(D, per_token, drop):
     q[..., 0] = 1
     c.q_bits = synth.round_to_bf16_bits(q)
     c.scale = float(drop * np.log(2) / 0.25)
+    _check(c, spread=0)
+
+
+# ------------------------------------------------------------------ V scales
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("factor", [1e3, 1e6, -3e7, 1e8, 1e30])
+def test_v_scale_of_a_token_that_a_row_does_not_see(D, factor):
+    """The rows before a token with an outlying V scale do not notice it."""
+    c = Chunk(43, [(60, 300), (40, 40)], 2, 4, D, 16, True)
+    for r, tok in ((0, 290), (0, 250), (1, 17)):
+        blk, off = _place(c, r, np.array([tok]))
+        c.vs[blk, :, off] *= factor
     _check(c)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("factor", [1e6, 1e8, 1e30])
+def test_v_scale_of_a_token_without_weight(D, factor):
+    """Tokens that are seen with a weight of 0 (keys far against the query) and
+    outlying V scales, in the first, a middle and the last key tile."""
+    c = Chunk(44, [(9, 600), (2, 5000)], 2, 4, D, 32, True)
+    q = np.abs(decode_bf16(c.q_bits))
+    c.q_bits = synth.round_to_bf16_bits(q + 0.25)
+    for r, toks in ((0, [3, 200, 590]), (1, [1, 2500, 4990])):
+        blk, off = _place(c, r, np.array(toks))
+        c.cache[blk, 0, :, off] = 0xFE                  # -448
+        c.ks[blk, :, off] = 0.08
+        c.vs[blk, :, off] *= factor
+    _check(c)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("decades", [1, 4, 15, 33])
+def test_v_scales_far_apart(D, decades):
+    """Scales over many decades within every key tile, zeros and signs among them."""
+    c = Chunk(45, [(150, 500), (1, 3000)], 1, 2, D, 16, True)
+    r = synth.rng(46)
+    live = ~np.isnan(c.vs)
+    x = 10.0 ** r.uniform(-decades, decades, c.vs.shape) * np.where(r.random(c.vs.shape) < 0.5, -1, 1)
+    x[r.random(c.vs.shape) < 0.1] = 0
+    c.vs[live] = x[live].astype(np.float32)
+    _check(c)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("order", [1, -1])
+def test_v_scales_that_differ_between_key_tiles(D, order):
+    """A tile of large scales and little weight beside one of small scales and all
+    the weight, in both orders: neither the values of the first nor the weights of
+    the second get lost (10^33 between the scales, e^-18 between the weights)."""
+    c = Chunk(47, [(3, 384)], 1, 4, D, 128, True)
+    q = np.abs(decode_bf16(c.q_bits)) + 0.25
+    q *= 4 / q.sum(axis=-1, keepdims=True)
+    c.q_bits = synth.round_to_bf16_bits(q)
+    c.scale = 1.0
+    blk = c.table[0, :3][::order].astype(np.int64)
+    c.cache[blk[0], 0], c.cache[blk[1:], 0] = 0xB8, 0x38          # -1 and 1
+    c.ks[blk] = 2.25                                              # logits -9 and 9
+    c.vs[blk[0]], c.vs[blk[1]], c.vs[blk[2]] = 1e30, 1e-3, 3e-3
+    _check(c)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("size", [1e-37, 1e-30, 1e33])
+def test_v_scales_near_the_ends_of_float32(D, size):
+    c = Chunk(48, [(20, 300), (1, 2000)], 2, 4, D, 16, True)
+    c.vs *= np.float32(size)
+    _check(c)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_v_scale_that_is_not_finite(D, bad):
+    """NaN in every dim of the rows that see the token, nothing elsewhere."""
+    c = Chunk(49, [(60, 300), (40, 40)], 2, 4, D, 16, True)
+    for r, tok, h in ((0, 270, 0), (0, 290, 1), (1, 17, 1)):
+        blk, off = _place(c, r, np.array([tok]))
+        c.vs[blk, h, off] = bad
+    out = _run(c)
+    clean = np.nan_to_num(c.vs, nan=1.0, posinf=1.0, neginf=1.0)
+    blind = np.zeros(out.shape, bool)
+    for r, tok, h in ((0, 270, 0), (0, 290, 1), (1, 17, 1)):
+        first = int(c.start[r]) + tok - int(c.lens[r] - (c.start[r + 1] - c.start[r]))
+        blind[first:int(c.start[r + 1]), h * 4:(h + 1) * 4] = True
+    assert np.array_equal(np.isnan(out), blind)
+    c.vs = np.where(np.isfinite(c.vs), c.vs, clean)
+    ref, tol = _reference(c)
+    assert np.all(np.abs(out - ref)[~blind] <= tol[~blind])
