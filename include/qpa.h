@@ -534,8 +534,9 @@ int kv_append_fp8(const void* k, const void* v, uint8_t* kv_cache, const int64_t
  * up to 2^8). Sums and softmax statistics are
  * float32. The output is bf16 only: probabilities of 11 bits would leave the
  * rest of a float32 output without meaning. A per-token V scale that is not
- * finite makes the rows that see its token NaN; logits beyond float32 are
- * outside the supported range.
+ * finite makes the rows that see its token NaN. Logits of 2^26 and more in
+ * magnitude, where float32's steps exceed f16's range of probabilities, are outside
+ * the supported range.
  *
  * Layouts: q bf16 [num_tokens][num_kv_heads*query_group][head_dim] with the
  * descriptor's strides (elements, multiples of 8); out bf16, contiguous;

@@ -280,9 +280,8 @@ __device__ __forceinline__ bool apart_tile(Apart& w) {
       }
     }
     if (pass == 0) {
-      mx *= w.c;
-      if (mx - w.m > kRoom + kLazy) {
-        const float mr = fmaxf(floorf(mx) - kRoom, kNoMax), d = mr - w.m;
+      if (fmaf(mx, w.c, -w.m) > kRoom + kLazy) {
+        const float mr = fmaxf(floorf(fmaf(mx, w.c, -kRoom)), kNoMax), d = mr - w.m;
         w.l *= ex2(-d);
         w.x -= d;
         w.m = mr;
@@ -539,18 +538,20 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
             for (int i = 2; i < 32; i += 2) mx4[j] = fmax3(mx4[j], s[j][i], s[j][i + 1]);
           }
         }
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+        // The largest exponent comes from the same fma as P's (a rounded s c - m may be off by
+        // a step of m, which is more than 1 from 2^24 on), so that P stays in f16's range
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         float nm;                                    // P = 2^(s c + nm)
         if constexpr (PT) {
-          const float most = kRoom + kLazy + fminf(x - e, 0.f);
-          if (__any_sync(0xffffffffu, t == t0 || mx - m > most)) {
-            if (mx - m > kRoom + kLazy) {
-              const float mr = fmaxf(floorf(mx) - kRoom, kNoMax), d = mr - m;
+          nm = e - x - m;
+          if (__any_sync(0xffffffffu, t == t0 || fmaf(mx, c, -m) > kRoom + kLazy || fmaf(mx, c, nm) > kRoom + kLazy)) {
+            if (fmaf(mx, c, -m) > kRoom + kLazy) {
+              const float mr = fmaxf(floorf(fmaf(mx, c, -kRoom)), kNoMax), d = mr - m;
               l *= ex2(-d);
               x -= d;
               m = mr;
             }
-            const float g = mx - m + e;              // largest P, but for x
+            const float g = fmaf(mx, c, -m) + e;     // largest P, but for x
             const bool grow = g - x > kRoom + kLazy;
             if (__any_sync(0xffffffffu, grow)) {
               const float xr = grow ? fmaxf(floorf(g) - kRoom, kNoMax) : x, f = ex2(x - xr);
@@ -562,14 +563,14 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
                 rescale_o<D>(to, f);
               }
             }
+            nm = e - x - m;
           }
-          nm = e - x - m;
         } else {
-          const float mr = mx - kRoom;
+          const float mr = fmaf(mx, c, -kRoom);
           if (t == t0) {
             m = fmaxf(mr, kNoMax);
           } else {
-            const bool grow = mr > m + kLazy;
+            const bool grow = fmaf(mx, c, -m) > kRoom + kLazy;
             if (__any_sync(0xffffffffu, grow)) {
               const float al = grow ? ex2(m - mr) : 1.f;
               if (grow) m = mr;

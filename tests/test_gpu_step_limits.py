@@ -225,3 +225,48 @@ def test_v_scale_that_is_not_finite(D, bad):
     c.vs = np.where(np.isfinite(c.vs), c.vs, clean)
     ref, tol = _reference(c)
     assert np.all(np.abs(out - ref)[~blind] <= tol[~blind])
+
+
+# ------------------------------------------------------------------ logits
+@pytest.mark.parametrize("D,per_token", VARIANTS)
+@pytest.mark.parametrize("size", [1e4, 3e6, 2e7, 6e7])
+def test_logits_far_from_zero(D, per_token, size):
+    """Logits of about `size` that differ by as much: each row is the V of its
+    largest, whatever float32's steps are there."""
+    c = Chunk(50, [(70, 400), (1, 700)], 1, 3, D, 16, per_token)
+    q = np.abs(decode_bf16(c.q_bits)) + 0.25
+    c.q_bits = synth.round_to_bf16_bits(q)
+    c.scale = float(size / 0.02 / q.sum(axis=-1).max())
+    c.ks[:] = 0.01
+    c.cache[:, 0] = 0x38
+    for r, tok in ((0, 40), (1, 699)):
+        blk, off = _place(c, r, np.array([tok]))
+        c.cache[blk, 0, :, off] = 0x40                  # 2 against 1
+    got = _run(c)
+    ref, _ = _reference(c)
+    # p is 1 and its product with V exact but for per-token scales (2^-10)
+    assert np.all(np.abs(got - ref) <= (2.0 ** -8 + (2.0 ** -10 if per_token else 0)) * np.abs(ref))
+
+
+@pytest.mark.parametrize("D,per_token", VARIANTS)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [1e4, 3e6, 2e7, 6e7])
+def test_large_logits_that_differ_little(D, per_token, sign, size):
+    """Logits around +-`size` whose differences are a few of float32's steps there and
+    grow along the sequence, V the same everywhere: the rows' weights sum to 1."""
+    c = Chunk(52, [(70, 1500), (1, 3000)], 2, 3, D, 16, per_token)
+    r = synth.rng(53)
+    q = np.ones_like(decode_bf16(c.q_bits))
+    q[..., 0] = 2.0 ** -15 * 2.0 ** r.integers(0, 8, q.shape[:2])
+    c.q_bits = synth.round_to_bf16_bits(q)
+    c.scale = float(sign * size / 0.01 / D)
+    c.ks[:] = 0.01
+    c.vs[:] = 0.5
+    c.cache[:, 0], c.cache[:, 1] = 0x38, 0x3C           # 1 and 1.5
+    for req, L in enumerate(c.lens):
+        pos = np.arange(L)
+        blk, off = _place(c, req, pos)
+        c.cache[blk, 0, :, off, 0] = np.clip(pos * 100 // L + r.integers(0, 20, L), 0, 119)[:, None]   # 0 to 240
+    got = _run(c)
+    # (p in f16 against a sum of p in float32, the V scale exact)
+    assert np.all(np.abs(got - 0.75) <= 0.75 * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18))
