@@ -185,7 +185,7 @@ size_t extent(long long tokens, long long heads, int dim, long long stride_tok, 
 }
 
 bool slot_shape_ok(const qpa_slot_desc* d) {
-  if (d->num_reqs < 0 || d->num_reqs > 16384 || !block_size_ok(d->block_size) || d->max_blocks_per_seq < 1) return false;
+  if (d->num_reqs < 0 || d->num_reqs > kMaxReqs || !block_size_ok(d->block_size) || d->max_blocks_per_seq < 1) return false;
   if (d->num_free < 0 || d->max_tokens < 0 || d->reserved != 0) return false;
   if (d->table_stride != 0 && d->table_stride < d->max_blocks_per_seq) return false;
   if ((long long)d->max_blocks_per_seq * d->block_size > 0x7fffffffLL) return false;

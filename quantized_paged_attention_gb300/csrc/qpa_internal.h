@@ -111,6 +111,7 @@ struct IdxLaunch {
 };
 
 // paged_slot_map
+constexpr int kMaxReqs = 16384;   // requests of a call: two running sums of them lie in shared memory
 struct SlotMapLaunch {
   const int32_t* new_lens;
   const int32_t* cached_lens;

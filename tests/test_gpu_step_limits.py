@@ -270,3 +270,34 @@ def test_large_logits_that_differ_little(D, per_token, sign, size):
     got = _run(c)
     # (p in f16 against a sum of p in float32, the V scale exact)
     assert np.all(np.abs(got - 0.75) <= 0.75 * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18))
+
+
+# ------------------------------------------------------------------ host
+def test_slot_maps_of_different_sizes_from_two_threads():
+    """Calls with more than 5119 requests take more shared memory than a launch may
+    without a limit of its own; sizes at once do not disturb each other. (The C
+    entry in tight loops: the binding's host time would keep the calls apart.)"""
+    lib, bad = qpa.load_library(), []
+
+    def work(R, stream, t):
+        d = qpa.SlotDesc(R, 16, 1, R, R, 0, 0)
+        args = [ctypes.c_void_p(x.data_ptr()) for x in t] + [ctypes.byref(d), ctypes.c_void_p(stream.cuda_stream)]
+        bad.extend(st for st in (lib.paged_slot_map(*args) for _ in range(20000)) if st)
+
+    threads, outs = [], []
+    for R in (16384, 6000, 11000):
+        new, old, free = _i32(np.ones(R)), _i32(np.zeros(R)), _i32(np.arange(R))
+        table, start, lens, pos, taken = (torch.zeros(n, dtype=torch.int32, device=dev()) for n in (R, R + 1, R, R, 1))
+        slots = torch.zeros(R, dtype=torch.int64, device=dev())
+        outs.append(slots)
+        threads.append(threading.Thread(target=work, args=(R, torch.cuda.Stream(), (
+            new, old, table, free, start, lens, slots, pos, taken))))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _clean()
+    assert not bad, f"{len(bad)} calls failed with {set(bad)}"
+    for x in outs:
+        assert torch.equal(x.cpu(), 16 * torch.arange(x.numel()))
