@@ -1373,6 +1373,13 @@ cudaError_t launch_chunk(const ChunkLaunch& a, cudaStream_t stream) {
   EncodeTiledFn enc = encode_tiled();
   if (!enc) return cudaErrorNotSupported;
   const int D = a.head_dim, bs = a.block_size;
+  // (ahead of the tensor map, whose encoding needs a context that is current in this
+  // host thread: the runtime's first call in a thread makes it so)
+  auto kernel = D == 64 ? (a.per_token ? pa_chunk_kernel<64, true> : pa_chunk_kernel<64, false>)
+                        : (a.per_token ? pa_chunk_kernel<128, true> : pa_chunk_kernel<128, false>);
+  const int smem = D == 64 ? Smem<64>::total : Smem<128>::total;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   CUtensorMap map;
   const cuuint64_t page_rows = (cuuint64_t)2 * a.num_kv_heads * bs;
   const cuuint64_t dims[3] = {(cuuint64_t)D, page_rows, (cuuint64_t)a.num_blocks};
@@ -1414,14 +1421,7 @@ cudaError_t launch_chunk(const ChunkLaunch& a, cudaStream_t stream) {
   const long long items = (long long)a.num_tokens / bt + std::min(a.num_reqs, a.num_tokens);
   const long long most = std::min(items * a.num_kv_heads, 1LL << 20) * ((p.max_len - 1) / TILE + 1 + ITEM_COST);
   const int grid = active_ctas(most, std::min(a.num_sms, MAX_GRID));
-  cudaError_t e = cudaSuccess;
-  auto launch = [&](auto kernel, int smem) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) kernel<<<grid, THREADS, smem, stream>>>(map, a.kv, p);
-  };
-  if (D == 64) a.per_token ? launch(pa_chunk_kernel<64, true>, Smem<64>::total) : launch(pa_chunk_kernel<64, false>, Smem<64>::total);
-  else a.per_token ? launch(pa_chunk_kernel<128, true>, Smem<128>::total) : launch(pa_chunk_kernel<128, false>, Smem<128>::total);
-  if (e != cudaSuccess) return e;
+  kernel<<<grid, THREADS, smem, stream>>>(map, a.kv, p);
   const dim3 cg(grid, (L.rows + 31) / 32);
   if (D == 64) chunk_combine_kernel<64><<<cg, 256, 0, stream>>>(p, grid);
   else chunk_combine_kernel<128><<<cg, 256, 0, stream>>>(p, grid);

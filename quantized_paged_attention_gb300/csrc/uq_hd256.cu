@@ -758,6 +758,10 @@ cudaError_t launch_uq_partition(const UqLaunch& a, cudaStream_t stream) {
   if (!enc) return cudaErrorNotSupported;
   const UqPlan pl = uq_plan(a.num_kv_heads, a.qg);
   if (pl.hg == 0) return cudaErrorInvalidValue;
+  // (ahead of the tensor map, whose encoding needs a context that is current in this
+  // host thread: the runtime's first call in a thread makes it so)
+  auto kern = a.flags & QPA_UQ_UE8M0_SCALES ? uq_partition_kernel<true> : uq_partition_kernel<false>;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
   CUtensorMap kv_map;
   const cuuint64_t dims[3] = {(cuuint64_t)(a.padded_slot / 8), (cuuint64_t)a.num_kv_heads,
                               (cuuint64_t)a.num_blocks * (cuuint64_t)a.block_size};
@@ -796,12 +800,7 @@ cudaError_t launch_uq_partition(const UqLaunch& a, cudaStream_t stream) {
   const long long items = (long long)a.num_seqs * (a.num_kv_heads / pl.hg) * a.num_partitions;
   if (items <= 0) return cudaSuccess;
   const int grid = (int)std::min<long long>(items, (long long)a.num_sms);
-  auto launch = [&](auto kern) {
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
-    kern<<<grid, uq::THREADS, pl.smem, stream>>>(kv_map, p);
-  };
-  if (a.flags & QPA_UQ_UE8M0_SCALES) launch(uq_partition_kernel<true>);
-  else launch(uq_partition_kernel<false>);
+  kern<<<grid, uq::THREADS, pl.smem, stream>>>(kv_map, p);
   return cudaGetLastError();
 }
 
