@@ -1244,7 +1244,7 @@ static cudaError_t launch_combine_t(const CombineLaunch& a, OutT* out, cudaStrea
   const int grid = a.num_seqs * a.num_kv_heads * (a.qg / rpc);
   const size_t smem = size_t(rpc) * (combine_smem_bytes(a.num_partitions, threads) + HD * sizeof(float));
   if (smem > 40 * 1024)
-    cudaFuncSetAttribute(combine_kernel<OutT, HD, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaFuncSetAttribute(combine_kernel<OutT, HD, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads * rpc);

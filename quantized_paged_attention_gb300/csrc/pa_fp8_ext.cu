@@ -52,7 +52,7 @@ static cudaError_t launch_fp8x_combine_t(const Fp8ExtCombineLaunch& a, OutT* out
   const int grid = a.num_seqs * a.num_kv_heads * (rows / rpc);
   const size_t smem = size_t(rpc) * (combine_smem_bytes(a.num_partitions, threads) + HD * sizeof(float));
   if (smem > 40 * 1024)
-    cudaFuncSetAttribute(combine_ext_kernel<OutT, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaFuncSetAttribute(combine_ext_kernel<OutT, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads * rpc);

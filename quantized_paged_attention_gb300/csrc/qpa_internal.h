@@ -110,6 +110,11 @@ struct IdxLaunch {
   int num_sms;
 };
 
+// The most dynamic shared memory that a launch may take. A kernel whose launches differ
+// in it always gets this as its limit, which belongs to the kernel: a smaller one, set
+// by another host thread between here and the launch, would make that fail.
+constexpr int kMaxDynamicSmem = 227 * 1024;
+
 // paged_slot_map
 constexpr int kMaxReqs = 16384;   // requests of a call: two running sums of them lie in shared memory
 struct SlotMapLaunch {

@@ -150,9 +150,7 @@ cudaError_t launch_slot_map(const SlotMapLaunch& a, cudaStream_t stream) {
   while ((1 << log2_bs) < a.block_size) ++log2_bs;
   const size_t smem = 2 * (size_t(a.num_reqs) + 1) * sizeof(uint32_t);
   if (smem > 40 * 1024) {
-    // always the most that a call may take: the limit belongs to the kernel, and another
-    // host thread may set it between here and this launch
-    constexpr int most = 2 * (kMaxReqs + 1) * sizeof(uint32_t);
+    constexpr int most = 2 * (kMaxReqs + 1) * sizeof(uint32_t);   // always the same, see kMaxDynamicSmem
     const cudaError_t e = cudaFuncSetAttribute(slot_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }

@@ -761,7 +761,7 @@ cudaError_t launch_uq_partition(const UqLaunch& a, cudaStream_t stream) {
   // (ahead of the tensor map, whose encoding needs a context that is current in this
   // host thread: the runtime's first call in a thread makes it so)
   auto kern = a.flags & QPA_UQ_UE8M0_SCALES ? uq_partition_kernel<true> : uq_partition_kernel<false>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem);
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, uq::SMEM_LIMIT);   // (as kMaxDynamicSmem)
   CUtensorMap kv_map;
   const cuuint64_t dims[3] = {(cuuint64_t)(a.padded_slot / 8), (cuuint64_t)a.num_kv_heads,
                               (cuuint64_t)a.num_blocks * (cuuint64_t)a.block_size};
@@ -810,7 +810,8 @@ static cudaError_t launch_uq_combine_t(const CombineLaunch& a, OutT* out, cudaSt
   const int threads = combine_threads(256, kCombineKmax256, a.num_partitions);
   const size_t smem = combine_smem_bytes(a.num_partitions, threads);
   if (smem > 40 * 1024)
-    cudaFuncSetAttribute(uq_combine_kernel<OutT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaFuncSetAttribute(uq_combine_kernel<OutT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         kMaxDynamicSmem - 256 * (int)sizeof(float));   // (the kernel's own row)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);

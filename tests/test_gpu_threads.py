@@ -70,3 +70,42 @@ def test_first_cuda_call_of_a_thread():
     assert not _together([lambda s: qpa.load_library().pa_chunk_fp8(*[_p(t[n]) for n in names], _p(out), ctypes.byref(cd),
                                                                     _p(ws), ws.nbytes, s)], 1)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_combines_of_different_partition_counts(fp8):
+    """Empty slots of 6000 to 20000 partitions, or of an eighth of that with 8 slots
+    each (48 to 160 KB of weights in shared memory), give 0."""
+    lib, calls, outs = qpa.load_library(), [], []
+    for P in (20000, 6000, 11000) if fp8 else (2500, 750, 1400):
+        D = 128 if fp8 else 256
+        q = torch.zeros(1, 1, D, dtype=torch.bfloat16, device=dev())
+        table = torch.zeros(1, 1, dtype=torch.int32, device=dev())
+        if fp8:
+            d = qpa.fp8_desc(q, torch.zeros(1, 2, 1, 16, D, dtype=torch.uint8, device=dev()), table, 1, None, torch.float32)
+            ws = torch.zeros(qpa.pa_decode_fp8_workspace_size(d, P), dtype=torch.uint8, device=dev())
+            fn = lib.pa_decode_fp8_combine
+        else:
+            d = UqDev(synth.make_uq_case(3, [5], num_kv_heads=1, query_group=1)).desc()
+            ws = torch.zeros(qpa.uq_decode_hd256_workspace_size(d, P), dtype=torch.uint8, device=dev())
+            fn = lib.uq_decode_hd256_combine
+        out = torch.full((1, 1, D), 9.0, device=dev())
+        outs.append(out)
+        calls.append(lambda s, fn=fn, P=P, out=out, d=d, ws=ws: fn(P, _p(out), ctypes.byref(d), _p(ws), ws.nbytes, s))
+    bad = _together(calls, 5000)
+    assert not bad, f"{len(bad)} calls failed with {set(bad)}"
+    assert all(bool((o == 0).all()) for o in outs)
+
+
+def test_hd256_decodes_of_different_head_counts():
+    """1, 2 and 4 KV heads take rings of different sizes."""
+    calls, outs = [], []
+    for Hk in (1, 2, 4):
+        c = UqDev(synth.make_uq_case(4, [40], num_kv_heads=Hk, query_group=8))
+        want, ws, d = c.run(1)
+        out = torch.zeros_like(want)
+        outs.append((out, want, c))
+        calls.append(_uq_call(c, out, d, ws))
+    bad = _together(calls, 5000)
+    assert not bad, f"{len(bad)} calls failed with {set(bad)}"
+    assert all(torch.equal(o, w) for o, w, _ in outs)
