@@ -61,7 +61,8 @@ int qpa_version(void);
  * produced an out-of-range slot, which its own bounds rule out; 5: a value
  * outside what the hd256 kernel represents, see QPA_UQ_UE8M0_SCALES and the
  * centroid table; 6: paged_slot_map ran out of free blocks or of table
- * columns). Returns QPA_ERR_CUDA
+ * columns). pa_chunk_fp8 has a word of its own: if both hold a code, this call
+ * returns the other kernels' and the next one pa_chunk_fp8's. Returns QPA_ERR_CUDA
  * if the synchronisation fails. Diagnostic only; the decode entry points
  * never call it. */
 int qpa_kernel_error(void* stream);

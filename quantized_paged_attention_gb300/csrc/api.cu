@@ -240,9 +240,9 @@ int qpa_kernel_error(void* stream) {
   int v = 0, z = 0;
   if (cudaMemcpyFromSymbol(&v, qpa::g_kernel_error, sizeof(int)) != cudaSuccess) return QPA_ERR_CUDA;
   if (cudaMemcpyToSymbol(qpa::g_kernel_error, &z, sizeof(int)) != cudaSuccess) return QPA_ERR_CUDA;
-  int w = 0;
-  if (take_chunk_error(&w) != cudaSuccess) return QPA_ERR_CUDA;
-  return v ? v : w;
+  // the chunk kernel's own word, for this call only if the shared one held nothing
+  if (v == 0 && take_chunk_error(&v) != cudaSuccess) return QPA_ERR_CUDA;
+  return v;
 }
 
 size_t pa_decode_fp8_workspace_size(const qpa_fp8_desc* d, int num_partitions) {

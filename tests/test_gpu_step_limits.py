@@ -301,3 +301,14 @@ def test_slot_maps_of_different_sizes_from_two_threads():
     assert not bad, f"{len(bad)} calls failed with {set(bad)}"
     for x in outs:
         assert torch.equal(x.cpu(), 16 * torch.arange(x.numel()))
+
+
+def test_two_errors_are_both_reported():
+    """paged_slot_map out of blocks, then a chunk call with a bad block id: one
+    query reports the one, the next the other."""
+    qpa.paged_slot_map(_i32([5]), _i32([0]), _i32([[0]]), _i32([]), 16, 5)
+    c = Chunk(51, [(4, 40)], 1, 2, 128, 16)
+    c.table[0, 1] = 9999
+    qpa.pa_chunk_fp8(**c.tensors())
+    torch.cuda.synchronize()
+    assert [qpa.kernel_error() for _ in range(3)] == [6, 3, 0]
