@@ -428,6 +428,8 @@ def _rows(block_table):
     if block_table.dtype != torch.int32 or block_table.dim() != 2:
         _fail("block_table must be int32 [num_reqs, max_blocks]")
     R, maxb = block_table.shape
+    if maxb >= 1 << 31:
+        _fail("block_table must have less than 2^31 columns")
     if R > 0 and maxb > 1 and block_table.stride(1) != 1:
         _fail("block_table must have contiguous rows")
     if R <= 1:
@@ -502,6 +504,9 @@ def paged_slot_map(new_lens, cached_lens, block_table, free_blocks, block_size: 
         if t.dtype != i32 or not t.is_contiguous():
             _fail("new_lens, cached_lens and free_blocks must be contiguous int32")
     maxb, stride = _rows(block_table)
+    # (ctypes cuts a number to its field's 32 bits without a word)
+    if not (0 <= max_tokens < 1 << 31 and 0 <= block_size < 1 << 31 and free_blocks.numel() < 1 << 31):
+        _fail("max_tokens, block_size and the free list's length must be below 2^31 and not negative")
     if cached_lens.numel() != R or block_table.shape[0] != R:
         _fail("new_lens, cached_lens and block_table must have one entry per request")
     for t, n, dt in ((query_start, R + 1, i32), (seq_lens, R, i32), (slots, max_tokens, torch.int64),
