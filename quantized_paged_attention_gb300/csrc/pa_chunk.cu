@@ -675,7 +675,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         if (!warp_wait(&wfull[(n - 1) % NW], ((n - 1) / NW) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
         const int4 marks = lds_i4(sb + S::flagOff + 16 * (k & 3));
         const bool anynan = (marks.x | marks.y | marks.z | marks.w) != 0;
-        if (anynan) find_nans<D, PT>(p, kv, it.req, it.head, it.t0 * TILE, min(end * TILE, it.L), lim, lane, nan);
+        // (end * TILE may pass 2^31 - 1 where L does not)
+        if (anynan)
+          find_nans<D, PT>(p, kv, it.req, it.head, it.t0 * TILE, end > it.L / TILE ? it.L : end * TILE, lim, lane, nan);
         // columns at a time: 16 keep the code small (per-token scales, head_dim 128: 931
         // us, 1040 with 32); head_dim 64 has registers for 32 (551 us, 590 with 16)
         constexpr int EC = D == 128 ? 16 : 32;

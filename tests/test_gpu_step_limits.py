@@ -272,6 +272,25 @@ def test_large_logits_that_differ_little(D, per_token, sign, size):
     assert np.all(np.abs(got - 0.75) <= 0.75 * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18))
 
 
+# ------------------------------------------------------------------ lengths
+def test_longest_request():
+    """2^31 - 16 tokens, all of one page but the last 16: the weights are equal and
+    their sums exact, and a NaN in the last token's V makes its dim NaN."""
+    bs, L = 16, (1 << 31) - 16
+    table = torch.zeros(1, L // bs, dtype=torch.int32, device=dev())
+    table[0, -1] = 1
+    cache = torch.zeros(2, 2, 1, bs, 64, dtype=torch.uint8, device=dev())
+    cache[:, 1] = 0x38                                  # 1
+    cache[1, 1, 0, 15, 5] = 0x7F
+    scale = torch.tensor([0.5], device=dev())
+    out = qpa.pa_chunk_fp8(torch.ones(1, 1, 64, dtype=torch.bfloat16, device=dev()), cache, table, _i32([0, 1]), _i32([L]),
+                           scale, scale, 1)
+    _clean()
+    want = torch.full((64,), 0.5)
+    want[5] = float("nan")
+    assert torch.equal(out.float().cpu().flatten().nan_to_num(9.0), want.nan_to_num(9.0))
+
+
 # ------------------------------------------------------------------ host
 def test_slot_maps_of_different_sizes_from_two_threads():
     """Calls with more than 5119 requests take more shared memory than a launch may
