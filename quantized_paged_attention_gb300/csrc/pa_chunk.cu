@@ -31,8 +31,8 @@
 //  * Per-token V scales: V enters as f16(scale 2^-e) times its codes, and the power of
 //    two 2^e goes into P, of which a row keeps a reference of its own: what f16 drops is
 //    small against the row's largest p times scale, whatever the tokens' scales are that it
-//    does not see or hardly weighs. A key tile has one e where its scales (but 0) lie
-//    within 2^7 or so; otherwise each token has its own and the tile takes the long way
+//    does not see or hardly weighs. A key tile has one e where its scales (but those of
+//    zeros) lie within 2^7 or so; otherwise each token has its own and the tile takes the long way
 //    (apart_tile).
 //  * Roles: 2 x 4 softmax warps (a thread owns one row: no exchange between
 //    lanes), one per row tile, so that the tensor core works for one while the
@@ -877,15 +877,16 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
           }
           // V enters as f16(v scale 2^(7-e)), below 2^7 (times 448: f16's range) for a
           // power of two 2^e above the scale, which goes into p: one for the tile if none of
-          // its scales (but 0) lies 2^kSpread further below, each token's own otherwise
+          // its scales lies 2^kSpread further below, each token's own otherwise. (Scales up to
+          // 2^-126 do not count: a token of zeros has that, and 448 times it is below 2^-117)
           hi = __reduce_max_sync(0xffffffffu, hi);
           auto pow2 = [](uint32_t x) { return max((int)(x >> 23) - 126, -119); };
           int e = pow2(hi);
           const uint32_t low = (uint32_t)(e + 126 - kSpread) << 23;   // 2^(e - 1 - kSpread)
           bool far = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) far = far || ax[i] - 1u < low - 1u;
-          const bool several = __any_sync(0xffffffffu, far && e > kSpread - 126);
+          for (int i = 0; i < 4; ++i) far = far || ax[i] - 0x00800001u < low - 0x00800001u;
+          const bool several = __any_sync(0xffffffffu, far && e > kSpread - 125);
           const int tk = 32 * cw + lane;
           const float kx = tk < live ? ldsf(sb + S::krawOff + 4 * (kb * TILE + tk)) : 0.f;
           stsf(sb + S::kscOff + 4 * (cb * TILE + tk), kx);

@@ -44,8 +44,8 @@ def _lib():
 
 
 def _reference(c, spread=7):
-    """(ref, tolerance), float64; rows of no request NaN."""
-    q = decode_bf16(c.q_bits)
+    """(ref, tolerance), float64, of the requests' rows."""
+    q = decode_bf16(c.q_bits)[:int(c.start[-1])]
     T, Hq, D = q.shape
     Hk = c.cache.shape[2]
     scale = D ** -0.5 if c.scale is None else c.scale
@@ -81,10 +81,14 @@ def _reference(c, spread=7):
 
 
 def _run(c):
+    """The requests' rows; those behind them are left as they were."""
     t = c.tensors()
-    out = qpa.pa_chunk_fp8(**t)
+    out = torch.full(tuple(t["q"].shape), 77.0, dtype=torch.bfloat16, device=dev())
+    qpa.pa_chunk_fp8(out=out, **t)
     _clean()
-    return out.double().cpu().numpy()
+    n = int(c.start[-1])
+    assert bool((out[n:] == 77).all())
+    return out[:n].double().cpu().numpy()
 
 
 def _check(c, spread=7):
@@ -204,6 +208,22 @@ def test_v_scales_that_differ_between_key_tiles(D, order):
 def test_v_scales_near_the_ends_of_float32(D, size):
     c = Chunk(48, [(20, 300), (1, 2000)], 2, 4, D, 16, True)
     c.vs *= np.float32(size)
+    _check(c)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_v_scales_of_zeros(D):
+    """Tokens whose V is 0, with the scale that kv_append_fp8 gives them, beside others
+    and alone; scales that small with codes beside others of their size."""
+    c = Chunk(54, [(40, 300), (20, 20), (30, 500)], 2, 4, D, 16, True)
+    r = synth.rng(55)
+    for req in (0, 1):
+        zero = np.arange(c.lens[req])[(r.random(c.lens[req]) < 0.5) | (req == 1)]
+        blk, off = _place(c, req, zero)
+        c.cache[blk, 1, :, off] = 0
+        c.vs[blk, :, off] = 2.0 ** -126
+    blk, off = _place(c, 2, np.arange(500))
+    c.vs[blk, :, off] = (2.0 ** r.uniform(-126, -115, (500, 2))).astype(np.float32)
     _check(c)
 
 
