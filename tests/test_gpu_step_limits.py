@@ -292,6 +292,17 @@ def test_large_logits_that_differ_little(D, per_token, sign, size):
     assert np.all(np.abs(got - 0.75) <= 0.75 * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18))
 
 
+# ------------------------------------------------------------------ batches
+@pytest.mark.parametrize("D,per_token", VARIANTS)
+def test_single_tokens_beside_a_chunk(D, per_token):
+    """One new token each of 60 requests over caches of 1 to 1500, two chunks among
+    them: more items than CTAs, cut between the heads and in the chunks."""
+    r = synth.rng(56)
+    reqs = [(1, int(n)) for n in r.integers(1, 1500, 60)]
+    reqs[17], reqs[40] = (200, 1400), (90, 90)
+    _check(Chunk(57, reqs, 3, 4, D, 32, per_token, pad=5))
+
+
 # ------------------------------------------------------------------ lengths
 def test_longest_request():
     """2^31 - 16 tokens, all of one page but the last 16: the weights are equal and
@@ -309,6 +320,30 @@ def test_longest_request():
     want = torch.full((64,), 0.5)
     want[5] = float("nan")
     assert torch.equal(out.float().cpu().flatten().nan_to_num(9.0), want.nan_to_num(9.0))
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("per_token", [False, True])
+def test_append_every_significand_of_a_scale(per_token):
+    """All 128 significands that a bf16 scale can have, per tensor and as the
+    largest element's, against all significands of 18 binades, both signs."""
+    sig = np.arange(128, 256) / 128
+    x = np.stack([np.concatenate([s * 2.0 ** -k for k in range(18)]) for s in (sig, -sig)]).reshape(1, -1)
+    for top in sig:
+        if per_token:        # 127 elements beside the largest
+            n = -(-x.size // 127)
+            y = np.zeros(n * 127)
+            y[:x.size] = x[0]
+            y[np.abs(y) > top] = 0
+            v = np.concatenate([np.full((n, 1), top), y.reshape(n, 127)], axis=1)
+            s = np.zeros((-(-n // 16), 1, 16), np.float32)
+        else:
+            v = x.reshape(-1, 128) * 2.0 ** 8
+            s = np.array([top], np.float32)
+        n = len(v)
+        bits = synth.round_to_bf16_bits(v).reshape(n, 1, 128)
+        cache = np.zeros((-(-n // 16), 2, 1, 16, 128), np.uint8)
+        _check_append(bits, bits[::-1].copy(), cache, np.arange(n, dtype=np.int64), s, s)
 
 
 # ------------------------------------------------------------------ host
