@@ -318,9 +318,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
   // 812 (64 single tokens, which one row tile computes, 318, 318, 300, 304); with
   // per-token scales, 1024 over 65536, 184/64/80 810, 192/64/64 825, 176/80/80 827;
   // head_dim 64, the same 184/88/56 502, 192/72/56 515, with per-token scales
-  // prompts 192/72/56 499, 184/80/64 519.
-  constexpr int REG_SOFTMAX = D == 128 ? (PT ? 184 : 168) : (PT ? 192 : 184);
-  constexpr int REG_CONV = D == 128 ? (PT ? 64 : 88) : (PT ? 72 : 88);
+  // 200/56/56 744 (prompts 512), 192/72/56 756 (525), 184/88/56 760 (510).
+  constexpr int REG_SOFTMAX = D == 128 ? (PT ? 184 : 168) : (PT ? 200 : 184);
+  constexpr int REG_CONV = D == 128 ? (PT ? 64 : 88) : (PT ? 56 : 88);
   constexpr int REG_REST = D == 128 ? (PT ? 80 : 88) : 56;
   static_assert(2 * REG_SOFTMAX + REG_CONV + REG_REST <= 512, "register budget");
   constexpr uint32_t T_O = 256, T_P = SEP ? 384 : 0, P_STEP = SEP ? 64 : 128;
@@ -662,9 +662,7 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
       const float xh = floorf(0.5f * (x - 7.f)), sv = PT ? ex2(x - 7.f - xh) : vscale;
       const float rl = none ? 0.f : PT ? __frcp_rn(l) * ex2(xh) : __frcp_rn(l);
       float* prow = p.part_o + ((long long)it.slot * p.part_rows + row) * D;
-      // (l of a row that sees no token is NaN if its query is not finite)
-      if (it.slot >= 0 && valid)
-        p.part_ml[(long long)it.slot * p.part_rows + row] = none ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
+      if (it.slot >= 0 && valid) p.part_ml[(long long)it.slot * p.part_rows + row] = make_float2(none ? -INFINITY : m, l);
       if (any) {
         // NaN codes in the item's V (none, as a rule) were taken out of the
         // products: look for them again and put NaN into the rows that see them
@@ -676,8 +674,8 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         const int4 marks = lds_i4(sb + S::flagOff + 16 * (k & 3));
         const bool anynan = (marks.x | marks.y | marks.z | marks.w) != 0;
         // (end * TILE may pass 2^31 - 1 where L does not)
-        if (anynan)
-          find_nans<D, PT>(p, kv, it.req, it.head, it.t0 * TILE, end > it.L / TILE ? it.L : end * TILE, lim, lane, nan);
+        const int last = (int)min((unsigned)end * TILE, (unsigned)it.L);
+        if (anynan) find_nans<D, PT>(p, kv, it.req, it.head, it.t0 * TILE, last, lim, lane, nan);
         // columns at a time: 16 keep the code small (per-token scales, head_dim 128: 931
         // us, 1040 with 32); head_dim 64 has registers for 32 (551 us, 590 with 16)
         constexpr int EC = D == 128 ? 16 : 32;
@@ -911,9 +909,9 @@ pa_chunk_kernel(const __grid_constant__ CUtensorMap kv_map, const uint8_t* kv, c
         const bool nf = PT && !(fabsf(vown) < INFINITY);
         const uint32_t vs16 = nf ? 0u : f32x2_to_f16x2(vown, vown);
         // a few steps at a time: fewer registers than all at once (per-token scales: 932
-        // us for 1024 over 65536 with all 8, 912 with 4; head_dim 64 502 with 1 of 4, 531
-        // with all, but without scales 517 with all, 538 with 2)
-        constexpr int NH = D == 128 ? 2 : PT ? 1 : NI;
+        // us for 1024 over 65536 with all 8, 912 with 4; head_dim 64 prompts 512 with 2 of 4,
+        // 517 with 1, but without scales 517 with all, 538 with 2)
+        constexpr int NH = D == 128 || PT ? 2 : NI;
 #pragma unroll 1
         for (int i0 = 0; i0 < NI; i0 += NH) {
           uint32_t bad = 0;
@@ -1327,7 +1325,8 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const Params p, cons
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        if (ml[u].y == 0.f) continue;                // the row saw no key of it, O is not written
+        // the row saw no key of it (l is not 0 but NaN then if the query is not finite)
+        if (ml[u].x == -INFINITY) continue;
         const float mn = fmaxf(M, ml[u].x);
         const float a0 = ex2(M - mn), w = ml[u].y * ex2(ml[u].x - mn);
         M = mn;
