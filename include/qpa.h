@@ -525,19 +525,20 @@ int kv_append_fp8(const void* k, const void* v, uint8_t* kv_cache, const int64_t
  * request's range are left as they were. Codes and scales of tokens that a
  * row does not see have no influence on it, NaN codes included.
  * Precision: each query row, scaled by a power of two, enters the tensor core
- * as 2 e4m3 terms (exact down to 2^-10 of the row's largest |q|, within 2^-18
- * of it below), K and V exactly; the probabilities enter as f16, scaled so that
- * one keeps its 11 bits down to 2^-21 of the row's largest and is within 2^-32 of
- * it below. Per-token V scales, and V scaled by them, are rounded to f16 without
- * their powers of two, which the probabilities take: those then keep 11 bits, and
- * the absolute error, against the row's largest probability times V scale (down to
- * 2^-13 of it, with an error of 2^-24 below, where scales of 128 tokens differ by
- * up to 2^8). Sums and softmax statistics are
- * float32. The output is bf16 only: probabilities of 11 bits would leave the
- * rest of a float32 output without meaning. A per-token V scale that is not
- * finite makes the rows that see its token NaN. Logits of 2^26 and more in
- * magnitude, where float32's steps exceed f16's range of probabilities, are outside
- * the supported range.
+ * as 2 e4m3 terms, exact down to 2^-9 of the row's largest |q| and within 2^-17 of
+ * it below; K and V enter exactly. The probabilities enter as f16, scaled so that
+ * one keeps 11 bits down to 2^-21 of the row's largest and is within 2^-32 of it
+ * below. Per-token V scales, without their powers of two, and V scaled by them are
+ * rounded to f16; the powers of two go into the probabilities, which are scaled by
+ * the row's largest probability times V scale then: 11 bits down to 2^-13 of that
+ * and within 2^-24 of it below (2^-20 and 2^-31 where the V scales lie within a
+ * factor of 2). Sums and softmax statistics are float32. The output is
+ * bf16 only: probabilities of 11 bits would leave the rest of a float32 output without
+ * meaning. A per-token V scale that is not finite makes the rows that see its token
+ * NaN. Scales of 128 tokens that differ by more than 2^8 take about four times
+ * as long (those of zeros, up to 2^-126, do not count). Logits of 2^26 and
+ * more in magnitude, where float32's steps exceed f16's range of probabilities,
+ * are outside the supported range.
  *
  * Layouts: q bf16 [num_tokens][num_kv_heads*query_group][head_dim] with the
  * descriptor's strides (elements, multiples of 8); out bf16, contiguous;

@@ -604,8 +604,8 @@ def pa_chunk_fp8(q, kv_cache, block_table, query_start, seq_lens, k_scale, v_sca
     it, see kv_append_fp8); block_table int32 [R, max_blocks]; query_start int32
     [R+1]; seq_lens int32 [R] counting the new tokens; k_scale / v_scale float32
     with one element or [NB, Hk, bs]. Returns out bf16 [T, Hq, D]; rows outside
-    every request's range are not written. `desc` (from chunk_desc for these
-    tensors) and `workspace` may be kept between calls."""
+    every request's range are not written. `workspace` may be kept between calls;
+    a `desc` (from chunk_desc) is compared with the tensors' own and saves no time."""
     NB, Hk, bs, _ = _cache_shape(kv_cache)
     per_token = _per_token_scales(NB, Hk, bs, k_scale, v_scale)
     if softmax_scale is None and desc is not None:

@@ -2,14 +2,16 @@
 //
 // A unit is the head vector of one (row, K or V, head): head_dim / 16 threads
 // take 16 elements each (32 bytes in, 16 bytes out). Bound: 4 bytes in and 2 out
-// per element pair. Measured (GB300): 16384 tokens x 8 heads x 128 in 20 us, 5.1
-// TB/s (25 us after other work has filled L2), 22.5 us with per-token scales;
-// 5003 tokens x 8 heads x 64 with per-token scales 9 us, half of it the launch.
+// per element pair. Measured (GB300), 16384 tokens x 8 heads x 128: 22 us a call on
+// fresh inputs, 4.5 TB/s, 17 on the same ones (21 with per-token scales), 18.5 under
+// ncu; 5003 tokens x 8 heads x 64 with per-token scales 4.4 us in a graph of 20, 8
+// under ncu.
 //
 // Rounding. The code is the nearest e4m3 value of the exact quotient x / s, a tie
 // going to the even code. Midpoints between codes have a significand m of 5 bits
-// at most, x has 8. With q = x hi + x lo, hi + lo = 1/s to 2^-40, a quotient that
-// is a midpoint comes out as that midpoint, and one that is 2^-18 of it away or
+// at most, x has 8. With q = x hi + x lo, hi + lo = 1/s to 2^-40, rounded once (an
+// fma takes x hi exactly), a quotient that is a midpoint comes out as that
+// midpoint, and one that is 2^-18 of it away or
 // more stays on its side. One in between, x = m s (1 - d) with 0 < |d| < 2^-18,
 // could end on the wrong side. But all of them have the same d for a given s:
 // s (1 - d) = x / m, and two such quotients of 8 and 5 bits are equal or 2^-13
@@ -109,7 +111,7 @@ __device__ __forceinline__ void amax2(uint32_t& m, uint32_t w) {
 // amax / 448 rounded to nearest, at least 2^-126 (infinity as the largest bf16)
 __device__ __forceinline__ Scale token_scale(float m) {
   m = fminf(m, 3.38953139e38f);
-  // 1/448 as two floats; the quotient of 8 bits by 7 is no closer than 1/7 of a
+  // 1/448 as two floats; the quotient of 8 bits by 7 is no closer than 1/14 of a
   // unit to where the rounding would turn, and this sum is within 2^-20 units
   float s = fmaf(m, 0.00223214295692741870880126953125f, m * -9.97845626e-11f);
   if (m < 8.2718e-25f) s = fmaxf(__fdiv_rn(m, 448.f), 1.17549435e-38f);    // 2^-80: the second part leaves the normals

@@ -48,14 +48,18 @@
 // maximum comes with the load of S from tensor memory, its exponentials take the
 // special function unit 512 clocks, twice) and P V follow one another, and only
 // the other row tile's chain overlaps them. Tensor memory is full (S and O of
-// both), so a third chain does not fit. Per-token scales add 1024 clocks of shared
-// memory reads per key tile, a scale per score of each of 8 warps.
-// Measured (GB300): 1024 new tokens over 65536, 8 x 4 heads of 128, 709 us, 1.56
-// PFLOP/s, 81 % of the measured bf16 rate, with per-token scales 810; a prompt of
-// 8192, 8 x 8 heads, 785 us, 1.40 PFLOP/s (5 us between items); 64 single tokens
-// over 1024..16384 318 us, 3.5 TB/s; head_dim 64, 1024 over 65536 500 us, 1.1
-// PFLOP/s, with per-token scales 740. Between items: the query rows' copies 2.5 us,
-// row tile 0's operand 2, its S and softmax 1.
+// both), so a third chain does not fit. What per-token scales cost was measured in
+// parts: without the K scales' loads (a scale per score, by each of 8 warps) 1.4 to
+// 4 %, without multiplying by them and the maximum from registers another 0 to 12 %
+// (head_dim 64 over a long context); with head_dim 64 no unit is over 39 % busy, and
+// what else holds it back has not been taken apart.
+// Measured (GB300), calls in a row, and with pauses between them (the power limit is
+// not reached then): 1024 new tokens over 65536, 8 x 4 heads of 128, 776 us, 1.43
+// PFLOP/s, 74 % of the measured bf16 rate (711 us), with per-token scales (810 to 824
+// us); a prompt of 8192, 8 x 8 heads, 822 us, 1.34 PFLOP/s (784 us; 5 us between
+// items); 64 single tokens over 1024..16384 302 us, 3.5 TB/s; head_dim 64, 1024 over
+// 65536 (497 us, 1.1 PFLOP/s), with per-token scales (744 us). Between items: the query
+// rows' copies 2.5 us, row tile 0's operand 2, its S and softmax 1.
 // Tried and slower: both row tiles' pipelines on alternate key tiles of an item
 // that has 128 rows at most, and its next S in the idle row tile's buffer (the
 // registers cost every other case 10 to 18 % and such items gained nothing: their
