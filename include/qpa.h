@@ -577,6 +577,140 @@ int pa_chunk_fp8(const void* q, const uint8_t* kv_cache, const int32_t* block_ta
                  const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* out,
                  const qpa_chunk_desc* d, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ========================================================================
+ * The 4-bit (NVFP4) paged cache: kv_append_nvfp4, kv_gather_nvfp4,
+ * pa_decode_nvfp4
+ *
+ * kv_cache uint8 [num_blocks][planes][num_kv_heads] chunks of
+ * block_size * (head_dim/2 + head_dim/16) bytes; plane 0 holds K, plane 1 V. A
+ * chunk is block_size * head_dim/2 bytes of e2m1 codes (head_dim/2 per token,
+ * dim 2i in the low nibble of byte i), then block_size * head_dim/16 e4m3fn
+ * scales (head_dim/16 per token, one per 16 dims). A value is
+ *     e2m1(code) * e4m3(scale) * g,    g = k_scale[0] or v_scale[0] (float, device).
+ * With head_dim 128, block_size 128, one plane and one head a chunk is a page of
+ * nvfp4_index_score (which knows no g: append with k_scale = 1).
+ * ====================================================================== */
+
+/* ------------------------------------------------------------------------
+ * kv_append_nvfp4 -- new keys and values quantised into the 4-bit pages
+ *
+ * For every row t with slots[t] >= 0, plane, KV head h and group of 16 dims, with
+ * x the group's values and a = max|x| (an infinity counts as the largest bf16):
+ *     s = max(e4m3(a / (6 g)), 2^-9),   code = e2m1(x / (s g)),
+ * where e4m3() and e2m1() are the nearest values of the exact quotients, ties to
+ * the even code, saturating at 448 and +-6. A group that holds a NaN, and every
+ * group if g is not positive and finite, gets the scale byte 0x7F (NaN) and codes
+ * 0, so that it reads as NaN.
+ * Rows with a negative slot are skipped; a slot at or past num_blocks *
+ * block_size is skipped and raises error word 3. Nothing else in the cache is
+ * written. Rows that share a slot: which one's bytes end there is not defined.
+ *
+ * Layouts: k, v bf16 [num_tokens][num_kv_heads][head_dim] with the strides of the
+ * descriptor (elements, multiples of 8); slots int64 [num_tokens] (as
+ * paged_slot_map writes). planes = 1: keys only, v and v_scale are ignored.
+ * kv_cache may overlap nothing else (QPA_ERR_OVERLAP).
+ * Supported: head_dim 64 or 128, block_size 16/32/64/128/256, num_kv_heads up to
+ * 65536. Alignment: k, v and kv_cache 16 bytes, slots 8, scales 4 bytes.
+ * ---------------------------------------------------------------------- */
+typedef struct qpa_nvfp4_append_desc {
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t planes;               /* 2 = K and V, 1 = K only */
+  int64_t k_stride_tok;         /* elements; 0 = num_kv_heads*head_dim */
+  int64_t k_stride_head;        /* elements; 0 = head_dim */
+  int64_t v_stride_tok;
+  int64_t v_stride_head;
+} qpa_nvfp4_append_desc;
+
+int kv_append_nvfp4(const void* k, const void* v, uint8_t* kv_cache, const int64_t* slots, const float* k_scale,
+                    const float* v_scale, const qpa_nvfp4_append_desc* d, void* stream);
+
+/* ------------------------------------------------------------------------
+ * kv_gather_nvfp4, kv_gather_fp8 -- tokens read back from the pages
+ *
+ * Request r owns the output rows query_start[r] .. query_start[r+1] - 1 (n of
+ * them): the last n of its L = seq_lens[r] cached tokens, row i being token
+ * L - n + i (all of them with n = L, a step's new ones with n = new_lens[r]).
+ *     out_k[row][h][d] = the value of K at (token, h, d), rounded once;
+ * likewise out_v. Rows of a token below 0 are 0; rows outside every request's
+ * range are left as they were. The fp8 cache is the one of kv_append_fp8, with
+ * scales per tensor or per token (kv_scale_per_token).
+ *
+ * Layouts: out_k, out_v [num_tokens][num_kv_heads][head_dim], float32 or bf16 per
+ * out_dtype, contiguous; block_table int32, row r at r * table_stride elements;
+ * query_start int32 [num_reqs+1], not decreasing, clamped to [0, num_tokens]; seq_lens int32
+ * [num_reqs], clamped to [0, max_blocks_per_seq*block_size]. planes = 1: out_v
+ * and v_scale are ignored. An invalid block id reads block 0 and raises error
+ * word 3. out_k and out_v may overlap nothing else (QPA_ERR_OVERLAP).
+ * Supported: as kv_append_nvfp4. Alignment: kv_cache and outputs 16 bytes.
+ * ---------------------------------------------------------------------- */
+typedef struct qpa_gather_desc {
+  int32_t num_reqs;
+  int32_t num_tokens;           /* rows of out_k and out_v */
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t max_blocks_per_seq;
+  int32_t planes;               /* 2 = K and V, 1 = K only */
+  int32_t kv_scale_per_token;   /* fp8: 0 = per-tensor, 1 = per-token; NVFP4: 0 */
+  int32_t out_dtype;            /* QPA_OUT_F32 or QPA_OUT_BF16 */
+  int64_t table_stride;         /* elements; 0 = max_blocks_per_seq */
+} qpa_gather_desc;
+
+int kv_gather_nvfp4(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* query_start,
+                    const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* out_k, void* out_v,
+                    const qpa_gather_desc* d, void* stream);
+int kv_gather_fp8(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* query_start,
+                  const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* out_k, void* out_v,
+                  const qpa_gather_desc* d, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_decode_nvfp4 -- attention of one new token per sequence over the 4-bit pages
+ *
+ * For every sequence s (length L = seq_lens[s], the new token counted), KV head h
+ * and query row g (query head h*query_group + g):
+ *     out = sum_t softmax_t(softmax_scale * q . k_t) v_t,   t = 0 .. L-1,
+ * with k_t and v_t the values of the 4-bit cache (planes = 2). L = 0 gives 0.
+ * Codes and scales of tokens past L have no influence, NaN scales included; a NaN
+ * scale of a token that is seen makes the rows of its sequence and head NaN (a V
+ * scale: the 16 dims of its group).
+ *
+ * Layouts: q bf16 [num_seqs][num_kv_heads*query_group][head_dim] with the
+ * descriptor's strides (elements, multiples of 8); out bf16, contiguous;
+ * block_table int32, row s at s * table_stride elements, only entries below
+ * ceil(L/block_size) are read; seq_lens int32 [num_seqs], clamped to
+ * [0, max_blocks_per_seq*block_size]. workspace: pa_decode_nvfp4_workspace_size()
+ * bytes, 256-byte aligned, no initialisation; calls that may overlap need a
+ * workspace each.
+ * Supported: head_dim 64 or 128, query_group 1..64, block_size 16/32/64/128/256.
+ * Alignment: q, kv_cache, out 16 bytes. out and workspace may overlap neither each
+ * other nor an input (QPA_ERR_OVERLAP). Errors as pa_decode_fp8; an invalid block id
+ * reads block 0 and raises error word 3.
+ * ---------------------------------------------------------------------- */
+typedef struct qpa_nvfp4_desc {
+  int32_t num_seqs;
+  int32_t num_kv_heads;
+  int32_t query_group;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t max_blocks_per_seq;
+  float softmax_scale;          /* 0 = 1/sqrt(head_dim) */
+  int64_t q_stride_seq;         /* elements; 0 = num_kv_heads*query_group*head_dim */
+  int64_t q_stride_head;        /* elements; 0 = head_dim */
+  int64_t table_stride;         /* elements; 0 = max_blocks_per_seq */
+} qpa_nvfp4_desc;
+
+size_t pa_decode_nvfp4_workspace_size(const qpa_nvfp4_desc* d);
+
+int pa_decode_nvfp4(const void* q, const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                    const float* k_scale, const float* v_scale, void* out, const qpa_nvfp4_desc* d, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -31,3 +31,4 @@ from .uq import (decode_uq_slots, perm_dest, perm_source, rotate_q_fp32, rotatio
                  uq_decode_hd256, wht_matrix)
 from .scorer import nvfp4_index_score, nvfp4_index_score_per_token, nvfp4_token_dots  # noqa: F401
 from .step import e4m3_nearest, kv_append_fp8, pa_chunk_fp8, paged_slot_map, token_scale  # noqa: F401
+from .nvfp4 import gather_rows, kv_append_nvfp4, pa_decode_nvfp4, quantise_nvfp4, values_nvfp4  # noqa: F401

@@ -93,6 +93,29 @@ class ChunkDesc(ctypes.Structure):
                 ("table_stride", ctypes.c_int64)]
 
 
+class Append4Desc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32), ("planes", ctypes.c_int32),
+                ("k_stride_tok", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+                ("v_stride_tok", ctypes.c_int64), ("v_stride_head", ctypes.c_int64)]
+
+
+class GatherDesc(ctypes.Structure):
+    _fields_ = [("num_reqs", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("max_blocks_per_seq", ctypes.c_int32), ("planes", ctypes.c_int32),
+                ("kv_scale_per_token", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("table_stride", ctypes.c_int64)]
+
+
+class Nvfp4Desc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("query_group", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("max_blocks_per_seq", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("q_stride_seq", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _SIGS = {
     "qpa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -123,6 +146,12 @@ _SIGS = {
     "pa_chunk_fp8_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(ChunkDesc)]),
     "pa_chunk_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(ChunkDesc), _P,
                                     ctypes.c_size_t, _P]),
+    "kv_append_nvfp4": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.POINTER(Append4Desc), _P]),
+    "kv_gather_nvfp4": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(GatherDesc), _P]),
+    "kv_gather_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(GatherDesc), _P]),
+    "pa_decode_nvfp4_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Nvfp4Desc)]),
+    "pa_decode_nvfp4": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(Nvfp4Desc), _P, ctypes.c_size_t,
+                                       _P]),
 }
 
 
@@ -629,4 +658,185 @@ def pa_chunk_fp8(q, kv_cache, block_table, query_start, seq_lens, k_scale, v_sca
     _launch("pa_chunk_fp8", index, stream, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
             query_start.data_ptr(), seq_lens.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(),
             ctypes.byref(want), workspace.data_ptr(), workspace.nbytes)
+    return out
+
+
+# --------------------------------------------------------------------- 4-bit (NVFP4) cache, reading back
+def nvfp4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int, planes: int = 2):
+    """Shape of a 4-bit cache, uint8: a (block, plane, head) holds block_size *
+    head_dim/2 bytes of codes and then block_size * head_dim/16 scales."""
+    return num_blocks, planes, num_kv_heads, block_size, head_dim // 2 + head_dim // 16
+
+
+def _cache4_shape(kv_cache):
+    """(num_blocks, planes, num_kv_heads, block_size, head_dim) of a 4-bit cache."""
+    if kv_cache.dtype != torch.uint8 or kv_cache.dim() != 5 or kv_cache.shape[1] not in (1, 2) or \
+            kv_cache.shape[4] % 9 or not kv_cache.is_contiguous():
+        _fail("kv_cache must be contiguous uint8 [num_blocks, 2 or 1, num_kv_heads, block_size, 9*head_dim/16]")
+    NB, planes, Hk, bs, row = kv_cache.shape
+    return NB, planes, Hk, bs, row // 9 * 16
+
+
+def _one_scale(scale):
+    if scale.dtype != torch.float32 or scale.numel() != 1:
+        _fail("k_scale and v_scale must be float32 with one element")
+
+
+def kv_append_nvfp4(k, v, kv_cache, slots, k_scale, v_scale, stream=None):
+    """Quantise new keys and values into the paged 4-bit cache, in place.
+
+    k, v bf16 [T, Hk, D] (slices of a fused projection allowed); kv_cache uint8 of
+    nvfp4_cache_shape(); slots int64 [T], negative = skip the row; k_scale / v_scale
+    float32 with one element. A cache with one plane takes keys only: v and v_scale
+    None (with D 128, block size 128, one head and k_scale 1 its blocks are the pages
+    of nvfp4_index_score). Returns kv_cache."""
+    NB, planes, Hk, bs, D = _cache4_shape(kv_cache)
+    T = slots.numel()
+    if slots.dtype != torch.int64 or not slots.is_contiguous():
+        _fail("slots must be contiguous int64")
+    if (planes == 2) != (v is not None) or (v is None) != (v_scale is None):
+        _fail("v and v_scale go with a cache of two planes, and only with one")
+    if k.dtype != torch.bfloat16 or tuple(k.shape) != (T, Hk, D) or (T and k.stride(2) != 1):
+        _fail("k must be bfloat16 [num_tokens, num_kv_heads, head_dim], a row per slot, contiguous along head_dim")
+    _one_scale(k_scale)
+    if v is not None:
+        if v.dtype != torch.bfloat16 or tuple(v.shape) != (T, Hk, D) or (T and v.stride(2) != 1):
+            _fail("v must be bfloat16 [num_tokens, num_kv_heads, head_dim], a row per slot, contiguous along head_dim")
+        _one_scale(v_scale)
+        index = _device_of(k, v, kv_cache, slots, k_scale, v_scale)
+        vp, vsp, vt, vh = v.data_ptr(), v_scale.data_ptr(), _dim_stride(v, 0), _dim_stride(v, 1)
+    else:
+        index = _device_of(k, kv_cache, slots, k_scale)
+        vp = vsp = vt = vh = 0
+    _below_2_31(T, Hk, NB)
+    d = Append4Desc(T, Hk, D, bs, NB, planes, _dim_stride(k, 0), _dim_stride(k, 1), vt, vh)
+    _launch("kv_append_nvfp4", index, stream, k.data_ptr(), vp, kv_cache.data_ptr(), slots.data_ptr(),
+            k_scale.data_ptr(), vsp, ctypes.byref(d))
+    return kv_cache
+
+
+def _below_2_31(*sizes):
+    # (ctypes cuts a number to its field's 32 bits without a word)
+    for n in sizes:
+        if not 0 <= n < 1 << 31:
+            _fail("sizes must be below 2^31 and not negative")
+
+
+def _gather(fn, shape, per_token, kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, num_tokens, out_k,
+            out_v, out_dtype, stream):
+    NB, planes, Hk, bs, D = shape
+    maxb, stride = _rows(block_table)
+    R = block_table.shape[0]
+    i32 = torch.int32
+    if query_start.dtype != i32 or seq_lens.dtype != i32 or not query_start.is_contiguous() or \
+            not seq_lens.is_contiguous() or query_start.numel() != R + 1 or seq_lens.numel() != R:
+        _fail("query_start must be contiguous int32 with one entry more than requests, seq_lens with one per request")
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        _fail("out_dtype must be bfloat16 or float32")
+    _below_2_31(num_tokens, NB, Hk)
+    rows = (num_tokens, Hk, D)
+    for o in (out_k, out_v):
+        if o is not None and (o.dtype != out_dtype or tuple(o.shape) != rows or not o.is_contiguous()):
+            _fail("outputs must be contiguous [num_tokens, num_kv_heads, head_dim] of out_dtype")
+    if out_k is None:
+        out_k = _empty(rows, out_dtype, kv_cache.device, stream)
+    if planes == 2 and out_v is None:
+        out_v = _empty(rows, out_dtype, kv_cache.device, stream)
+    if planes == 1 and (out_v is not None or v_scale is not None):
+        _fail("a cache of one plane holds no values: out_v and v_scale must be None")
+    if planes == 2:
+        index = _device_of(kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, out_k, out_v)
+        vp, op = v_scale.data_ptr(), out_v.data_ptr()
+    else:
+        index = _device_of(kv_cache, block_table, query_start, seq_lens, k_scale, out_k)
+        vp = op = 0
+    d = GatherDesc(R, num_tokens, Hk, D, bs, NB, maxb, planes, 1 if per_token else 0,
+                   QPA_OUT_F32 if out_dtype is torch.float32 else QPA_OUT_BF16, stride)
+    _launch(fn, index, stream, kv_cache.data_ptr(), block_table.data_ptr(), query_start.data_ptr(),
+            seq_lens.data_ptr(), k_scale.data_ptr(), vp, out_k.data_ptr(), op, ctypes.byref(d))
+    return out_k, out_v
+
+
+def kv_gather_nvfp4(kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, num_tokens: int, out_k=None,
+                    out_v=None, out_dtype=torch.bfloat16, stream=None):
+    """Tokens read back from the paged 4-bit cache.
+
+    Request r owns the output rows query_start[r] .. query_start[r+1] - 1: the last
+    so many of its seq_lens[r] tokens. kv_cache uint8 of nvfp4_cache_shape();
+    block_table int32 [R, max_blocks]; query_start int32 [R+1]; seq_lens int32 [R];
+    k_scale / v_scale float32 with one element. Returns (k, v), bf16 or float32
+    [num_tokens, Hk, D] each (v None with a cache of one plane); rows of no request
+    are not written."""
+    shape = _cache4_shape(kv_cache)
+    _one_scale(k_scale)
+    if shape[1] == 2:
+        if v_scale is None:
+            _fail("v_scale is missing")
+        _one_scale(v_scale)
+    return _gather("kv_gather_nvfp4", shape, False, kv_cache, block_table, query_start, seq_lens, k_scale, v_scale,
+                   num_tokens, out_k, out_v, out_dtype, stream)
+
+
+def kv_gather_fp8(kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, num_tokens: int, out_k=None,
+                  out_v=None, out_dtype=torch.bfloat16, stream=None):
+    """kv_gather_nvfp4 for the paged fp8 cache: kv_cache uint8 [NB, 2, Hk, bs, D];
+    k_scale / v_scale float32 with one element or [NB, Hk, bs] (per token)."""
+    NB, Hk, bs, D = _cache_shape(kv_cache)
+    per_token = _per_token_scales(NB, Hk, bs, k_scale, v_scale)
+    return _gather("kv_gather_fp8", (NB, 2, Hk, bs, D), per_token, kv_cache, block_table, query_start, seq_lens,
+                   k_scale, v_scale, num_tokens, out_k, out_v, out_dtype, stream)
+
+
+def nvfp4_desc(q, kv_cache, block_table, query_group, softmax_scale=None):
+    """Descriptor of pa_decode_nvfp4 for q bf16 [B, Hq, D]."""
+    NB, planes, Hk, bs, D = _cache4_shape(kv_cache)
+    if planes != 2:
+        _fail("kv_cache must have two planes, keys and values")
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[1] != Hk * query_group or q.shape[2] != D:
+        _fail("q must be bfloat16 [num_seqs, num_kv_heads*query_group, head_dim]")
+    B = q.shape[0]
+    if B and q.stride(2) != 1:
+        _fail("q must be contiguous along head_dim")
+    maxb, stride = _rows(block_table)
+    if block_table.shape[0] != B:
+        _fail("block_table must have one row per sequence")
+    _below_2_31(B, NB, Hk, query_group)
+    return Nvfp4Desc(B, Hk, query_group, D, bs, NB, maxb, 0.0 if softmax_scale is None else float(softmax_scale),
+                     _dim_stride(q, 0), _dim_stride(q, 1), stride)
+
+
+def pa_decode_nvfp4_workspace_size(desc: Nvfp4Desc) -> int:
+    return int(load_library().pa_decode_nvfp4_workspace_size(ctypes.byref(desc)))
+
+
+def pa_decode_nvfp4(q, kv_cache, block_table, seq_lens, k_scale, v_scale, query_group: int, out=None, workspace=None,
+                    softmax_scale=None, stream=None, desc=None):
+    """Attention of one new token per sequence over the paged 4-bit cache.
+
+    q bf16 [B, Hq, D]; kv_cache uint8 of nvfp4_cache_shape() (the new token is in it,
+    see kv_append_nvfp4); block_table int32 [B, max_blocks]; seq_lens int32 [B];
+    k_scale / v_scale float32 with one element. Returns out bf16 [B, Hq, D].
+    `workspace` may be kept between calls; a `desc` (from nvfp4_desc) is compared with
+    the tensors' own and saves no time."""
+    if softmax_scale is None and desc is not None:
+        softmax_scale = desc.softmax_scale
+    want = nvfp4_desc(q, kv_cache, block_table, query_group, softmax_scale)
+    if desc is not None and bytes(desc) != bytes(want):
+        _fail("desc does not describe these tensors")
+    _one_scale(k_scale)
+    _one_scale(v_scale)
+    if seq_lens.dtype != torch.int32 or not seq_lens.is_contiguous() or seq_lens.numel() != want.num_seqs:
+        _fail("seq_lens must be contiguous int32 with one entry per sequence")
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
+        _fail("out must be contiguous bfloat16 of the shape of q")
+    if workspace is None:
+        workspace = _empty(max(pa_decode_nvfp4_workspace_size(want), 256), torch.uint8, q.device, stream)
+    elif not workspace.is_contiguous():
+        _fail("workspace must be contiguous")
+    index = _device_of(q, kv_cache, block_table, seq_lens, k_scale, v_scale, out, workspace)
+    _launch("pa_decode_nvfp4", index, stream, q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
+            seq_lens.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(), ctypes.byref(want),
+            workspace.data_ptr(), workspace.nbytes)
     return out

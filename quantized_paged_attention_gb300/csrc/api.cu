@@ -212,6 +212,82 @@ bool chunk_shape_ok(const qpa_chunk_desc* d) {
   return true;
 }
 
+// ------------------------------------------------------------------ 4-bit cache, reading back
+bool append4_shape_ok(const qpa_nvfp4_append_desc* d) {
+  if (d->num_tokens < 0 || d->num_kv_heads < 1 || (d->head_dim != 64 && d->head_dim != 128)) return false;
+  if (!block_size_ok(d->block_size) || d->num_blocks < 1 || (d->planes != 1 && d->planes != 2)) return false;
+  return d->num_kv_heads <= kMaxHeads;
+}
+
+bool gather_shape_ok(const qpa_gather_desc* d) {
+  if (d->num_reqs < 0 || d->num_tokens < 0 || d->num_kv_heads < 1 || d->num_kv_heads > kMaxHeads) return false;
+  if ((d->head_dim != 64 && d->head_dim != 128) || !block_size_ok(d->block_size)) return false;
+  if (d->num_blocks < 1 || d->max_blocks_per_seq < 1 || (d->planes != 1 && d->planes != 2)) return false;
+  if (d->out_dtype != QPA_OUT_F32 && d->out_dtype != QPA_OUT_BF16) return false;
+  if (d->kv_scale_per_token != 0 && d->kv_scale_per_token != 1) return false;
+  if (d->table_stride != 0 && d->table_stride < d->max_blocks_per_seq) return false;
+  return (long long)d->max_blocks_per_seq * d->block_size <= 0x7fffffffLL;
+}
+
+// bytes of a 4-bit cache
+size_t cache4_bytes(long long blocks, long long planes, long long heads, int bs, int dim) {
+  return size_t(blocks) * planes * heads * bs * (dim / 2 + dim / 16);
+}
+
+int gather_check(bool fp4, const uint8_t* kv, const int32_t* bt, const int32_t* qs, const int32_t* sl, const float* ks,
+                 const float* vs, void* out_k, void* out_v, const qpa_gather_desc* d, GatherLaunch& a) {
+  if (!d) return QPA_ERR_NULL;
+  if (!gather_shape_ok(d) || (fp4 && d->kv_scale_per_token)) return QPA_ERR_SHAPE;
+  a.num_tokens = 0;
+  if (d->num_reqs == 0 || d->num_tokens == 0) return QPA_OK;
+  const bool v = d->planes == 2;
+  if (!kv || !bt || !qs || !sl || !ks || !out_k || (v && (!vs || !out_v))) return QPA_ERR_NULL;
+  if (!aligned(kv, 16) || !aligned(out_k, 16) || !aligned(bt, 4) || !aligned(qs, 4) || !aligned(sl, 4) || !aligned(ks, 4))
+    return QPA_ERR_ALIGN;
+  if (v && (!aligned(out_v, 16) || !aligned(vs, 4))) return QPA_ERR_ALIGN;
+  a.table_stride = d->table_stride ? d->table_stride : d->max_blocks_per_seq;
+  const size_t slots = size_t(d->num_blocks) * d->num_kv_heads * d->block_size;
+  const size_t sn = d->kv_scale_per_token ? slots * 4 : 4;
+  const size_t on = size_t(d->num_tokens) * d->num_kv_heads * d->head_dim * (d->out_dtype == QPA_OUT_F32 ? 4 : 2);
+  const Span in[] = {{kv, fp4 ? cache4_bytes(d->num_blocks, d->planes, d->num_kv_heads, d->block_size, d->head_dim)
+                              : slots * d->planes * d->head_dim},
+                     {bt, (size_t(d->num_reqs - 1) * a.table_stride + d->max_blocks_per_seq) * 4},
+                     {qs, size_t(d->num_reqs) * 4 + 4}, {sl, size_t(d->num_reqs) * 4}, {ks, sn}, {vs, v ? sn : 0}};
+  const Span outs[] = {{out_k, on}, {out_v, v ? on : 0}};
+  if (overlap(outs, in)) return QPA_ERR_OVERLAP;
+  a.kv = kv;
+  a.block_table = bt;
+  a.query_start = qs;
+  a.seq_lens = sl;
+  a.k_scale = ks;
+  a.v_scale = v ? vs : ks;
+  a.out_k = out_k;
+  a.out_v = v ? out_v : out_k;
+  a.num_reqs = d->num_reqs;
+  a.num_tokens = d->num_tokens;
+  a.num_kv_heads = d->num_kv_heads;
+  a.head_dim = d->head_dim;
+  a.block_size = d->block_size;
+  a.num_blocks = d->num_blocks;
+  a.max_blocks = d->max_blocks_per_seq;
+  a.planes = d->planes;
+  a.fp4 = fp4;
+  a.per_token = d->kv_scale_per_token;
+  a.out_f32 = d->out_dtype == QPA_OUT_F32;
+  a.num_sms = num_sms_current();
+  return a.num_sms > 0 ? QPA_OK : QPA_ERR_CUDA;
+}
+
+bool decode4_shape_ok(const qpa_nvfp4_desc* d) {
+  if (d->num_seqs < 0 || d->num_kv_heads < 1 || d->num_kv_heads > kMaxHeads) return false;
+  if (d->query_group < 1 || d->query_group > 64 || (d->head_dim != 64 && d->head_dim != 128)) return false;
+  if (!block_size_ok(d->block_size) || d->num_blocks < 1 || d->max_blocks_per_seq < 1) return false;
+  if (d->table_stride != 0 && d->table_stride < d->max_blocks_per_seq) return false;
+  if ((long long)d->max_blocks_per_seq * d->block_size > 0x7fffffffLL) return false;
+  // (sequence, query head) rows are counted in 32 bits
+  return (long long)d->num_seqs * d->num_kv_heads * d->query_group <= 0x7fffffffLL;
+}
+
 }  // namespace
 }  // namespace qpa
 
@@ -651,6 +727,113 @@ int pa_chunk_fp8(const void* q, const uint8_t* kv_cache, const int32_t* block_ta
   a.num_sms = num_sms_current();
   if (a.num_sms <= 0) return QPA_ERR_CUDA;
   return launch_chunk(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QPA_OK : QPA_ERR_CUDA;
+}
+
+int kv_append_nvfp4(const void* k, const void* v, uint8_t* kv_cache, const int64_t* slots, const float* k_scale,
+                    const float* v_scale, const qpa_nvfp4_append_desc* d, void* stream) {
+  if (!d) return QPA_ERR_NULL;
+  if (!append4_shape_ok(d)) return QPA_ERR_SHAPE;
+  if (d->num_tokens == 0) return QPA_OK;
+  const bool two = d->planes == 2;
+  if (!k || !kv_cache || !slots || !k_scale || (two && (!v || !v_scale))) return QPA_ERR_NULL;
+  Append4Launch a;
+  const long long row = (long long)d->num_kv_heads * d->head_dim;
+  a.k_stride_tok = d->k_stride_tok ? d->k_stride_tok : row;
+  a.v_stride_tok = d->v_stride_tok ? d->v_stride_tok : row;
+  a.k_stride_head = d->k_stride_head ? d->k_stride_head : d->head_dim;
+  a.v_stride_head = d->v_stride_head ? d->v_stride_head : d->head_dim;
+  for (long long s : {a.k_stride_tok, a.v_stride_tok, a.k_stride_head, a.v_stride_head})
+    if (s < 0 || s % 8) return QPA_ERR_ALIGN;
+  if (!aligned(k, 16) || !aligned(kv_cache, 16) || !aligned(slots, 8) || !aligned(k_scale, 4)) return QPA_ERR_ALIGN;
+  if (two && (!aligned(v, 16) || !aligned(v_scale, 4))) return QPA_ERR_ALIGN;
+  const Span in[] = {{k, extent(d->num_tokens, d->num_kv_heads, d->head_dim, a.k_stride_tok, a.k_stride_head)},
+                     {v, two ? extent(d->num_tokens, d->num_kv_heads, d->head_dim, a.v_stride_tok, a.v_stride_head) : 0},
+                     {slots, size_t(d->num_tokens) * 8}, {k_scale, 4}, {v_scale, size_t(two ? 4 : 0)}};
+  const Span outs[] = {{kv_cache, cache4_bytes(d->num_blocks, d->planes, d->num_kv_heads, d->block_size, d->head_dim)}};
+  if (overlap(outs, in)) return QPA_ERR_OVERLAP;
+  a.k = k;
+  a.v = two ? v : k;
+  a.kv = kv_cache;
+  a.slots = slots;
+  a.k_scale = k_scale;
+  a.v_scale = two ? v_scale : k_scale;
+  a.num_tokens = d->num_tokens;
+  a.num_kv_heads = d->num_kv_heads;
+  a.head_dim = d->head_dim;
+  a.block_size = d->block_size;
+  a.num_blocks = d->num_blocks;
+  a.planes = d->planes;
+  a.num_sms = num_sms_current();
+  if (a.num_sms <= 0) return QPA_ERR_CUDA;
+  return launch_append4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QPA_OK : QPA_ERR_CUDA;
+}
+
+int kv_gather_nvfp4(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* query_start,
+                    const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* out_k, void* out_v,
+                    const qpa_gather_desc* d, void* stream) {
+  GatherLaunch a;
+  const int st = gather_check(true, kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, out_k, out_v, d, a);
+  if (st != QPA_OK || a.num_tokens == 0) return st;
+  return launch_gather(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QPA_OK : QPA_ERR_CUDA;
+}
+
+int kv_gather_fp8(const uint8_t* kv_cache, const int32_t* block_table, const int32_t* query_start,
+                  const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* out_k, void* out_v,
+                  const qpa_gather_desc* d, void* stream) {
+  GatherLaunch a;
+  const int st = gather_check(false, kv_cache, block_table, query_start, seq_lens, k_scale, v_scale, out_k, out_v, d, a);
+  if (st != QPA_OK || a.num_tokens == 0) return st;
+  return launch_gather(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QPA_OK : QPA_ERR_CUDA;
+}
+
+size_t pa_decode_nvfp4_workspace_size(const qpa_nvfp4_desc* d) {
+  if (!d || !decode4_shape_ok(d)) return 0;
+  return decode4_workspace_bytes(d->query_group, d->head_dim);
+}
+
+int pa_decode_nvfp4(const void* q, const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                    const float* k_scale, const float* v_scale, void* out, const qpa_nvfp4_desc* d, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!d) return QPA_ERR_NULL;
+  if (!decode4_shape_ok(d)) return QPA_ERR_SHAPE;
+  if (d->num_seqs == 0) return QPA_OK;
+  if (!q || !kv_cache || !block_table || !seq_lens || !k_scale || !v_scale || !out || !workspace) return QPA_ERR_NULL;
+  Decode4Launch a;
+  const long long heads = (long long)d->num_kv_heads * d->query_group;
+  a.q_stride_head = d->q_stride_head ? d->q_stride_head : d->head_dim;
+  a.q_stride_seq = d->q_stride_seq ? d->q_stride_seq : heads * d->head_dim;
+  a.table_stride = d->table_stride ? d->table_stride : d->max_blocks_per_seq;
+  if (a.q_stride_head < 0 || a.q_stride_seq < 0 || (a.q_stride_head % 8) || (a.q_stride_seq % 8)) return QPA_ERR_ALIGN;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return QPA_ERR_ALIGN;
+  for (const void* w : {(const void*)block_table, (const void*)seq_lens, (const void*)k_scale, (const void*)v_scale})
+    if (!aligned(w, 4)) return QPA_ERR_ALIGN;
+  const size_t ws = decode4_workspace_bytes(d->query_group, d->head_dim);
+  if (workspace_bytes < ws) return QPA_ERR_WORKSPACE;
+  const Span in[] = {{q, extent(d->num_seqs, heads, d->head_dim, a.q_stride_seq, a.q_stride_head)},
+                     {kv_cache, cache4_bytes(d->num_blocks, 2, d->num_kv_heads, d->block_size, d->head_dim)},
+                     {block_table, (size_t(d->num_seqs - 1) * a.table_stride + d->max_blocks_per_seq) * 4},
+                     {seq_lens, size_t(d->num_seqs) * 4}, {k_scale, 4}, {v_scale, 4}};
+  const Span outs[] = {{out, size_t(d->num_seqs) * heads * d->head_dim * 2}, {workspace, ws}};
+  if (overlap(outs, in)) return QPA_ERR_OVERLAP;
+  a.q = q;
+  a.kv = kv_cache;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.out = out;
+  a.workspace = workspace;
+  a.num_seqs = d->num_seqs;
+  a.num_kv_heads = d->num_kv_heads;
+  a.qg = d->query_group;
+  a.head_dim = d->head_dim;
+  a.block_size = d->block_size;
+  a.num_blocks = d->num_blocks;
+  a.max_blocks = d->max_blocks_per_seq;
+  a.softmax_scale = d->softmax_scale != 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)d->head_dim);
+  a.num_sms = num_sms_current();
+  if (a.num_sms <= 0) return QPA_ERR_CUDA;
+  return launch_decode4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QPA_OK : QPA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,181 @@
+// kv_gather_nvfp4, kv_gather_fp8: tokens read back from the pages as bf16 or float32
+// rows.
+//
+// A block takes a tile of consecutive rows. First its threads find one row each: the
+// request by a binary search of query_start, the token's slot through the block table,
+// into shared memory. Then a thread keeps its place (plane, head, 8 dims) and steps
+// through the tile, UN rows in flight: 4 bytes of e2m1 codes and a scale byte, or 8 e4m3
+// codes, to 16 bytes of bf16. Bound: 0.5625 (fp8: 1) bytes in and 2 out per element.
+//
+// A value is code * group scale (exact in float32: 2 by 4 bits) times the tensor's
+// scale of 24 bits, rounded once: the product is cut to float32 with the lost bits as a
+// sticky last bit, which the rounding to bf16 then sees.
+#include <type_traits>
+
+#include "qpa.h"
+#include "common.cuh"
+#include "qpa_internal.h"
+
+namespace qpa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTile = 64;        // rows of a block
+enum : long long { kSkip = -1, kZero = -2 };
+
+// x * g rounded to bf16 once (as bits in the low half)
+__device__ __forceinline__ uint32_t mul_sticky(float x, float g) {
+  const float p = __fmul_rz(x, g);
+  return __float_as_uint(p) | (fmaf(x, g, -p) != 0.f ? 1u : 0u);
+}
+__device__ __forceinline__ uint32_t bf16x2(uint32_t lo, uint32_t hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(__uint_as_float(lo)), "f"(__uint_as_float(hi)));
+  return r;
+}
+
+// 8 dims of a token: `lo`, `hi` the code bytes (NVFP4: lo only), `s` the group scale
+// byte (NVFP4), `g` the tensor's or token's scale
+template <bool FP4>
+__device__ __forceinline__ void values8(uint32_t lo, uint32_t hi, uint32_t s, float (&x)[8]) {
+  uint32_t h[4];
+  if constexpr (FP4) {
+    const uint32_t sc = e4m3x2_lo_to_f16x2(s | (s << 8));
+    h[0] = hmul2(e2m1x2_to_f16x2<0>(lo), sc);
+    h[1] = hmul2(e2m1x2_to_f16x2<1>(lo), sc);
+    h[2] = hmul2(e2m1x2_to_f16x2<2>(lo), sc);
+    h[3] = hmul2(e2m1x2_to_f16x2<3>(lo), sc);
+  } else {
+    h[0] = e4m3x2_lo_to_f16x2(lo);
+    h[1] = e4m3x2_hi_to_f16x2(lo);
+    h[2] = e4m3x2_lo_to_f16x2(hi);
+    h[3] = e4m3x2_hi_to_f16x2(hi);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = f16_lo_to_f32(h[j]);
+    x[2 * j + 1] = f16_hi_to_f32(h[j]);
+  }
+}
+
+template <bool FP4, int HD, bool F32>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const GatherLaunch p, const int log2_bs, const int side,
+                                                          const int tile) {
+  constexpr int TPR = HD / 8;                  // threads per head vector
+  constexpr int UN = 4;
+  __shared__ long long s_slot[kMaxTile];
+  const int Hk = p.num_kv_heads, bs = p.block_size, R = p.num_reqs;
+  const long long row0 = (long long)blockIdx.x * tile;
+  const int rows = (int)min((long long)tile, p.num_tokens - row0);
+  if ((int)threadIdx.x < rows) {
+    // the request: the largest r with start[r] <= row (starts clamped to [0, num_tokens])
+    const int row = (int)row0 + threadIdx.x;
+    auto start = [&](int r) { return max(0, min(__ldg(p.query_start + r), p.num_tokens)); };
+    int lo = 0, hi = R + 1;
+    while (lo < hi) {                          // first entry above row
+      const int mid = (lo + hi) >> 1;
+      if (start(mid) <= row) lo = mid + 1;
+      else hi = mid;
+    }
+    const int r = lo - 1;
+    long long slot = kSkip;
+    if (r >= 0 && r < R) {
+      const long long cap = (long long)p.max_blocks * bs;
+      const long long L = max(0LL, min((long long)__ldg(p.seq_lens + r), cap));
+      const long long t = L - (start(r + 1) - row);
+      slot = kZero;
+      if (t >= 0) {
+        int blk = __ldg(p.block_table + r * p.table_stride + (t >> log2_bs));
+        if (blk < 0 || blk >= p.num_blocks) {
+          atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
+          blk = 0;
+        }
+        slot = (long long)blk * bs + (t & (bs - 1));
+      }
+    }
+    s_slot[threadIdx.x] = slot;
+  }
+  __syncthreads();
+  const int tpt = p.planes * Hk * TPR;         // threads per token
+  const int mine = threadIdx.x / tpt;
+  constexpr int CB = FP4 ? HD / 2 : HD;        // code bytes of a token and head
+  const size_t chunk = size_t(bs) * (FP4 ? HD / 2 + HD / 16 : HD);
+  for (int i0 = 0; i0 < tpt; i0 += kThreads) {
+    const int i = side > 1 ? threadIdx.x - mine * tpt : i0 + threadIdx.x;
+    if (side > 1 ? mine >= side : i >= tpt) break;
+    const int part = i % TPR, vec = i / TPR, kv = vec >= Hk && p.planes > 1, h = vec - kv * Hk;
+    const float* scales = kv ? p.v_scale : p.k_scale;
+    const float g0 = p.per_token ? 0.f : __ldg(scales);
+    const size_t esz = F32 ? 4 : 2;
+    uint8_t* out = static_cast<uint8_t*>(kv ? p.out_v : p.out_k) + (row0 * Hk + h) * (HD * esz) + part * (8 * esz);
+    for (int r0 = side > 1 ? mine : 0; r0 < rows; r0 += UN * side) {
+      uint32_t lo[UN], hi[UN], sc[UN];
+      float g[UN];
+      long long slot[UN];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int r = r0 + u * side;
+        slot[u] = r < rows ? s_slot[r] : (long long)kSkip;
+        lo[u] = hi[u] = sc[u] = 0;
+        g[u] = g0;
+        if (slot[u] >= 0) {
+          const long long blk = slot[u] >> log2_bs;
+          const int off = (int)(slot[u] & (bs - 1));
+          const uint8_t* src = p.kv + ((blk * p.planes + kv) * Hk + h) * chunk;
+          if constexpr (FP4) {
+            lo[u] = __ldcs(reinterpret_cast<const uint32_t*>(src + size_t(off) * CB) + part);
+            sc[u] = __ldcs(src + size_t(bs) * CB + size_t(off) * (HD / 16) + (part >> 1));
+          } else {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src + size_t(off) * CB) + part);
+            lo[u] = v.x;
+            hi[u] = v.y;
+            if (p.per_token) g[u] = __ldg(scales + (blk * Hk + h) * bs + off);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        if (slot[u] == kSkip) continue;
+        float x[8];
+        values8<FP4>(lo[u], hi[u], sc[u], x);
+        if (slot[u] < 0) g[u] = 0.f;
+        uint8_t* dst = out + size_t(r0 + u * side) * Hk * (HD * esz);
+        if constexpr (F32) {
+          reinterpret_cast<float4*>(dst)[0] = make_float4(x[0] * g[u], x[1] * g[u], x[2] * g[u], x[3] * g[u]);
+          reinterpret_cast<float4*>(dst)[1] = make_float4(x[4] * g[u], x[5] * g[u], x[6] * g[u], x[7] * g[u]);
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = bf16x2(mul_sticky(x[2 * j], g[u]), mul_sticky(x[2 * j + 1], g[u]));
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    if (side > 1) break;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gather(const GatherLaunch& a, cudaStream_t stream) {
+  int log2_bs = 0;
+  while ((1 << log2_bs) < a.block_size) ++log2_bs;
+  const long long tpt = (long long)a.planes * a.num_kv_heads * (a.head_dim / 8);
+  const int side = (int)std::max(1LL, kThreads / tpt);
+  // tiles small enough that every SM has a few blocks, large enough to share the search
+  const long long per = ((long long)a.num_tokens + 8LL * a.num_sms - 1) / (8LL * a.num_sms);
+  const int tile = (int)std::min<long long>(kMaxTile, std::max<long long>(per, side));
+  const int grid = (int)(((long long)a.num_tokens + tile - 1) / tile);
+  auto launch = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(a, log2_bs, side, tile); };
+  auto by_out = [&](auto f32) {
+    constexpr bool F = decltype(f32)::value;
+    if (a.fp4) a.head_dim == 64 ? launch(gather_kernel<true, 64, F>) : launch(gather_kernel<true, 128, F>);
+    else a.head_dim == 64 ? launch(gather_kernel<false, 64, F>) : launch(gather_kernel<false, 128, F>);
+  };
+  if (a.out_f32) by_out(std::true_type{});
+  else by_out(std::false_type{});
+  return cudaGetLastError();
+}
+
+}  // namespace qpa

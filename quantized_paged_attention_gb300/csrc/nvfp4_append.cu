@@ -1,0 +1,223 @@
+// kv_append_nvfp4: new keys and values quantised to NVFP4 (e2m1 codes, an e4m3
+// scale per 16 dims) and put into the pages.
+//
+// A thread takes one scale group: 16 elements (32 bytes in, 8 bytes of codes and
+// a scale byte out). Bound: 2 bytes in and 0.5625 out per element.
+//
+// Rounding, exact as kv_append_fp8's. With g the tensor's scale and a the group's
+// largest |x|:
+//  * s = e4m3(a / 6g): the quotient in float32 gives the code below it, and the
+//    sign of the fma a - 6 m g (m the midpoint above, 5 bits, 6 m has 7: exact)
+//    decides between the two.
+//  * code = e2m1(x / S), S = s g held as two floats (28 bits: exact). q = x hi + x lo
+//    with hi + lo = 1/S to 2^-40, so a midpoint comes out as that midpoint and a
+//    quotient 2^-18 away from one stays on its side. Midpoints have significands
+//    1, 3, 5 and 7, x has 8 bits: for a given S all quotients that are within 2^-18
+//    of a midpoint without being one lie on the same side of theirs (two of 8 by 3
+//    bits are equal or 2^-11 apart), and hi is moved by 2^-20 to that side.
+#include "qpa.h"
+#include "common.cuh"
+#include "qpa_internal.h"
+
+namespace qpa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kTiny = 1.2379400392853803e-27f;     // 2^-90
+constexpr float kHuge = 1.2379400392853803e+27f;     // 2^90
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// max(m, |w|) of bf16 pairs; a NaN stays
+__device__ __forceinline__ void amax2_nan(uint32_t& m, uint32_t w) {
+  asm("{ .reg .b32 t; abs.bf16x2 t, %1; max.NaN.bf16x2 %0, %0, t; }" : "+r"(m) : "r"(w));
+}
+
+// The e4m3 code nearest to a / (6 g), ties to even, 0x01 .. 0x7E; a >= 0 finite,
+// g > 0 finite.
+__device__ __forceinline__ uint32_t scale_code(float a, float g) {
+  if (g < 1.f) {                                   // keeps tiny products out of the subnormals (exact, or a large code)
+    a *= 18446744073709551616.f;
+    g *= 18446744073709551616.f;
+  } else if (g > 1.2676506002282294e30f) {         // and huge scales within the division's range (2^100)
+    a *= 5.421010862427522e-20f;
+    g *= 5.421010862427522e-20f;
+  }
+  const float q = __fdividef(a, g) * 0.16666667163372040f;
+  if (!(q < 464.f)) return 0x7eu;                  // 448 and its upper neighbour's midpoint
+  // below the smallest normal 2^-6 the codes are 2^-9 apart, as they are in [2^-6, 2^-5)
+  const float base = q < 0.015625f ? 0.015625f : 0.f;
+  const uint32_t t = __float_as_uint(q + base);
+  const float m = __uint_as_float((t & 0xfff00000u) | 0x00080000u) - base;
+  const float r = fmaf(-6.f * m, g, a);
+  uint32_t c = t >> 20;                            // exponent and 3 mantissa bits
+  c += (r > 0.f || (r == 0.f && (c & 1u))) ? 1u : 0u;
+  c -= (120u << 3) + (base != 0.f ? 8u : 0u);
+  return max(1u, min(c, 0x7eu));
+}
+
+// The code of |x| / (s g) by exact comparisons, for scales that the reciprocal
+// does not serve.
+__device__ __noinline__ uint32_t e2m1_exact(float x, float s, float g) {
+  const uint32_t sign = (__float_as_uint(x) >> 28) & 8u;
+  float ax = fabsf(x);
+  if (g < 1.f) {
+    ax *= 18446744073709551616.f;
+    g *= 18446744073709551616.f;
+  }
+  uint32_t c = 0;
+#pragma unroll 1
+  for (int i = 0; i < 7; ++i) {
+    const float mid = i < 4 ? 0.25f + 0.5f * i : i < 6 ? 2.5f + (i - 4) : 5.f;
+    const float r = fmaf(-mid * s, g, ax);         // mid s: 3 by 4 bits
+    c += (r > 0.f || (r == 0.f && (i & 1))) ? 1u : 0u;
+  }
+  return c | sign;
+}
+
+// (a, b) * hi + (a, b) * lo as two e2m1 codes, a in the low nibble
+__device__ __forceinline__ uint32_t quant2(float a, float b, float hi, float lo) {
+  uint32_t r;
+  asm("{ .reg .b64 x, y, z; .reg .b8 t; .reg .f32 u, v; mov.b64 x, {%1, %2}; mov.b64 y, {%3, %3}; mov.b64 z, {%4, %4}; "
+      "mul.rn.f32x2 z, x, z; fma.rn.f32x2 x, x, y, z; mov.b64 {u, v}, x; "
+      "cvt.rn.satfinite.e2m1x2.f32 t, v, u; cvt.u32.u8 %0, t; }" : "=r"(r) : "f"(a), "f"(b), "f"(hi), "f"(lo));
+  return r;
+}
+
+// 16 elements (bf16 pairs w) -> 8 bytes of codes, the scale byte in `sc`. `ok`: g is
+// positive and finite.
+__device__ __forceinline__ uint2 quantise16(const uint32_t (&w)[8], float g, bool ok, uint32_t& sc) {
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax2_nan(m2, w[j]);
+  float a = fmaxf(bf_lo(m2), bf_hi(m2));
+  const bool nan = (m2 & 0x7fffu) > 0x7f80u || ((m2 >> 16) & 0x7fffu) > 0x7f80u;
+  if (nan || !ok) {
+    sc = 0x7fu;
+    return make_uint2(0, 0);
+  }
+  a = fminf(a, 3.38953139e38f);                    // an infinity counts as the largest bf16
+  sc = scale_code(a, g);
+  const uint32_t e = sc >> 3, f = sc & 7u;
+  const float s = e ? __uint_as_float(((e + 120u) << 23) | (f << 20)) : (float)f * 0.001953125f;
+  if (!(g > kTiny && g < kHuge)) {
+    uint32_t o[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v |= (e2m1_exact(bf_lo(w[4 * h + j]), s, g) | (e2m1_exact(bf_hi(w[4 * h + j]), s, g) << 4)) << (8 * j);
+      o[h] = v;
+    }
+    return make_uint2(o[0], o[1]);
+  }
+  const float S = s * g, Sl = fmaf(s, g, -S);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(S));       // within 2^-23
+  const float h = r * (1.f - 2.38418579e-7f);                 // 2^-22: below 1/S, so that lo has the sign of hi
+  const float lo = (fmaf(-S, h, 1.f) - Sl * h) * h;
+  float side = 0.f;                                           // the sign of m S - x for the near midpoints
+#pragma unroll
+  for (int k = 1; k < 8; k += 2) {
+    const float v = k * S, x = __bfloat162float(__float2bfloat16_rn(v));
+    const float d = fmaf(k * s, g, -x);
+    side = (fabsf(v - x) <= v * 3.81469727e-6f && d != 0.f) ? d : side;
+  }
+  const float hi = h * (side > 0.f ? 1.f - 9.53674316e-7f : side < 0.f ? 1.f + 9.53674316e-7f : 1.f);
+  uint32_t o[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t c0 = quant2(bf_lo(w[4 * q]), bf_hi(w[4 * q]), hi, lo);
+    const uint32_t c1 = quant2(bf_lo(w[4 * q + 1]), bf_hi(w[4 * q + 1]), hi, lo);
+    const uint32_t c2 = quant2(bf_lo(w[4 * q + 2]), bf_hi(w[4 * q + 2]), hi, lo);
+    const uint32_t c3 = quant2(bf_lo(w[4 * q + 3]), bf_hi(w[4 * q + 3]), hi, lo);
+    o[q] = prmt(c0 | (c1 << 8), c2 | (c3 << 8), 0x5410u);
+  }
+  return make_uint2(o[0], o[1]);
+}
+
+// A token's planes * Hk head vectors take TPR threads each (in rounds, if more than
+// the block has); a block holds as many tokens side by side as fit. A thread keeps its
+// place (plane, head, 16 dims) and steps through the tokens, UN of them in flight.
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 4) append4_kernel(const Append4Launch p, const int log2_bs, const int side) {
+  constexpr int TPR = HD / 16;                 // threads per head vector
+  constexpr int UN = 2;
+  const int Hk = p.num_kv_heads, bs = p.block_size;
+  const int tpt = p.planes * Hk * TPR;         // threads per token
+  const long long slots = (long long)p.num_blocks * bs;
+  const size_t chunk = size_t(bs) * (HD / 2 + HD / 16);
+  const int mine = threadIdx.x / tpt;          // token of the block's side-by-side ones
+  const int round = kThreads / TPR * TPR;      // threads of a round (tpt > kThreads: one token)
+  const int step = gridDim.x * side;
+  for (int i0 = 0; i0 < tpt; i0 += round) {
+    const int i = side > 1 ? threadIdx.x - mine * tpt : i0 + threadIdx.x;
+    const bool place = side > 1 ? mine < side : i < tpt;
+    const int part = i % TPR, vec = i / TPR, kv = vec >= Hk && p.planes > 1, h = vec - kv * Hk;
+    const uint16_t* src = static_cast<const uint16_t*>(kv ? p.v : p.k) + h * (kv ? p.v_stride_head : p.k_stride_head);
+    const long long stride = kv ? p.v_stride_tok : p.k_stride_tok;
+    const float g = __ldg(kv ? p.v_scale : p.k_scale);
+    const bool ok = g > 0.f && g < INFINITY;
+    // whole warps stay in the loop (the scale bytes are shuffled together)
+    for (long long t0 = (long long)blockIdx.x * side; t0 < p.num_tokens; t0 += (long long)UN * step) {
+      long long slot[UN];
+      uint4 a[UN], b[UN];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const long long t = t0 + (long long)u * step + (side > 1 ? mine : 0);
+        slot[u] = place && t < p.num_tokens ? __ldg(p.slots + t) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const long long t = t0 + (long long)u * step + (side > 1 ? mine : 0);
+        if (slot[u] >= slots) {
+          atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
+          slot[u] = -1;
+        }
+        a[u] = b[u] = make_uint4(0, 0, 0, 0);
+        if (slot[u] >= 0) {
+          const uint4* s4 = reinterpret_cast<const uint4*>(src + t * stride) + 2 * part;
+          a[u] = __ldcs(s4);
+          b[u] = __ldcs(s4 + 1);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const uint32_t w[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
+        uint32_t sc;
+        const uint2 code = quantise16(w, g, ok, sc);
+        // the scale bytes of four neighbours as one word
+        uint32_t s4 = sc << (8 * (part & 3));
+        s4 |= __shfl_xor_sync(0xffffffffu, s4, 1);
+        s4 |= __shfl_xor_sync(0xffffffffu, s4, 2);
+        if (slot[u] < 0) continue;
+        const long long blk = slot[u] >> log2_bs;
+        const int off = (int)(slot[u] & (bs - 1));
+        uint8_t* dst = p.kv + ((blk * p.planes + kv) * Hk + h) * chunk;
+        reinterpret_cast<uint2*>(dst + size_t(off) * (HD / 2))[part] = code;
+        if ((part & 3) == 0)
+          reinterpret_cast<uint32_t*>(dst + size_t(bs) * (HD / 2) + size_t(off) * (HD / 16))[part >> 2] = s4;
+      }
+    }
+    if (side > 1) break;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append4(const Append4Launch& a, cudaStream_t stream) {
+  int log2_bs = 0;
+  while ((1 << log2_bs) < a.block_size) ++log2_bs;
+  const long long tpt = (long long)a.planes * a.num_kv_heads * (a.head_dim / 16);
+  const int side = (int)std::max(1LL, kThreads / tpt);
+  const long long want = ((long long)a.num_tokens + side - 1) / side;
+  const int grid = (int)std::min(want, (long long)a.num_sms * 4);
+  if (a.head_dim == 64) append4_kernel<64><<<grid, kThreads, 0, stream>>>(a, log2_bs, side);
+  else append4_kernel<128><<<grid, kThreads, 0, stream>>>(a, log2_bs, side);
+  return cudaGetLastError();
+}
+
+}  // namespace qpa

@@ -162,6 +162,54 @@ struct ChunkLaunch {
   int num_sms;
 };
 
+// KV heads of the 4-bit cache's calls and of reading back (keeps per-token counts in 32 bits)
+constexpr int kMaxHeads = 65536;
+
+// kv_append_nvfp4
+struct Append4Launch {
+  const void* k;
+  const void* v;
+  uint8_t* kv;
+  const int64_t* slots;
+  const float* k_scale;
+  const float* v_scale;
+  long long k_stride_tok, k_stride_head, v_stride_tok, v_stride_head;   // elements
+  int num_tokens, num_kv_heads, head_dim, block_size, num_blocks, planes;
+  int num_sms;
+};
+
+// kv_gather_nvfp4, kv_gather_fp8
+struct GatherLaunch {
+  const uint8_t* kv;
+  const int32_t* block_table;
+  const int32_t* query_start;
+  const int32_t* seq_lens;
+  const float* k_scale;
+  const float* v_scale;
+  void* out_k;
+  void* out_v;
+  long long table_stride;   // elements
+  int num_reqs, num_tokens, num_kv_heads, head_dim, block_size, num_blocks, max_blocks, planes;
+  int fp4, per_token, out_f32;
+  int num_sms;
+};
+
+// pa_decode_nvfp4
+struct Decode4Launch {
+  const void* q;
+  const uint8_t* kv;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* k_scale;
+  const float* v_scale;
+  void* out;
+  void* workspace;
+  long long q_stride_seq, q_stride_head, table_stride;   // elements
+  int num_seqs, num_kv_heads, qg, head_dim, block_size, num_blocks, max_blocks;
+  float softmax_scale;
+  int num_sms;
+};
+
 __device__ __forceinline__ void store4(float* dst, float a, float b, float c, float d) {
   *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
 }
@@ -195,6 +243,11 @@ size_t chunk_workspace_bytes(int num_tokens, int query_group, int head_dim);
 // Reads and clears the chunk kernel's own error word of the current device.
 cudaError_t take_chunk_error(int* v);
 cudaError_t launch_chunk(const ChunkLaunch& a, cudaStream_t stream);
+cudaError_t launch_append4(const Append4Launch& a, cudaStream_t stream);
+cudaError_t launch_gather(const GatherLaunch& a, cudaStream_t stream);
+// Workspace bytes of a 4-bit decode (independent of the device).
+size_t decode4_workspace_bytes(int query_group, int head_dim);
+cudaError_t launch_decode4(const Decode4Launch& a, cudaStream_t stream);
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
