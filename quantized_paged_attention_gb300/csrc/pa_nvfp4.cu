@@ -1,100 +1,860 @@
 // pa_decode_nvfp4: attention of one new token per sequence over the 4-bit pages.
 //
-// One CTA per (sequence, query head); its warps take the tokens in turn, each with
-// its own running maximum, sum and output, merged at the end. No tensor core: the
-// kernel to compare others with.
+// Mathematics: out = sum_t p_t v_t / sum_t p_t, p_t = 2^(c s_t - m) with s_t the dot
+// product, c the logits' factor in base 2 and m a running reference per row.
+//
+// Bound: the pages' bytes, 2 (D/2 + D/16) per (token, KV head).
+//
+// One persistent CTA per SM, the work (KV head and block of query rows, sequence, tile
+// of 128 tokens) in one list that is cut into equal ranges:
+//  * 4 copy warps stream the tiles (K and V codes and scales, 18 KB with head_dim
+//    128) into a ring by cp.async, tokens past the end as zeros, and build the item's
+//    query operand.
+//  * One warp issues the products S^T = K Q'^T on the block-scaled fp4 tensor core
+//    (kind::mxf4nvf4): the pages' e2m1 codes and e4m3 scales are the operand as they
+//    are, 128 tokens x 64 dims at a time. Q' holds each query row as 6 e2m1 terms of
+//    weights 1, 1/8, .. 8^-5 (3 bits each) with a power of two per 16 dims, so a query
+//    is within 2^-17 of its 16 dims' largest, and exact down to 2^-9 of it.
+//  * Groups of 4 consumer warps take the tiles in turn; each warp owns 32 tokens of a
+//    tile and its own softmax state, so nothing is exchanged before the item's end: it
+//    reads S from tensor memory (a lane a token), forms p in f16, and multiplies V on
+//    f16 mma.sync. V is taken from shared memory once, as pairs of tokens per dim: the
+//    nibbles of two tokens are put in one byte, converted (cvt, exact) and multiplied
+//    with the two tokens' scales (exact in f16: 2 by 4 bits). Through the tensor core's
+//    shared-memory operands the converted V would cost its bytes four times over:
+//    written and read at 2 bytes an element where the page has half a byte.
+//    The sum of p is one more row of V, of ones.
+//  * The reference m is put 8 below the largest logit (in base 2) and moves only when one
+//    exceeds it by 14: f16 holds 11 bits of p down to 2^-22 of the largest, and the common
+//    path has no exchange of maxima and no rescaling.
+// An item that its range does not cut is written out; pieces go to the workspace (two
+// slots per CTA: a range begins in at most one cut item and ends in another), and a
+// second kernel joins them in order.
 #include "qpa.h"
 #include "common.cuh"
 #include "qpa_internal.h"
+#include "tc.cuh"
 
 namespace qpa {
 
-namespace {
+namespace d4 {
+constexpr int TILE = 128;           // tokens per tile
+constexpr int QT = 6;               // e2m1 terms of a query
+constexpr int MAX_CTAS = 160;
+constexpr float kNoMax = -1e30f;    // no token seen yet: finite, so that differences stay defined
+constexpr float kBelow = 8.f;       // the reference is set this far below the largest logit (p up to 2^8)
+constexpr float kTop = 14.f;        // and moves when a logit is this far above it (p up to 2^14 in f16)
 
-constexpr int kWarps = 4;
+template <int NT, int HD>
+struct Smem {
+  static constexpr int NWG = NT == 1 ? 3 : 2;      // consumer groups of 4 warps
+  static constexpr int NCW = 4 * NWG;
+  static constexpr int WARP_COPY = NCW;
+  static constexpr int WARP_MMA = NCW + 4;
+  static constexpr int THREADS = (WARP_MMA + 1) * 32;
+  static constexpr int R = 8 * NT;                 // query rows (padded)
+  static constexpr int KS = HD / 64;               // K steps of the fp4 product
+  static constexpr int NQ = 8 * QT * NT;           // columns of S: row block x term x 8 rows
+  static constexpr int ROW = HD / 2;               // code bytes of a token
+  static constexpr int V_OFF = TILE * ROW;
+  static constexpr int KS_OFF = 2 * TILE * ROW;    // K scales [KS][token % 32][token / 32][4]
+  static constexpr int VS_OFF = KS_OFF + KS * 512; // V scales [token][HD / 16]
+  static constexpr int SLOT = VS_OFF + TILE * (HD / 16);
+  static constexpr int NSB = 4;                    // S buffers
+  static constexpr int qBytes = NQ * ROW;
+  static constexpr int STG_ROW = HD + 4;           // floats of a staged row (padded against bank conflicts)
+  static constexpr int stgBytes = NCW * R * STG_ROW * 4;
+  static constexpr int pBytes = 32 * 16 * NT;      // a warp's P [32 tokens][8 rows] f16 per row block
+  static constexpr int miscBytes = 2 * KS * 512 + NCW * pBytes + NCW * R * 8 + 2 * R * 4 + 2 * 64 + 64 * 8 + 64;
+  static constexpr int NS = (227 * 1024 - 1024 - 2 * qBytes - stgBytes - miscBytes) / SLOT > 16
+                                ? 16 : (227 * 1024 - 1024 - 2 * qBytes - stgBytes - miscBytes) / SLOT;
+  static constexpr int qOff = NS * SLOT;
+  static constexpr int qsOff = qOff + 2 * qBytes;             // [2][KS][512] query scales
+  static constexpr int stgOff = qsOff + 2 * KS * 512;         // [NCW][R][STG_ROW] f32
+  static constexpr int pOff = stgOff + stgBytes;              // [NCW] P
+  static constexpr int mlOff = pOff + NCW * pBytes;           // [NCW][R] {m, l}
+  static constexpr int cOff = mlOff + NCW * R * 8;            // [2][R] logit factor per row
+  static constexpr int infoOff = cOff + 2 * R * 4;            // [2] item
+  static constexpr int barOff = infoOff + 2 * 64;
+  static constexpr int NBAR = 2 * NS + 4 + 2 * NSB + 3;
+  static constexpr int miscOff = barOff + NBAR * 8;
+  static constexpr int total = miscOff + 16 + 1024;           // + alignment slack
+  static_assert(SLOT % 1024 == 0 && qBytes % 512 == 0 && NBAR <= 64 && total <= 227 * 1024, "shared memory");
+  // tensor memory: S buffers, K scales per S buffer, query scales per operand
+  static constexpr int SFA_COL = NSB * NQ, SFB_COL = SFA_COL + NSB * 4 * KS;
+  static constexpr int TMEM_COLS = SFB_COL + 2 * 4 * KS <= 256 ? 256 : 512;
+  static_assert(SFB_COL + 2 * 4 * KS <= TMEM_COLS, "tensor memory");
+};
 
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const float m = (c & 7u) < 2u ? 0.5f * (c & 1u) : __uint_as_float((126u + ((c >> 1) & 3u)) << 23 | (c & 1u) << 22);
-  return (c & 8u) ? -m : m;
+struct Params {
+  const uint16_t* q;
+  const uint8_t* kv;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* k_scale;
+  const float* v_scale;
+  uint16_t* out;                    // bf16
+  float* part_o;                    // [2 CTAs][16][HD], relative to m, not divided by l
+  float2* part_ml;                  // [2 CTAs][16] {m, l}
+  int4* meta;                       // [CTAs] {pieces (0: none), sequence, virtual head, 0}
+  long long q_stride_seq, q_stride_head, table_stride;
+  int num_seqs, num_kv_heads, qg, row_blocks, block_size, log2_bs, num_blocks, max_blocks;
+  float softmax_scale;
+};
+
+// kind::mxf4nvf4 instruction descriptor: e2m1 operands, K-major, unsigned e4m3 scales
+__host__ __device__ constexpr uint32_t idesc_fp4(int m, int n) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p; }"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+}
+// 512 bytes of scales (32 rows of 16) to 4 columns of all four lane quarters
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small_zfill(uint32_t dst, const void* src, bool valid, uint64_t policy) {
+  asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %2, %3, %4;"
+               ::"r"(dst), "l"(src), "n"(N), "r"(valid ? N : 0), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// (x, y) * w + (a, b)
+__device__ __forceinline__ void fma2(float& x, float& y, float w, float a, float b) {
+  asm("{ .reg .b64 p, q, r; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %2}; mov.b64 r, {%3, %4}; "
+      "fma.rn.f32x2 p, p, q, r; mov.b64 {%0, %1}, p; }" : "+f"(x), "+f"(y) : "f"(w), "f"(a), "f"(b));
+}
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{ .reg .b8 t; cvt.rn.satfinite.e2m1x2.f32 t, %2, %1; cvt.u32.u8 %0, t; }" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
 }
 
-template <int HD>
-__global__ void __launch_bounds__(32 * kWarps) decode4_simple_kernel(const Decode4Launch p, const int log2_bs) {
-  constexpr int N = HD / 32;                        // dims of a lane
-  __shared__ float s_o[kWarps][HD], s_m[kWarps], s_l[kWarps];
-  const int Hq = p.num_kv_heads * p.qg, bs = p.block_size;
-  const int seq = blockIdx.x / Hq, hq = blockIdx.x % Hq, h = hq / p.qg;
+// (up to 2^31 - 1 tokens)
+__device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len + TILE - 1) / TILE); }
+
+// The beginning of an item: sequence s of length L and T tiles, virtual head vh (KV head
+// vh / RB, row block vh % RB).
+struct Cursor {
+  int s, vh, L, T;
+  long long off;      // tiles of the sequences before s
+  int t;              // first tile of the item
+};
+
+}  // namespace d4
+
+template <int NT, int HD>
+__global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(const d4::Params p) {
+  using namespace d4;
+  using S = Smem<NT, HD>;
+  constexpr int R = S::R, NQ = S::NQ, NS = S::NS, NSB = S::NSB, NWG = S::NWG, NCW = S::NCW, KS = S::KS, ROW = S::ROW;
+  constexpr uint32_t SWZ = HD == 128 ? kSwizzle64B : 6u;      // rows of 64 or 32 bytes
+  constexpr int MT = HD / 16;                                 // m-tiles of V^T
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (sb - raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::barOff);   // [NS] tile copied (128 copy lanes)
+  uint64_t* empty = full + NS;         // [NS] tile consumed (MMA commit, a group's 4 warps)
+  uint64_t* qfull = empty + NS;        // [2] item published (4 copy warps)
+  uint64_t* qempty = qfull + 2;        // [2] item done (MMA commit, consumer warps)
+  uint64_t* sfull = qempty + 2;        // [NSB] S ready (MMA commit)
+  uint64_t* sfree = sfull + NSB;       // [NSB] S read (4 warps)
+  uint64_t* staged = sfree + NSB;      // item states published (consumer warps)
+  uint64_t* merged = staged + 1;       // item states read (consumer warps)
+  uint64_t* done = merged + 1;         // all MMAs finished
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::miscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::miscOff + 4);
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int L = max(0, min(__ldg(p.seq_lens + seq), p.max_blocks * bs));
-  const size_t chunk = size_t(bs) * (HD / 2 + HD / 16);
-  const uint16_t* qp = static_cast<const uint16_t*>(p.q) + seq * p.q_stride_seq + hq * p.q_stride_head + lane * N;
-  float q[N], o[N], m = -INFINITY, l = 0.f;
-  const float c = p.softmax_scale * __ldg(p.k_scale);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = __uint_as_float(uint32_t(qp[i]) << 16) * c;
-    o[i] = 0.f;
-  }
-  for (int t = warp; t < L; t += kWarps) {
-    int blk = __ldg(p.block_table + seq * p.table_stride + (t >> log2_bs));
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (lane == 0) atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
-      blk = 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 128);
+      mbar_init(&empty[i], 1 + 4);
     }
-    const int off = t & (bs - 1);
-    const uint8_t* kc = p.kv + ((size_t(blk) * 2) * p.num_kv_heads + h) * chunk;
-    const uint8_t* vc = kc + p.num_kv_heads * chunk;
-    float k[N], v[N];
-    const size_t code = size_t(off) * (HD / 2) + lane * (N / 2), sc = size_t(bs) * (HD / 2) + off * (HD / 16) + lane * N / 16;
-    const float ks = f16_lo_to_f32(e4m3x2_lo_to_f16x2(kc[sc])), vs = f16_lo_to_f32(e4m3x2_lo_to_f16x2(vc[sc]));
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      k[i] = e2m1_value((kc[code + i / 2] >> (4 * (i & 1))) & 15u) * ks;
-      v[i] = e2m1_value((vc[code + i / 2] >> (4 * (i & 1))) & 15u) * vs;
-      dot = fmaf(q[i], k[i], dot);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qfull[i], 4);
+      mbar_init(&qempty[i], 1 + NCW);
     }
-#pragma unroll
-    for (int s = 16; s; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-    const float mn = fmaxf(m, dot), alpha = m == -INFINITY ? 0.f : __expf(m - mn), w = __expf(dot - mn);
-    l = fmaf(l, alpha, w);
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = fmaf(o[i], alpha, w * v[i]);
+    for (int i = 0; i < NSB; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sfree[i], 4);
+    }
+    mbar_init(staged, NCW);
+    mbar_init(merged, NCW);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) s_o[warp][lane * N + i] = o[i];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
+  if (warp == S::WARP_MMA) tmem_alloc(tmem_slot, S::TMEM_COLS);
+  tc_fence_before();
   __syncthreads();
-  float M = -INFINITY, den = 0.f;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-  const float vg = __ldg(p.v_scale);
-  for (int d = threadIdx.x; d < HD; d += blockDim.x) {
-    float num = 0.f;
-    den = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      if (s_l[w] == 0.f) continue;
-      const float f = __expf(s_m[w] - M);
-      num = fmaf(f, s_o[w][d], num);
-      den = fmaf(f, s_l[w], den);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int bs = p.block_size, lbs = p.log2_bs, Hk = p.num_kv_heads, RB = p.row_blocks, B = p.num_seqs;
+  const int Hq = Hk * p.qg;
+  auto seq_len = [&](int s) -> int { return max(0, min(__ldg(p.seq_lens + s), p.max_blocks * bs)); };
+
+  if (warp < NCW) {
+    // ======================================================== consumer warps
+    const int wg = warp >> 2, wq = warp & 3;
+    const int g = lane >> 2, c = lane & 3;
+    // sequences without tokens give 0
+    for (int s = blockIdx.x * NCW + warp; s < B; s += gridDim.x * NCW)
+      if (seq_len(s) == 0)
+        for (long long i = lane; i < (long long)Hq * HD / 8; i += 32)
+          reinterpret_cast<uint4*>(p.out + (long long)s * Hq * HD)[i] = make_uint4(0, 0, 0, 0);
+    const uint32_t tl = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t psm = sb + S::pOff + warp * S::pBytes;
+    // ldmatrix row of this lane: token 16 (i / 2) + 8 (i % 2) + 4 (j % 2) + j / 2 of matrix i = lane / 8, row j
+    const int mi = lane >> 3, mj = lane & 7;
+    const uint32_t prow = psm + 16 * (16 * (mi >> 1) + 8 * (mi & 1) + 4 * (mj & 1) + (mj >> 1));
+    // V of token 4 u + c: 8 or 4 bytes, the lane's 16 or 8 dims
+    const uint32_t vlane = HD == 128 ? S::V_OFF + (32 * wq + c) * 64 + (((g >> 1) ^ (c & 2)) << 4) + 8 * (g & 1)
+                                     : S::V_OFF + (32 * wq + c) * 32 + 4 * g;
+    const uint32_t slane = S::VS_OFF + (32 * wq + c) * (HD / 16) + (HD == 128 ? g : g >> 1);
+    const float vscale = __ldg(p.v_scale);
+    float o[NT][MT][4], ol[NT][4], m[R];
+    int j = 0;                                       // tiles of the CTA so far
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int qb = n & 1;
+      if (!warp_wait(&qfull[qb], (n >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+      const int4 inf = lds_i4(sb + S::infoOff + 64 * qb);               // L, first tile, tiles, part (-1: whole)
+      const int4 who = lds_i4(sb + S::infoOff + 64 * qb + 16);          // sequence, virtual head
+      const int L = inf.x, t0 = inf.y, nt = inf.z;
+      if (nt == 0) break;
+#pragma unroll
+      for (int nb = 0; nb < NT; ++nb) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.f;
+        ol[nb][0] = ol[nb][1] = ol[nb][2] = ol[nb][3] = 0.f;
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) m[r] = kNoMax;
+      for (int i = 0; i < nt; ++i, ++j) {
+        if (j % NWG != wg) continue;
+        const int b = j % NSB, s = j % NS;
+        const int tok = (t0 + i) * TILE + 32 * wq + lane;               // this lane's token
+        const bool cut = (t0 + i + 1) * (long long)TILE > L;            // the sequence ends in this tile
+        if (!warp_wait(&sfull[b], (j / NSB) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int nb = 0; nb < NT; ++nb) {
+          // ---- logits of 8 rows for this token: terms of weights 8^-k, times the row's factor
+          float v[32], w[16];
+          tmem_ld32(tl + b * NQ + nb * 8 * QT, v);
+          tmem_ld16(tl + b * NQ + nb * 8 * QT + 32, w);
+          tmem_wait_ld();
+          if (nb == NT - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfree[b]);
+          }
+          float x[8], e[8];
+#pragma unroll
+          for (int r = 0; r < 8; r += 2) {
+            x[r] = w[8 + r];
+            x[r + 1] = w[9 + r];
+            fma2(x[r], x[r + 1], 0.125f, w[r], w[r + 1]);
+            fma2(x[r], x[r + 1], 0.125f, v[24 + r], v[25 + r]);
+            fma2(x[r], x[r + 1], 0.125f, v[16 + r], v[17 + r]);
+            fma2(x[r], x[r + 1], 0.125f, v[8 + r], v[9 + r]);
+            fma2(x[r], x[r + 1], 0.125f, v[r], v[r + 1]);
+          }
+          float f[8];
+          {
+            const float4 f0 = lds_f4(sb + S::cOff + 4 * (qb * R + 8 * nb)), f1 = lds_f4(sb + S::cOff + 4 * (qb * R + 8 * nb) + 16);
+            f[0] = f0.x; f[1] = f0.y; f[2] = f0.z; f[3] = f0.w;
+            f[4] = f1.x; f[5] = f1.y; f[6] = f1.z; f[7] = f1.w;
+          }
+#pragma unroll
+          for (int r = 0; r < 8; ++r) e[r] = fmaf(x[r], f[r], -m[8 * nb + r]);
+          if (cut && tok >= L) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) e[r] = -INFINITY;
+          }
+          const float top = fmaxf(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])), fmaxf(fmaxf(e[4], e[5]), fmaxf(e[6], e[7])));
+          if (__any_sync(0xffffffffu, top > kTop)) {
+            // ---- move the references of the rows that need it
+            float a0 = 1.f, a1 = 1.f;                                   // of this lane's output columns, rows 2c and 2c + 1
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              // (x f of a masked token does not count; NaN is ignored)
+              const float best = warp_max(cut && tok >= L ? -INFINITY : x[r] * f[r]);
+              const float old = m[8 * nb + r];
+              const float now = best > old + kTop ? best - kBelow : old;
+              const float alpha = ex2(old - now);
+              m[8 * nb + r] = now;
+              e[r] = cut && tok >= L ? -INFINITY : fmaf(x[r], f[r], -now);
+              if (r == 2 * c) a0 = alpha;
+              if (r == 2 * c + 1) a1 = alpha;
+            }
+#pragma unroll
+            for (int k = 0; k < MT; ++k) {
+              o[nb][k][0] *= a0;
+              o[nb][k][1] *= a1;
+              o[nb][k][2] *= a0;
+              o[nb][k][3] *= a1;
+            }
+            ol[nb][0] *= a0;
+            ol[nb][1] *= a1;
+          }
+          // ---- p in f16, a row of the warp's P
+          const uint32_t p0 = f32x2_to_f16x2(ex2(e[0]), ex2(e[1])), p1 = f32x2_to_f16x2(ex2(e[2]), ex2(e[3]));
+          const uint32_t p2 = f32x2_to_f16x2(ex2(e[4]), ex2(e[5])), p3 = f32x2_to_f16x2(ex2(e[6]), ex2(e[7]));
+          sts_i4(psm + 512 * nb + 16 * lane, make_int4(p0, p1, p2, p3));
+        }
+        __syncwarp();
+        uint32_t pb[NT][4];
+#pragma unroll
+        for (int nb = 0; nb < NT; ++nb) ldsm_x4_trans(prow + 512 * nb, pb[nb]);
+        // ---- O^T += V^T P^T, 16 tokens at a time
+        if (!warp_wait(&full[s], (j / NS) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        const uint32_t slot = sb + s * S::SLOT;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t w[4][HD / 64], sc[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t a = slot + vlane + (16 * k + 4 * u) * ROW;
+            if constexpr (HD == 128) {
+              const uint2 d = lds64(a);
+              w[u][0] = d.x;
+              w[u][1] = d.y;
+            } else {
+              w[u][0] = lds32(a);
+            }
+            sc[u] = lds8(slot + slane + (16 * k + 4 * u) * (HD / 16));
+          }
+          const uint32_t s01 = e4m3x2_lo_to_f16x2(sc[0] | (sc[1] << 8)), s23 = e4m3x2_lo_to_f16x2(sc[2] | (sc[3] << 8));
+#pragma unroll
+          for (int h = 0; h < HD / 64; ++h) {
+            // nibbles of two tokens per byte: dims 2 i and 2 i + 1
+            const uint32_t ev01 = (w[0][h] & 0x0f0f0f0fu) | ((w[1][h] << 4) & 0xf0f0f0f0u);
+            const uint32_t od01 = ((w[0][h] >> 4) & 0x0f0f0f0fu) | (w[1][h] & 0xf0f0f0f0u);
+            const uint32_t ev23 = (w[2][h] & 0x0f0f0f0fu) | ((w[3][h] << 4) & 0xf0f0f0f0u);
+            const uint32_t od23 = ((w[2][h] >> 4) & 0x0f0f0f0fu) | (w[3][h] & 0xf0f0f0f0u);
+            auto tile = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+              a0 = hmul2(a0, s01);
+              a1 = hmul2(a1, s01);
+              a2 = hmul2(a2, s23);
+              a3 = hmul2(a3, s23);
+#pragma unroll
+              for (int nb = 0; nb < NT; ++nb) mma_f16_16816(o[nb][4 * h + i], a0, a1, a2, a3, pb[nb][2 * k], pb[nb][2 * k + 1]);
+            };
+            tile(0, e2m1x2_to_f16x2<0>(ev01), e2m1x2_to_f16x2<0>(od01), e2m1x2_to_f16x2<0>(ev23), e2m1x2_to_f16x2<0>(od23));
+            tile(1, e2m1x2_to_f16x2<1>(ev01), e2m1x2_to_f16x2<1>(od01), e2m1x2_to_f16x2<1>(ev23), e2m1x2_to_f16x2<1>(od23));
+            tile(2, e2m1x2_to_f16x2<2>(ev01), e2m1x2_to_f16x2<2>(od01), e2m1x2_to_f16x2<2>(ev23), e2m1x2_to_f16x2<2>(od23));
+            tile(3, e2m1x2_to_f16x2<3>(ev01), e2m1x2_to_f16x2<3>(od01), e2m1x2_to_f16x2<3>(ev23), e2m1x2_to_f16x2<3>(od23));
+          }
+#pragma unroll
+          for (int nb = 0; nb < NT; ++nb)      // the sum of p: a row of ones
+            mma_f16_16816(ol[nb], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[nb][2 * k], pb[nb][2 * k + 1]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qempty[qb]);
+      // ---- item done: the warps' states to shared memory, each warp joins a share of the rows
+      if (n > 0 && !warp_wait(merged, (n - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
+      const uint32_t stg = sb + S::stgOff;
+#pragma unroll
+      for (int nb = 0; nb < NT; ++nb)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t a = stg + 4 * ((warp * R + 8 * nb + 2 * c + hh) * S::STG_ROW + 2 * MT * g);
+#pragma unroll
+          for (int k = 0; k < MT; k += 2)
+            sts_i4(a + 8 * k, make_int4(__float_as_int(o[nb][k][hh]), __float_as_int(o[nb][k][2 + hh]),
+                                        __float_as_int(o[nb][k + 1][hh]), __float_as_int(o[nb][k + 1][2 + hh])));
+          if (g == 0) stsf(sb + S::mlOff + 8 * (warp * R + 8 * nb + 2 * c + hh) + 4, ol[nb][hh]);
+        }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (lane == r) stsf(sb + S::mlOff + 8 * (warp * R + r), m[r]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(staged);
+      if (!warp_wait(staged, n & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+      const int rbase = 16 * (who.y % RB), kvh = who.y / RB;
+      const int rows = min(R, p.qg - rbase);
+      for (int r = warp; r < rows; r += NCW) {
+        float mw[NCW], M = kNoMax, l = 0.f;
+#pragma unroll
+        for (int k = 0; k < NCW; ++k) {
+          mw[k] = ldsf(sb + S::mlOff + 8 * (k * R + r));
+          M = fmaxf(M, mw[k]);
+        }
+        float acc[HD / 32];
+#pragma unroll
+        for (int d = 0; d < HD / 32; ++d) acc[d] = 0.f;
+#pragma unroll
+        for (int k = 0; k < NCW; ++k) {
+          const float f = ex2(mw[k] - M);
+          l = fmaf(f, ldsf(sb + S::mlOff + 8 * (k * R + r) + 4), l);
+          const uint32_t a = stg + 4 * ((k * R + r) * S::STG_ROW + (HD / 32) * lane);
+          if constexpr (HD == 128) {
+            const float4 d = lds_f4(a);
+            acc[0] = fmaf(f, d.x, acc[0]);
+            acc[1] = fmaf(f, d.y, acc[1]);
+            acc[2] = fmaf(f, d.z, acc[2]);
+            acc[3] = fmaf(f, d.w, acc[3]);
+          } else {
+            const uint2 d = lds64(a);
+            acc[0] = fmaf(f, __uint_as_float(d.x), acc[0]);
+            acc[1] = fmaf(f, __uint_as_float(d.y), acc[1]);
+          }
+        }
+        if (inf.w < 0) {
+          const float inv = vscale / l;
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) +
+                               ((long long)who.x * Hq + kvh * p.qg + rbase + r) * HD + (HD / 32) * lane;
+          if constexpr (HD == 128) store4(dst, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+          else *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
+        } else {
+          float* dst = p.part_o + ((long long)inf.w * 16 + r) * HD + (HD / 32) * lane;
+          if constexpr (HD == 128) store4(dst, acc[0], acc[1], acc[2], acc[3]);
+          else *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
+          if (lane == 0) p.part_ml[inf.w * 16 + r] = make_float2(M, l);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(merged);
     }
-    static_cast<__nv_bfloat16*>(p.out)[(size_t(seq) * Hq + hq) * HD + d] = __float2bfloat16_rn(L > 0 ? num / den * vg : 0.f);
+  } else if (warp < S::WARP_MMA) {
+    // ======================================================== copy warps
+    const int pw = warp - S::WARP_COPY, pt = 32 * pw + lane;
+    const uint64_t pol = policy_evict_first();
+    constexpr int CPR = ROW / 16, RPI = 32 / CPR, NII = 32 / RPI;       // 16-byte chunks per token, tokens per instruction
+    const int lr = lane / CPR, cc = lane % CPR;
+    const uint32_t kdst = (32 * pw + lr) * ROW + ((HD == 128 ? cc ^ ((lr >> 1) & 3) : cc ^ ((lr >> 2) & 1)) << 4);
+    const uint32_t vdst = S::V_OFF + (32 * pw + lr) * ROW + ((HD == 128 ? cc ^ (lr & 2) : cc) << 4);
+    const size_t chunk = size_t(bs) * (HD / 2 + HD / 16), plane = size_t(Hk) * chunk;
+
+    // ---- the CTA's range of units, and the item that holds its first one
+    long long W = 0;
+    for (int s0 = 0; s0 < B; s0 += 32)
+      if (s0 + lane < B) W += tiles_of(seq_len(s0 + lane));
+#pragma unroll
+    for (int sh = 16; sh; sh >>= 1) W += __shfl_xor_sync(0xffffffffu, W, sh);
+    const long long U = W * (Hk * (long long)RB);
+    const int G = gridDim.x;
+    const long long per = div_nonneg(U, G), rem = U - per * G;          // the first `rem` ranges have one more
+    auto first_of = [&](long long cta) -> long long { return per * cta + min(cta, rem); };
+    long long u = first_of(blockIdx.x);
+    const long long u1 = first_of(blockIdx.x + 1LL);
+    // the first sequence with tiles behind tile x of the head's list
+    auto find = [&](int s, long long off, long long x) -> Cursor {
+      for (int s0 = s; s0 < B; s0 += 32) {
+        const int L = s0 + lane < B ? seq_len(s0 + lane) : 0;
+        const int T = tiles_of(L);
+        long long incl = T;
+#pragma unroll
+        for (int sh = 1; sh < 32; sh <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, sh);
+          if (lane >= sh) incl += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, off + incl > x);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          Cursor c;
+          c.s = s0 + src;
+          c.vh = 0;
+          c.L = __shfl_sync(0xffffffffu, L, src);
+          c.T = __shfl_sync(0xffffffffu, T, src);
+          c.off = off + __shfl_sync(0xffffffffu, incl, src) - c.T;
+          c.t = (int)(x - c.off);
+          return c;
+        }
+        off += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      return Cursor{-1, 0, 0, 0, 0, 0};      // (not reached: x < W)
+    };
+    Cursor cur{-1, 0, 0, 0, 0, 0};
+    if (u < u1) {
+      const long long vh = div_nonneg(u, W);
+      cur = find(0, 0, u - vh * W);
+      cur.vh = (int)vh;
+    }
+    // the item that begins at unit `at`, behind item c
+    auto next = [&](const Cursor& c, long long at) -> Cursor {
+      if (at >= u1) return Cursor{-1, 0, 0, 0, 0, 0};
+      const long long off = c.off + c.T;
+      Cursor n = off < W ? find(c.s + 1, off, off) : find(0, 0, 0);
+      n.vh = off < W ? c.vh : c.vh + 1;
+      return n;
+    };
+    // query row pt / 16 (and + 8) of a row block, dims 8 (pt % 16) ..
+    const int qrow = pt >> 4, h16 = pt & 15;
+    auto load_q = [&](const Cursor& c, uint4 (&qv)[NT]) {
+#pragma unroll
+      for (int h = 0; h < NT; ++h) {
+        qv[h] = make_uint4(0, 0, 0, 0);
+        if (c.s < 0 || h16 >= HD / 8) continue;
+        const int row = 16 * (c.vh % RB) + qrow + 8 * h;
+        if (row < p.qg)
+          qv[h] = __ldg(reinterpret_cast<const uint4*>(p.q + c.s * p.q_stride_seq +
+                                                       ((long long)(c.vh / RB) * p.qg + row) * p.q_stride_head) + h16);
+      }
+    };
+    // 32 table entries from entry e0 on
+    auto load_entries = [&](int s, int e0) -> int32_t {
+      return s >= 0 && e0 + lane < p.max_blocks ? __ldg(p.block_table + (long long)s * p.table_stride + e0 + lane) : 0;
+    };
+    const float base = __ldg(p.k_scale) * p.softmax_scale * kLog2e;
+    uint4 qv[NT];
+    load_q(cur, qv);
+    int32_t ent0 = load_entries(cur.s, (int)(((long long)cur.t * TILE) >> lbs));
+    int j = 0, n = 0;
+    int4 meta = make_int4(0, 0, 0, 0);
+    bool ok = true;
+    while (cur.s >= 0 && ok) {
+      const int te = (int)min((long long)cur.T, cur.t + (u1 - u)), nt = te - cur.t;
+      int part = -1;
+      if (cur.t > 0) {
+        part = 2 * blockIdx.x;
+      } else if (te < cur.T) {
+        // begins here: the pieces are this CTA's and those of the ranges up to the sequence's last unit
+        part = 2 * blockIdx.x + 1;
+        const long long last = u + cur.T - 1, head = rem * (per + 1);
+        const long long cta = last < head ? div_nonneg(last, per + 1) : rem + div_nonneg(last - head, per);
+        meta = make_int4((int)cta - (int)blockIdx.x + 1, cur.s, cur.vh, 0);
+      }
+      const Cursor nxt = next(cur, u + nt);
+      uint4 qn[NT];
+      load_q(nxt, qn);
+      const int32_t ent0n = load_entries(nxt.s, (int)(((long long)nxt.t * TILE) >> lbs));
+      const int L = cur.L;
+      const uint8_t* kbase = p.kv + size_t(cur.vh / RB) * chunk;
+      int e0 = (int)(((long long)cur.t * TILE) >> lbs);
+      int32_t ent = ent0, ent_next = load_entries(cur.s, e0 + 32);
+      int ti = 0;
+      auto issue_to = [&](int end) -> bool {
+        for (; ti < end; ++ti, ++j) {
+          const int s = j % NS;
+          if (j >= NS && !warp_wait(&empty[s], (j / NS - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
+          const int tok0 = (cur.t + ti) * TILE + 32 * pw;               // this warp's 32 tokens
+          if (((cur.t + ti) * TILE >> lbs) - e0 >= 32) {
+            e0 += 32;
+            ent = ent_next;
+            ent_next = load_entries(cur.s, e0 + 32);
+          }
+          // (a tile's blocks never straddle two groups of 32 entries: 32 blocks are whole tiles, from a tile's first on)
+          int pa = __shfl_sync(0xffffffffu, ent, ((tok0 >> lbs) - e0) & 31);
+          int pb = __shfl_sync(0xffffffffu, ent, (((tok0 + 16) >> lbs) - e0) & 31);
+          if (pa < 0 || pa >= p.num_blocks) {
+            if (tok0 < L && lane == 0) atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
+            pa = 0;
+          }
+          if (pb < 0 || pb >= p.num_blocks) {
+            if (tok0 + 16 < L && lane == 0) atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
+            pb = 0;
+          }
+          // tokens tok0 .. + 15 lie in block pa at offset oa, tokens tok0 + 16 .. in pb at ob
+          const int oa = tok0 & (bs - 1), ob = (tok0 + 16) & (bs - 1);
+          const uint8_t* ca = kbase + size_t(pa) * 2 * plane;
+          const uint8_t* cb = kbase + size_t(pb) * 2 * plane;
+          const uint32_t slot = sb + s * S::SLOT;
+#pragma unroll
+          for (int ii = 0; ii < NII; ++ii) {
+            const int r = lr + RPI * ii;
+            const bool lowhalf = RPI * ii < 16;
+            const uint8_t* src = (lowhalf ? ca + size_t(oa + r) * ROW : cb + size_t(ob + r - 16) * ROW) + 16 * cc;
+            const bool valid = tok0 + r < L;
+            cp_async16_zfill(slot + kdst + RPI * ii * ROW, src, valid, pol);
+            cp_async16_zfill(slot + vdst + RPI * ii * ROW, src + plane, valid, pol);
+          }
+          {
+            const uint8_t* src = (lane < 16 ? ca + size_t(oa + lane) * (HD / 16) : cb + size_t(ob + lane - 16) * (HD / 16)) +
+                                 size_t(bs) * ROW;
+            const bool valid = tok0 + lane < L;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+              cp_async_small_zfill<4>(slot + S::KS_OFF + 512 * k + 16 * lane + 4 * pw, src + 4 * k, valid, pol);
+            cp_async_small_zfill<HD / 16>(slot + S::VS_OFF + (32 * pw + lane) * (HD / 16), src + plane, valid, pol);
+          }
+          cp_async_arrive_noinc(&full[s]);
+        }
+        return true;
+      };
+      // the first tile goes out before the operand is built
+      if (n == 0 && !issue_to(1)) break;
+      const int qb = n & 1;
+      if (n >= 2 && !warp_wait(&qempty[qb], ((n >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
+      // ---- query operand
+#pragma unroll
+      for (int h = 0; h < NT; ++h) {
+        const uint32_t ws[4] = {qv[h].x, qv[h].y, qv[h].z, qv[h].w};
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[2 * k] = __uint_as_float(ws[k] << 16);
+          x[2 * k + 1] = __uint_as_float(ws[k] & 0xffff0000u);
+        }
+        float amax = 0.f;
+        bool finite = true;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          amax = fmaxf(amax, fabsf(x[k]));
+          finite = finite && fabsf(x[k]) < INFINITY;
+        }
+        // rows with a value that is not finite give NaN through their factor
+        const unsigned fin = __ballot_sync(0xffffffffu, finite);
+        const bool row_ok = ((fin >> (lane & 16)) & 0xffffu) == 0xffffu;
+        if (!row_ok) amax = 0.f;
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));      // of 16 dims
+        // exponent that puts the 16 dims' largest into (2, 4]; the row's largest exponent
+        int eb = -200;
+        if (amax > 0.f) {
+          int ex;
+          const float fr = frexpf(amax, &ex);                           // amax = fr 2^ex, fr in [1/2, 1)
+          eb = (fr == 0.5f ? ex - 1 : ex) - 2;
+        }
+        int er = eb;
+#pragma unroll
+        for (int sh = 2; sh < 16; sh <<= 1) er = max(er, __shfl_xor_sync(0xffffffffu, er, sh));
+        if (er == -200) er = 0;
+        const int rel = max(eb - er, -17);                              // scales 2^8 .. 2^-9
+        // x 2^-(er + rel), in two factors that are floats
+        const int sh = -(er + rel), s1 = max(-126, min(126, sh)), s2 = sh - s1;
+        const float up = __uint_as_float(uint32_t(127 + s1) << 23), up2 = __uint_as_float(uint32_t(127 + s2) << 23);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = row_ok ? x[k] * up * up2 : 0.f;
+        const int es = rel + 8;                                          // e4m3: 2^es
+        const uint32_t sbyte = es >= -6 ? uint32_t(es + 7) << 3 : 1u << (es + 9);
+        const int row8 = qrow;
+#pragma unroll
+        for (int term = 0; term < QT; ++term) {
+          uint32_t word = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t code = f32x2_to_e2m1x2(x[2 * k], x[2 * k + 1]);
+            const uint32_t back = e2m1x2_to_f16x2<0>(code);
+            x[2 * k] = (x[2 * k] - f16_lo_to_f32(back)) * 8.f;
+            x[2 * k + 1] = (x[2 * k + 1] - f16_hi_to_f32(back)) * 8.f;
+            word |= code << (8 * k);
+          }
+          const int col = 8 * QT * h + 8 * term + row8;
+          if (h16 < HD / 8) {
+            const int ch = HD == 128 ? (h16 >> 2) ^ ((col >> 1) & 3) : (h16 >> 2) ^ ((col >> 2) & 1);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb + S::qOff + qb * S::qBytes + col * ROW + 16 * ch + 4 * (h16 & 3)),
+                         "r"(word) : "memory");
+            if ((h16 & 1) == 0)
+              sts8(sb + S::qsOff + (qb * KS + (h16 >> 3)) * 512 + (col & 31) * 16 + (col >> 5) * 4 + ((h16 >> 1) & 3), sbyte);
+          }
+        }
+        if (h16 == 0) {
+          // the row's factor takes 2^(er - 8)
+          const int a = er - 8, a1 = max(-126, min(126, a)), a2 = a - a1;
+          const float f = base * __uint_as_float(uint32_t(127 + a1) << 23) * __uint_as_float(uint32_t(127 + a2) << 23);
+          const bool used = 16 * (cur.vh % RB) + qrow + 8 * h < p.qg;
+          stsf(sb + S::cOff + 4 * (qb * R + 8 * h + qrow), !row_ok ? __int_as_float(0x7fffffff) : used ? f : 0.f);
+        }
+      }
+      if (pt == 0) {
+        sts_i4(sb + S::infoOff + 64 * qb, make_int4(L, cur.t, nt, part));
+        sts_i4(sb + S::infoOff + 64 * qb + 16, make_int4(cur.s, cur.vh, 0, 0));
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qfull[qb]);
+      ++n;
+      if (!issue_to(nt)) break;
+      u += nt;
+      cur = nxt;
+#pragma unroll
+      for (int h = 0; h < NT; ++h) qv[h] = qn[h];
+      ent0 = ent0n;
+    }
+    if (cur.s < 0) {
+      // no more items
+      const int qb = n & 1;
+      if (n < 2 || warp_wait(&qempty[qb], ((n >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) {
+        if (pt == 0) sts_i4(sb + S::infoOff + 64 * qb, make_int4(0, 0, 0, 0));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[qb]);
+      }
+    }
+    if (pt == 0) p.meta[blockIdx.x] = meta;
+    cp_async_wait_all();
+  } else {
+    // ======================================================== MMA warp
+    if (lane == 0) {
+      int j = 0;
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const int qb = n & 1;
+        if (!role_wait(&qfull[qb], (n >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+        const int nt = lds_i4(sb + S::infoOff + 64 * qb).z;
+        if (nt == 0) break;
+        const uint32_t qa = sb + S::qOff + qb * S::qBytes, sfb = tmem + S::SFB_COL + qb * 4 * KS;
+        for (int i = 0; i < nt; ++i, ++j) {
+          const int s = j % NS, b = j % NSB;
+          if (!role_wait(&full[s], (j / NS) & 1, abort_flag, KERR_TIMEOUT_FULL) ||
+              (j >= NSB && !role_wait(&sfree[b], (j / NSB - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY))) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async();     // the copied bytes (generic proxy) become visible to the tensor core
+          tc_fence_after();
+          const uint32_t ka = sb + s * S::SLOT, sfa = tmem + S::SFA_COL + b * 4 * KS;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            if (i == 0) copy_scales(sfb + 4 * k, umma_desc(sb + S::qsOff + (qb * KS + k) * 512, 16, 128, kSwizzleNone));
+            copy_scales(sfa + 4 * k, umma_desc(ka + S::KS_OFF + 512 * k, 16, 128, kSwizzleNone));
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            mma_fp4(tmem + b * NQ, umma_desc(ka + 32 * k, 16, 8 * ROW, SWZ), umma_desc(qa + 32 * k, 16, 8 * ROW, SWZ),
+                    idesc_fp4(128, NQ), sfa + 4 * k, sfb + 4 * k, k);
+          umma_commit(&sfull[b]);
+          umma_commit(&empty[s]);
+          if (i == nt - 1) umma_commit(&qempty[qb]);
+        }
+      }
+      // every MMA must finish before the tensor memory is released
+      umma_commit(done);
+      if (!mbar_try_wait(done, 0)) {
+        const unsigned long long t0 = globaltimer();
+        while (!mbar_try_wait(done, 0)) {
+          if (globaltimer() - t0 > kWaitLimitNs) {
+            atomicExch(&g_kernel_error, (int)KERR_TIMEOUT_FULL);
+            break;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == S::WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::TMEM_COLS);
   }
 }
 
-}  // namespace
+// Joins the pieces of the item that begins in range blockIdx.x and continues: out = sum_i
+// 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, row blockIdx.y of its row block; each warp takes
+// every NW-th piece.
+template <int HD>
+__global__ void __launch_bounds__(128) decode4_combine_kernel(const d4::Params p) {
+  using namespace d4;
+  constexpr int NW = 4, V = HD / 32;
+  __shared__ float s_o[NW][HD], s_l[NW];
+  const int4 meta = p.meta[blockIdx.x];
+  const int r = blockIdx.y, rbase = 16 * (meta.z % p.row_blocks);
+  if (meta.x == 0 || rbase + r >= p.qg) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto slot = [&](int i) -> int { return i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i); };
+  float M = kNoMax;
+  for (int i = lane; i < meta.x; i += 32) M = fmaxf(M, p.part_ml[slot(i) * 16 + r].x);
+  M = warp_max(M);
+  float acc[V], l = 0.f;
+#pragma unroll
+  for (int d = 0; d < V; ++d) acc[d] = 0.f;
+#pragma unroll 8
+  for (int i = warp; i < meta.x; i += NW) {
+    const float2 ml = p.part_ml[slot(i) * 16 + r];
+    const float* src = p.part_o + ((long long)slot(i) * 16 + r) * HD + V * lane;
+    const float f = ex2(ml.x - M);
+    l = fmaf(f, ml.y, l);
+    if constexpr (HD == 128) {
+      const float4 d = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(f, d.x, acc[0]);
+      acc[1] = fmaf(f, d.y, acc[1]);
+      acc[2] = fmaf(f, d.z, acc[2]);
+      acc[3] = fmaf(f, d.w, acc[3]);
+    } else {
+      const float2 d = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(f, d.x, acc[0]);
+      acc[1] = fmaf(f, d.y, acc[1]);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < V; ++d) s_o[warp][V * lane + d] = acc[d];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  if (threadIdx.x < HD) {
+    float num = 0.f, den = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      num += s_o[w][threadIdx.x];
+      den += s_l[w];
+    }
+    const long long row = (long long)meta.y * p.num_kv_heads * p.qg + (meta.z / p.row_blocks) * p.qg + rbase + r;
+    reinterpret_cast<__nv_bfloat16*>(p.out)[row * HD + threadIdx.x] = __float2bfloat16_rn(num * (__ldg(p.v_scale) / den));
+  }
+}
 
-size_t decode4_workspace_bytes(int, int) { return 256; }
+// two slots of 16 rows per CTA, and what begins in it
+size_t decode4_workspace_bytes(int, int head_dim) {
+  return size_t(d4::MAX_CTAS) * (2 * 16 * (size_t(head_dim) * 4 + 8) + 16);
+}
 
 cudaError_t launch_decode4(const Decode4Launch& a, cudaStream_t stream) {
-  int log2_bs = 0;
-  while ((1 << log2_bs) < a.block_size) ++log2_bs;
-  const unsigned grid = unsigned((long long)a.num_seqs * a.num_kv_heads * a.qg);
-  if (a.head_dim == 64) decode4_simple_kernel<64><<<grid, 32 * kWarps, 0, stream>>>(a, log2_bs);
-  else decode4_simple_kernel<128><<<grid, 32 * kWarps, 0, stream>>>(a, log2_bs);
+  d4::Params p;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.kv = a.kv;
+  p.block_table = a.block_table;
+  p.seq_lens = a.seq_lens;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.out = static_cast<uint16_t*>(a.out);
+  p.part_o = static_cast<float*>(a.workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + size_t(d4::MAX_CTAS) * 2 * 16 * a.head_dim);
+  p.meta = reinterpret_cast<int4*>(p.part_ml + size_t(d4::MAX_CTAS) * 2 * 16);
+  p.q_stride_seq = a.q_stride_seq;
+  p.q_stride_head = a.q_stride_head;
+  p.table_stride = a.table_stride;
+  p.num_seqs = a.num_seqs;
+  p.num_kv_heads = a.num_kv_heads;
+  p.qg = a.qg;
+  p.row_blocks = (a.qg + 15) / 16;
+  p.block_size = a.block_size;
+  p.log2_bs = 0;
+  while ((1 << p.log2_bs) < a.block_size) ++p.log2_bs;
+  p.num_blocks = a.num_blocks;
+  p.max_blocks = a.max_blocks;
+  p.softmax_scale = a.softmax_scale;
+  // no more CTAs than units there can be
+  const long long tiles = ((long long)a.max_blocks * a.block_size + d4::TILE - 1) / d4::TILE;
+  const long long units = std::min(tiles, 1LL << 20) * a.num_seqs * a.num_kv_heads * p.row_blocks;
+  const int grid = (int)std::min<long long>(units, std::min(a.num_sms, d4::MAX_CTAS));
+  auto launch = [&](auto kernel, int threads, int smem) {
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    kernel<<<grid, threads, smem, stream>>>(p);
+  };
+  const bool one = a.qg <= 8;
+  if (a.head_dim == 64) {
+    if (one) launch(decode4_kernel<1, 64>, d4::Smem<1, 64>::THREADS, d4::Smem<1, 64>::total);
+    else launch(decode4_kernel<2, 64>, d4::Smem<2, 64>::THREADS, d4::Smem<2, 64>::total);
+  } else {
+    if (one) launch(decode4_kernel<1, 128>, d4::Smem<1, 128>::THREADS, d4::Smem<1, 128>::total);
+    else launch(decode4_kernel<2, 128>, d4::Smem<2, 128>::THREADS, d4::Smem<2, 128>::total);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || grid <= 0) return e;
+  const dim3 cgrid(grid, std::min(16, a.qg));
+  if (a.head_dim == 64) decode4_combine_kernel<64><<<cgrid, 128, 0, stream>>>(p);
+  else decode4_combine_kernel<128><<<cgrid, 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

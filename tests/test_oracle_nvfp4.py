@@ -76,11 +76,11 @@ def test_decode_against_a_dense_softmax():
     slots = table[0, np.arange(37) // 16] * 16 + np.arange(37) % 16
     cache = oracle.kv_append_nvfp4(k, v, np.zeros((3, 2, 2, 16, 36), dtype=np.uint8), slots, 0.1, 0.2)
     q = synth.round_to_bf16_bits(r.standard_normal((1, 6, 64)))
-    out, bound, slack = oracle.pa_decode_nvfp4(q, cache, table, [37], 0.1, 0.2, 3)
+    out, bound, total, slack = oracle.pa_decode_nvfp4(q, cache, table, [37], 0.1, 0.2, 3)
     K, V = (oracle.values_nvfp4(cache, i, g, slots // 16, slots % 16) for i, g in ((0, 0.1), (1, 0.2)))
     assert np.all(np.abs(K - oracle.decode_bf16(k)) <= 0.2 * np.abs(oracle.decode_bf16(k)).max())
     for hq in range(6):
         x = K[:, hq // 3] @ oracle.decode_bf16(q)[0, hq] / 8
         w = np.exp(x) / np.exp(x).sum()
         assert np.allclose(out[0, hq], w @ V[:, hq // 3], rtol=1e-12, atol=1e-12)
-        assert np.all(bound[0, hq] >= np.abs(out[0, hq]) - 1e-12) and 0 < slack[0, hq] < 1e-2
+        assert np.all(bound[0, hq] >= np.abs(out[0, hq]) - 1e-12) and np.all(total[0, hq] >= bound[0, hq]) and 0 < slack[0, hq] < 1e-2
