@@ -19,7 +19,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 # compiled whole (no relocatable device code): the compiler ignores register
 # budgets per warp group (setmaxnreg) in code that other units may call
-WHOLE = {"pa_chunk.cu"}
+WHOLE = {"pa_chunk.cu", "pa_nvfp4.cu"}
 
 
 def _nvcc() -> str:

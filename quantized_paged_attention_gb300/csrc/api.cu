@@ -316,8 +316,9 @@ int qpa_kernel_error(void* stream) {
   int v = 0, z = 0;
   if (cudaMemcpyFromSymbol(&v, qpa::g_kernel_error, sizeof(int)) != cudaSuccess) return QPA_ERR_CUDA;
   if (cudaMemcpyToSymbol(qpa::g_kernel_error, &z, sizeof(int)) != cudaSuccess) return QPA_ERR_CUDA;
-  // the chunk kernel's own word, for this call only if the shared one held nothing
+  // the chunk kernel's own word, and the 4-bit decode's, for this call only if the ones before held nothing
   if (v == 0 && take_chunk_error(&v) != cudaSuccess) return QPA_ERR_CUDA;
+  if (v == 0 && take_decode4_error(&v) != cudaSuccess) return QPA_ERR_CUDA;
   return v;
 }
 

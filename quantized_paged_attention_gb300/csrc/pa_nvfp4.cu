@@ -30,6 +30,7 @@
 // An item that its range does not cut is written out; pieces go to the workspace (two
 // slots per CTA: a range begins in at most one cut item and ends in another), and a
 // second kernel joins them in order.
+#define QPA_WHOLE_UNIT
 #include "qpa.h"
 #include "common.cuh"
 #include "qpa_internal.h"
@@ -47,11 +48,14 @@ constexpr float kTop = 14.f;        // and moves when a logit is this far above 
 
 template <int NT, int HD>
 struct Smem {
-  static constexpr int NWG = NT == 1 ? 3 : 2;      // consumer groups of 4 warps
+  static constexpr int NWG = 2;                    // consumer groups of 4 warps
   static constexpr int NCW = 4 * NWG;
   static constexpr int WARP_COPY = NCW;
-  static constexpr int WARP_MMA = NCW + 4;
-  static constexpr int THREADS = (WARP_MMA + 1) * 32;
+  static constexpr int WARP_MMA = NCW + 4;         // one per consumer group
+  static constexpr int THREADS = (WARP_MMA + 4) * 32;   // (whole warpgroups, for the register budgets)
+  // registers of the roles' threads; their sum is the launch's, 512 x 128
+  static constexpr int REG_CONSUMER = 168, REG_COPY = 104, REG_MMA = 72;
+  static_assert(NWG == 2 && 256 * REG_CONSUMER + 128 * REG_COPY + 128 * REG_MMA == THREADS * 128, "registers");
   static constexpr int R = 8 * NT;                 // query rows (padded)
   static constexpr int KS = HD / 64;               // K steps of the fp4 product
   static constexpr int NQ = 8 * QT * NT;           // columns of S: row block x term x 8 rows
@@ -60,30 +64,33 @@ struct Smem {
   static constexpr int KS_OFF = 2 * TILE * ROW;    // K scales [KS][token % 32][token / 32][4]
   static constexpr int VS_OFF = KS_OFF + KS * 512; // V scales [token][HD / 16]
   static constexpr int SLOT = VS_OFF + TILE * (HD / 16);
-  static constexpr int NSB = 4;                    // S buffers
+  static constexpr int NSB = 2 * NWG;              // S buffers, two per group
   static constexpr int qBytes = NQ * ROW;
   static constexpr int STG_ROW = HD + 4;           // floats of a staged row (padded against bank conflicts)
-  static constexpr int stgBytes = NCW * R * STG_ROW * 4;
+  static constexpr int stgBytes = NCW * 8 * STG_ROW * 4;   // one row block at a time
   static constexpr int pBytes = 32 * 16 * NT;      // a warp's P [32 tokens][8 rows] f16 per row block
-  static constexpr int miscBytes = 2 * KS * 512 + NCW * pBytes + NCW * R * 8 + 2 * R * 4 + 2 * 64 + 64 * 8 + 64;
-  static constexpr int NS = (227 * 1024 - 1024 - 2 * qBytes - stgBytes - miscBytes) / SLOT > 16
-                                ? 16 : (227 * 1024 - 1024 - 2 * qBytes - stgBytes - miscBytes) / SLOT;
+  // ring slots. A multiple of the copy warps and of the groups: a slot then has one
+  // copy warp and one group, which see every phase of its barriers (a wait on a parity
+  // cannot mistake a phase for the one before the last)
+  static constexpr int NS = HD == 128 ? 8 : 16;
+  static_assert(NS % 4 == 0 && NS % NWG == 0, "ring");
   static constexpr int qOff = NS * SLOT;
   static constexpr int qsOff = qOff + 2 * qBytes;             // [2][KS][512] query scales
-  static constexpr int stgOff = qsOff + 2 * KS * 512;         // [NCW][R][STG_ROW] f32
+  static constexpr int stgOff = qsOff + 2 * KS * 512;         // [NCW][8][STG_ROW] f32
   static constexpr int pOff = stgOff + stgBytes;              // [NCW] P
-  static constexpr int mlOff = pOff + NCW * pBytes;           // [NCW][R] {m, l}
-  static constexpr int cOff = mlOff + NCW * R * 8;            // [2][R] logit factor per row
+  static constexpr int mlOff = pOff + NCW * pBytes;           // [NCW][8] {m, l}
+  static constexpr int cOff = mlOff + NCW * 8 * 8;            // [2][R] logit factor per row
   static constexpr int infoOff = cOff + 2 * R * 4;            // [2] item
   static constexpr int barOff = infoOff + 2 * 64;
   static constexpr int NBAR = 2 * NS + 4 + 2 * NSB + 3;
   static constexpr int miscOff = barOff + NBAR * 8;
   static constexpr int total = miscOff + 16 + 1024;           // + alignment slack
-  static_assert(SLOT % 1024 == 0 && qBytes % 512 == 0 && NBAR <= 64 && total <= 227 * 1024, "shared memory");
-  // tensor memory: S buffers, K scales per S buffer, query scales per operand
+  static_assert(SLOT % 1024 == 0 && qBytes % 512 == 0 && total <= 227 * 1024, "shared memory");
+  // tensor memory: S buffers, K scales per S buffer, query scales per group and operand
   static constexpr int SFA_COL = NSB * NQ, SFB_COL = SFA_COL + NSB * 4 * KS;
-  static constexpr int TMEM_COLS = SFB_COL + 2 * 4 * KS <= 256 ? 256 : 512;
-  static_assert(SFB_COL + 2 * 4 * KS <= TMEM_COLS, "tensor memory");
+  static constexpr int USED_COLS = SFB_COL + 2 * NWG * 4 * KS;
+  static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
+  static_assert(USED_COLS <= TMEM_COLS, "tensor memory");
 };
 
 struct Params {
@@ -106,16 +113,17 @@ struct Params {
 __host__ __device__ constexpr uint32_t idesc_fp4(int m, int n) {
   return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        uint32_t accumulate) {
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %6, 0; "
-      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p; }"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+      "{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %7, 0; mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3}; "
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %4, [%5], [%6], p; }"
+      ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
 }
 // 512 bytes of scales (32 rows of 16) to 4 columns of all four lane quarters
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo, uint32_t hi) {
+  asm volatile("{ .reg .b64 d; mov.b64 d, {%1, %2}; tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d; }"
+               ::"r"(taddr), "r"(lo), "r"(hi) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_small_zfill(uint32_t dst, const void* src, bool valid, uint64_t policy) {
@@ -145,6 +153,27 @@ __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
   return r;
 }
 
+// The tiles of one of `of` takers that take them in turn: the ring slot and its phase, how
+// many so far, and the item's first one (counted from the item's beginning).
+struct Turn {
+  int slot, first, count, ns, of;
+  uint32_t phase;
+  __device__ __forceinline__ Turn(int me, int ns_, int of_) : slot(me), first(me), count(0), ns(ns_), of(of_), phase(0) {}
+  __device__ __forceinline__ void step() {
+    ++count;
+    slot += of;
+    if (slot >= ns) {
+      slot -= ns;
+      phase ^= 1;
+    }
+  }
+  // behind an item of nt tiles
+  __device__ __forceinline__ void item(int nt) {
+    const int r = (first - nt) % of;
+    first = r < 0 ? r + of : r;
+  }
+};
+
 // (up to 2^31 - 1 tokens)
 __device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len + TILE - 1) / TILE); }
 
@@ -169,10 +198,10 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sb = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (sb - raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::barOff);   // [NS] tile copied (128 copy lanes)
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::barOff);   // [NS] tile copied (a copy warp's lanes)
   uint64_t* empty = full + NS;         // [NS] tile consumed (MMA commit, a group's 4 warps)
   uint64_t* qfull = empty + NS;        // [2] item published (4 copy warps)
-  uint64_t* qempty = qfull + 2;        // [2] item done (MMA commit, consumer warps)
+  uint64_t* qempty = qfull + 2;        // [2] item done (MMA commits, consumer warps)
   uint64_t* sfull = qempty + 2;        // [NSB] S ready (MMA commit)
   uint64_t* sfree = sfull + NSB;       // [NSB] S read (4 warps)
   uint64_t* staged = sfree + NSB;      // item states published (consumer warps)
@@ -184,12 +213,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 128);
+      mbar_init(&full[i], 32);
       mbar_init(&empty[i], 1 + 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], 4);
-      mbar_init(&qempty[i], 1 + NCW);
+      mbar_init(&qempty[i], NWG + NCW);
     }
     for (int i = 0; i < NSB; ++i) {
       mbar_init(&sfull[i], 1);
@@ -197,7 +226,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     }
     mbar_init(staged, NCW);
     mbar_init(merged, NCW);
-    mbar_init(done, 1);
+    mbar_init(done, NWG);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -212,6 +241,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 
   if (warp < NCW) {
     // ======================================================== consumer warps
+    reg_inc<S::REG_CONSUMER>();
     const int wg = warp >> 2, wq = warp & 3;
     const int g = lane >> 2, c = lane & 3;
     // sequences without tokens give 0
@@ -230,7 +260,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     const uint32_t slane = S::VS_OFF + (32 * wq + c) * (HD / 16) + (HD == 128 ? g : g >> 1);
     const float vscale = __ldg(p.v_scale);
     float o[NT][MT][4], ol[NT][4], m[R];
-    int j = 0;                                       // tiles of the CTA so far
+    Turn tn(wg, NS, NWG);
+    int merges = 0;                                  // row blocks joined so far
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int qb = n & 1;
@@ -247,19 +278,34 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) m[r] = kNoMax;
-      for (int i = 0; i < nt; ++i, ++j) {
-        if (j % NWG != wg) continue;
-        const int b = j % NSB, s = j % NS;
+      for (int i = tn.first; i < nt; i += NWG, tn.step()) {
+        const int b = 2 * wg + (tn.count & 1), s = tn.slot;
+        const uint32_t slot = sb + s * S::SLOT;
         const int tok = (t0 + i) * TILE + 32 * wq + lane;               // this lane's token
         const bool cut = (t0 + i + 1) * (long long)TILE > L;            // the sequence ends in this tile
-        if (!warp_wait(&sfull[b], (j / NSB) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        // ---- V's bytes, on their way while S is awaited
+        if (!warp_wait(&full[s], tn.phase, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        uint32_t w[8][HD / 64], sc[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t a = slot + vlane + 4 * u * ROW;
+          if constexpr (HD == 128) {
+            const uint2 d = lds64(a);
+            w[u][0] = d.x;
+            w[u][1] = d.y;
+          } else {
+            w[u][0] = lds32(a);
+          }
+          sc[u] = lds8(slot + slane + 4 * u * (HD / 16));
+        }
+        if (!warp_wait(&sfull[b], (tn.count >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
         for (int nb = 0; nb < NT; ++nb) {
           // ---- logits of 8 rows for this token: terms of weights 8^-k, times the row's factor
-          float v[32], w[16];
+          float v[32], v2[16];
           tmem_ld32(tl + b * NQ + nb * 8 * QT, v);
-          tmem_ld16(tl + b * NQ + nb * 8 * QT + 32, w);
+          tmem_ld16(tl + b * NQ + nb * 8 * QT + 32, v2);
           tmem_wait_ld();
           if (nb == NT - 1) {
             tc_fence_before();
@@ -269,9 +315,9 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           float x[8], e[8];
 #pragma unroll
           for (int r = 0; r < 8; r += 2) {
-            x[r] = w[8 + r];
-            x[r + 1] = w[9 + r];
-            fma2(x[r], x[r + 1], 0.125f, w[r], w[r + 1]);
+            x[r] = v2[8 + r];
+            x[r + 1] = v2[9 + r];
+            fma2(x[r], x[r + 1], 0.125f, v2[r], v2[r + 1]);
             fma2(x[r], x[r + 1], 0.125f, v[24 + r], v[25 + r]);
             fma2(x[r], x[r + 1], 0.125f, v[16 + r], v[17 + r]);
             fma2(x[r], x[r + 1], 0.125f, v[8 + r], v[9 + r]);
@@ -325,31 +371,17 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
         for (int nb = 0; nb < NT; ++nb) ldsm_x4_trans(prow + 512 * nb, pb[nb]);
         // ---- O^T += V^T P^T, 16 tokens at a time
-        if (!warp_wait(&full[s], (j / NS) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-        const uint32_t slot = sb + s * S::SLOT;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint32_t w[4][HD / 64], sc[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint32_t a = slot + vlane + (16 * k + 4 * u) * ROW;
-            if constexpr (HD == 128) {
-              const uint2 d = lds64(a);
-              w[u][0] = d.x;
-              w[u][1] = d.y;
-            } else {
-              w[u][0] = lds32(a);
-            }
-            sc[u] = lds8(slot + slane + (16 * k + 4 * u) * (HD / 16));
-          }
-          const uint32_t s01 = e4m3x2_lo_to_f16x2(sc[0] | (sc[1] << 8)), s23 = e4m3x2_lo_to_f16x2(sc[2] | (sc[3] << 8));
+          const uint32_t s01 = e4m3x2_lo_to_f16x2(sc[4 * k] | (sc[4 * k + 1] << 8));
+          const uint32_t s23 = e4m3x2_lo_to_f16x2(sc[4 * k + 2] | (sc[4 * k + 3] << 8));
 #pragma unroll
           for (int h = 0; h < HD / 64; ++h) {
             // nibbles of two tokens per byte: dims 2 i and 2 i + 1
-            const uint32_t ev01 = (w[0][h] & 0x0f0f0f0fu) | ((w[1][h] << 4) & 0xf0f0f0f0u);
-            const uint32_t od01 = ((w[0][h] >> 4) & 0x0f0f0f0fu) | (w[1][h] & 0xf0f0f0f0u);
-            const uint32_t ev23 = (w[2][h] & 0x0f0f0f0fu) | ((w[3][h] << 4) & 0xf0f0f0f0u);
-            const uint32_t od23 = ((w[2][h] >> 4) & 0x0f0f0f0fu) | (w[3][h] & 0xf0f0f0f0u);
+            const uint32_t ev01 = (w[4 * k][h] & 0x0f0f0f0fu) | ((w[4 * k + 1][h] << 4) & 0xf0f0f0f0u);
+            const uint32_t od01 = ((w[4 * k][h] >> 4) & 0x0f0f0f0fu) | (w[4 * k + 1][h] & 0xf0f0f0f0u);
+            const uint32_t ev23 = (w[4 * k + 2][h] & 0x0f0f0f0fu) | ((w[4 * k + 3][h] << 4) & 0xf0f0f0f0u);
+            const uint32_t od23 = ((w[4 * k + 2][h] >> 4) & 0x0f0f0f0fu) | (w[4 * k + 3][h] & 0xf0f0f0f0u);
             auto tile = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
               a0 = hmul2(a0, s01);
               a1 = hmul2(a1, s01);
@@ -371,81 +403,87 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         if (lane == 0) mbar_arrive(&empty[s]);
       }
       if (!ok) break;
+      tn.item(nt);
       __syncwarp();
       if (lane == 0) mbar_arrive(&qempty[qb]);
-      // ---- item done: the warps' states to shared memory, each warp joins a share of the rows
-      if (n > 0 && !warp_wait(merged, (n - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
+      // ---- item done: the warps' states to shared memory, a row block at a time; each warp
+      // joins one row of it
+      const int rbase = 16 * (who.y % RB), kvh = who.y / RB;
+      const int rows = min(R, p.qg - rbase);
       const uint32_t stg = sb + S::stgOff;
 #pragma unroll
-      for (int nb = 0; nb < NT; ++nb)
+      for (int nb = 0; nb < NT; ++nb, ++merges) {
+        if (merges > 0 && !warp_wait(merged, (merges - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t a = stg + 4 * ((warp * R + 8 * nb + 2 * c + hh) * S::STG_ROW + 2 * MT * g);
+          const uint32_t a = stg + 4 * ((warp * 8 + 2 * c + hh) * S::STG_ROW + 2 * MT * g);
 #pragma unroll
           for (int k = 0; k < MT; k += 2)
             sts_i4(a + 8 * k, make_int4(__float_as_int(o[nb][k][hh]), __float_as_int(o[nb][k][2 + hh]),
                                         __float_as_int(o[nb][k + 1][hh]), __float_as_int(o[nb][k + 1][2 + hh])));
-          if (g == 0) stsf(sb + S::mlOff + 8 * (warp * R + 8 * nb + 2 * c + hh) + 4, ol[nb][hh]);
+          if (g == 0) stsf(sb + S::mlOff + 8 * (warp * 8 + 2 * c + hh) + 4, ol[nb][hh]);
         }
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (lane == r) stsf(sb + S::mlOff + 8 * (warp * R + r), m[r]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(staged);
-      if (!warp_wait(staged, n & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
-      const int rbase = 16 * (who.y % RB), kvh = who.y / RB;
-      const int rows = min(R, p.qg - rbase);
-      for (int r = warp; r < rows; r += NCW) {
-        float mw[NCW], M = kNoMax, l = 0.f;
+        for (int r = 0; r < 8; ++r)
+          if (lane == r) stsf(sb + S::mlOff + 8 * (warp * 8 + r), m[8 * nb + r]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(staged);
+        if (!warp_wait(staged, merges & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        const int row = 8 * nb + warp;
+        if (row < rows) {
+          float mw[NCW], M = kNoMax, l = 0.f;
 #pragma unroll
-        for (int k = 0; k < NCW; ++k) {
-          mw[k] = ldsf(sb + S::mlOff + 8 * (k * R + r));
-          M = fmaxf(M, mw[k]);
-        }
-        float acc[HD / 32];
+          for (int k = 0; k < NCW; ++k) {
+            mw[k] = ldsf(sb + S::mlOff + 8 * (k * 8 + warp));
+            M = fmaxf(M, mw[k]);
+          }
+          float acc[HD / 32];
 #pragma unroll
-        for (int d = 0; d < HD / 32; ++d) acc[d] = 0.f;
+          for (int d = 0; d < HD / 32; ++d) acc[d] = 0.f;
 #pragma unroll
-        for (int k = 0; k < NCW; ++k) {
-          const float f = ex2(mw[k] - M);
-          l = fmaf(f, ldsf(sb + S::mlOff + 8 * (k * R + r) + 4), l);
-          const uint32_t a = stg + 4 * ((k * R + r) * S::STG_ROW + (HD / 32) * lane);
-          if constexpr (HD == 128) {
-            const float4 d = lds_f4(a);
-            acc[0] = fmaf(f, d.x, acc[0]);
-            acc[1] = fmaf(f, d.y, acc[1]);
-            acc[2] = fmaf(f, d.z, acc[2]);
-            acc[3] = fmaf(f, d.w, acc[3]);
+          for (int k = 0; k < NCW; ++k) {
+            const float f = ex2(mw[k] - M);
+            l = fmaf(f, ldsf(sb + S::mlOff + 8 * (k * 8 + warp) + 4), l);
+            const uint32_t a = stg + 4 * ((k * 8 + warp) * S::STG_ROW + (HD / 32) * lane);
+            if constexpr (HD == 128) {
+              const float4 d = lds_f4(a);
+              acc[0] = fmaf(f, d.x, acc[0]);
+              acc[1] = fmaf(f, d.y, acc[1]);
+              acc[2] = fmaf(f, d.z, acc[2]);
+              acc[3] = fmaf(f, d.w, acc[3]);
+            } else {
+              const uint2 d = lds64(a);
+              acc[0] = fmaf(f, __uint_as_float(d.x), acc[0]);
+              acc[1] = fmaf(f, __uint_as_float(d.y), acc[1]);
+            }
+          }
+          if (inf.w < 0) {
+            const float inv = vscale / l;
+            __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) +
+                                 ((long long)who.x * Hq + (long long)kvh * p.qg + rbase + row) * HD + (HD / 32) * lane;
+            if constexpr (HD == 128) store4(dst, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+            else *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
           } else {
-            const uint2 d = lds64(a);
-            acc[0] = fmaf(f, __uint_as_float(d.x), acc[0]);
-            acc[1] = fmaf(f, __uint_as_float(d.y), acc[1]);
+            float* dst = p.part_o + ((long long)inf.w * 16 + row) * HD + (HD / 32) * lane;
+            if constexpr (HD == 128) store4(dst, acc[0], acc[1], acc[2], acc[3]);
+            else *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
+            if (lane == 0) p.part_ml[inf.w * 16 + row] = make_float2(M, l);
           }
         }
-        if (inf.w < 0) {
-          const float inv = vscale / l;
-          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) +
-                               ((long long)who.x * Hq + kvh * p.qg + rbase + r) * HD + (HD / 32) * lane;
-          if constexpr (HD == 128) store4(dst, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-          else *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
-        } else {
-          float* dst = p.part_o + ((long long)inf.w * 16 + r) * HD + (HD / 32) * lane;
-          if constexpr (HD == 128) store4(dst, acc[0], acc[1], acc[2], acc[3]);
-          else *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
-          if (lane == 0) p.part_ml[inf.w * 16 + r] = make_float2(M, l);
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(merged);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(merged);
     }
   } else if (warp < S::WARP_MMA) {
     // ======================================================== copy warps
+    reg_dec<S::REG_COPY>();
     const int pw = warp - S::WARP_COPY, pt = 32 * pw + lane;
     const uint64_t pol = policy_evict_first();
-    constexpr int CPR = ROW / 16, RPI = 32 / CPR, NII = 32 / RPI;       // 16-byte chunks per token, tokens per instruction
+    constexpr int CPR = ROW / 16, RPI = 32 / CPR;                       // 16-byte chunks per token, tokens per instruction
     const int lr = lane / CPR, cc = lane % CPR;
-    const uint32_t kdst = (32 * pw + lr) * ROW + ((HD == 128 ? cc ^ ((lr >> 1) & 3) : cc ^ ((lr >> 2) & 1)) << 4);
-    const uint32_t vdst = S::V_OFF + (32 * pw + lr) * ROW + ((HD == 128 ? cc ^ (lr & 2) : cc) << 4);
+    const uint32_t kdst = lr * ROW + ((HD == 128 ? cc ^ ((lr >> 1) & 3) : cc ^ ((lr >> 2) & 1)) << 4);
+    const uint32_t vdst = S::V_OFF + lr * ROW + ((HD == 128 ? cc ^ (lr & 2) : cc) << 4);
+    const uint32_t src_lane = lr * ROW + 16 * cc;
     const size_t chunk = size_t(bs) * (HD / 2 + HD / 16), plane = size_t(Hk) * chunk;
 
     // ---- the CTA's range of units, and the item that holds its first one
@@ -522,7 +560,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     uint4 qv[NT];
     load_q(cur, qv);
     int32_t ent0 = load_entries(cur.s, (int)(((long long)cur.t * TILE) >> lbs));
-    int j = 0, n = 0;
+    Turn tn(pw, NS, 4);
+    int n = 0;
     int4 meta = make_int4(0, 0, 0, 0);
     bool ok = true;
     while (cur.s >= 0 && ok) {
@@ -545,57 +584,58 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       const uint8_t* kbase = p.kv + size_t(cur.vh / RB) * chunk;
       int e0 = (int)(((long long)cur.t * TILE) >> lbs);
       int32_t ent = ent0, ent_next = load_entries(cur.s, e0 + 32);
-      int ti = 0;
+      int ti = tn.first;
+      // this warp's tiles of the item, below `end`
       auto issue_to = [&](int end) -> bool {
-        for (; ti < end; ++ti, ++j) {
-          const int s = j % NS;
-          if (j >= NS && !warp_wait(&empty[s], (j / NS - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
-          const int tok0 = (cur.t + ti) * TILE + 32 * pw;               // this warp's 32 tokens
-          if (((cur.t + ti) * TILE >> lbs) - e0 >= 32) {
+        for (; ti < end; ti += 4, tn.step()) {
+          const int s = tn.slot, tok0 = (cur.t + ti) * TILE;
+          if (tn.count * 4 + pw >= NS && !warp_wait(&empty[s], tn.phase ^ 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
+          while ((tok0 >> lbs) - e0 >= 32) {
             e0 += 32;
             ent = ent_next;
             ent_next = load_entries(cur.s, e0 + 32);
           }
           // (a tile's blocks never straddle two groups of 32 entries: 32 blocks are whole tiles, from a tile's first on)
-          int pa = __shfl_sync(0xffffffffu, ent, ((tok0 >> lbs) - e0) & 31);
-          int pb = __shfl_sync(0xffffffffu, ent, (((tok0 + 16) >> lbs) - e0) & 31);
-          if (pa < 0 || pa >= p.num_blocks) {
-            if (tok0 < L && lane == 0) atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
-            pa = 0;
-          }
-          if (pb < 0 || pb >= p.num_blocks) {
-            if (tok0 + 16 < L && lane == 0) atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
-            pb = 0;
-          }
-          // tokens tok0 .. + 15 lie in block pa at offset oa, tokens tok0 + 16 .. in pb at ob
-          const int oa = tok0 & (bs - 1), ob = (tok0 + 16) & (bs - 1);
-          const uint8_t* ca = kbase + size_t(pa) * 2 * plane;
-          const uint8_t* cb = kbase + size_t(pb) * 2 * plane;
           const uint32_t slot = sb + s * S::SLOT;
+          const bool whole = tok0 + (TILE - 1) < L;
+          const uint8_t* base_lo = nullptr;
 #pragma unroll
-          for (int ii = 0; ii < NII; ++ii) {
-            const int r = lr + RPI * ii;
-            const bool lowhalf = RPI * ii < 16;
-            const uint8_t* src = (lowhalf ? ca + size_t(oa + r) * ROW : cb + size_t(ob + r - 16) * ROW) + 16 * cc;
-            const bool valid = tok0 + r < L;
-            cp_async16_zfill(slot + kdst + RPI * ii * ROW, src, valid, pol);
-            cp_async16_zfill(slot + vdst + RPI * ii * ROW, src + plane, valid, pol);
-          }
-          {
-            const uint8_t* src = (lane < 16 ? ca + size_t(oa + lane) * (HD / 16) : cb + size_t(ob + lane - 16) * (HD / 16)) +
-                                 size_t(bs) * ROW;
-            const bool valid = tok0 + lane < L;
+          for (int q = 0; q < TILE / 16; ++q) {
+            // tokens 16 q .. 16 q + 15 of the tile lie in one block
+            const int tok = tok0 + 16 * q;
+            int blk = __shfl_sync(0xffffffffu, ent, ((tok >> lbs) - e0) & 31);
+            if (blk < 0 || blk >= p.num_blocks) {
+              if (tok < L && lane == 0) atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
+              blk = 0;
+            }
+            const int off = tok & (bs - 1);
+            const uint8_t* base = kbase + size_t(blk) * 2 * plane;
+            const uint8_t* src = base + uint32_t(off * ROW) + src_lane;
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
-              cp_async_small_zfill<4>(slot + S::KS_OFF + 512 * k + 16 * lane + 4 * pw, src + 4 * k, valid, pol);
-            cp_async_small_zfill<HD / 16>(slot + S::VS_OFF + (32 * pw + lane) * (HD / 16), src + plane, valid, pol);
+            for (int ii = 0; ii < 16 / RPI; ++ii) {
+              const bool valid = whole || tok + RPI * ii + lr < L;
+              cp_async16_zfill(slot + kdst + (16 * q + RPI * ii) * ROW, src + RPI * ii * ROW, valid, pol);
+              cp_async16_zfill(slot + vdst + (16 * q + RPI * ii) * ROW, src + plane + RPI * ii * ROW, valid, pol);
+            }
+            // scales, 32 tokens at a time: lane = token
+            const uint8_t* sbase = base + uint32_t(bs * ROW + off * (HD / 16));
+            if (q & 1) {
+              const uint8_t* ssrc = lane < 16 ? base_lo + lane * (HD / 16) : sbase + (lane - 16) * (HD / 16);
+              const bool valid = whole || tok - 16 + lane < L;
+#pragma unroll
+              for (int k = 0; k < KS; ++k)
+                cp_async_small_zfill<4>(slot + S::KS_OFF + 512 * k + 16 * lane + 4 * (q >> 1), ssrc + 4 * k, valid, pol);
+              cp_async_small_zfill<HD / 16>(slot + S::VS_OFF + (16 * (q - 1) + lane) * (HD / 16), ssrc + plane, valid, pol);
+            } else {
+              base_lo = sbase;
+            }
           }
           cp_async_arrive_noinc(&full[s]);
         }
         return true;
       };
-      // the first tile goes out before the operand is built
-      if (n == 0 && !issue_to(1)) break;
+      // the first tiles go out before the operand is built
+      if (n == 0 && !issue_to(min(nt, 4))) break;
       const int qb = n & 1;
       if (n >= 2 && !warp_wait(&qempty[qb], ((n >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       // ---- query operand
@@ -677,6 +717,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       if (lane == 0) mbar_arrive(&qfull[qb]);
       ++n;
       if (!issue_to(nt)) break;
+      tn.item(nt);
       u += nt;
       cur = nxt;
 #pragma unroll
@@ -695,40 +736,54 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     if (pt == 0) p.meta[blockIdx.x] = meta;
     cp_async_wait_all();
   } else {
-    // ======================================================== MMA warp
-    if (lane == 0) {
-      int j = 0;
-      bool ok = true;
-      for (int n = 0; ok; ++n) {
-        const int qb = n & 1;
-        if (!role_wait(&qfull[qb], (n >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
-        const int nt = lds_i4(sb + S::infoOff + 64 * qb).z;
-        if (nt == 0) break;
-        const uint32_t qa = sb + S::qOff + qb * S::qBytes, sfb = tmem + S::SFB_COL + qb * 4 * KS;
-        for (int i = 0; i < nt; ++i, ++j) {
-          const int s = j % NS, b = j % NSB;
-          if (!role_wait(&full[s], (j / NS) & 1, abort_flag, KERR_TIMEOUT_FULL) ||
-              (j >= NSB && !role_wait(&sfree[b], (j / NSB - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY))) {
-            ok = false;
-            break;
-          }
-          fence_proxy_async();     // the copied bytes (generic proxy) become visible to the tensor core
-          tc_fence_after();
-          const uint32_t ka = sb + s * S::SLOT, sfa = tmem + S::SFA_COL + b * 4 * KS;
+    // ======================================================== MMA warps, one per consumer group
+    reg_dec<S::REG_MMA>();
+    const int wg = warp - S::WARP_MMA;
+    if (wg < NWG) {
+    Turn tn(wg, NS, NWG);
+    bool ok = true;
+    const uint32_t sfb0 = tmem + S::SFB_COL + wg * 8 * KS;
+    // descriptors: the low half is the address (plus constants), the high half constant
+    constexpr uint32_t OP_HI = desc_hi(8 * ROW, SWZ), SC_HI = desc_hi(128, kSwizzleNone);
+    for (int n = 0; ok; ++n) {
+      const int qb = n & 1;
+      if (!warp_wait(&qfull[qb], (n >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+      const int nt = lds_i4(sb + S::infoOff + 64 * qb).z;
+      if (nt == 0) break;
+      const uint32_t sfb = sfb0 + qb * 4 * KS;
+      const uint32_t q_lo = desc_lo(sb + S::qOff + qb * S::qBytes, 16);
+      if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            if (i == 0) copy_scales(sfb + 4 * k, umma_desc(sb + S::qsOff + (qb * KS + k) * 512, 16, 128, kSwizzleNone));
-            copy_scales(sfa + 4 * k, umma_desc(ka + S::KS_OFF + 512 * k, 16, 128, kSwizzleNone));
-          }
+        for (int k = 0; k < KS; ++k)
+          copy_scales(sfb + 4 * k, desc_lo(sb + S::qsOff + (qb * KS + k) * 512, 16), SC_HI);
+      }
+      for (int i = tn.first; i < nt; i += NWG, tn.step()) {
+        const int s = tn.slot, b = 2 * wg + (tn.count & 1);
+        if ((tn.count >= 2 && !warp_wait(&sfree[b], ((tn.count >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) ||
+            !warp_wait(&full[s], tn.phase, abort_flag, KERR_TIMEOUT_FULL)) {
+          ok = false;
+          break;
+        }
+        fence_proxy_async();     // the copied bytes (generic proxy) become visible to the tensor core
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t k_lo = desc_lo(sb + s * S::SLOT, 16), sfa = tmem + S::SFA_COL + b * 4 * KS;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) copy_scales(sfa + 4 * k, k_lo + (S::KS_OFF + 512 * k) / 16, SC_HI);
 #pragma unroll
           for (int k = 0; k < KS; ++k)
-            mma_fp4(tmem + b * NQ, umma_desc(ka + 32 * k, 16, 8 * ROW, SWZ), umma_desc(qa + 32 * k, 16, 8 * ROW, SWZ),
-                    idesc_fp4(128, NQ), sfa + 4 * k, sfb + 4 * k, k);
+            mma_fp4(tmem + b * NQ, k_lo + 2 * k, q_lo + 2 * k, OP_HI, idesc_fp4(128, NQ), sfa + 4 * k, sfb + 4 * k, k);
           umma_commit(&sfull[b]);
           umma_commit(&empty[s]);
-          if (i == nt - 1) umma_commit(&qempty[qb]);
         }
+        __syncwarp();
       }
+      if (!ok) break;
+      tn.item(nt);
+      if (elect_one()) umma_commit(&qempty[qb]);
+      __syncwarp();
+    }
+    if (elect_one()) {
       // every MMA must finish before the tensor memory is released
       umma_commit(done);
       if (!mbar_try_wait(done, 0)) {
@@ -742,6 +797,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       }
     }
     __syncwarp();
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -802,6 +858,12 @@ __global__ void __launch_bounds__(128) decode4_combine_kernel(const d4::Params p
     const long long row = (long long)meta.y * p.num_kv_heads * p.qg + (meta.z / p.row_blocks) * p.qg + rbase + r;
     reinterpret_cast<__nv_bfloat16*>(p.out)[row * HD + threadIdx.x] = __float2bfloat16_rn(num * (__ldg(p.v_scale) / den));
   }
+}
+
+cudaError_t take_decode4_error(int* v) {
+  const int z = 0;
+  const cudaError_t e = cudaMemcpyFromSymbol(v, g_kernel_error, sizeof(int));
+  return e == cudaSuccess && *v ? cudaMemcpyToSymbol(g_kernel_error, &z, sizeof(int)) : e;
 }
 
 // two slots of 16 rows per CTA, and what begins in it

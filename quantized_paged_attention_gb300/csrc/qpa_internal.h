@@ -247,6 +247,8 @@ cudaError_t launch_append4(const Append4Launch& a, cudaStream_t stream);
 cudaError_t launch_gather(const GatherLaunch& a, cudaStream_t stream);
 // Workspace bytes of a 4-bit decode (independent of the device).
 size_t decode4_workspace_bytes(int query_group, int head_dim);
+// Reads and clears the 4-bit decode's own error word of the current device.
+cudaError_t take_decode4_error(int* v);
 cudaError_t launch_decode4(const Decode4Launch& a, cudaStream_t stream);
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
