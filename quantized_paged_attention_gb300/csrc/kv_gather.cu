@@ -7,9 +7,15 @@
 // through the tile, UN rows in flight: 4 bytes of e2m1 codes and a scale byte, or 8 e4m3
 // codes, to 16 bytes of bf16. Bound: 0.5625 (fp8: 1) bytes in and 2 out per element.
 //
-// A value is code * group scale (exact in float32: 2 by 4 bits) times the tensor's
-// scale of 24 bits, rounded once: the product is cut to float32 with the lost bits as a
-// sticky last bit, which the rounding to bf16 then sees.
+// A value is code * group scale (x, at most 6 bits, exact in f16) times a scale g of 24
+// bits, rounded once. Rounded to float32 first, a product next to a midpoint of two bf16
+// would land on it and then go to the wrong side. For one g all such products lie on the
+// same side of theirs: g is m / x times 1 + d, |d| < 2^-24, for a midpoint m of 9 bits, and
+// two such quotients are equal or 2^-15 apart. So a g per tensor is moved by one step to
+// d's side where there is such an x (13 odd ones tried by as many lanes), and a value
+// costs one multiplication. Scales per token keep the lost bits of a truncated product as
+// a sticky last bit instead. (Sticky bits for all: 7.5 instructions per element, ALU 62 %
+// busy, 52 us where this takes {READ}.)
 #include <type_traits>
 
 #include "qpa.h"
@@ -24,10 +30,28 @@ constexpr int kThreads = 256;
 constexpr int kMaxTile = 64;        // rows of a block
 enum : long long { kSkip = -1, kZero = -2 };
 
-// x * g rounded to bf16 once (as bits in the low half)
+// x * g cut to float32, the last bit set if bits were lost
 __device__ __forceinline__ uint32_t mul_sticky(float x, float g) {
   const float p = __fmul_rz(x, g);
-  return __float_as_uint(p) | (fmaf(x, g, -p) != 0.f ? 1u : 0u);
+  return __float_as_uint(p) | min(__float_as_uint(fmaf(x, g, -p)), 1u);
+}
+// g such that x * g in float32 rounds to bf16 as the exact product does, for the x of at
+// most 6 bits that codes and group scales make; in every lane of a warp.
+__device__ __forceinline__ float side_of_midpoints(float g, int lane) {
+  // odd parts of (1, 3) by (1, 3, .. 15): 1, 3, .. 15, 21, 27, 33, 39, 45
+  const int odd = (lane & 15) < 8 ? 2 * (lane & 7) + 1 : min(21 + 6 * (lane & 7), 45);
+  const float x = (float)odd, p = x * g, d = fmaf(x, g, -p);
+  const bool on = (__float_as_uint(p) & 0xffffu) == 0x8000u;
+  // (relative to g's sign, so that the step is one of g's magnitude)
+  const unsigned above = __ballot_sync(0xffffffffu, on && (g > 0.f ? d > 0.f : d < 0.f));
+  const unsigned below = __ballot_sync(0xffffffffu, on && (g > 0.f ? d < 0.f : d > 0.f));
+  return above ? __uint_as_float(__float_as_uint(g) + 1) : below ? __uint_as_float(__float_as_uint(g) - 1) : g;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(float a, float b, float g) {
+  uint32_t r;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%1, %2}; mov.b64 y, {%3, %3}; mul.rn.f32x2 x, x, y; .reg .f32 u, v; "
+      "mov.b64 {u, v}, x; cvt.rn.bf16x2.f32 %0, v, u; }" : "=r"(r) : "f"(a), "f"(b), "f"(g));
+  return r;
 }
 __device__ __forceinline__ uint32_t bf16x2(uint32_t lo, uint32_t hi) {
   uint32_t r;
@@ -64,8 +88,12 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherLaunch p, 
                                                           const int tile) {
   constexpr int TPR = HD / 8;                  // threads per head vector
   constexpr int UN = 4;
-  __shared__ long long s_slot[kMaxTile];
+  __shared__ long long s_at[kMaxTile];        // the row's code bytes (of plane 0, head 0) in the cache, or kSkip, kZero
+  __shared__ long long s_scale[FP4 ? 1 : kMaxTile];   // its scale of head 0 (per token)
+  __shared__ int s_off[kMaxTile];              // its offset in the block
   const int Hk = p.num_kv_heads, bs = p.block_size, R = p.num_reqs;
+  constexpr int CB = FP4 ? HD / 2 : HD;        // code bytes of a token and head
+  const size_t chunk = size_t(bs) * (FP4 ? HD / 2 + HD / 16 : HD), block_bytes = p.planes * Hk * chunk;
   const long long row0 = (long long)blockIdx.x * tile;
   const int rows = (int)min((long long)tile, p.num_tokens - row0);
   if ((int)threadIdx.x < rows) {
@@ -79,75 +107,87 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherLaunch p, 
       else hi = mid;
     }
     const int r = lo - 1;
-    long long slot = kSkip;
+    long long at = kSkip;
+    int off = 0;
     if (r >= 0 && r < R) {
       const long long cap = (long long)p.max_blocks * bs;
       const long long L = max(0LL, min((long long)__ldg(p.seq_lens + r), cap));
       const long long t = L - (start(r + 1) - row);
-      slot = kZero;
+      at = kZero;
       if (t >= 0) {
         int blk = __ldg(p.block_table + r * p.table_stride + (t >> log2_bs));
         if (blk < 0 || blk >= p.num_blocks) {
           atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
           blk = 0;
         }
-        slot = (long long)blk * bs + (t & (bs - 1));
+        off = (int)(t & (bs - 1));
+        at = (long long)(blk * block_bytes) + off * CB;
+        if (!FP4) s_scale[threadIdx.x] = (long long)blk * Hk * bs + off;
       }
     }
-    s_slot[threadIdx.x] = slot;
+    s_at[threadIdx.x] = at;
+    s_off[threadIdx.x] = off;
+  }
+  float gk = 0.f, gv = 0.f;
+  if (!F32 && !p.per_token) {
+    gk = side_of_midpoints(__ldg(p.k_scale), threadIdx.x & 31);
+    gv = side_of_midpoints(__ldg(p.v_scale), threadIdx.x & 31);
   }
   __syncthreads();
   const int tpt = p.planes * Hk * TPR;         // threads per token
   const int mine = threadIdx.x / tpt;
-  constexpr int CB = FP4 ? HD / 2 : HD;        // code bytes of a token and head
-  const size_t chunk = size_t(bs) * (FP4 ? HD / 2 + HD / 16 : HD);
   for (int i0 = 0; i0 < tpt; i0 += kThreads) {
     const int i = side > 1 ? threadIdx.x - mine * tpt : i0 + threadIdx.x;
     if (side > 1 ? mine >= side : i >= tpt) break;
     const int part = i % TPR, vec = i / TPR, kv = vec >= Hk && p.planes > 1, h = vec - kv * Hk;
     const float* scales = kv ? p.v_scale : p.k_scale;
-    const float g0 = p.per_token ? 0.f : __ldg(scales);
+    const float g0 = p.per_token ? 0.f : F32 ? __ldg(scales) : kv ? gv : gk;
     const size_t esz = F32 ? 4 : 2;
+    const uint8_t* in = p.kv + (size_t(kv) * Hk + h) * chunk + part * (FP4 ? 4 : 8);
+    const uint32_t to_scale = bs * CB + (part >> 1) - 4 * part;         // (NVFP4, at offset 0)
+    const size_t row_bytes = size_t(Hk) * (HD * esz);
     uint8_t* out = static_cast<uint8_t*>(kv ? p.out_v : p.out_k) + (row0 * Hk + h) * (HD * esz) + part * (8 * esz);
     for (int r0 = side > 1 ? mine : 0; r0 < rows; r0 += UN * side) {
       uint32_t lo[UN], hi[UN], sc[UN];
       float g[UN];
-      long long slot[UN];
+      long long at[UN];
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
         const int r = r0 + u * side;
-        slot[u] = r < rows ? s_slot[r] : (long long)kSkip;
+        at[u] = r < rows ? s_at[r] : (long long)kSkip;
         lo[u] = hi[u] = sc[u] = 0;
         g[u] = g0;
-        if (slot[u] >= 0) {
-          const long long blk = slot[u] >> log2_bs;
-          const int off = (int)(slot[u] & (bs - 1));
-          const uint8_t* src = p.kv + ((blk * p.planes + kv) * Hk + h) * chunk;
+        if (at[u] >= 0) {
+          const uint8_t* src = in + at[u];
           if constexpr (FP4) {
-            lo[u] = __ldcs(reinterpret_cast<const uint32_t*>(src + size_t(off) * CB) + part);
-            sc[u] = __ldcs(src + size_t(bs) * CB + size_t(off) * (HD / 16) + (part >> 1));
+            lo[u] = __ldg(reinterpret_cast<const uint32_t*>(src));
+            sc[u] = __ldg(src + to_scale - s_off[r] * (CB - HD / 16));
           } else {
-            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src + size_t(off) * CB) + part);
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
             lo[u] = v.x;
             hi[u] = v.y;
-            if (p.per_token) g[u] = __ldg(scales + (blk * Hk + h) * bs + off);
+            if (p.per_token) {
+              g[u] = __ldg(scales + s_scale[r] + (long long)h * bs);
+            }
           }
         }
       }
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
-        if (slot[u] == kSkip) continue;
+        if (at[u] == kSkip) continue;
         float x[8];
         values8<FP4>(lo[u], hi[u], sc[u], x);
-        if (slot[u] < 0) g[u] = 0.f;
-        uint8_t* dst = out + size_t(r0 + u * side) * Hk * (HD * esz);
+        if (at[u] < 0) g[u] = 0.f;
+        uint8_t* dst = out + size_t(r0 + u * side) * row_bytes;
         if constexpr (F32) {
           reinterpret_cast<float4*>(dst)[0] = make_float4(x[0] * g[u], x[1] * g[u], x[2] * g[u], x[3] * g[u]);
           reinterpret_cast<float4*>(dst)[1] = make_float4(x[4] * g[u], x[5] * g[u], x[6] * g[u], x[7] * g[u]);
         } else {
           uint32_t w[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = bf16x2(mul_sticky(x[2 * j], g[u]), mul_sticky(x[2 * j + 1], g[u]));
+          for (int j = 0; j < 4; ++j)
+            w[j] = !FP4 && p.per_token ? bf16x2(mul_sticky(x[2 * j], g[u]), mul_sticky(x[2 * j + 1], g[u]))
+                                       : mul_bf16x2(x[2 * j], x[2 * j + 1], g[u]);
           *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
@@ -164,7 +204,7 @@ cudaError_t launch_gather(const GatherLaunch& a, cudaStream_t stream) {
   const long long tpt = (long long)a.planes * a.num_kv_heads * (a.head_dim / 8);
   const int side = (int)std::max(1LL, kThreads / tpt);
   // tiles small enough that every SM has a few blocks, large enough to share the search
-  const long long per = ((long long)a.num_tokens + 8LL * a.num_sms - 1) / (8LL * a.num_sms);
+  const long long per = ((long long)a.num_tokens + 4LL * a.num_sms - 1) / (4LL * a.num_sms);
   const int tile = (int)std::min<long long>(kMaxTile, std::max<long long>(per, side));
   const int grid = (int)(((long long)a.num_tokens + tile - 1) / tile);
   auto launch = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(a, log2_bs, side, tile); };

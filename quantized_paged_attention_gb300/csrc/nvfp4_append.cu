@@ -4,17 +4,16 @@
 // A thread takes one scale group: 16 elements (32 bytes in, 8 bytes of codes and
 // a scale byte out). Bound: 2 bytes in and 0.5625 out per element.
 //
-// Rounding, exact as kv_append_fp8's. With g the tensor's scale and a the group's
-// largest |x|:
-//  * s = e4m3(a / 6g): the quotient in float32 gives the code below it, and the
-//    sign of the fma a - 6 m g (m the midpoint above, 5 bits, 6 m has 7: exact)
-//    decides between the two.
-//  * code = e2m1(x / S), S = s g held as two floats (28 bits: exact). q = x hi + x lo
-//    with hi + lo = 1/S to 2^-40, so a midpoint comes out as that midpoint and a
-//    quotient 2^-18 away from one stays on its side. Midpoints have significands
-//    1, 3, 5 and 7, x has 8 bits: for a given S all quotients that are within 2^-18
-//    of a midpoint without being one lie on the same side of theirs (two of 8 by 3
-//    bits are equal or 2^-11 apart), and hi is moved by 2^-20 to that side.
+// Rounding, exact as kv_append_fp8's: with q = x hi + x lo, hi + lo = 1/S to 2^-40, a
+// quotient that is a midpoint of two codes comes out as that midpoint and one 2^-18 away
+// stays on its side. x has 8 bits and a midpoint's significand 3 (e2m1) or 5 (e4m3): for one
+// S all quotients within 2^-18 of a midpoint without being one lie on the same side of
+// theirs (two such are equal or 2^-11, 2^-13 apart), and hi is moved by 2^-20 to that side.
+//  * s = e4m3(a / 6g), a the group's largest |x|: S = 6 g, the same for the whole call.
+//  * code = e2m1(x / (s g)): S = s g, held as two floats (28 bits: exact), one of 126 for
+//    a call. A block makes the 126 pairs (hi, lo) once, into shared memory, and a group
+//    looks its own up. (Made per group: 170 instructions more, ALU-bound, 27 us for 16384
+//    tokens x 8 heads x 128 where this takes {APP}.)
 #include "qpa.h"
 #include "common.cuh"
 #include "qpa_internal.h"
@@ -77,66 +76,84 @@ __device__ __noinline__ uint32_t e2m1_exact(float x, float s, float g) {
   return c | sign;
 }
 
-// (a, b) * hi + (a, b) * lo as two e2m1 codes, a in the low nibble
-__device__ __forceinline__ uint32_t quant2(float a, float b, float hi, float lo) {
+// 8 bf16 (pairs a, b, c, d) times hi + lo as e2m1 codes, the first in the lowest nibble
+__device__ __forceinline__ uint32_t quant8(uint32_t a, uint32_t b, uint32_t c, uint32_t d, float hi, float lo) {
   uint32_t r;
-  asm("{ .reg .b64 x, y, z; .reg .b8 t; .reg .f32 u, v; mov.b64 x, {%1, %2}; mov.b64 y, {%3, %3}; mov.b64 z, {%4, %4}; "
-      "mul.rn.f32x2 z, x, z; fma.rn.f32x2 x, x, y, z; mov.b64 {u, v}, x; "
-      "cvt.rn.satfinite.e2m1x2.f32 t, v, u; cvt.u32.u8 %0, t; }" : "=r"(r) : "f"(a), "f"(b), "f"(hi), "f"(lo));
+  asm("{ .reg .b64 x, y, z, h, l; .reg .b8 p, q, r, s; .reg .f32 u, v; mov.b64 h, {%9, %9}; mov.b64 l, {%10, %10}; "
+      "mov.b64 x, {%1, %2}; mul.rn.f32x2 z, x, l; fma.rn.f32x2 x, x, h, z; mov.b64 {u, v}, x; cvt.rn.satfinite.e2m1x2.f32 p, v, u; "
+      "mov.b64 x, {%3, %4}; mul.rn.f32x2 z, x, l; fma.rn.f32x2 x, x, h, z; mov.b64 {u, v}, x; cvt.rn.satfinite.e2m1x2.f32 q, v, u; "
+      "mov.b64 x, {%5, %6}; mul.rn.f32x2 z, x, l; fma.rn.f32x2 x, x, h, z; mov.b64 {u, v}, x; cvt.rn.satfinite.e2m1x2.f32 r, v, u; "
+      "mov.b64 x, {%7, %8}; mul.rn.f32x2 z, x, l; fma.rn.f32x2 x, x, h, z; mov.b64 {u, v}, x; cvt.rn.satfinite.e2m1x2.f32 s, v, u; "
+      "mov.b32 %0, {p, q, r, s}; }"
+      : "=r"(r)
+      : "f"(bf_lo(a)), "f"(bf_hi(a)), "f"(bf_lo(b)), "f"(bf_hi(b)), "f"(bf_lo(c)), "f"(bf_hi(c)), "f"(bf_lo(d)),
+        "f"(bf_hi(d)), "f"(hi), "f"(lo));
   return r;
 }
 
-// 16 elements (bf16 pairs w) -> 8 bytes of codes, the scale byte in `sc`. `ok`: g is
-// positive and finite.
-__device__ __forceinline__ uint2 quantise16(const uint32_t (&w)[8], float g, bool ok, uint32_t& sc) {
-  uint32_t m2 = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) amax2_nan(m2, w[j]);
-  float a = fmaxf(bf_lo(m2), bf_hi(m2));
-  const bool nan = (m2 & 0x7fffu) > 0x7f80u || ((m2 >> 16) & 0x7fffu) > 0x7f80u;
-  if (nan || !ok) {
-    sc = 0x7fu;
-    return make_uint2(0, 0);
-  }
-  a = fminf(a, 3.38953139e38f);                    // an infinity counts as the largest bf16
-  sc = scale_code(a, g);
-  const uint32_t e = sc >> 3, f = sc & 7u;
-  const float s = e ? __uint_as_float(((e + 120u) << 23) | (f << 20)) : (float)f * 0.001953125f;
-  if (!(g > kTiny && g < kHuge)) {
-    uint32_t o[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t v = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v |= (e2m1_exact(bf_lo(w[4 * h + j]), s, g) | (e2m1_exact(bf_hi(w[4 * h + j]), s, g) << 4)) << (8 * j);
-      o[h] = v;
-    }
-    return make_uint2(o[0], o[1]);
-  }
+__device__ __forceinline__ float e4m3_value(uint32_t c) {       // 0 .. 0x7E
+  const uint32_t e = c >> 3, f = c & 7u;
+  return e ? __uint_as_float(((e + 120u) << 23) | (f << 20)) : (float)f * 0.001953125f;
+}
+
+// hi + lo = 1/(s g), hi moved past the near midpoints of significands 1, 3, .. up to `odd`.
+// g in (2^-90, 2^90), s in 2^-9 .. 448.
+__device__ __forceinline__ float2 reciprocal(float s, float g, int odd) {
   const float S = s * g, Sl = fmaf(s, g, -S);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(S));       // within 2^-23
   const float h = r * (1.f - 2.38418579e-7f);                 // 2^-22: below 1/S, so that lo has the sign of hi
   const float lo = (fmaf(-S, h, 1.f) - Sl * h) * h;
   float side = 0.f;                                           // the sign of m S - x for the near midpoints
-#pragma unroll
-  for (int k = 1; k < 8; k += 2) {
+  for (int k = 1; k <= odd; k += 2) {
     const float v = k * S, x = __bfloat162float(__float2bfloat16_rn(v));
     const float d = fmaf(k * s, g, -x);
     side = (fabsf(v - x) <= v * 3.81469727e-6f && d != 0.f) ? d : side;
   }
-  const float hi = h * (side > 0.f ? 1.f - 9.53674316e-7f : side < 0.f ? 1.f + 9.53674316e-7f : 1.f);
-  uint32_t o[2];
+  return make_float2(h * (side > 0.f ? 1.f - 9.53674316e-7f : side < 0.f ? 1.f + 9.53674316e-7f : 1.f), lo);
+}
+
+// A plane's scale: g, its kind, 1/6g
+struct Tensor {
+  float g;
+  bool ok, fast;           // positive and finite; within the reciprocals' range
+  float2 sixth;
+};
+
+// 16 elements (bf16 pairs w) -> 8 bytes of codes, the scale byte in `sc`
+__device__ __forceinline__ uint2 quantise16(const uint32_t (&w)[8], const Tensor& t, const float2* table, uint32_t& sc) {
+  uint32_t m2 = 0;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint32_t c0 = quant2(bf_lo(w[4 * q]), bf_hi(w[4 * q]), hi, lo);
-    const uint32_t c1 = quant2(bf_lo(w[4 * q + 1]), bf_hi(w[4 * q + 1]), hi, lo);
-    const uint32_t c2 = quant2(bf_lo(w[4 * q + 2]), bf_hi(w[4 * q + 2]), hi, lo);
-    const uint32_t c3 = quant2(bf_lo(w[4 * q + 3]), bf_hi(w[4 * q + 3]), hi, lo);
-    o[q] = prmt(c0 | (c1 << 8), c2 | (c3 << 8), 0x5410u);
+  for (int j = 0; j < 8; ++j) amax2_nan(m2, w[j]);
+  float a = fmaxf(bf_lo(m2), bf_hi(m2));
+  // (a NaN's bits are above infinity's; fmaxf keeps a number beside a NaN)
+  const bool nan = max(m2 & 0xffffu, m2 >> 16) > 0x7f80u;
+  a = fminf(a, 3.38953139e38f);                    // an infinity counts as the largest bf16
+  if (!t.fast) {
+    if (nan || !t.ok) {
+      sc = 0x7fu;
+      return make_uint2(0, 0);
+    }
+    sc = scale_code(a, t.g);
+    const float s = e4m3_value(sc);
+    uint32_t o[2];
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = h ? w[4 + j] : w[j];
+        v |= (e2m1_exact(bf_lo(x), s, t.g) | (e2m1_exact(bf_hi(x), s, t.g) << 4)) << (8 * j);
+      }
+      o[h] = v;
+    }
+    return make_uint2(o[0], o[1]);
   }
-  return make_uint2(o[0], o[1]);
+  const float q = fmaf(a, t.sixth.x, a * t.sixth.y);
+  sc = max(f32x2_to_e4m3x2(q, 0.f), 1u);
+  const float2 r = table[sc];
+  if (nan) sc = 0x7fu;
+  return nan ? make_uint2(0, 0) : make_uint2(quant8(w[0], w[1], w[2], w[3], r.x, r.y), quant8(w[4], w[5], w[6], w[7], r.x, r.y));
 }
 
 // A token's planes * Hk head vectors take TPR threads each (in rounds, if more than
@@ -149,18 +166,29 @@ __global__ void __launch_bounds__(kThreads, 4) append4_kernel(const Append4Launc
   const int Hk = p.num_kv_heads, bs = p.block_size;
   const int tpt = p.planes * Hk * TPR;         // threads per token
   const long long slots = (long long)p.num_blocks * bs;
-  const size_t chunk = size_t(bs) * (HD / 2 + HD / 16);
+  const uint32_t chunk = uint32_t(bs) * (HD / 2 + HD / 16), block_bytes = p.planes * Hk * chunk;   // at most 2.4 GB
   const int mine = threadIdx.x / tpt;          // token of the block's side-by-side ones
   const int round = kThreads / TPR * TPR;      // threads of a round (tpt > kThreads: one token)
   const int step = gridDim.x * side;
+  __shared__ float2 s_table[2][128];           // [plane][scale code] 1/(s g)
+  for (int i = threadIdx.x; i < 128 * p.planes; i += kThreads) {
+    const float g = __ldg(i < 128 ? p.k_scale : p.v_scale);
+    if ((i & 127) > 0 && (i & 127) < 127 && g > kTiny && g < kHuge) s_table[i >> 7][i & 127] = reciprocal(e4m3_value(i & 127), g, 7);
+  }
+  __syncthreads();
   for (int i0 = 0; i0 < tpt; i0 += round) {
     const int i = side > 1 ? threadIdx.x - mine * tpt : i0 + threadIdx.x;
     const bool place = side > 1 ? mine < side : i < tpt;
     const int part = i % TPR, vec = i / TPR, kv = vec >= Hk && p.planes > 1, h = vec - kv * Hk;
-    const uint16_t* src = static_cast<const uint16_t*>(kv ? p.v : p.k) + h * (kv ? p.v_stride_head : p.k_stride_head);
+    const uint16_t* src = static_cast<const uint16_t*>(kv ? p.v : p.k) + h * (kv ? p.v_stride_head : p.k_stride_head) + 16 * part;
     const long long stride = kv ? p.v_stride_tok : p.k_stride_tok;
-    const float g = __ldg(kv ? p.v_scale : p.k_scale);
-    const bool ok = g > 0.f && g < INFINITY;
+    uint8_t* const to = p.kv + size_t(kv * Hk + h) * chunk;
+    Tensor ten;
+    ten.g = __ldg(kv ? p.v_scale : p.k_scale);
+    ten.ok = ten.g > 0.f && ten.g < INFINITY;
+    ten.fast = ten.g > kTiny && ten.g < kHuge;
+    ten.sixth = ten.fast ? reciprocal(6.f, ten.g, 31) : make_float2(0.f, 0.f);
+    const float2* table = s_table[kv];
     // whole warps stay in the loop (the scale bytes are shuffled together)
     for (long long t0 = (long long)blockIdx.x * side; t0 < p.num_tokens; t0 += (long long)UN * step) {
       long long slot[UN];
@@ -179,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 4) append4_kernel(const Append4Launc
         }
         a[u] = b[u] = make_uint4(0, 0, 0, 0);
         if (slot[u] >= 0) {
-          const uint4* s4 = reinterpret_cast<const uint4*>(src + t * stride) + 2 * part;
+          const uint4* s4 = reinterpret_cast<const uint4*>(src + t * stride);
           a[u] = __ldcs(s4);
           b[u] = __ldcs(s4 + 1);
         }
@@ -188,18 +216,16 @@ __global__ void __launch_bounds__(kThreads, 4) append4_kernel(const Append4Launc
       for (int u = 0; u < UN; ++u) {
         const uint32_t w[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
         uint32_t sc;
-        const uint2 code = quantise16(w, g, ok, sc);
+        const uint2 code = quantise16(w, ten, table, sc);
         // the scale bytes of four neighbours as one word
         uint32_t s4 = sc << (8 * (part & 3));
         s4 |= __shfl_xor_sync(0xffffffffu, s4, 1);
         s4 |= __shfl_xor_sync(0xffffffffu, s4, 2);
         if (slot[u] < 0) continue;
-        const long long blk = slot[u] >> log2_bs;
-        const int off = (int)(slot[u] & (bs - 1));
-        uint8_t* dst = p.kv + ((blk * p.planes + kv) * Hk + h) * chunk;
-        reinterpret_cast<uint2*>(dst + size_t(off) * (HD / 2))[part] = code;
-        if ((part & 3) == 0)
-          reinterpret_cast<uint32_t*>(dst + size_t(bs) * (HD / 2) + size_t(off) * (HD / 16))[part >> 2] = s4;
+        const uint32_t blk = (uint32_t)(slot[u] >> log2_bs), off = (uint32_t)slot[u] & (bs - 1);
+        uint8_t* dst = to + (unsigned long long)blk * block_bytes;
+        *reinterpret_cast<uint2*>(dst + (off * (HD / 2) + 8 * part)) = code;
+        if ((part & 3) == 0) *reinterpret_cast<uint32_t*>(dst + (bs * (HD / 2) + off * (HD / 16) + part)) = s4;
       }
     }
     if (side > 1) break;

@@ -48,14 +48,15 @@ constexpr float kTop = 14.f;        // and moves when a logit is this far above 
 
 template <int NT, int HD>
 struct Smem {
-  static constexpr int NWG = 2;                    // consumer groups of 4 warps
+  static constexpr int NWG = NT == 1 ? 3 : 2;      // consumer groups of 4 warps
   static constexpr int NCW = 4 * NWG;
   static constexpr int WARP_COPY = NCW;
   static constexpr int WARP_MMA = NCW + 4;         // one per consumer group
   static constexpr int THREADS = (WARP_MMA + 4) * 32;   // (whole warpgroups, for the register budgets)
-  // registers of the roles' threads; their sum is the launch's, 512 x 128
-  static constexpr int REG_CONSUMER = 168, REG_COPY = 104, REG_MMA = 72;
-  static_assert(NWG == 2 && 256 * REG_CONSUMER + 128 * REG_COPY + 128 * REG_MMA == THREADS * 128, "registers");
+  // registers of the roles' threads; their sum is the launch's
+  static constexpr int REG_CONSUMER = NWG == 3 ? 112 : 168, REG_COPY = NWG == 3 ? 88 : 104, REG_MMA = NWG == 3 ? 56 : 72;
+  static constexpr int REG_LAUNCH = 65536 / THREADS / 8 * 8;
+  static_assert(128 * (NWG * REG_CONSUMER + REG_COPY + REG_MMA) <= THREADS * REG_LAUNCH, "registers");
   static constexpr int R = 8 * NT;                 // query rows (padded)
   static constexpr int KS = HD / 64;               // K steps of the fp4 product
   static constexpr int NQ = 8 * QT * NT;           // columns of S: row block x term x 8 rows
@@ -66,14 +67,14 @@ struct Smem {
   static constexpr int SLOT = VS_OFF + TILE * (HD / 16);
   static constexpr int NSB = 2 * NWG;              // S buffers, two per group
   static constexpr int qBytes = NQ * ROW;
-  static constexpr int STG_ROW = HD + 4;           // floats of a staged row (padded against bank conflicts)
+  static constexpr int STG_ROW = HD;               // floats of a staged row
   static constexpr int stgBytes = NCW * 8 * STG_ROW * 4;   // one row block at a time
   static constexpr int pBytes = 32 * 16 * NT;      // a warp's P [32 tokens][8 rows] f16 per row block
-  // ring slots. A multiple of the copy warps and of the groups: a slot then has one
-  // copy warp and one group, which see every phase of its barriers (a wait on a parity
-  // cannot mistake a phase for the one before the last)
-  static constexpr int NS = HD == 128 ? 8 : 16;
-  static_assert(NS % 4 == 0 && NS % NWG == 0, "ring");
+  // Ring slots, NSG per group. A group has its own slots and its own copy warp, which see
+  // every phase of their barriers: a wait on a parity cannot mistake a phase for the one
+  // before the last.
+  static constexpr int NSG = (NT == 1 ? 3 : 4) * (HD == 128 ? 1 : 2);
+  static constexpr int NS = NWG * NSG;
   static constexpr int qOff = NS * SLOT;
   static constexpr int qsOff = qOff + 2 * qBytes;             // [2][KS][512] query scales
   static constexpr int stgOff = qsOff + 2 * KS * 512;         // [NCW][8][STG_ROW] f32
@@ -126,6 +127,10 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo, uint32_
                ::"r"(taddr), "r"(lo), "r"(hi) : "memory");
 }
 template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "l"(policy) : "memory");
+}
+template <int N>
 __device__ __forceinline__ void cp_async_small_zfill(uint32_t dst, const void* src, bool valid, uint64_t policy) {
   asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %2, %3, %4;"
                ::"r"(dst), "l"(src), "n"(N), "r"(valid ? N : 0), "l"(policy) : "memory");
@@ -153,17 +158,16 @@ __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
   return r;
 }
 
-// The tiles of one of `of` takers that take them in turn: the ring slot and its phase, how
-// many so far, and the item's first one (counted from the item's beginning).
+// A group's tiles, every `of`-th of the CTA's: the ring slot (of the group's ns) and its phase,
+// how many so far, and the item's first one (counted from the item's beginning).
 struct Turn {
   int slot, first, count, ns, of;
   uint32_t phase;
-  __device__ __forceinline__ Turn(int me, int ns_, int of_) : slot(me), first(me), count(0), ns(ns_), of(of_), phase(0) {}
+  __device__ __forceinline__ Turn(int me, int ns_, int of_) : slot(0), first(me), count(0), ns(ns_), of(of_), phase(0) {}
   __device__ __forceinline__ void step() {
     ++count;
-    slot += of;
-    if (slot >= ns) {
-      slot -= ns;
+    if (++slot == ns) {
+      slot = 0;
       phase ^= 1;
     }
   }
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     const uint32_t slane = S::VS_OFF + (32 * wq + c) * (HD / 16) + (HD == 128 ? g : g >> 1);
     const float vscale = __ldg(p.v_scale);
     float o[NT][MT][4], ol[NT][4], m[R];
-    Turn tn(wg, NS, NWG);
+    Turn tn(wg, S::NSG, NWG);
     int merges = 0;                                  // row blocks joined so far
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
       for (int r = 0; r < R; ++r) m[r] = kNoMax;
       for (int i = tn.first; i < nt; i += NWG, tn.step()) {
-        const int b = 2 * wg + (tn.count & 1), s = tn.slot;
+        const int b = 2 * wg + (tn.count & 1), s = wg * S::NSG + tn.slot;
         const uint32_t slot = sb + s * S::SLOT;
         const int tok = (t0 + i) * TILE + 32 * wq + lane;               // this lane's token
         const bool cut = (t0 + i + 1) * (long long)TILE > L;            // the sequence ends in this tile
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     const int lr = lane / CPR, cc = lane % CPR;
     const uint32_t kdst = lr * ROW + ((HD == 128 ? cc ^ ((lr >> 1) & 3) : cc ^ ((lr >> 2) & 1)) << 4);
     const uint32_t vdst = S::V_OFF + lr * ROW + ((HD == 128 ? cc ^ (lr & 2) : cc) << 4);
-    const uint32_t src_lane = lr * ROW + 16 * cc;
+    const uint32_t src_lane = lr * ROW + 16 * cc, sc_lane = (lane & 15) * (HD / 16);
     const size_t chunk = size_t(bs) * (HD / 2 + HD / 16), plane = size_t(Hk) * chunk;
 
     // ---- the CTA's range of units, and the item that holds its first one
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     uint4 qv[NT];
     load_q(cur, qv);
     int32_t ent0 = load_entries(cur.s, (int)(((long long)cur.t * TILE) >> lbs));
-    Turn tn(pw, NS, 4);
+    Turn tn(pw, S::NSG, NWG);                                           // (the other warps only build operands)
     int n = 0;
     int4 meta = make_int4(0, 0, 0, 0);
     bool ok = true;
@@ -581,53 +585,72 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       load_q(nxt, qn);
       const int32_t ent0n = load_entries(nxt.s, (int)(((long long)nxt.t * TILE) >> lbs));
       const int L = cur.L;
-      const uint8_t* kbase = p.kv + size_t(cur.vh / RB) * chunk;
+      const uint64_t kbase = reinterpret_cast<uint64_t>(p.kv) + size_t(cur.vh / RB) * chunk;
       int e0 = (int)(((long long)cur.t * TILE) >> lbs);
       int32_t ent = ent0, ent_next = load_entries(cur.s, e0 + 32);
       int ti = tn.first;
       // this warp's tiles of the item, below `end`
       auto issue_to = [&](int end) -> bool {
-        for (; ti < end; ti += 4, tn.step()) {
-          const int s = tn.slot, tok0 = (cur.t + ti) * TILE;
-          if (tn.count * 4 + pw >= NS && !warp_wait(&empty[s], tn.phase ^ 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
+        for (; pw < NWG && ti < end; ti += NWG, tn.step()) {
+          const int s = pw * S::NSG + tn.slot, tok0 = (cur.t + ti) * TILE;
+          if (tn.count >= S::NSG && !warp_wait(&empty[s], tn.phase ^ 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
           while ((tok0 >> lbs) - e0 >= 32) {
             e0 += 32;
             ent = ent_next;
             ent_next = load_entries(cur.s, e0 + 32);
           }
           // (a tile's blocks never straddle two groups of 32 entries: 32 blocks are whole tiles, from a tile's first on)
+          // lane q: K codes of the tile's tokens 16 q .. (which lie in one block)
+          const int tok = tok0 + 16 * (lane & 7);
+          int blk = __shfl_sync(0xffffffffu, ent, ((tok >> lbs) - e0) & 31);
+          if (blk < 0 || blk >= p.num_blocks) {
+            if (tok < L) atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
+            blk = 0;
+          }
+          const int off = tok & (bs - 1);
+          const uint64_t codes = kbase + size_t(blk) * (2 * plane) + uint32_t(off * ROW);
+          const uint32_t to_scales = bs * ROW - off * (ROW - HD / 16);
           const uint32_t slot = sb + s * S::SLOT;
-          const bool whole = tok0 + (TILE - 1) < L;
-          const uint8_t* base_lo = nullptr;
+          if (tok0 + TILE <= L) {
 #pragma unroll
-          for (int q = 0; q < TILE / 16; ++q) {
-            // tokens 16 q .. 16 q + 15 of the tile lie in one block
-            const int tok = tok0 + 16 * q;
-            int blk = __shfl_sync(0xffffffffu, ent, ((tok >> lbs) - e0) & 31);
-            if (blk < 0 || blk >= p.num_blocks) {
-              if (tok < L && lane == 0) atomicExch(&g_kernel_error, (int)KERR_BAD_BLOCK);
-              blk = 0;
-            }
-            const int off = tok & (bs - 1);
-            const uint8_t* base = kbase + size_t(blk) * 2 * plane;
-            const uint8_t* src = base + uint32_t(off * ROW) + src_lane;
+            for (int q = 0; q < TILE / 16; ++q) {
+              const uint64_t src = __shfl_sync(0xffffffffu, codes, q) + src_lane;
 #pragma unroll
-            for (int ii = 0; ii < 16 / RPI; ++ii) {
-              const bool valid = whole || tok + RPI * ii + lr < L;
-              cp_async16_zfill(slot + kdst + (16 * q + RPI * ii) * ROW, src + RPI * ii * ROW, valid, pol);
-              cp_async16_zfill(slot + vdst + (16 * q + RPI * ii) * ROW, src + plane + RPI * ii * ROW, valid, pol);
+              for (int ii = 0; ii < 16 / RPI; ++ii) {
+                cp_async16(slot + kdst + (16 * q + RPI * ii) * ROW, reinterpret_cast<const uint8_t*>(src) + RPI * ii * ROW, pol);
+                cp_async16(slot + vdst + (16 * q + RPI * ii) * ROW, reinterpret_cast<const uint8_t*>(src + plane) + RPI * ii * ROW, pol);
+              }
             }
-            // scales, 32 tokens at a time: lane = token
-            const uint8_t* sbase = base + uint32_t(bs * ROW + off * (HD / 16));
-            if (q & 1) {
-              const uint8_t* ssrc = lane < 16 ? base_lo + lane * (HD / 16) : sbase + (lane - 16) * (HD / 16);
-              const bool valid = whole || tok - 16 + lane < L;
+#pragma unroll
+            for (int q = 0; q < TILE / 32; ++q) {
+              const int from = 2 * q + (lane >> 4);
+              const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, codes + to_scales, from)) + sc_lane;
 #pragma unroll
               for (int k = 0; k < KS; ++k)
-                cp_async_small_zfill<4>(slot + S::KS_OFF + 512 * k + 16 * lane + 4 * (q >> 1), ssrc + 4 * k, valid, pol);
-              cp_async_small_zfill<HD / 16>(slot + S::VS_OFF + (16 * (q - 1) + lane) * (HD / 16), ssrc + plane, valid, pol);
-            } else {
-              base_lo = sbase;
+                cp_async_small<4>(slot + S::KS_OFF + 512 * k + 16 * lane + 4 * q, src + 4 * k, pol);
+              cp_async_small<HD / 16>(slot + S::VS_OFF + (32 * q + lane) * (HD / 16), src + plane, pol);
+            }
+          } else {
+            // the sequence ends in this tile: zeros behind it
+#pragma unroll 1
+            for (int q = 0; q < TILE / 16; ++q) {
+              const uint64_t src = __shfl_sync(0xffffffffu, codes, q) + src_lane;
+#pragma unroll 1
+              for (int ii = 0; ii < 16 / RPI; ++ii) {
+                const bool valid = tok0 + 16 * q + RPI * ii + lr < L;
+                cp_async16_zfill(slot + kdst + (16 * q + RPI * ii) * ROW, reinterpret_cast<const uint8_t*>(src) + RPI * ii * ROW, valid, pol);
+                cp_async16_zfill(slot + vdst + (16 * q + RPI * ii) * ROW, reinterpret_cast<const uint8_t*>(src + plane) + RPI * ii * ROW, valid, pol);
+              }
+            }
+#pragma unroll 1
+            for (int q = 0; q < TILE / 32; ++q) {
+              const int from = 2 * q + (lane >> 4);
+              const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, codes + to_scales, from)) + sc_lane;
+              const bool valid = tok0 + 32 * q + lane < L;
+#pragma unroll
+              for (int k = 0; k < KS; ++k)
+                cp_async_small_zfill<4>(slot + S::KS_OFF + 512 * k + 16 * lane + 4 * q, src + 4 * k, valid, pol);
+              cp_async_small_zfill<HD / 16>(slot + S::VS_OFF + (32 * q + lane) * (HD / 16), src + plane, valid, pol);
             }
           }
           cp_async_arrive_noinc(&full[s]);
@@ -635,7 +658,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         return true;
       };
       // the first tiles go out before the operand is built
-      if (n == 0 && !issue_to(min(nt, 4))) break;
+      if (n == 0 && !issue_to(min(nt, NWG))) break;
       const int qb = n & 1;
       if (n >= 2 && !warp_wait(&qempty[qb], ((n >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       // ---- query operand
@@ -740,7 +763,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     reg_dec<S::REG_MMA>();
     const int wg = warp - S::WARP_MMA;
     if (wg < NWG) {
-    Turn tn(wg, NS, NWG);
+    Turn tn(wg, S::NSG, NWG);
     bool ok = true;
     const uint32_t sfb0 = tmem + S::SFB_COL + wg * 8 * KS;
     // descriptors: the low half is the address (plus constants), the high half constant
@@ -758,7 +781,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           copy_scales(sfb + 4 * k, desc_lo(sb + S::qsOff + (qb * KS + k) * 512, 16), SC_HI);
       }
       for (int i = tn.first; i < nt; i += NWG, tn.step()) {
-        const int s = tn.slot, b = 2 * wg + (tn.count & 1);
+        const int s = wg * S::NSG + tn.slot, b = 2 * wg + (tn.count & 1);
         if ((tn.count >= 2 && !warp_wait(&sfree[b], ((tn.count >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) ||
             !warp_wait(&full[s], tn.phase, abort_flag, KERR_TIMEOUT_FULL)) {
           ok = false;
