@@ -14,7 +14,13 @@
 //    (kind::mxf4nvf4): the pages' e2m1 codes and e4m3 scales are the operand as they
 //    are, 128 tokens x 64 dims at a time. Q' holds each query row as 6 e2m1 terms of
 //    weights 1, 1/8, .. 8^-5 (3 bits each) with a power of two per 16 dims, so a query
-//    is within 2^-17 of its 16 dims' largest, and exact down to 2^-9 of it.
+//    is within 2^-17 of its 16 dims' largest, and exact down to 2^-9 of it. Three passes
+//    accumulate terms 0, 1, 2 into 8 columns of S and 3, 4, 5 into 8 others, the weights
+//    1, 1/8, 1/64 of a pass in its scales: S is a column plus 2^-9 of another. (All six
+//    terms in columns of their own: 20 packed FMAs more per token, 69 us for 16 x 16384
+//    tokens, 8 x 8 heads, where this takes {D16}.) e4m3 holds the scales' powers from
+//    2^8 to 2^-9: a term whose scale would be smaller, in 16 dims 2^11 or more below the
+//    row's largest, is left out, and such dims are within 2^-17 of the row's largest.
 //  * Groups of 4 consumer warps take the tiles in turn; each warp owns 32 tokens of a
 //    tile and its own softmax state, so nothing is exchanged before the item's end: it
 //    reads S from tensor memory (a lane a token), forms p in f16, and multiplies V on
@@ -41,6 +47,7 @@ namespace qpa {
 namespace d4 {
 constexpr int TILE = 128;           // tokens per tile
 constexpr int QT = 6;               // e2m1 terms of a query
+constexpr int PASSES = 3;           // of the QK product: terms k and k + 3
 constexpr int MAX_CTAS = 160;
 constexpr float kNoMax = -1e30f;    // no token seen yet: finite, so that differences stay defined
 constexpr float kBelow = 8.f;       // the reference is set this far below the largest logit (p up to 2^8)
@@ -48,36 +55,37 @@ constexpr float kTop = 14.f;        // and moves when a logit is this far above 
 
 template <int NT, int HD>
 struct Smem {
-  static constexpr int NWG = NT == 1 ? 3 : 2;      // consumer groups of 4 warps
+  static constexpr int NWG = 2;                    // consumer groups of 4 warps
   static constexpr int NCW = 4 * NWG;
   static constexpr int WARP_COPY = NCW;
   static constexpr int WARP_MMA = NCW + 4;         // one per consumer group
   static constexpr int THREADS = (WARP_MMA + 4) * 32;   // (whole warpgroups, for the register budgets)
   // registers of the roles' threads; their sum is the launch's
-  static constexpr int REG_CONSUMER = NWG == 3 ? 112 : 168, REG_COPY = NWG == 3 ? 88 : 104, REG_MMA = NWG == 3 ? 56 : 72;
+  static constexpr int REG_CONSUMER = 168, REG_COPY = 104, REG_MMA = 72;
   static constexpr int REG_LAUNCH = 65536 / THREADS / 8 * 8;
   static_assert(128 * (NWG * REG_CONSUMER + REG_COPY + REG_MMA) <= THREADS * REG_LAUNCH, "registers");
   static constexpr int R = 8 * NT;                 // query rows (padded)
   static constexpr int KS = HD / 64;               // K steps of the fp4 product
-  static constexpr int NQ = 8 * QT * NT;           // columns of S: row block x term x 8 rows
+  static constexpr int NQ = 16 * NT;               // columns of S: row block x (terms 0-2, 3-5) x 8 rows
   static constexpr int ROW = HD / 2;               // code bytes of a token
   static constexpr int V_OFF = TILE * ROW;
   static constexpr int KS_OFF = 2 * TILE * ROW;    // K scales [KS][token % 32][token / 32][4]
   static constexpr int VS_OFF = KS_OFF + KS * 512; // V scales [token][HD / 16]
   static constexpr int SLOT = VS_OFF + TILE * (HD / 16);
   static constexpr int NSB = 2 * NWG;              // S buffers, two per group
-  static constexpr int qBytes = NQ * ROW;
+  static constexpr int qBytes = PASSES * NQ * ROW;
   static constexpr int STG_ROW = HD;               // floats of a staged row
   static constexpr int stgBytes = NCW * 8 * STG_ROW * 4;   // one row block at a time
   static constexpr int pBytes = 32 * 16 * NT;      // a warp's P [32 tokens][8 rows] f16 per row block
-  // Ring slots, NSG per group. A group has its own slots and its own copy warp, which see
-  // every phase of their barriers: a wait on a parity cannot mistake a phase for the one
-  // before the last.
-  static constexpr int NSG = (NT == 1 ? 3 : 4) * (HD == 128 ? 1 : 2);
+  // Ring slots, NSG per group. A slot has one group and one copy warp, which see every phase
+  // of its barriers: a wait on a parity cannot mistake a phase for the one before the last.
+  static constexpr int CPG = 4 / NWG;              // copy warps of a group, taking its tiles in turn
+  static constexpr int NSG = 4 * (HD == 128 ? 1 : 2);
+  static_assert(NSG % CPG == 0, "ring");
   static constexpr int NS = NWG * NSG;
   static constexpr int qOff = NS * SLOT;
-  static constexpr int qsOff = qOff + 2 * qBytes;             // [2][KS][512] query scales
-  static constexpr int stgOff = qsOff + 2 * KS * 512;         // [NCW][8][STG_ROW] f32
+  static constexpr int qsOff = qOff + 2 * qBytes;             // [2][PASSES][KS][512] query scales
+  static constexpr int stgOff = qsOff + 2 * PASSES * KS * 512;         // [NCW][8][STG_ROW] f32
   static constexpr int pOff = stgOff + stgBytes;              // [NCW] P
   static constexpr int mlOff = pOff + NCW * pBytes;           // [NCW][8] {m, l}
   static constexpr int cOff = mlOff + NCW * 8 * 8;            // [2][R] logit factor per row
@@ -89,7 +97,7 @@ struct Smem {
   static_assert(SLOT % 1024 == 0 && qBytes % 512 == 0 && total <= 227 * 1024, "shared memory");
   // tensor memory: S buffers, K scales per S buffer, query scales per group and operand
   static constexpr int SFA_COL = NSB * NQ, SFB_COL = SFA_COL + NSB * 4 * KS;
-  static constexpr int USED_COLS = SFB_COL + 2 * NWG * 4 * KS;
+  static constexpr int USED_COLS = SFB_COL + 2 * NWG * PASSES * 4 * KS;
   static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
   static_assert(USED_COLS <= TMEM_COLS, "tensor memory");
 };
@@ -158,16 +166,19 @@ __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
   return r;
 }
 
-// A group's tiles, every `of`-th of the CTA's: the ring slot (of the group's ns) and its phase,
-// how many so far, and the item's first one (counted from the item's beginning).
+// A taker's tiles, every `of`-th of the CTA's: the ring slot (of the group's ns, every by-th) and
+// its phase, how many so far, and the item's first one (counted from the item's beginning).
 struct Turn {
   int slot, first, count, ns, of;
   uint32_t phase;
-  __device__ __forceinline__ Turn(int me, int ns_, int of_) : slot(0), first(me), count(0), ns(ns_), of(of_), phase(0) {}
+  int by;
+  __device__ __forceinline__ Turn(int me, int ns_, int of_, int slot_ = 0, int by_ = 1)
+      : slot(slot_), first(me), count(0), ns(ns_), of(of_), phase(0), by(by_) {}
   __device__ __forceinline__ void step() {
     ++count;
-    if (++slot == ns) {
-      slot = 0;
+    slot += by;
+    if (slot >= ns) {
+      slot -= ns;
       phase ^= 1;
     }
   }
@@ -282,14 +293,14 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) m[r] = kNoMax;
-      for (int i = tn.first; i < nt; i += NWG, tn.step()) {
-        const int b = 2 * wg + (tn.count & 1), s = wg * S::NSG + tn.slot;
+      uint32_t w[8][HD / 64], sc[8];                 // V of this warp's 32 tokens: 4 u + c, u < 8
+      float x[R];                                    // logits without the row's factor
+      float v[NT][16];                               // S: terms 0-2, 3-5 x 8 rows
+      // V's bytes into registers; the slot is free then
+      auto load_v = [&]() -> bool {
+        const int s = wg * S::NSG + tn.slot;
+        if (!warp_wait(&full[s], tn.phase, abort_flag, KERR_TIMEOUT_FULL)) return false;
         const uint32_t slot = sb + s * S::SLOT;
-        const int tok = (t0 + i) * TILE + 32 * wq + lane;               // this lane's token
-        const bool cut = (t0 + i + 1) * (long long)TILE > L;            // the sequence ends in this tile
-        // ---- V's bytes, on their way while S is awaited
-        if (!warp_wait(&full[s], tn.phase, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
-        uint32_t w[8][HD / 64], sc[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const uint32_t a = slot + vlane + 4 * u * ROW;
@@ -302,39 +313,58 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           }
           sc[u] = lds8(slot + slane + 4 * u * (HD / 16));
         }
-        if (!warp_wait(&sfull[b], (tn.count >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        return true;
+      };
+      // S on its way to registers
+      auto wait_s = [&](int count) -> bool {
+        if (!warp_wait(&sfull[2 * wg + (count & 1)], (count >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) return false;
         tc_fence_after();
+        return true;
+      };
+      auto load_s = [&](int count) {
 #pragma unroll
-        for (int nb = 0; nb < NT; ++nb) {
-          // ---- logits of 8 rows for this token: terms of weights 8^-k, times the row's factor
-          float v[32], v2[16];
-          tmem_ld32(tl + b * NQ + nb * 8 * QT, v);
-          tmem_ld16(tl + b * NQ + nb * 8 * QT + 32, v2);
-          tmem_wait_ld();
-          if (nb == NT - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sfree[b]);
-          }
-          float x[8], e[8];
+        for (int nb = 0; nb < NT; ++nb) tmem_ld16(tl + (2 * wg + (count & 1)) * NQ + 16 * nb, v[nb]);
+      };
+      // S has come: its halves joined (v is free then)
+      auto join_terms = [&]() {
+        tmem_wait_ld();
+#pragma unroll
+        for (int nb = 0; nb < NT; ++nb)
 #pragma unroll
           for (int r = 0; r < 8; r += 2) {
-            x[r] = v2[8 + r];
-            x[r + 1] = v2[9 + r];
-            fma2(x[r], x[r + 1], 0.125f, v2[r], v2[r + 1]);
-            fma2(x[r], x[r + 1], 0.125f, v[24 + r], v[25 + r]);
-            fma2(x[r], x[r + 1], 0.125f, v[16 + r], v[17 + r]);
-            fma2(x[r], x[r + 1], 0.125f, v[8 + r], v[9 + r]);
-            fma2(x[r], x[r + 1], 0.125f, v[r], v[r + 1]);
+            x[8 * nb + r] = v[nb][8 + r];
+            x[8 * nb + r + 1] = v[nb][9 + r];
+            fma2(x[8 * nb + r], x[8 * nb + r + 1], 0.001953125f, v[nb][r], v[nb][r + 1]);
           }
-          float f[8];
+      };
+      auto free_s = [&](int count) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfree[2 * wg + (count & 1)]);
+      };
+      if (tn.first < nt) {
+        if (!load_v() || !wait_s(tn.count)) { ok = false; break; }
+        load_s(tn.count);
+        join_terms();
+        free_s(tn.count);
+      }
+      for (int i = tn.first; i < nt; i += NWG) {
+        const int tok = (t0 + i) * TILE + 32 * wq + lane;               // this lane's token
+        const bool cut = (t0 + i + 1) * (long long)TILE > L;            // the sequence ends in this tile
+        const bool more = i + NWG < nt;
+#pragma unroll
+        for (int nb = 0; nb < NT; ++nb) {
+          // ---- logits of 8 rows for this token, relative to the references
+          float f[8], e[8];
           {
             const float4 f0 = lds_f4(sb + S::cOff + 4 * (qb * R + 8 * nb)), f1 = lds_f4(sb + S::cOff + 4 * (qb * R + 8 * nb) + 16);
             f[0] = f0.x; f[1] = f0.y; f[2] = f0.z; f[3] = f0.w;
             f[4] = f1.x; f[5] = f1.y; f[6] = f1.z; f[7] = f1.w;
           }
 #pragma unroll
-          for (int r = 0; r < 8; ++r) e[r] = fmaf(x[r], f[r], -m[8 * nb + r]);
+          for (int r = 0; r < 8; ++r) e[r] = fmaf(x[8 * nb + r], f[r], -m[8 * nb + r]);
           if (cut && tok >= L) {
 #pragma unroll
             for (int r = 0; r < 8; ++r) e[r] = -INFINITY;
@@ -346,12 +376,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
               // (x f of a masked token does not count; NaN is ignored)
-              const float best = warp_max(cut && tok >= L ? -INFINITY : x[r] * f[r]);
+              const float best = warp_max(cut && tok >= L ? -INFINITY : x[8 * nb + r] * f[r]);
               const float old = m[8 * nb + r];
               const float now = best > old + kTop ? best - kBelow : old;
               const float alpha = ex2(old - now);
               m[8 * nb + r] = now;
-              e[r] = cut && tok >= L ? -INFINITY : fmaf(x[r], f[r], -now);
+              e[r] = cut && tok >= L ? -INFINITY : fmaf(x[8 * nb + r], f[r], -now);
               if (r == 2 * c) a0 = alpha;
               if (r == 2 * c + 1) a1 = alpha;
             }
@@ -374,6 +404,11 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         uint32_t pb[NT][4];
 #pragma unroll
         for (int nb = 0; nb < NT; ++nb) ldsm_x4_trans(prow + 512 * nb, pb[nb]);
+        // one row block: the next tile's S comes while this one's V is multiplied (two: no registers for it)
+        if (NT == 1 && more) {
+          if (!wait_s(tn.count + 1)) { ok = false; break; }
+          load_s(tn.count + 1);
+        }
         // ---- O^T += V^T P^T, 16 tokens at a time
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -402,9 +437,18 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
           for (int nb = 0; nb < NT; ++nb)      // the sum of p: a row of ones
             mma_f16_16816(ol[nb], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[nb][2 * k], pb[nb][2 * k + 1]);
+          if (NT == 1 && k == 0) join_terms();       // (of what v holds, if there is no next tile)
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
+        tn.step();
+        if (more) {
+          if constexpr (NT > 1) {
+            if (!wait_s(tn.count)) { ok = false; break; }
+            load_s(tn.count);
+            join_terms();
+          }
+          free_s(tn.count);
+          if (!load_v()) { ok = false; break; }
+        }
       }
       if (!ok) break;
       tn.item(nt);
@@ -564,7 +608,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     uint4 qv[NT];
     load_q(cur, qv);
     int32_t ent0 = load_entries(cur.s, (int)(((long long)cur.t * TILE) >> lbs));
-    Turn tn(pw, S::NSG, NWG);                                           // (the other warps only build operands)
+    Turn tn(pw, S::NSG, NWG * S::CPG, pw / NWG, S::CPG);                // (a warp without a group only builds operands)
+    const int wg = pw % NWG;
     int n = 0;
     int4 meta = make_int4(0, 0, 0, 0);
     bool ok = true;
@@ -591,9 +636,9 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       int ti = tn.first;
       // this warp's tiles of the item, below `end`
       auto issue_to = [&](int end) -> bool {
-        for (; pw < NWG && ti < end; ti += NWG, tn.step()) {
-          const int s = pw * S::NSG + tn.slot, tok0 = (cur.t + ti) * TILE;
-          if (tn.count >= S::NSG && !warp_wait(&empty[s], tn.phase ^ 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
+        for (; pw < NWG * S::CPG && ti < end; ti += NWG * S::CPG, tn.step()) {
+          const int s = wg * S::NSG + tn.slot, tok0 = (cur.t + ti) * TILE;
+          if (tn.count * S::CPG >= S::NSG && !warp_wait(&empty[s], tn.phase ^ 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
           while ((tok0 >> lbs) - e0 >= 32) {
             e0 += 32;
             ent = ent_next;
@@ -658,7 +703,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         return true;
       };
       // the first tiles go out before the operand is built
-      if (n == 0 && !issue_to(min(nt, NWG))) break;
+      if (n == 0 && !issue_to(min(nt, NWG * S::CPG))) break;
       const int qb = n & 1;
       if (n >= 2 && !warp_wait(&qempty[qb], ((n >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       // ---- query operand
@@ -700,11 +745,11 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         const float up = __uint_as_float(uint32_t(127 + s1) << 23), up2 = __uint_as_float(uint32_t(127 + s2) << 23);
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = row_ok ? x[k] * up * up2 : 0.f;
-        const int es = rel + 8;                                          // e4m3: 2^es
-        const uint32_t sbyte = es >= -6 ? uint32_t(es + 7) << 3 : 1u << (es + 9);
         const int row8 = qrow;
 #pragma unroll
         for (int term = 0; term < QT; ++term) {
+          // terms k and k + 3: pass k, scale 2^(rel + 8 - 3 k), in columns 0 .. 7 and 8 .. 15 of the row block
+          const int pass = term % PASSES, es = rel + 8 - 3 * pass;
           uint32_t word = 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -714,13 +759,15 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
             x[2 * k + 1] = (x[2 * k + 1] - f16_hi_to_f32(back)) * 8.f;
             word |= code << (8 * k);
           }
-          const int col = 8 * QT * h + 8 * term + row8;
+          if (es < -9) word = 0;
+          const int col = 16 * h + 8 * (term / PASSES) + row8;
           if (h16 < HD / 8) {
             const int ch = HD == 128 ? (h16 >> 2) ^ ((col >> 1) & 3) : (h16 >> 2) ^ ((col >> 2) & 1);
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb + S::qOff + qb * S::qBytes + col * ROW + 16 * ch + 4 * (h16 & 3)),
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb + S::qOff + qb * S::qBytes + (pass * NQ + col) * ROW + 16 * ch + 4 * (h16 & 3)),
                          "r"(word) : "memory");
             if ((h16 & 1) == 0)
-              sts8(sb + S::qsOff + (qb * KS + (h16 >> 3)) * 512 + (col & 31) * 16 + (col >> 5) * 4 + ((h16 >> 1) & 3), sbyte);
+              sts8(sb + S::qsOff + ((qb * PASSES + pass) * KS + (h16 >> 3)) * 512 + col * 16 + ((h16 >> 1) & 3),
+                   es >= -6 ? uint32_t(es + 7) << 3 : es >= -9 ? 1u << (es + 9) : 1u);
           }
         }
         if (h16 == 0) {
@@ -765,7 +812,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     if (wg < NWG) {
     Turn tn(wg, S::NSG, NWG);
     bool ok = true;
-    const uint32_t sfb0 = tmem + S::SFB_COL + wg * 8 * KS;
+    const uint32_t sfb0 = tmem + S::SFB_COL + wg * 2 * PASSES * 4 * KS;
     // descriptors: the low half is the address (plus constants), the high half constant
     constexpr uint32_t OP_HI = desc_hi(8 * ROW, SWZ), SC_HI = desc_hi(128, kSwizzleNone);
     for (int n = 0; ok; ++n) {
@@ -773,12 +820,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       if (!warp_wait(&qfull[qb], (n >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
       const int nt = lds_i4(sb + S::infoOff + 64 * qb).z;
       if (nt == 0) break;
-      const uint32_t sfb = sfb0 + qb * 4 * KS;
+      const uint32_t sfb = sfb0 + qb * PASSES * 4 * KS;
       const uint32_t q_lo = desc_lo(sb + S::qOff + qb * S::qBytes, 16);
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-          copy_scales(sfb + 4 * k, desc_lo(sb + S::qsOff + (qb * KS + k) * 512, 16), SC_HI);
+        for (int k = 0; k < PASSES * KS; ++k)
+          copy_scales(sfb + 4 * k, desc_lo(sb + S::qsOff + (qb * PASSES * KS + k) * 512, 16), SC_HI);
       }
       for (int i = tn.first; i < nt; i += NWG, tn.step()) {
         const int s = wg * S::NSG + tn.slot, b = 2 * wg + (tn.count & 1);
@@ -794,8 +841,11 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
           for (int k = 0; k < KS; ++k) copy_scales(sfa + 4 * k, k_lo + (S::KS_OFF + 512 * k) / 16, SC_HI);
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
-            mma_fp4(tmem + b * NQ, k_lo + 2 * k, q_lo + 2 * k, OP_HI, idesc_fp4(128, NQ), sfa + 4 * k, sfb + 4 * k, k);
+          for (int pass = 0; pass < PASSES; ++pass)
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+              mma_fp4(tmem + b * NQ, k_lo + 2 * k, q_lo + pass * (NQ * ROW / 16) + 2 * k, OP_HI, idesc_fp4(128, NQ), sfa + 4 * k,
+                      sfb + 4 * (pass * KS + k), pass + k);
           umma_commit(&sfull[b]);
           umma_commit(&empty[s]);
         }
