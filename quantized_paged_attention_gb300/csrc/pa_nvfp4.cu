@@ -55,13 +55,14 @@ constexpr float kTop = 14.f;        // and moves when a logit is this far above 
 
 template <int NT, int HD>
 struct Smem {
-  static constexpr int NWG = 2;                    // consumer groups of 4 warps
+  static constexpr int NWG = NT == 1 ? 3 : 2;      // consumer groups of 4 warps
   static constexpr int NCW = 4 * NWG;
+  static constexpr bool AHEAD = NWG == 2 && NT == 1;   // the next S is loaded while V is multiplied
   static constexpr int WARP_COPY = NCW;
   static constexpr int WARP_MMA = NCW + 4;         // one per consumer group
   static constexpr int THREADS = (WARP_MMA + 4) * 32;   // (whole warpgroups, for the register budgets)
   // registers of the roles' threads; their sum is the launch's
-  static constexpr int REG_CONSUMER = 168, REG_COPY = 104, REG_MMA = 72;
+  static constexpr int REG_CONSUMER = NWG == 3 ? 120 : 168, REG_COPY = NWG == 3 ? 80 : 104, REG_MMA = NWG == 3 ? 40 : 72;
   static constexpr int REG_LAUNCH = 65536 / THREADS / 8 * 8;
   static_assert(128 * (NWG * REG_CONSUMER + REG_COPY + REG_MMA) <= THREADS * REG_LAUNCH, "registers");
   static constexpr int R = 8 * NT;                 // query rows (padded)
@@ -69,7 +70,7 @@ struct Smem {
   static constexpr int NQ = 16 * NT;               // columns of S: row block x (terms 0-2, 3-5) x 8 rows
   static constexpr int ROW = HD / 2;               // code bytes of a token
   static constexpr int V_OFF = TILE * ROW;
-  static constexpr int KS_OFF = 2 * TILE * ROW;    // K scales [KS][token % 32][token / 32][4]
+  static constexpr int KS_OFF = 2 * TILE * ROW;    // K scales as V's, then (MMA warp) [KS][token % 32][token / 32][4]
   static constexpr int VS_OFF = KS_OFF + KS * 512; // V scales [token][HD / 16]
   static constexpr int SLOT = VS_OFF + TILE * (HD / 16);
   static constexpr int NSB = 2 * NWG;              // S buffers, two per group
@@ -80,20 +81,21 @@ struct Smem {
   // Ring slots, NSG per group. A slot has one group and one copy warp, which see every phase
   // of its barriers: a wait on a parity cannot mistake a phase for the one before the last.
   static constexpr int CPG = 4 / NWG;              // copy warps of a group, taking its tiles in turn
-  static constexpr int NSG = 4 * (HD == 128 ? 1 : 2);
+  static constexpr int NSG = (NWG == 3 ? 3 : 4) * (HD == 128 ? 1 : 2);
   static_assert(NSG % CPG == 0, "ring");
   static constexpr int NS = NWG * NSG;
   static constexpr int qOff = NS * SLOT;
   static constexpr int qsOff = qOff + 2 * qBytes;             // [2][PASSES][KS][512] query scales
   static constexpr int stgOff = qsOff + 2 * PASSES * KS * 512;         // [NCW][8][STG_ROW] f32
-  static constexpr int pOff = stgOff + stgBytes;              // [NCW] P
-  static constexpr int mlOff = pOff + NCW * pBytes;           // [NCW][8] {m, l}
+  // (a warp's P lies at the beginning of its staged rows)
+  static constexpr int mlOff = stgOff + stgBytes;             // [NCW][8] {m, l}
   static constexpr int cOff = mlOff + NCW * 8 * 8;            // [2][R] logit factor per row
   static constexpr int infoOff = cOff + 2 * R * 4;            // [2] item
   static constexpr int barOff = infoOff + 2 * 64;
   static constexpr int NBAR = 2 * NS + 4 + 2 * NSB + 3;
   static constexpr int miscOff = barOff + NBAR * 8;
   static constexpr int total = miscOff + 16 + 1024;           // + alignment slack
+  static_assert(pBytes <= 8 * STG_ROW * 4, "P");
   static_assert(SLOT % 1024 == 0 && qBytes % 512 == 0 && total <= 227 * 1024, "shared memory");
   // tensor memory: S buffers, K scales per S buffer, query scales per group and operand
   static constexpr int SFA_COL = NSB * NQ, SFB_COL = SFA_COL + NSB * 4 * KS;
@@ -134,14 +136,10 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo, uint32_
   asm volatile("{ .reg .b64 d; mov.b64 d, {%1, %2}; tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d; }"
                ::"r"(taddr), "r"(lo), "r"(hi) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, uint64_t policy) {
-  asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "l"(policy) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_small_zfill(uint32_t dst, const void* src, bool valid, uint64_t policy) {
-  asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %2, %3, %4;"
-               ::"r"(dst), "l"(src), "n"(N), "r"(valid ? N : 0), "l"(policy) : "memory");
+// 16 bytes, those behind the first `bytes` as zeros (and not read)
+__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void* src, int bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;"
+               ::"r"(dst), "l"(src), "r"(bytes), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -226,23 +224,17 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::miscOff + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 32);
-      mbar_init(&empty[i], 1 + 4);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&qfull[i], 4);
-      mbar_init(&qempty[i], NWG + NCW);
-    }
-    for (int i = 0; i < NSB; ++i) {
-      mbar_init(&sfull[i], 1);
-      mbar_init(&sfree[i], 4);
-    }
-    mbar_init(staged, NCW);
-    mbar_init(merged, NCW);
-    mbar_init(done, NWG);
-    *abort_flag = 0;
+  // (on their way while the barriers are set up)
+  const int bs = p.block_size, lbs = p.log2_bs, Hk = p.num_kv_heads, RB = p.row_blocks, B = p.num_seqs;
+  auto seq_len = [&](int s) -> int { return max(0, min(__ldg(p.seq_lens + s), p.max_blocks * bs)); };
+  const int len0 = lane < B ? seq_len(lane) : 0;
+  const float kscale = __ldg(p.k_scale), vscale = __ldg(p.v_scale);
+  static_assert(S::NBAR <= 64, "a thread each");
+  if (threadIdx.x < S::NBAR) {
+    uint64_t* bar = full + threadIdx.x;
+    mbar_init(bar, bar < empty ? 32 : bar < qfull ? 1 + 4 : bar < qempty ? 4 : bar < sfull ? NWG + NCW : bar < sfree ? 1
+                   : bar < staged ? 4 : bar < done ? NCW : NWG);
+    if (threadIdx.x == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == S::WARP_MMA) tmem_alloc(tmem_slot, S::TMEM_COLS);
@@ -250,9 +242,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int bs = p.block_size, lbs = p.log2_bs, Hk = p.num_kv_heads, RB = p.row_blocks, B = p.num_seqs;
   const int Hq = Hk * p.qg;
-  auto seq_len = [&](int s) -> int { return max(0, min(__ldg(p.seq_lens + s), p.max_blocks * bs)); };
 
   if (warp < NCW) {
     // ======================================================== consumer warps
@@ -265,7 +255,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         for (long long i = lane; i < (long long)Hq * HD / 8; i += 32)
           reinterpret_cast<uint4*>(p.out + (long long)s * Hq * HD)[i] = make_uint4(0, 0, 0, 0);
     const uint32_t tl = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t psm = sb + S::pOff + warp * S::pBytes;
+    const uint32_t psm = sb + S::stgOff + warp * (8 * S::STG_ROW * 4);
     // ldmatrix row of this lane: token 16 (i / 2) + 8 (i % 2) + 4 (j % 2) + j / 2 of matrix i = lane / 8, row j
     const int mi = lane >> 3, mj = lane & 7;
     const uint32_t prow = psm + 16 * (16 * (mi >> 1) + 8 * (mi & 1) + 4 * (mj & 1) + (mj >> 1));
@@ -273,7 +263,6 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     const uint32_t vlane = HD == 128 ? S::V_OFF + (32 * wq + c) * 64 + (((g >> 1) ^ (c & 2)) << 4) + 8 * (g & 1)
                                      : S::V_OFF + (32 * wq + c) * 32 + 4 * g;
     const uint32_t slane = S::VS_OFF + (32 * wq + c) * (HD / 16) + (HD == 128 ? g : g >> 1);
-    const float vscale = __ldg(p.v_scale);
     float o[NT][MT][4], ol[NT][4], m[R];
     Turn tn(wg, S::NSG, NWG);
     int merges = 0;                                  // row blocks joined so far
@@ -350,6 +339,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         join_terms();
         free_s(tn.count);
       }
+      // (P and the staged rows share their memory)
+      if (merges > 0 && !warp_wait(merged, (merges - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       for (int i = tn.first; i < nt; i += NWG) {
         const int tok = (t0 + i) * TILE + 32 * wq + lane;               // this lane's token
         const bool cut = (t0 + i + 1) * (long long)TILE > L;            // the sequence ends in this tile
@@ -405,7 +396,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
         for (int nb = 0; nb < NT; ++nb) ldsm_x4_trans(prow + 512 * nb, pb[nb]);
         // one row block: the next tile's S comes while this one's V is multiplied (two: no registers for it)
-        if (NT == 1 && more) {
+        if (S::AHEAD && more) {
           if (!wait_s(tn.count + 1)) { ok = false; break; }
           load_s(tn.count + 1);
         }
@@ -437,11 +428,11 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
           for (int nb = 0; nb < NT; ++nb)      // the sum of p: a row of ones
             mma_f16_16816(ol[nb], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[nb][2 * k], pb[nb][2 * k + 1]);
-          if (NT == 1 && k == 0) join_terms();       // (of what v holds, if there is no next tile)
+          if (S::AHEAD && k == 0) join_terms();       // (of what v holds, if there is no next tile)
         }
         tn.step();
         if (more) {
-          if constexpr (NT > 1) {
+          if constexpr (!S::AHEAD) {
             if (!wait_s(tn.count)) { ok = false; break; }
             load_s(tn.count);
             join_terms();
@@ -451,9 +442,11 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         }
       }
       if (!ok) break;
+      const bool had = tn.first < nt;                 // this group had tiles of the item
       tn.item(nt);
       __syncwarp();
       if (lane == 0) mbar_arrive(&qempty[qb]);
+      __syncwarp();
       // ---- item done: the warps' states to shared memory, a row block at a time; each warp
       // joins one row of it
       const int rbase = 16 * (who.y % RB), kvh = who.y / RB;
@@ -461,7 +454,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       const uint32_t stg = sb + S::stgOff;
 #pragma unroll
       for (int nb = 0; nb < NT; ++nb, ++merges) {
-        if (merges > 0 && !warp_wait(merged, (merges - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
+        if (nb > 0 && !warp_wait(merged, (merges - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
+        if (had)                                         // (a group without tiles stages no rows)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const uint32_t a = stg + 4 * ((warp * 8 + 2 * c + hh) * S::STG_ROW + 2 * MT * g);
@@ -469,7 +463,10 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           for (int k = 0; k < MT; k += 2)
             sts_i4(a + 8 * k, make_int4(__float_as_int(o[nb][k][hh]), __float_as_int(o[nb][k][2 + hh]),
                                         __float_as_int(o[nb][k + 1][hh]), __float_as_int(o[nb][k + 1][2 + hh])));
-          if (g == 0) stsf(sb + S::mlOff + 8 * (warp * 8 + 2 * c + hh) + 4, ol[nb][hh]);
+        }
+        if (g == 0) {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) stsf(sb + S::mlOff + 8 * (warp * 8 + 2 * c + hh) + 4, ol[nb][hh]);
         }
 #pragma unroll
         for (int r = 0; r < 8; ++r)
@@ -479,10 +476,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         if (!warp_wait(staged, merges & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
         const int row = 8 * nb + warp;
         if (row < rows) {
-          float mw[NCW], M = kNoMax, l = 0.f;
+          float mw[NCW], lw[NCW], M = kNoMax, l = 0.f;
 #pragma unroll
           for (int k = 0; k < NCW; ++k) {
-            mw[k] = ldsf(sb + S::mlOff + 8 * (k * 8 + warp));
+            const uint2 d = lds64(sb + S::mlOff + 8 * (k * 8 + warp));
+            mw[k] = __uint_as_float(d.x);
+            lw[k] = __uint_as_float(d.y);
             M = fmaxf(M, mw[k]);
           }
           float acc[HD / 32];
@@ -490,8 +489,9 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           for (int d = 0; d < HD / 32; ++d) acc[d] = 0.f;
 #pragma unroll
           for (int k = 0; k < NCW; ++k) {
+            if (lw[k] == 0.f) continue;                  // no token: no rows
             const float f = ex2(mw[k] - M);
-            l = fmaf(f, ldsf(sb + S::mlOff + 8 * (k * 8 + warp) + 4), l);
+            l = fmaf(f, lw[k], l);
             const uint32_t a = stg + 4 * ((k * 8 + warp) * S::STG_ROW + (HD / 32) * lane);
             if constexpr (HD == 128) {
               const float4 d = lds_f4(a);
@@ -531,15 +531,15 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     const int lr = lane / CPR, cc = lane % CPR;
     const uint32_t kdst = lr * ROW + ((HD == 128 ? cc ^ ((lr >> 1) & 3) : cc ^ ((lr >> 2) & 1)) << 4);
     const uint32_t vdst = S::V_OFF + lr * ROW + ((HD == 128 ? cc ^ (lr & 2) : cc) << 4);
-    const uint32_t src_lane = lr * ROW + 16 * cc, sc_lane = (lane & 15) * (HD / 16);
+    const uint32_t src_lane = lr * ROW + 16 * cc;
+    constexpr int SPC = 16 / (HD / 16);                                 // tokens whose scales 16 bytes hold
     const size_t chunk = size_t(bs) * (HD / 2 + HD / 16), plane = size_t(Hk) * chunk;
 
     // ---- the CTA's range of units, and the item that holds its first one
+    // (32 sequences have at most 2^29 tiles)
     long long W = 0;
     for (int s0 = 0; s0 < B; s0 += 32)
-      if (s0 + lane < B) W += tiles_of(seq_len(s0 + lane));
-#pragma unroll
-    for (int sh = 16; sh; sh >>= 1) W += __shfl_xor_sync(0xffffffffu, W, sh);
+      W += __reduce_add_sync(0xffffffffu, (unsigned)tiles_of(s0 == 0 ? len0 : s0 + lane < B ? seq_len(s0 + lane) : 0));
     const long long U = W * (Hk * (long long)RB);
     const int G = gridDim.x;
     const long long per = div_nonneg(U, G), rem = U - per * G;          // the first `rem` ranges have one more
@@ -549,12 +549,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     // the first sequence with tiles behind tile x of the head's list
     auto find = [&](int s, long long off, long long x) -> Cursor {
       for (int s0 = s; s0 < B; s0 += 32) {
-        const int L = s0 + lane < B ? seq_len(s0 + lane) : 0;
+        const int L = s0 == 0 ? len0 : s0 + lane < B ? seq_len(s0 + lane) : 0;   // (s: of the first 32, or a later one)
         const int T = tiles_of(L);
-        long long incl = T;
+        int incl = T;
 #pragma unroll
         for (int sh = 1; sh < 32; sh <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, incl, sh);
+          const int v = __shfl_up_sync(0xffffffffu, incl, sh);
           if (lane >= sh) incl += v;
         }
         const unsigned hit = __ballot_sync(0xffffffffu, off + incl > x);
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     auto load_entries = [&](int s, int e0) -> int32_t {
       return s >= 0 && e0 + lane < p.max_blocks ? __ldg(p.block_table + (long long)s * p.table_stride + e0 + lane) : 0;
     };
-    const float base = __ldg(p.k_scale) * p.softmax_scale * kLog2e;
+    const float base = kscale * p.softmax_scale * kLog2e;
     uint4 qv[NT];
     load_q(cur, qv);
     int32_t ent0 = load_entries(cur.s, (int)(((long long)cur.t * TILE) >> lbs));
@@ -615,20 +615,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     bool ok = true;
     while (cur.s >= 0 && ok) {
       const int te = (int)min((long long)cur.T, cur.t + (u1 - u)), nt = te - cur.t;
-      int part = -1;
-      if (cur.t > 0) {
-        part = 2 * blockIdx.x;
-      } else if (te < cur.T) {
-        // begins here: the pieces are this CTA's and those of the ranges up to the sequence's last unit
-        part = 2 * blockIdx.x + 1;
-        const long long last = u + cur.T - 1, head = rem * (per + 1);
-        const long long cta = last < head ? div_nonneg(last, per + 1) : rem + div_nonneg(last - head, per);
-        meta = make_int4((int)cta - (int)blockIdx.x + 1, cur.s, cur.vh, 0);
-      }
-      const Cursor nxt = next(cur, u + nt);
-      uint4 qn[NT];
-      load_q(nxt, qn);
-      const int32_t ent0n = load_entries(nxt.s, (int)(((long long)nxt.t * TILE) >> lbs));
+      const int part = cur.t > 0 ? 2 * (int)blockIdx.x : te < cur.T ? 2 * (int)blockIdx.x + 1 : -1;
       const int L = cur.L;
       const uint64_t kbase = reinterpret_cast<uint64_t>(p.kv) + size_t(cur.vh / RB) * chunk;
       int e0 = (int)(((long long)cur.t * TILE) >> lbs);
@@ -666,36 +653,33 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
                 cp_async16(slot + vdst + (16 * q + RPI * ii) * ROW, reinterpret_cast<const uint8_t*>(src + plane) + RPI * ii * ROW, pol);
               }
             }
+            // scales: 16 bytes hold SPC tokens', a block of 16 tokens HD / 16 such pieces
 #pragma unroll
-            for (int q = 0; q < TILE / 32; ++q) {
-              const int from = 2 * q + (lane >> 4);
-              const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, codes + to_scales, from)) + sc_lane;
-#pragma unroll
-              for (int k = 0; k < KS; ++k)
-                cp_async_small<4>(slot + S::KS_OFF + 512 * k + 16 * lane + 4 * q, src + 4 * k, pol);
-              cp_async_small<HD / 16>(slot + S::VS_OFF + (32 * q + lane) * (HD / 16), src + plane, pol);
+            for (int q = 0; q < TILE / 32 / SPC; ++q) {
+              const int piece = 32 * q + lane;
+              const uint64_t src = __shfl_sync(0xffffffffu, codes + to_scales, piece / (HD / 16)) + (piece % (HD / 16)) * 16;
+              cp_async16(slot + S::KS_OFF + 16 * piece, reinterpret_cast<const uint8_t*>(src), pol);
+              cp_async16(slot + S::VS_OFF + 16 * piece, reinterpret_cast<const uint8_t*>(src + plane), pol);
             }
           } else {
             // the sequence ends in this tile: zeros behind it
-#pragma unroll 1
+#pragma unroll
             for (int q = 0; q < TILE / 16; ++q) {
               const uint64_t src = __shfl_sync(0xffffffffu, codes, q) + src_lane;
-#pragma unroll 1
+#pragma unroll
               for (int ii = 0; ii < 16 / RPI; ++ii) {
                 const bool valid = tok0 + 16 * q + RPI * ii + lr < L;
                 cp_async16_zfill(slot + kdst + (16 * q + RPI * ii) * ROW, reinterpret_cast<const uint8_t*>(src) + RPI * ii * ROW, valid, pol);
                 cp_async16_zfill(slot + vdst + (16 * q + RPI * ii) * ROW, reinterpret_cast<const uint8_t*>(src + plane) + RPI * ii * ROW, valid, pol);
               }
             }
-#pragma unroll 1
-            for (int q = 0; q < TILE / 32; ++q) {
-              const int from = 2 * q + (lane >> 4);
-              const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, codes + to_scales, from)) + sc_lane;
-              const bool valid = tok0 + 32 * q + lane < L;
 #pragma unroll
-              for (int k = 0; k < KS; ++k)
-                cp_async_small_zfill<4>(slot + S::KS_OFF + 512 * k + 16 * lane + 4 * q, src + 4 * k, valid, pol);
-              cp_async_small_zfill<HD / 16>(slot + S::VS_OFF + (32 * q + lane) * (HD / 16), src + plane, valid, pol);
+            for (int q = 0; q < TILE / 32 / SPC; ++q) {
+              const int piece = 32 * q + lane;
+              const uint64_t src = __shfl_sync(0xffffffffu, codes + to_scales, piece / (HD / 16)) + (piece % (HD / 16)) * 16;
+              const int bytes = max(0, min(16, (L - tok0 - SPC * piece) * (HD / 16)));
+              cp_async16_part(slot + S::KS_OFF + 16 * piece, reinterpret_cast<const uint8_t*>(src), bytes, pol);
+              cp_async16_part(slot + S::VS_OFF + 16 * piece, reinterpret_cast<const uint8_t*>(src + plane), bytes, pol);
             }
           }
           cp_async_arrive_noinc(&full[s]);
@@ -706,10 +690,11 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       if (n == 0 && !issue_to(min(nt, NWG * S::CPG))) break;
       const int qb = n & 1;
       if (n >= 2 && !warp_wait(&qempty[qb], ((n >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
-      // ---- query operand
-#pragma unroll
+      // ---- query operand (the second row block by the first one's code: code that runs once per item has to be fetched)
+#pragma unroll 1
       for (int h = 0; h < NT; ++h) {
-        const uint32_t ws[4] = {qv[h].x, qv[h].y, qv[h].z, qv[h].w};
+        const uint4 qw = NT > 1 && h ? qv[NT - 1] : qv[0];
+        const uint32_t ws[4] = {qw.x, qw.y, qw.z, qw.w};
         float x[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -728,13 +713,10 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         const bool row_ok = ((fin >> (lane & 16)) & 0xffffu) == 0xffffu;
         if (!row_ok) amax = 0.f;
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));      // of 16 dims
-        // exponent that puts the 16 dims' largest into (2, 4]; the row's largest exponent
-        int eb = -200;
-        if (amax > 0.f) {
-          int ex;
-          const float fr = frexpf(amax, &ex);                           // amax = fr 2^ex, fr in [1/2, 1)
-          eb = (fr == 0.5f ? ex - 1 : ex) - 2;
-        }
+        // exponent eb that puts the 16 dims' largest into [2, 4]: amax <= 2^(eb + 2), amax >= 2^(eb + 1); the row's
+        // largest exponent er
+        const uint32_t ab = __float_as_uint(amax);
+        const int eb = ab == 0 ? -200 : int(ab >> 23) - 128 + ((ab & 0x7fffffu) != 0 ? 0 : -1);   // (subnormals as 2^-126)
         int er = eb;
 #pragma unroll
         for (int sh = 2; sh < 16; sh <<= 1) er = max(er, __shfl_xor_sync(0xffffffffu, er, sh));
@@ -745,26 +727,31 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         const float up = __uint_as_float(uint32_t(127 + s1) << 23), up2 = __uint_as_float(uint32_t(127 + s2) << 23);
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = row_ok ? x[k] * up * up2 : 0.f;
-        const int row8 = qrow;
+        uint32_t words[QT];
 #pragma unroll
         for (int term = 0; term < QT; ++term) {
-          // terms k and k + 3: pass k, scale 2^(rel + 8 - 3 k), in columns 0 .. 7 and 8 .. 15 of the row block
-          const int pass = term % PASSES, es = rel + 8 - 3 * pass;
-          uint32_t word = 0;
+          words[term] = 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t code = f32x2_to_e2m1x2(x[2 * k], x[2 * k + 1]);
-            const uint32_t back = e2m1x2_to_f16x2<0>(code);
-            x[2 * k] = (x[2 * k] - f16_lo_to_f32(back)) * 8.f;
-            x[2 * k + 1] = (x[2 * k + 1] - f16_hi_to_f32(back)) * 8.f;
-            word |= code << (8 * k);
+            words[term] |= code << (8 * k);
+            if (term < QT - 1) {
+              // (x - code) 8, the residual
+              const uint32_t back = e2m1x2_to_f16x2<0>(code);
+              x[2 * k] = fmaf(-8.f, f16_lo_to_f32(back), 8.f * x[2 * k]);
+              x[2 * k + 1] = fmaf(-8.f, f16_hi_to_f32(back), 8.f * x[2 * k + 1]);
+            }
           }
-          if (es < -9) word = 0;
-          const int col = 16 * h + 8 * (term / PASSES) + row8;
-          if (h16 < HD / 8) {
+        }
+        if (h16 < HD / 8) {
+#pragma unroll
+          for (int term = 0; term < QT; ++term) {
+            // terms k and k + 3: pass k, scale 2^(rel + 8 - 3 k), in columns 0 .. 7 and 8 .. 15 of the row block
+            const int pass = term % PASSES, es = rel + 8 - 3 * pass;
+            const int col = 16 * h + 8 * (term / PASSES) + qrow;
             const int ch = HD == 128 ? (h16 >> 2) ^ ((col >> 1) & 3) : (h16 >> 2) ^ ((col >> 2) & 1);
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb + S::qOff + qb * S::qBytes + (pass * NQ + col) * ROW + 16 * ch + 4 * (h16 & 3)),
-                         "r"(word) : "memory");
+                         "r"(es < -9 ? 0u : words[term]) : "memory");
             if ((h16 & 1) == 0)
               sts8(sb + S::qsOff + ((qb * PASSES + pass) * KS + (h16 >> 3)) * 512 + col * 16 + ((h16 >> 1) & 3),
                    es >= -6 ? uint32_t(es + 7) << 3 : es >= -9 ? 1u << (es + 9) : 1u);
@@ -786,13 +773,19 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       __syncwarp();
       if (lane == 0) mbar_arrive(&qfull[qb]);
       ++n;
+      if (cur.t == 0 && te < cur.T) {
+        // begins here and goes on: the pieces are this CTA's and those of the ranges up to the sequence's last unit
+        const long long last = u + cur.T - 1, head = rem * (per + 1);
+        const long long cta = last < head ? div_nonneg(last, per + 1) : rem + div_nonneg(last - head, per);
+        meta = make_int4((int)cta - (int)blockIdx.x + 1, cur.s, cur.vh, 0);
+      }
+      const Cursor nxt = next(cur, u + nt);
+      load_q(nxt, qv);
+      ent0 = load_entries(nxt.s, (int)(((long long)nxt.t * TILE) >> lbs));
       if (!issue_to(nt)) break;
       tn.item(nt);
       u += nt;
       cur = nxt;
-#pragma unroll
-      for (int h = 0; h < NT; ++h) qv[h] = qn[h];
-      ent0 = ent0n;
     }
     if (cur.s < 0) {
       // no more items
@@ -834,7 +827,26 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           ok = false;
           break;
         }
-        fence_proxy_async();     // the copied bytes (generic proxy) become visible to the tensor core
+        // K's scales in the tensor core's order: 16 bytes are those of tokens i, i + 32, i + 64 and i + 96
+        {
+          const uint32_t ksm = sb + s * S::SLOT + S::KS_OFF;
+          uint32_t d[4][KS];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (KS == 2) {
+              const uint2 e = lds64(ksm + 8 * (32 * q + lane));
+              d[q][0] = e.x;
+              d[q][1] = e.y;
+            } else {
+              d[q][0] = lds32(ksm + 4 * (32 * q + lane));
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < KS; ++k) sts_i4(ksm + 512 * k + 16 * lane, make_int4(d[0][k], d[1][k], d[2][k], d[3][k]));
+        }
+        fence_proxy_async();     // these and the copied bytes (generic proxy) become visible to the tensor core
+        __syncwarp();
         tc_fence_after();
         if (elect_one()) {
           const uint32_t k_lo = desc_lo(sb + s * S::SLOT, 16), sfa = tmem + S::SFA_COL + b * 4 * KS;
@@ -882,54 +894,79 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 
 // Joins the pieces of the item that begins in range blockIdx.x and continues: out = sum_i
 // 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, row blockIdx.y of its row block; each warp takes
-// every NW-th piece.
+// every NW-th piece. What the first PRE pieces of a warp hold is read before it is known
+// whether there are such pieces (the slots exist), so that a call costs one trip to memory.
 template <int HD>
-__global__ void __launch_bounds__(128) decode4_combine_kernel(const d4::Params p) {
+__global__ void __launch_bounds__(128) decode4_combine_kernel(const d4::Params p, const int slots) {
   using namespace d4;
-  constexpr int NW = 4, V = HD / 32;
-  __shared__ float s_o[NW][HD], s_l[NW];
-  const int4 meta = p.meta[blockIdx.x];
-  const int r = blockIdx.y, rbase = 16 * (meta.z % p.row_blocks);
-  if (meta.x == 0 || rbase + r >= p.qg) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto slot = [&](int i) -> int { return i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i); };
-  float M = kNoMax;
-  for (int i = lane; i < meta.x; i += 32) M = fmaxf(M, p.part_ml[slot(i) * 16 + r].x);
-  M = warp_max(M);
-  float acc[V], l = 0.f;
-#pragma unroll
-  for (int d = 0; d < V; ++d) acc[d] = 0.f;
-#pragma unroll 8
-  for (int i = warp; i < meta.x; i += NW) {
-    const float2 ml = p.part_ml[slot(i) * 16 + r];
-    const float* src = p.part_o + ((long long)slot(i) * 16 + r) * HD + V * lane;
-    const float f = ex2(ml.x - M);
-    l = fmaf(f, ml.y, l);
+  constexpr int NW = 4, V = HD / 32, PRE = 2;
+  __shared__ float s_o[NW][HD], s_l[NW], s_m[NW];
+  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  struct Piece {
+    float2 ml;
+    float o[V];
+  };
+  auto load = [&](int i) -> Piece {
+    const int slot = min(i == 0 ? 2 * (int)blockIdx.x + 1 : 2 * ((int)blockIdx.x + i), slots - 1);
+    Piece q;
+    q.ml = p.part_ml[slot * 16 + r];
+    const float* src = p.part_o + ((long long)slot * 16 + r) * HD + V * lane;
     if constexpr (HD == 128) {
       const float4 d = *reinterpret_cast<const float4*>(src);
-      acc[0] = fmaf(f, d.x, acc[0]);
-      acc[1] = fmaf(f, d.y, acc[1]);
-      acc[2] = fmaf(f, d.z, acc[2]);
-      acc[3] = fmaf(f, d.w, acc[3]);
+      q.o[0] = d.x; q.o[1] = d.y; q.o[2] = d.z; q.o[3] = d.w;
     } else {
       const float2 d = *reinterpret_cast<const float2*>(src);
-      acc[0] = fmaf(f, d.x, acc[0]);
-      acc[1] = fmaf(f, d.y, acc[1]);
+      q.o[0] = d.x; q.o[1] = d.y;
     }
+    return q;
+  };
+  const int4 meta = p.meta[blockIdx.x];
+  Piece pre[PRE];
+#pragma unroll
+  for (int i = 0; i < PRE; ++i) pre[i] = load(warp + NW * i);
+  const float vscale = __ldg(p.v_scale);
+  const int rbase = 16 * (meta.z % p.row_blocks);
+  if (meta.x == 0 || rbase + r >= p.qg) return;
+  float M = kNoMax, acc[V], l = 0.f;
+#pragma unroll
+  for (int d = 0; d < V; ++d) acc[d] = 0.f;
+  auto add = [&](const Piece& q) {
+    const float now = fmaxf(M, q.ml.x), a = ex2(M - now), f = ex2(q.ml.x - now);
+    M = now;
+    l = fmaf(f, q.ml.y, l * a);
+#pragma unroll
+    for (int d = 0; d < V; ++d) acc[d] = fmaf(f, q.o[d], acc[d] * a);
+  };
+#pragma unroll
+  for (int i = 0; i < PRE; ++i)
+    if (warp + NW * i < meta.x) add(pre[i]);
+  for (int i = warp + NW * PRE; i < meta.x; i += 4 * NW) {
+    Piece q[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) q[u] = load(i + NW * u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + NW * u < meta.x) add(q[u]);
   }
 #pragma unroll
   for (int d = 0; d < V; ++d) s_o[warp][V * lane + d] = acc[d];
-  if (lane == 0) s_l[warp] = l;
+  if (lane == 0) {
+    s_l[warp] = l;
+    s_m[warp] = M;
+  }
   __syncthreads();
   if (threadIdx.x < HD) {
-    float num = 0.f, den = 0.f;
+    float top = kNoMax, num = 0.f, den = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, s_m[w]);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      num += s_o[w][threadIdx.x];
-      den += s_l[w];
+      const float f = ex2(s_m[w] - top);
+      num = fmaf(f, s_o[w][threadIdx.x], num);
+      den = fmaf(f, s_l[w], den);
     }
     const long long row = (long long)meta.y * p.num_kv_heads * p.qg + (meta.z / p.row_blocks) * p.qg + rbase + r;
-    reinterpret_cast<__nv_bfloat16*>(p.out)[row * HD + threadIdx.x] = __float2bfloat16_rn(num * (__ldg(p.v_scale) / den));
+    reinterpret_cast<__nv_bfloat16*>(p.out)[row * HD + threadIdx.x] = __float2bfloat16_rn(num * (vscale / den));
   }
 }
 
@@ -988,8 +1025,8 @@ cudaError_t launch_decode4(const Decode4Launch& a, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || grid <= 0) return e;
   const dim3 cgrid(grid, std::min(16, a.qg));
-  if (a.head_dim == 64) decode4_combine_kernel<64><<<cgrid, 128, 0, stream>>>(p);
-  else decode4_combine_kernel<128><<<cgrid, 128, 0, stream>>>(p);
+  if (a.head_dim == 64) decode4_combine_kernel<64><<<cgrid, 128, 0, stream>>>(p, 2 * grid);
+  else decode4_combine_kernel<128><<<cgrid, 128, 0, stream>>>(p, 2 * grid);
   return cudaGetLastError();
 }
 
