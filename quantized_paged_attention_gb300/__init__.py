@@ -792,17 +792,24 @@ def nvfp4_desc(q, kv_cache, block_table, query_group, softmax_scale=None):
     NB, planes, Hk, bs, D = _cache4_shape(kv_cache)
     if planes != 2:
         _fail("kv_cache must have two planes, keys and values")
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[1] != Hk * query_group or q.shape[2] != D:
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[1:] != (Hk * query_group, D):
         _fail("q must be bfloat16 [num_seqs, num_kv_heads*query_group, head_dim]")
     B = q.shape[0]
-    if B and q.stride(2) != 1:
-        _fail("q must be contiguous along head_dim")
     maxb, stride = _rows(block_table)
     if block_table.shape[0] != B:
         _fail("block_table must have one row per sequence")
-    _below_2_31(B, NB, Hk, query_group)
+    if not (B < 1 << 31 and NB < 1 << 31 and Hk < 1 << 31 and 0 <= query_group < 1 << 31):
+        _below_2_31(B, NB, Hk, query_group)
+    if q.is_contiguous():
+        return Nvfp4Desc(B, Hk, query_group, D, bs, NB, maxb, 0.0 if softmax_scale is None else float(softmax_scale),
+                         0, 0, stride)
+    if B and q.stride(2) != 1:
+        _fail("q must be contiguous along head_dim")
     return Nvfp4Desc(B, Hk, query_group, D, bs, NB, maxb, 0.0 if softmax_scale is None else float(softmax_scale),
                      _dim_stride(q, 0), _dim_stride(q, 1), stride)
+
+
+_DECODE4_WORKSPACE = {}                # head_dim -> bytes
 
 
 def pa_decode_nvfp4_workspace_size(desc: Nvfp4Desc) -> int:
@@ -823,8 +830,10 @@ def pa_decode_nvfp4(q, kv_cache, block_table, seq_lens, k_scale, v_scale, query_
     want = nvfp4_desc(q, kv_cache, block_table, query_group, softmax_scale)
     if desc is not None and bytes(desc) != bytes(want):
         _fail("desc does not describe these tensors")
-    _one_scale(k_scale)
-    _one_scale(v_scale)
+    f32 = torch.float32
+    if k_scale.dtype != f32 or v_scale.dtype != f32 or k_scale.numel() != 1 or v_scale.numel() != 1:
+        _one_scale(k_scale)
+        _one_scale(v_scale)
     if seq_lens.dtype != torch.int32 or not seq_lens.is_contiguous() or seq_lens.numel() != want.num_seqs:
         _fail("seq_lens must be contiguous int32 with one entry per sequence")
     if out is None:
@@ -832,7 +841,12 @@ def pa_decode_nvfp4(q, kv_cache, block_table, seq_lens, k_scale, v_scale, query_
     elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
         _fail("out must be contiguous bfloat16 of the shape of q")
     if workspace is None:
-        workspace = _empty(max(pa_decode_nvfp4_workspace_size(want), 256), torch.uint8, q.device, stream)
+        nbytes = _DECODE4_WORKSPACE.get(want.head_dim)
+        if nbytes is None:             # (depends on nothing else; 0: the call will be refused)
+            nbytes = max(pa_decode_nvfp4_workspace_size(want), 256)
+            if nbytes > 256:
+                _DECODE4_WORKSPACE[want.head_dim] = nbytes
+        workspace = _empty(nbytes, torch.uint8, q.device, stream)
     elif not workspace.is_contiguous():
         _fail("workspace must be contiguous")
     index = _device_of(q, kv_cache, block_table, seq_lens, k_scale, v_scale, out, workspace)

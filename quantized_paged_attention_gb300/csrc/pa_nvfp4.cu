@@ -35,7 +35,9 @@
 //    path has no exchange of maxima and no rescaling.
 // An item that its range does not cut is written out; pieces go to the workspace (two
 // slots per CTA: a range begins in at most one cut item and ends in another), and a
-// second kernel joins them in order.
+// second kernel joins them in order. Where no sequence can have more than 4 tiles
+// (max_blocks_per_seq * block_size <= 512) the list is of whole sequences and the second
+// kernel is not launched: {SHORT}.
 #define QPA_WHOLE_UNIT
 #include "qpa.h"
 #include "common.cuh"
@@ -117,6 +119,7 @@ struct Params {
   int4* meta;                       // [CTAs] {pieces (0: none), sequence, virtual head, 0}
   long long q_stride_seq, q_stride_head, table_stride;
   int num_seqs, num_kv_heads, qg, row_blocks, block_size, log2_bs, num_blocks, max_blocks;
+  int whole;                        // a unit of work is a sequence, not a tile: no item is cut
   float softmax_scale;
 };
 
@@ -194,7 +197,7 @@ __device__ __forceinline__ int tiles_of(int len) { return (int)(((unsigned)len +
 // vh / RB, row block vh % RB).
 struct Cursor {
   int s, vh, L, T;
-  long long off;      // tiles of the sequences before s
+  long long off;      // work of the sequences before s
   int t;              // first tile of the item
 };
 
@@ -536,10 +539,11 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     const size_t chunk = size_t(bs) * (HD / 2 + HD / 16), plane = size_t(Hk) * chunk;
 
     // ---- the CTA's range of units, and the item that holds its first one
-    // (32 sequences have at most 2^29 tiles)
+    // work of a sequence of T tiles (32 sequences have at most 2^29 tiles)
+    auto work = [&](int T) -> int { return p.whole ? min(T, 1) : T; };
     long long W = 0;
     for (int s0 = 0; s0 < B; s0 += 32)
-      W += __reduce_add_sync(0xffffffffu, (unsigned)tiles_of(s0 == 0 ? len0 : s0 + lane < B ? seq_len(s0 + lane) : 0));
+      W += __reduce_add_sync(0xffffffffu, (unsigned)work(tiles_of(s0 == 0 ? len0 : s0 + lane < B ? seq_len(s0 + lane) : 0)));
     const long long U = W * (Hk * (long long)RB);
     const int G = gridDim.x;
     const long long per = div_nonneg(U, G), rem = U - per * G;          // the first `rem` ranges have one more
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       for (int s0 = s; s0 < B; s0 += 32) {
         const int L = s0 == 0 ? len0 : s0 + lane < B ? seq_len(s0 + lane) : 0;   // (s: of the first 32, or a later one)
         const int T = tiles_of(L);
-        int incl = T;
+        int incl = work(T);
 #pragma unroll
         for (int sh = 1; sh < 32; sh <<= 1) {
           const int v = __shfl_up_sync(0xffffffffu, incl, sh);
@@ -565,7 +569,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           c.vh = 0;
           c.L = __shfl_sync(0xffffffffu, L, src);
           c.T = __shfl_sync(0xffffffffu, T, src);
-          c.off = off + __shfl_sync(0xffffffffu, incl, src) - c.T;
+          c.off = off + __shfl_sync(0xffffffffu, incl, src) - work(c.T);
           c.t = (int)(x - c.off);
           return c;
         }
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     // the item that begins at unit `at`, behind item c
     auto next = [&](const Cursor& c, long long at) -> Cursor {
       if (at >= u1) return Cursor{-1, 0, 0, 0, 0, 0};
-      const long long off = c.off + c.T;
+      const long long off = c.off + work(c.T);
       Cursor n = off < W ? find(c.s + 1, off, off) : find(0, 0, 0);
       n.vh = off < W ? c.vh : c.vh + 1;
       return n;
@@ -614,7 +618,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     int4 meta = make_int4(0, 0, 0, 0);
     bool ok = true;
     while (cur.s >= 0 && ok) {
-      const int te = (int)min((long long)cur.T, cur.t + (u1 - u)), nt = te - cur.t;
+      const int te = p.whole ? cur.T : (int)min((long long)cur.T, cur.t + (u1 - u)), nt = te - cur.t;
+      const long long behind = u + work(nt);
       const int part = cur.t > 0 ? 2 * (int)blockIdx.x : te < cur.T ? 2 * (int)blockIdx.x + 1 : -1;
       const int L = cur.L;
       const uint64_t kbase = reinterpret_cast<uint64_t>(p.kv) + size_t(cur.vh / RB) * chunk;
@@ -779,12 +784,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         const long long cta = last < head ? div_nonneg(last, per + 1) : rem + div_nonneg(last - head, per);
         meta = make_int4((int)cta - (int)blockIdx.x + 1, cur.s, cur.vh, 0);
       }
-      const Cursor nxt = next(cur, u + nt);
+      const Cursor nxt = next(cur, behind);
       load_q(nxt, qv);
       ent0 = load_entries(nxt.s, (int)(((long long)nxt.t * TILE) >> lbs));
       if (!issue_to(nt)) break;
       tn.item(nt);
-      u += nt;
+      u = behind;
       cur = nxt;
     }
     if (cur.s < 0) {
@@ -1008,7 +1013,8 @@ cudaError_t launch_decode4(const Decode4Launch& a, cudaStream_t stream) {
   p.softmax_scale = a.softmax_scale;
   // no more CTAs than units there can be
   const long long tiles = ((long long)a.max_blocks * a.block_size + d4::TILE - 1) / d4::TILE;
-  const long long units = std::min(tiles, 1LL << 20) * a.num_seqs * a.num_kv_heads * p.row_blocks;
+  p.whole = tiles <= 4;
+  const long long units = (p.whole ? 1 : std::min(tiles, 1LL << 20)) * a.num_seqs * a.num_kv_heads * p.row_blocks;
   const int grid = (int)std::min<long long>(units, std::min(a.num_sms, d4::MAX_CTAS));
   auto launch = [&](auto kernel, int threads, int smem) {
     cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1023,7 +1029,7 @@ cudaError_t launch_decode4(const Decode4Launch& a, cudaStream_t stream) {
     else launch(decode4_kernel<2, 128>, d4::Smem<2, 128>::THREADS, d4::Smem<2, 128>::total);
   }
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || grid <= 0) return e;
+  if (e != cudaSuccess || p.whole) return e;
   const dim3 cgrid(grid, std::min(16, a.qg));
   if (a.head_dim == 64) decode4_combine_kernel<64><<<cgrid, 128, 0, stream>>>(p, 2 * grid);
   else decode4_combine_kernel<128><<<cgrid, 128, 0, stream>>>(p, 2 * grid);
