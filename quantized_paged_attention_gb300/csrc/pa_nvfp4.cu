@@ -51,6 +51,7 @@ constexpr int TILE = 128;           // tokens per tile
 constexpr int QT = 6;               // e2m1 terms of a query
 constexpr int PASSES = 3;           // of the QK product: terms k and k + 3
 constexpr int MAX_CTAS = 160;
+constexpr int COMBINE_WARPS = 4;
 constexpr float kNoMax = -1e30f;    // no token seen yet: finite, so that differences stay defined
 constexpr float kBelow = 8.f;       // the reference is set this far below the largest logit (p up to 2^8)
 constexpr float kTop = 14.f;        // and moves when a logit is this far above it (p up to 2^14 in f16)
@@ -156,6 +157,10 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
 __device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// Order of the 16-byte pieces of staged rows 2 c and 2 c + 1: a store's 8 lanes of a phase (c = 0 .. 3, two dims groups
+// that lie 4 (head_dim 128) or 2 pieces apart) then go to 8 different ones.
+template <int HD>
+__device__ __forceinline__ int stage_swizzle(int c) { return HD == 128 ? c : (c & 1) | ((c & 2) << 1); }
 // (x, y) * w + (a, b)
 __device__ __forceinline__ void fma2(float& x, float& y, float w, float a, float b) {
   asm("{ .reg .b64 p, q, r; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %2}; mov.b64 r, {%3, %4}; "
@@ -455,25 +460,41 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       const int rbase = 16 * (who.y % RB), kvh = who.y / RB;
       const int rows = min(R, p.qg - rbase);
       const uint32_t stg = sb + S::stgOff;
-#pragma unroll
+      // (a loop, the second row block moved to the first one's registers: this runs once per item, and its code has to
+      // be fetched)
+#pragma unroll 1
       for (int nb = 0; nb < NT; ++nb, ++merges) {
         if (nb > 0 && !warp_wait(merged, (merges - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
         if (had)                                         // (a group without tiles stages no rows)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t a = stg + 4 * ((warp * 8 + 2 * c + hh) * S::STG_ROW + 2 * MT * g);
+          // (16-byte pieces of a row in an order of the row's own: the rows of a store's lanes lie in the same banks)
+          const uint32_t a = stg + 4 * ((warp * 8 + 2 * c + hh) * S::STG_ROW);
 #pragma unroll
           for (int k = 0; k < MT; k += 2)
-            sts_i4(a + 8 * k, make_int4(__float_as_int(o[nb][k][hh]), __float_as_int(o[nb][k][2 + hh]),
-                                        __float_as_int(o[nb][k + 1][hh]), __float_as_int(o[nb][k + 1][2 + hh])));
+            sts_i4(a + 16 * ((MT / 2 * g + k / 2) ^ stage_swizzle<HD>(c)), make_int4(__float_as_int(o[0][k][hh]), __float_as_int(o[0][k][2 + hh]),
+                                        __float_as_int(o[0][k + 1][hh]), __float_as_int(o[0][k + 1][2 + hh])));
         }
-        if (g == 0) {
+        {
+          // lane r < 8: m of row r (selected: a branch per row takes 100 cycles), l from the lane c = r / 2 of g = 0
+          float mr = m[0];
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) stsf(sb + S::mlOff + 8 * (warp * 8 + 2 * c + hh) + 4, ol[nb][hh]);
+          for (int r = 1; r < 8; ++r) mr = lane == r ? m[r] : mr;
+          const float l0 = __shfl_sync(0xffffffffu, ol[0][0], (lane >> 1) & 3), l1 = __shfl_sync(0xffffffffu, ol[0][1], (lane >> 1) & 3);
+          if (lane < 8)
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sb + S::mlOff + 8 * (warp * 8 + lane)), "f"(mr),
+                         "f"(lane & 1 ? l1 : l0) : "memory");
         }
+        if constexpr (NT > 1) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (lane == r) stsf(sb + S::mlOff + 8 * (warp * 8 + r), m[8 * nb + r]);
+          for (int k = 0; k < MT; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[0][k][e] = o[NT - 1][k][e];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) ol[0][e] = ol[NT - 1][e];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) m[r] = m[R - 8 + r];
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(staged);
         if (!warp_wait(staged, merges & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
@@ -490,22 +511,24 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           float acc[HD / 32];
 #pragma unroll
           for (int d = 0; d < HD / 32; ++d) acc[d] = 0.f;
+          // (rows of a warp that saw no token hold anything: taken as 0)
 #pragma unroll
           for (int k = 0; k < NCW; ++k) {
-            if (lw[k] == 0.f) continue;                  // no token: no rows
             const float f = ex2(mw[k] - M);
+            const bool some = lw[k] != 0.f;
             l = fmaf(f, lw[k], l);
-            const uint32_t a = stg + 4 * ((k * 8 + warp) * S::STG_ROW + (HD / 32) * lane);
+            const uint32_t a = stg + 4 * ((k * 8 + warp) * S::STG_ROW) +
+                               16 * ((lane * (HD / 32) / 4) ^ stage_swizzle<HD>((warp >> 1) & 3)) + (HD == 128 ? 0 : 8 * (lane & 1));
             if constexpr (HD == 128) {
               const float4 d = lds_f4(a);
-              acc[0] = fmaf(f, d.x, acc[0]);
-              acc[1] = fmaf(f, d.y, acc[1]);
-              acc[2] = fmaf(f, d.z, acc[2]);
-              acc[3] = fmaf(f, d.w, acc[3]);
+              acc[0] = fmaf(f, some ? d.x : 0.f, acc[0]);
+              acc[1] = fmaf(f, some ? d.y : 0.f, acc[1]);
+              acc[2] = fmaf(f, some ? d.z : 0.f, acc[2]);
+              acc[3] = fmaf(f, some ? d.w : 0.f, acc[3]);
             } else {
               const uint2 d = lds64(a);
-              acc[0] = fmaf(f, __uint_as_float(d.x), acc[0]);
-              acc[1] = fmaf(f, __uint_as_float(d.y), acc[1]);
+              acc[0] = fmaf(f, some ? __uint_as_float(d.x) : 0.f, acc[0]);
+              acc[1] = fmaf(f, some ? __uint_as_float(d.y) : 0.f, acc[1]);
             }
           }
           if (inf.w < 0) {
@@ -757,9 +780,14 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
             const int ch = HD == 128 ? (h16 >> 2) ^ ((col >> 1) & 3) : (h16 >> 2) ^ ((col >> 2) & 1);
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb + S::qOff + qb * S::qBytes + (pass * NQ + col) * ROW + 16 * ch + 4 * (h16 & 3)),
                          "r"(es < -9 ? 0u : words[term]) : "memory");
-            if ((h16 & 1) == 0)
+          }
+          if ((h16 & 1) == 0) {
+#pragma unroll
+            for (int term = 0; term < QT; ++term) {
+              const int pass = term % PASSES, es = rel + 8 - 3 * pass, col = 16 * h + 8 * (term / PASSES) + qrow;
               sts8(sb + S::qsOff + ((qb * PASSES + pass) * KS + (h16 >> 3)) * 512 + col * 16 + ((h16 >> 1) & 3),
                    es >= -6 ? uint32_t(es + 7) << 3 : es >= -9 ? 1u << (es + 9) : 1u);
+            }
           }
         }
         if (h16 == 0) {
@@ -899,12 +927,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 
 // Joins the pieces of the item that begins in range blockIdx.x and continues: out = sum_i
 // 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, row blockIdx.y of its row block; each warp takes
-// every NW-th piece. What the first PRE pieces of a warp hold is read before it is known
-// whether there are such pieces (the slots exist), so that a call costs one trip to memory.
+// every NW-th piece. What its first PRE ones hold is read before it is known whether there
+// are such pieces (the slots exist), so that few pieces cost one trip to memory.
 template <int HD>
-__global__ void __launch_bounds__(128) decode4_combine_kernel(const d4::Params p, const int slots) {
+__global__ void __launch_bounds__(32 * d4::COMBINE_WARPS) decode4_combine_kernel(const d4::Params p, const int slots) {
   using namespace d4;
-  constexpr int NW = 4, V = HD / 32, PRE = 2;
+  constexpr int NW = COMBINE_WARPS, V = HD / 32, PRE = 2, UN = 4;
   __shared__ float s_o[NW][HD], s_l[NW], s_m[NW];
   const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   struct Piece {
@@ -945,12 +973,12 @@ __global__ void __launch_bounds__(128) decode4_combine_kernel(const d4::Params p
 #pragma unroll
   for (int i = 0; i < PRE; ++i)
     if (warp + NW * i < meta.x) add(pre[i]);
-  for (int i = warp + NW * PRE; i < meta.x; i += 4 * NW) {
-    Piece q[4];
+  for (int i = warp + NW * PRE; i < meta.x; i += UN * NW) {
+    Piece q[UN];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) q[u] = load(i + NW * u);
+    for (int u = 0; u < UN; ++u) q[u] = load(min(i + NW * u, meta.x - 1));
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < UN; ++u)
       if (i + NW * u < meta.x) add(q[u]);
   }
 #pragma unroll
@@ -1031,8 +1059,8 @@ cudaError_t launch_decode4(const Decode4Launch& a, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.whole) return e;
   const dim3 cgrid(grid, std::min(16, a.qg));
-  if (a.head_dim == 64) decode4_combine_kernel<64><<<cgrid, 128, 0, stream>>>(p, 2 * grid);
-  else decode4_combine_kernel<128><<<cgrid, 128, 0, stream>>>(p, 2 * grid);
+  if (a.head_dim == 64) decode4_combine_kernel<64><<<cgrid, 32 * d4::COMBINE_WARPS, 0, stream>>>(p, 2 * grid);
+  else decode4_combine_kernel<128><<<cgrid, 32 * d4::COMBINE_WARPS, 0, stream>>>(p, 2 * grid);
   return cudaGetLastError();
 }
 
