@@ -157,6 +157,16 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
 __device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// mbar_arrive by the lanes with `on`, without a branch (a branch of one lane costs the warp about 100 cycles)
+__device__ __forceinline__ void arrive_if(bool on, uint64_t* bar) {
+  asm volatile("{ .reg .pred p; .reg .b64 st; setp.ne.u32 p, %1, 0; @p mbarrier.arrive.release.cta.shared::cta.b64 st, [%0]; }"
+               ::"r"(smem_u32(bar)), "r"((uint32_t)on) : "memory");
+}
+// warp_wait, whose own path the warp takes only if a lane's first try fails
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait(bar, parity, abort_flag, err);
+}
 // Order of the 16-byte pieces of staged rows 2 c and 2 c + 1: a store's 8 lanes of a phase (c = 0 .. 3, two dims groups
 // that lie 4 (head_dim 128) or 2 pieces apart) then go to 8 different ones.
 template <int HD>
@@ -277,7 +287,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int qb = n & 1;
-      if (!warp_wait(&qfull[qb], (n >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+      if (!wait_bar(&qfull[qb], (n >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
       const int4 inf = lds_i4(sb + S::infoOff + 64 * qb);               // L, first tile, tiles, part (-1: whole)
       const int4 who = lds_i4(sb + S::infoOff + 64 * qb + 16);          // sequence, virtual head
       const int L = inf.x, t0 = inf.y, nt = inf.z;
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       // V's bytes into registers; the slot is free then
       auto load_v = [&]() -> bool {
         const int s = wg * S::NSG + tn.slot;
-        if (!warp_wait(&full[s], tn.phase, abort_flag, KERR_TIMEOUT_FULL)) return false;
+        if (!wait_bar(&full[s], tn.phase, abort_flag, KERR_TIMEOUT_FULL)) return false;
         const uint32_t slot = sb + s * S::SLOT;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -311,12 +321,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           sc[u] = lds8(slot + slane + 4 * u * (HD / 16));
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
+        arrive_if(lane == 0, &empty[s]);
         return true;
       };
       // S on its way to registers
       auto wait_s = [&](int count) -> bool {
-        if (!warp_wait(&sfull[2 * wg + (count & 1)], (count >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) return false;
+        if (!wait_bar(&sfull[2 * wg + (count & 1)], (count >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) return false;
         tc_fence_after();
         return true;
       };
@@ -339,7 +349,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       auto free_s = [&](int count) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sfree[2 * wg + (count & 1)]);
+        arrive_if(lane == 0, &sfree[2 * wg + (count & 1)]);
       };
       if (tn.first < nt) {
         if (!load_v() || !wait_s(tn.count)) { ok = false; break; }
@@ -348,7 +358,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         free_s(tn.count);
       }
       // (P and the staged rows share their memory)
-      if (merges > 0 && !warp_wait(merged, (merges - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
+      if (merges > 0 && !wait_bar(merged, (merges - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       for (int i = tn.first; i < nt; i += NWG) {
         const int tok = (t0 + i) * TILE + 32 * wq + lane;               // this lane's token
         const bool cut = (t0 + i + 1) * (long long)TILE > L;            // the sequence ends in this tile
@@ -453,7 +463,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       const bool had = tn.first < nt;                 // this group had tiles of the item
       tn.item(nt);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&qempty[qb]);
+      arrive_if(lane == 0, &qempty[qb]);
       __syncwarp();
       // ---- item done: the warps' states to shared memory, a row block at a time; each warp
       // joins one row of it
@@ -464,7 +474,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       // be fetched)
 #pragma unroll 1
       for (int nb = 0; nb < NT; ++nb, ++merges) {
-        if (nb > 0 && !warp_wait(merged, (merges - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
+        if (nb > 0 && !wait_bar(merged, (merges - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) { ok = false; break; }
         if (had)                                         // (a group without tiles stages no rows)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -496,8 +506,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           for (int r = 0; r < 8; ++r) m[r] = m[R - 8 + r];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(staged);
-        if (!warp_wait(staged, merges & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
+        arrive_if(lane == 0, staged);
+        if (!wait_bar(staged, merges & 1, abort_flag, KERR_TIMEOUT_FULL)) { ok = false; break; }
         const int row = 8 * nb + warp;
         if (row < rows) {
           float mw[NCW], lw[NCW], M = kNoMax, l = 0.f;
@@ -545,7 +555,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(merged);
+        arrive_if(lane == 0, merged);
       }
     }
   } else if (warp < S::WARP_MMA) {
@@ -653,7 +663,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       auto issue_to = [&](int end) -> bool {
         for (; pw < NWG * S::CPG && ti < end; ti += NWG * S::CPG, tn.step()) {
           const int s = wg * S::NSG + tn.slot, tok0 = (cur.t + ti) * TILE;
-          if (tn.count * S::CPG >= S::NSG && !warp_wait(&empty[s], tn.phase ^ 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
+          if (tn.count * S::CPG >= S::NSG && !wait_bar(&empty[s], tn.phase ^ 1, abort_flag, KERR_TIMEOUT_EMPTY)) return false;
           while ((tok0 >> lbs) - e0 >= 32) {
             e0 += 32;
             ent = ent_next;
@@ -717,7 +727,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       // the first tiles go out before the operand is built
       if (n == 0 && !issue_to(min(nt, NWG * S::CPG))) break;
       const int qb = n & 1;
-      if (n >= 2 && !warp_wait(&qempty[qb], ((n >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
+      if (n >= 2 && !wait_bar(&qempty[qb], ((n >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       // ---- query operand (the second row block by the first one's code: code that runs once per item has to be fetched)
 #pragma unroll 1
       for (int h = 0; h < NT; ++h) {
@@ -804,7 +814,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&qfull[qb]);
+      arrive_if(lane == 0, &qfull[qb]);
       ++n;
       if (cur.t == 0 && te < cur.T) {
         // begins here and goes on: the pieces are this CTA's and those of the ranges up to the sequence's last unit
@@ -823,10 +833,10 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     if (cur.s < 0) {
       // no more items
       const int qb = n & 1;
-      if (n < 2 || warp_wait(&qempty[qb], ((n >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) {
+      if (n < 2 || wait_bar(&qempty[qb], ((n >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) {
         if (pt == 0) sts_i4(sb + S::infoOff + 64 * qb, make_int4(0, 0, 0, 0));
         __syncwarp();
-        if (lane == 0) mbar_arrive(&qfull[qb]);
+        arrive_if(lane == 0, &qfull[qb]);
       }
     }
     if (pt == 0) p.meta[blockIdx.x] = meta;
@@ -843,7 +853,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     constexpr uint32_t OP_HI = desc_hi(8 * ROW, SWZ), SC_HI = desc_hi(128, kSwizzleNone);
     for (int n = 0; ok; ++n) {
       const int qb = n & 1;
-      if (!warp_wait(&qfull[qb], (n >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
+      if (!wait_bar(&qfull[qb], (n >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
       const int nt = lds_i4(sb + S::infoOff + 64 * qb).z;
       if (nt == 0) break;
       const uint32_t sfb = sfb0 + qb * PASSES * 4 * KS;
@@ -855,8 +865,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       }
       for (int i = tn.first; i < nt; i += NWG, tn.step()) {
         const int s = wg * S::NSG + tn.slot, b = 2 * wg + (tn.count & 1);
-        if ((tn.count >= 2 && !warp_wait(&sfree[b], ((tn.count >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) ||
-            !warp_wait(&full[s], tn.phase, abort_flag, KERR_TIMEOUT_FULL)) {
+        if ((tn.count >= 2 && !wait_bar(&sfree[b], ((tn.count >> 1) - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) ||
+            !wait_bar(&full[s], tn.phase, abort_flag, KERR_TIMEOUT_FULL)) {
           ok = false;
           break;
         }
