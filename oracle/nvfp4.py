@@ -102,8 +102,8 @@ def gather_rows(block_table, query_start, seq_lens, block_size):
 def pa_decode_nvfp4(q_bits, kv_cache, block_table, seq_lens, k_scale, v_scale, query_group, softmax_scale=None):
     """(out, bound, total, slack) float64 [B, Hq, D] (slack [B, Hq]): the attention;
     sum_t p_t |v_t|, by which relative errors of the probabilities scale; sum_t |v_t|,
-    by which absolute ones do; and the largest error of a logit for queries within 2^-17 of their group's largest (small groups: of
-    their row's), and sums of float32."""
+    by which absolute ones do; and the largest error of a logit for queries within 2^-17 of their group's largest and 2^-31 of
+    their row's, and sums of float32."""
     q = decode_bf16(q_bits)
     B, Hq, D = q.shape
     Hk, bs = kv_cache.shape[2], kv_cache.shape[3]
@@ -124,10 +124,9 @@ def pa_decode_nvfp4(q_bits, kv_cache, block_table, seq_lens, k_scale, v_scale, q
                 w /= w.sum(axis=1, keepdims=True)
                 out[s, hs], bound[s, hs], total[s, hs] = w @ V[:, h], w @ np.abs(V[:, h]), np.abs(V[:, h]).sum(axis=0)
                 near = np.repeat(np.abs(q[s, hs]).reshape(query_group, -1, 16).max(axis=-1), 16, axis=-1)
-                row = np.abs(q[s, hs]).max(axis=-1, keepdims=True)
                 # 6 terms of 3 bits: half of the last step, 2^-2 8^-5 of the power of two at or above the group's
-                # largest. Groups 2^-10 and more below the row's largest may lack terms: at most 2^-17 of that
-                err = (np.where(near >= row * 2.0 ** -10, near, row) * 2.0 ** -17
-                       + np.abs(q[s, hs]) * 2.0 ** -20) @ np.abs(K[:, h]).T
+                # largest; groups far below the row's largest: 2^-31 of that
+                err = (near * 2.0 ** -17 + np.abs(q[s, hs]) * 2.0 ** -20
+                       + np.abs(q[s, hs]).max(axis=-1, keepdims=True) * 2.0 ** -31) @ np.abs(K[:, h]).T
                 slack[s, hs] = abs(scale) * err.max(axis=1) + 2.0 ** -21 * np.abs(x).max(axis=1)
     return out, bound, total, slack

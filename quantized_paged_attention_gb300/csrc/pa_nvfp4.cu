@@ -14,13 +14,10 @@
 //    (kind::mxf4nvf4): the pages' e2m1 codes and e4m3 scales are the operand as they
 //    are, 128 tokens x 64 dims at a time. Q' holds each query row as 6 e2m1 terms of
 //    weights 1, 1/8, .. 8^-5 (3 bits each) with a power of two per 16 dims, so a query
-//    is within 2^-17 of its 16 dims' largest, and exact down to 2^-9 of it. Three passes
-//    accumulate terms 0, 1, 2 into 8 columns of S and 3, 4, 5 into 8 others, the weights
-//    1, 1/8, 1/64 of a pass in its scales: S is a column plus 2^-9 of another. (All six
-//    terms in columns of their own: 20 packed FMAs more per token, 69 us for 16 x 16384
-//    tokens, 8 x 8 heads, where this takes {D16}.) e4m3 holds the scales' powers from
-//    2^8 to 2^-9: a term whose scale would be smaller, in 16 dims 2^11 or more below the
-//    row's largest, is left out, and such dims are within 2^-17 of the row's largest.
+//    is within 2^-17 of its 16 dims' largest (or 2^-31 of the row's, which e4m3's range of
+//    powers leaves of much smaller ones), and exact down to 2^-9 of it. With head_dim 128
+//    two passes accumulate terms 0, 2, 4 and 1, 3, 5, the weight 1/8 in the scales, so that
+//    S has three columns per row; with 64 one pass gives six.
 //  * Groups of 4 consumer warps take the tiles in turn; each warp owns 32 tokens of a
 //    tile and its own softmax state, so nothing is exchanged before the item's end: it
 //    reads S from tensor memory (a lane a token), forms p in f16, and multiplies V on
@@ -49,7 +46,6 @@ namespace qpa {
 namespace d4 {
 constexpr int TILE = 128;           // tokens per tile
 constexpr int QT = 6;               // e2m1 terms of a query
-constexpr int PASSES = 3;           // of the QK product: terms k and k + 3
 constexpr int MAX_CTAS = 160;
 constexpr int COMBINE_WARPS = 4;
 constexpr float kNoMax = -1e30f;    // no token seen yet: finite, so that differences stay defined
@@ -70,7 +66,11 @@ struct Smem {
   static_assert(128 * (NWG * REG_CONSUMER + REG_COPY + REG_MMA) <= THREADS * REG_LAUNCH, "registers");
   static constexpr int R = 8 * NT;                 // query rows (padded)
   static constexpr int KS = HD / 64;               // K steps of the fp4 product
-  static constexpr int NQ = 16 * NT;               // columns of S: row block x (terms 0-2, 3-5) x 8 rows
+  // passes of the product (pass k accumulates terms k, k + PASSES, ..), groups of 8 columns of S per row block. A pass
+  // reads K's tile from shared memory once more, a group costs the softmax a packed FMA per pair of rows. 16 x 16384
+  // tokens, 8 x 8 heads of 128: 65.1 us with 1 pass, 61.6 with 2, 63.6 with 3; 32 sequences, heads of 64: 43.9, 45.9, 45.9
+  static constexpr int PASSES = HD == 128 ? 2 : 1, CG = QT / PASSES;
+  static constexpr int NQ = (8 * CG * NT + 15) / 16 * 16;   // columns of S: row block x group x 8 rows
   static constexpr int ROW = HD / 2;               // code bytes of a token
   static constexpr int V_OFF = TILE * ROW;
   static constexpr int KS_OFF = 2 * TILE * ROW;    // K scales as V's, then (MMA warp) [KS][token % 32][token / 32][4]
@@ -134,6 +134,32 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a_lo, uint32_t b_lo
       "{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %7, 0; mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3}; "
       "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %4, [%5], [%6], p; }"
       ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+}
+// N consecutive columns of this warp's 32 lanes (as tmem_ld32)
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N]) {
+  int at = 0;
+  if constexpr (N >= 32) {
+    float r[32];
+    tmem_ld32(taddr, r);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = r[i];
+    at = 32;
+  }
+  if constexpr (N % 32 >= 16) {
+    float r[16];
+    tmem_ld16(taddr + at, r);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[(N >= 32 ? 32 : 0) + i] = r[i];
+    at += 16;
+  }
+  if constexpr (N % 16 == 8) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr + at));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[N - 8 + i] = __uint_as_float(r[i]);
+  }
 }
 // 512 bytes of scales (32 rows of 16) to 4 columns of all four lane quarters
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo, uint32_t hi) {
@@ -222,6 +248,7 @@ template <int NT, int HD>
 __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(const d4::Params p) {
   using namespace d4;
   using S = Smem<NT, HD>;
+  constexpr int PASSES = S::PASSES, CG = S::CG;
   constexpr int R = S::R, NQ = S::NQ, NS = S::NS, NSB = S::NSB, NWG = S::NWG, NCW = S::NCW, KS = S::KS, ROW = S::ROW;
   constexpr uint32_t SWZ = HD == 128 ? kSwizzle64B : 6u;      // rows of 64 or 32 bytes
   constexpr int MT = HD / 16;                                 // m-tiles of V^T
@@ -302,7 +329,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       for (int r = 0; r < R; ++r) m[r] = kNoMax;
       uint32_t w[8][HD / 64], sc[8];                 // V of this warp's 32 tokens: 4 u + c, u < 8
       float x[R];                                    // logits without the row's factor
-      float v[NT][16];                               // S: terms 0-2, 3-5 x 8 rows
+      float v[NT][8 * CG];                           // S: groups of terms x 8 rows
       // V's bytes into registers; the slot is free then
       auto load_v = [&]() -> bool {
         const int s = wg * S::NSG + tn.slot;
@@ -332,7 +359,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       };
       auto load_s = [&](int count) {
 #pragma unroll
-        for (int nb = 0; nb < NT; ++nb) tmem_ld16(tl + (2 * wg + (count & 1)) * NQ + 16 * nb, v[nb]);
+        for (int nb = 0; nb < NT; ++nb) tmem_ld_cols(tl + (2 * wg + (count & 1)) * NQ + 8 * CG * nb, v[nb]);
       };
       // S has come: its halves joined (v is free then)
       auto join_terms = [&]() {
@@ -341,9 +368,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         for (int nb = 0; nb < NT; ++nb)
 #pragma unroll
           for (int r = 0; r < 8; r += 2) {
-            x[8 * nb + r] = v[nb][8 + r];
-            x[8 * nb + r + 1] = v[nb][9 + r];
-            fma2(x[8 * nb + r], x[8 * nb + r + 1], 0.001953125f, v[nb][r], v[nb][r + 1]);
+            float x0 = v[nb][8 * (CG - 1) + r], x1 = v[nb][8 * (CG - 1) + r + 1];
+#pragma unroll
+            for (int k = CG - 2; k >= 0; --k)
+              fma2(x0, x1, 1.f / (1 << (3 * PASSES)), v[nb][8 * k + r], v[nb][8 * k + r + 1]);
+            x[8 * nb + r] = x0;
+            x[8 * nb + r + 1] = x1;
           }
       };
       auto free_s = [&](int count) {
@@ -759,7 +789,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
         for (int sh = 2; sh < 16; sh <<= 1) er = max(er, __shfl_xor_sync(0xffffffffu, er, sh));
         if (er == -200) er = 0;
-        const int rel = max(eb - er, -17);                              // scales 2^8 .. 2^-9
+        const int rel = max(eb - er, -17 + 3 * (PASSES - 1));           // scales 2^8 .. 2^-9, those of the last pass too
         // x 2^-(er + rel), in two factors that are floats
         const int sh = -(er + rel), s1 = max(-126, min(126, sh)), s2 = sh - s1;
         const float up = __uint_as_float(uint32_t(127 + s1) << 23), up2 = __uint_as_float(uint32_t(127 + s2) << 23);
@@ -784,19 +814,18 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         if (h16 < HD / 8) {
 #pragma unroll
           for (int term = 0; term < QT; ++term) {
-            // terms k and k + 3: pass k, scale 2^(rel + 8 - 3 k), in columns 0 .. 7 and 8 .. 15 of the row block
-            const int pass = term % PASSES, es = rel + 8 - 3 * pass;
-            const int col = 16 * h + 8 * (term / PASSES) + qrow;
+            const int pass = term % PASSES, col = 8 * CG * h + 8 * (term / PASSES) + qrow;
             const int ch = HD == 128 ? (h16 >> 2) ^ ((col >> 1) & 3) : (h16 >> 2) ^ ((col >> 2) & 1);
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb + S::qOff + qb * S::qBytes + (pass * NQ + col) * ROW + 16 * ch + 4 * (h16 & 3)),
-                         "r"(es < -9 ? 0u : words[term]) : "memory");
+                         "r"(words[term]) : "memory");
           }
+          // their scales 2^(rel + 8 - 3 pass), a byte per 16 dims
           if ((h16 & 1) == 0) {
 #pragma unroll
             for (int term = 0; term < QT; ++term) {
-              const int pass = term % PASSES, es = rel + 8 - 3 * pass, col = 16 * h + 8 * (term / PASSES) + qrow;
-              sts8(sb + S::qsOff + ((qb * PASSES + pass) * KS + (h16 >> 3)) * 512 + col * 16 + ((h16 >> 1) & 3),
-                   es >= -6 ? uint32_t(es + 7) << 3 : es >= -9 ? 1u << (es + 9) : 1u);
+              const int pass = term % PASSES, es = rel + 8 - 3 * pass, col = 8 * CG * h + 8 * (term / PASSES) + qrow;
+              sts8(sb + S::qsOff + ((qb * PASSES + pass) * KS + (h16 >> 3)) * 512 + (col & 31) * 16 + (col >> 5) * 4 + ((h16 >> 1) & 3),
+                   es >= -6 ? uint32_t(es + 7) << 3 : 1u << (es + 9));
             }
           }
         }
