@@ -635,8 +635,8 @@ int kv_append_nvfp4(const void* k, const void* v, uint8_t* kv_cache, const int64
  * Request r owns the output rows query_start[r] .. query_start[r+1] - 1 (n of
  * them): the last n of its L = seq_lens[r] cached tokens, row i being token
  * L - n + i (all of them with n = L, a step's new ones with n = new_lens[r]).
- *     out_k[row][h][d] = the value of K at (token, h, d), rounded once;
- * likewise out_v. Rows of a token below 0 are 0; rows outside every request's
+ *     out_k[row][h][d] = the value of K at (token, h, d), rounded once
+ * (bf16 values below 2^-126: to float32 first); likewise out_v. Rows of a token below 0 are 0; rows outside every request's
  * range are left as they were. The fp8 cache is the one of kv_append_fp8, with
  * scales per tensor or per token (kv_scale_per_token).
  *

@@ -13,7 +13,7 @@
 //  * code = e2m1(x / (s g)): S = s g, held as two floats (28 bits: exact), one of 126 for
 //    a call. A block makes the 126 pairs (hi, lo) once, into shared memory, and a group
 //    looks its own up. (Made per group: 170 instructions more, ALU-bound, 27 us for 16384
-//    tokens x 8 heads x 128 where this takes {APP}.)
+//    tokens x 8 heads x 128 where this takes 24.)
 #include "qpa.h"
 #include "common.cuh"
 #include "qpa_internal.h"

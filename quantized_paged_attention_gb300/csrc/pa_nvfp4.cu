@@ -34,7 +34,8 @@
 // slots per CTA: a range begins in at most one cut item and ends in another), and a
 // second kernel joins them in order. Where no sequence can have more than 4 tiles
 // (max_blocks_per_seq * block_size <= 512) the list is of whole sequences and the second
-// kernel is not launched: {SHORT}.
+// kernel is not launched: a call of four sequences of up to 200 tokens takes 20 us of wall clock
+// instead of 25, 9 us of a graph.
 #define QPA_WHOLE_UNIT
 #include "qpa.h"
 #include "common.cuh"
@@ -48,7 +49,7 @@ constexpr int TILE = 128;           // tokens per tile
 constexpr int QT = 6;               // e2m1 terms of a query
 constexpr int MAX_CTAS = 160;
 constexpr int COMBINE_WARPS = 4;
-constexpr float kNoMax = -1e30f;    // no token seen yet: finite, so that differences stay defined
+constexpr float kNoMax = -3e38f;    // no token seen yet: finite, so that differences stay defined, and below any logit
 constexpr float kBelow = 8.f;       // the reference is set this far below the largest logit (p up to 2^8)
 constexpr float kTop = 14.f;        // and moves when a logit is this far above it (p up to 2^14 in f16)
 
@@ -56,7 +57,6 @@ template <int NT, int HD>
 struct Smem {
   static constexpr int NWG = NT == 1 ? 3 : 2;      // consumer groups of 4 warps
   static constexpr int NCW = 4 * NWG;
-  static constexpr bool AHEAD = NWG == 2 && NT == 1;   // the next S is loaded while V is multiplied
   static constexpr int WARP_COPY = NCW;
   static constexpr int WARP_MMA = NCW + 4;         // one per consumer group
   static constexpr int THREADS = (WARP_MMA + 4) * 32;   // (whole warpgroups, for the register budgets)
@@ -202,6 +202,15 @@ __device__ __forceinline__ void fma2(float& x, float& y, float w, float a, float
   asm("{ .reg .b64 p, q, r; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %2}; mov.b64 r, {%3, %4}; "
       "fma.rn.f32x2 p, p, q, r; mov.b64 {%0, %1}, p; }" : "+f"(x), "+f"(y) : "f"(w), "f"(a), "f"(b));
 }
+// (x, y) * (a, b); (x, y) - (a, b)
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
+  asm("{ .reg .b64 p, q; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %3}; mul.rn.f32x2 p, p, q; mov.b64 {%0, %1}, p; }"
+      : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void sub2(float& x, float& y, float a, float b) {
+  asm("{ .reg .b64 p, q; mov.b64 p, {%0, %1}; mov.b64 q, {%2, %3}; sub.rn.f32x2 p, p, q; mov.b64 {%0, %1}, p; }"
+      : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
 __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
   uint32_t r;
   asm("{ .reg .b8 t; cvt.rn.satfinite.e2m1x2.f32 t, %2, %1; cvt.u32.u8 %0, t; }" : "=r"(r) : "f"(lo), "f"(hi));
@@ -328,7 +337,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
       for (int r = 0; r < R; ++r) m[r] = kNoMax;
       uint32_t w[8][HD / 64], sc[8];                 // V of this warp's 32 tokens: 4 u + c, u < 8
-      float x[R];                                    // logits without the row's factor
+      float x[R];                                    // logits (base 2)
       float v[NT][8 * CG];                           // S: groups of terms x 8 rows
       // V's bytes into registers; the slot is free then
       auto load_v = [&]() -> bool {
@@ -361,20 +370,26 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
         for (int nb = 0; nb < NT; ++nb) tmem_ld_cols(tl + (2 * wg + (count & 1)) * NQ + 8 * CG * nb, v[nb]);
       };
-      // S has come: its halves joined (v is free then)
+      // S has come: its groups joined, times the rows' factors (v is free then). The product is rounded before the
+      // reference is taken off, as it is where the reference comes from: a fused one is off by more than 14, f16's
+      // room, from logits of 2^28 on.
       auto join_terms = [&]() {
         tmem_wait_ld();
 #pragma unroll
-        for (int nb = 0; nb < NT; ++nb)
+        for (int nb = 0; nb < NT; ++nb) {
+          const float4 f0 = lds_f4(sb + S::cOff + 4 * (qb * R + 8 * nb)), f1 = lds_f4(sb + S::cOff + 4 * (qb * R + 8 * nb) + 16);
+          const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
           for (int r = 0; r < 8; r += 2) {
             float x0 = v[nb][8 * (CG - 1) + r], x1 = v[nb][8 * (CG - 1) + r + 1];
 #pragma unroll
             for (int k = CG - 2; k >= 0; --k)
               fma2(x0, x1, 1.f / (1 << (3 * PASSES)), v[nb][8 * k + r], v[nb][8 * k + r + 1]);
+            mul2(x0, x1, f[r], f[r + 1]);
             x[8 * nb + r] = x0;
             x[8 * nb + r + 1] = x1;
           }
+        }
       };
       auto free_s = [&](int count) {
         tc_fence_before();
@@ -396,14 +411,13 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
         for (int nb = 0; nb < NT; ++nb) {
           // ---- logits of 8 rows for this token, relative to the references
-          float f[8], e[8];
-          {
-            const float4 f0 = lds_f4(sb + S::cOff + 4 * (qb * R + 8 * nb)), f1 = lds_f4(sb + S::cOff + 4 * (qb * R + 8 * nb) + 16);
-            f[0] = f0.x; f[1] = f0.y; f[2] = f0.z; f[3] = f0.w;
-            f[4] = f1.x; f[5] = f1.y; f[6] = f1.z; f[7] = f1.w;
-          }
+          float e[8];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) e[r] = fmaf(x[8 * nb + r], f[r], -m[8 * nb + r]);
+          for (int r = 0; r < 8; r += 2) {
+            e[r] = x[8 * nb + r];
+            e[r + 1] = x[8 * nb + r + 1];
+            sub2(e[r], e[r + 1], m[8 * nb + r], m[8 * nb + r + 1]);
+          }
           if (cut && tok >= L) {
 #pragma unroll
             for (int r = 0; r < 8; ++r) e[r] = -INFINITY;
@@ -414,13 +428,13 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
             float a0 = 1.f, a1 = 1.f;                                   // of this lane's output columns, rows 2c and 2c + 1
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-              // (x f of a masked token does not count; NaN is ignored)
-              const float best = warp_max(cut && tok >= L ? -INFINITY : x[8 * nb + r] * f[r]);
+              // (a masked token does not count; NaN is ignored)
+              const float best = warp_max(cut && tok >= L ? -INFINITY : x[8 * nb + r]);
               const float old = m[8 * nb + r];
               const float now = best > old + kTop ? best - kBelow : old;
               const float alpha = ex2(old - now);
               m[8 * nb + r] = now;
-              e[r] = cut && tok >= L ? -INFINITY : fmaf(x[8 * nb + r], f[r], -now);
+              e[r] = cut && tok >= L ? -INFINITY : x[8 * nb + r] - now;
               if (r == 2 * c) a0 = alpha;
               if (r == 2 * c + 1) a1 = alpha;
             }
@@ -443,11 +457,6 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         uint32_t pb[NT][4];
 #pragma unroll
         for (int nb = 0; nb < NT; ++nb) ldsm_x4_trans(prow + 512 * nb, pb[nb]);
-        // one row block: the next tile's S comes while this one's V is multiplied (two: no registers for it)
-        if (S::AHEAD && more) {
-          if (!wait_s(tn.count + 1)) { ok = false; break; }
-          load_s(tn.count + 1);
-        }
         // ---- O^T += V^T P^T, 16 tokens at a time
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -476,15 +485,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
 #pragma unroll
           for (int nb = 0; nb < NT; ++nb)      // the sum of p: a row of ones
             mma_f16_16816(ol[nb], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[nb][2 * k], pb[nb][2 * k + 1]);
-          if (S::AHEAD && k == 0) join_terms();       // (of what v holds, if there is no next tile)
         }
         tn.step();
         if (more) {
-          if constexpr (!S::AHEAD) {
-            if (!wait_s(tn.count)) { ok = false; break; }
-            load_s(tn.count);
-            join_terms();
-          }
+          if (!wait_s(tn.count)) { ok = false; break; }
+          load_s(tn.count);
+          join_terms();
           free_s(tn.count);
           if (!load_v()) { ok = false; break; }
         }
@@ -711,7 +717,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           const uint64_t codes = kbase + size_t(blk) * (2 * plane) + uint32_t(off * ROW);
           const uint32_t to_scales = bs * ROW - off * (ROW - HD / 16);
           const uint32_t slot = sb + s * S::SLOT;
-          if (tok0 + TILE <= L) {
+          if (L - tok0 >= TILE) {
 #pragma unroll
             for (int q = 0; q < TILE / 16; ++q) {
               const uint64_t src = __shfl_sync(0xffffffffu, codes, q) + src_lane;
@@ -1053,6 +1059,20 @@ size_t decode4_workspace_bytes(int, int head_dim) {
   return size_t(d4::MAX_CTAS) * (2 * 16 * (size_t(head_dim) * 4 + 8) + 16);
 }
 
+template <int NT, int HD>
+static cudaError_t launch_decode4_t(const d4::Params& p, int grid, cudaStream_t stream) {
+  using S = d4::Smem<NT, HD>;
+  // the roles' register budgets draw on what the kernel is launched with: built with less, it would wait for ever
+  static const bool built = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, decode4_kernel<NT, HD>) == cudaSuccess && f.numRegs == S::REG_LAUNCH;
+  }();
+  if (!built) return cudaErrorInvalidConfiguration;
+  cudaFuncSetAttribute(decode4_kernel<NT, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::total);
+  decode4_kernel<NT, HD><<<grid, S::THREADS, S::total, stream>>>(p);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_decode4(const Decode4Launch& a, cudaStream_t stream) {
   d4::Params p;
   p.q = static_cast<const uint16_t*>(a.q);
@@ -1083,19 +1103,9 @@ cudaError_t launch_decode4(const Decode4Launch& a, cudaStream_t stream) {
   p.whole = tiles <= 4;
   const long long units = (p.whole ? 1 : std::min(tiles, 1LL << 20)) * a.num_seqs * a.num_kv_heads * p.row_blocks;
   const int grid = (int)std::min<long long>(units, std::min(a.num_sms, d4::MAX_CTAS));
-  auto launch = [&](auto kernel, int threads, int smem) {
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    kernel<<<grid, threads, smem, stream>>>(p);
-  };
   const bool one = a.qg <= 8;
-  if (a.head_dim == 64) {
-    if (one) launch(decode4_kernel<1, 64>, d4::Smem<1, 64>::THREADS, d4::Smem<1, 64>::total);
-    else launch(decode4_kernel<2, 64>, d4::Smem<2, 64>::THREADS, d4::Smem<2, 64>::total);
-  } else {
-    if (one) launch(decode4_kernel<1, 128>, d4::Smem<1, 128>::THREADS, d4::Smem<1, 128>::total);
-    else launch(decode4_kernel<2, 128>, d4::Smem<2, 128>::THREADS, d4::Smem<2, 128>::total);
-  }
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = a.head_dim == 64 ? (one ? launch_decode4_t<1, 64>(p, grid, stream) : launch_decode4_t<2, 64>(p, grid, stream))
+                                   : (one ? launch_decode4_t<1, 128>(p, grid, stream) : launch_decode4_t<2, 128>(p, grid, stream));
   if (e != cudaSuccess || p.whole) return e;
   const dim3 cgrid(grid, std::min(16, a.qg));
   if (a.head_dim == 64) decode4_combine_kernel<64><<<cgrid, 32 * d4::COMBINE_WARPS, 0, stream>>>(p, 2 * grid);

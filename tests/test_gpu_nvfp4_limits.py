@@ -162,3 +162,85 @@ def test_outputs_and_rows_of_no_request_stay():
     done()
     c.check(got)
     assert got.data_ptr() == big[1:3].data_ptr() and bool((big[0] == 3).all()) and bool((big[3:] == 3).all())
+
+
+def test_last_tile_below_2_to_the_31():
+    """Tokens up to 2^31 - 17 in blocks of 16: the last tile's end lies past 32 bits. All but the last 130 tokens
+    have keys of 0 and values of NaN-free block 1; behind the last token are NaN scales."""
+    r = synth.rng(77)
+    bs, D = 16, 64
+    maxb = (2 ** 31 - 1) // bs
+    L = maxb * bs - 1
+    table = torch.ones(1, maxb, dtype=torch.int32, device=dev())
+    table[0, -9:] = t32(np.arange(2, 11))
+    cache = rand_cache(r, 11, 1, bs, D, smax=48)
+    codes, scales = oracle.nvfp4._split(cache)
+    scales[0], scales[10, :, :, -1] = 0x7F, 0x7F
+    codes[1, 0] = 0
+    codes[2:11, 0] &= 0x77                                                  # positive keys, scales up to 0.9375
+    cache = oracle.nvfp4._join(codes, scales)
+    # logits (base e) of the last tokens about 100 above the others': 2^31 e^-50 is nothing
+    q = synth.round_to_bf16_bits(np.full((1, 1, D), 16.0))
+    out = qpa.pa_decode_nvfp4(bf16_tensor(q, dev()), torch.from_numpy(cache).to(dev()), table, t32([L]), f32(1.0), f32(1.0), 1)
+    done()
+    blk, off = np.repeat(np.arange(2, 11), bs)[:-1], np.tile(np.arange(bs), 9)[:-1]
+    K, V = (oracle.values_nvfp4(cache, i, 1.0, blk, off)[:, 0] for i in range(2))
+    x = 16.0 * K.sum(axis=1) / 8
+    assert x.max() > 60
+    w = np.exp(x - x.max())
+    w /= w.sum()
+    want, bound = w @ V, w @ np.abs(V)
+    # 2^-8 of the result; weights as in the other tests (the query is exact); the 2^31 others: below 2^31 e^-60
+    tol = 2.0 ** -8 * np.abs(want) + bound * (2 * 2.0 ** -11 + 2 * np.expm1(2.0 ** -21 * x.max()) + 2.0 ** -18)
+    tol = tol + 2.0 ** 31 * np.exp(-60.0) * (np.abs(V).max() + 6 * 0.9375) + 2.0 ** -33 * (np.abs(V).sum(axis=0) + 144 * np.abs(want))
+    err = np.abs(out[0, 0].float().cpu().numpy() - want)
+    assert np.all(err <= tol), (err / tol).max()
+
+
+@pytest.mark.parametrize("amp", [-1e20, -1e33, -1e36])
+def test_logits_far_below_zero(amp):
+    """Equal keys, logits of down to -10^36: the result is the mean of the values (2^-8 of it, and the weights are
+    exact: 2^-18 sum |v| for the sums)."""
+    r = synth.rng(78)
+    lens = [300, 1000]
+    table, NB = rand_table(r, lens, 16)
+    cache = rand_cache(r, NB, 1, 16, 64, smax=60)
+    codes, scales = oracle.nvfp4._split(cache)
+    codes[:, 0], scales[:, 0] = 0x22, 0x38                                  # 1 x 1
+    cache = oracle.nvfp4._join(codes, scales)
+    q = synth.round_to_bf16_bits(np.full((2, 3, 64), amp))
+    out = qpa.pa_decode_nvfp4(bf16_tensor(q, dev()), torch.from_numpy(cache).to(dev()), t32(table), t32(lens), f32(1.0), f32(.3), 3)
+    done()
+    for s, L in enumerate(lens):
+        V = oracle.values_nvfp4(cache, 1, .3, table[s, np.arange(L) // 16], np.arange(L) % 16)[:, 0]
+        want = V.mean(axis=0)
+        err = np.abs(out[s].float().cpu().numpy() - want)
+        assert np.all(err <= 2.0 ** -8 * np.abs(want) + 2.0 ** -18 * np.abs(V).mean(axis=0))
+
+
+@pytest.mark.parametrize("fp4", [True, False])
+def test_every_value_read_back_with_many_scales(fp4):
+    """All codes with all group scales (fp8: all codes), scales of few bits (many midpoints) and of many: rounded once."""
+    r = synth.rng(79)
+    gs = [(1 + i / 128) * 2.0 ** r.integers(-60, 60) for i in range(128)] + list(np.exp(r.uniform(-60, 60, 60)))
+    gs += [np.nextafter(np.float32(m / x), np.float32(d)) for x in (3, 5, 7, 9, 11, 13, 15, 21, 27, 33, 39, 45)
+           for m in (257, 259, 301, 511) for d in (0, 1e9)] + [-0.3, 0.0]
+    gs = np.array(gs, dtype=np.float32)
+    D, bs = 64, 256
+    if fp4:
+        code = np.tile((np.arange(16) + 16 * ((np.arange(16) + 1) % 16)).astype(np.uint8)[::2], (bs, 4))
+        sc = (np.arange(bs * 4) % 128).astype(np.uint8)
+        cache = np.concatenate([code.reshape(-1), sc])[None, None, None].reshape(1, 1, 1, bs, 36)
+    else:
+        cache = np.resize(np.arange(256, dtype=np.uint8), (1, 2, 1, bs, D))
+    dc = torch.from_numpy(cache).to(dev())
+    for g in gs:
+        if fp4:
+            k, _ = qpa.kv_gather_nvfp4(dc, t32([[0]]), t32([0, bs]), t32([bs]), f32(float(g)), None, bs)
+            want = oracle.values_nvfp4(cache, 0, g, np.zeros(bs, dtype=int), np.arange(bs))
+        else:
+            k, _ = qpa.kv_gather_fp8(dc, t32([[0]]), t32([0, bs]), t32([bs]), f32(float(g)), f32(1.0), bs)
+            want = oracle.decode_e4m3fn(cache[0, 0, 0])[:, None] * float(g)
+        with np.errstate(invalid="ignore"):
+            same_bf16(k, want)
+    done()
