@@ -15,9 +15,9 @@
 //    are, 128 tokens x 64 dims at a time. Q' holds each query row as 6 e2m1 terms of
 //    weights 1, 1/8, .. 8^-5 (3 bits each) with a power of two per 16 dims, so a query
 //    is within 2^-17 of its 16 dims' largest (or 2^-31 of the row's, which e4m3's range of
-//    powers leaves of much smaller ones), and exact down to 2^-9 of it. With head_dim 128
-//    two passes accumulate terms 0, 2, 4 and 1, 3, 5, the weight 1/8 in the scales, so that
-//    S has three columns per row; with 64 one pass gives six.
+//    powers leaves of much smaller ones), and exact down to 2^-9 of it. Two passes
+//    accumulate terms 0, 2, 4 and 1, 3, 5, the weight 1/8 in the scales, so that S has three
+//    columns per row.
 //  * Groups of 4 consumer warps take the tiles in turn; each warp owns 32 tokens of a
 //    tile and its own softmax state, so nothing is exchanged before the item's end: it
 //    reads S from tensor memory (a lane a token), forms p in f16, and multiplies V on
@@ -55,21 +55,25 @@ constexpr float kTop = 14.f;        // and moves when a logit is this far above 
 
 template <int NT, int HD>
 struct Smem {
-  static constexpr int NWG = NT == 1 ? 3 : 2;      // consumer groups of 4 warps
+  static constexpr int NWG = NT == 2 ? 2 : HD == 128 ? 3 : 4;   // consumer groups of 4 warps
   static constexpr int NCW = 4 * NWG;
   static constexpr int WARP_COPY = NCW;
   static constexpr int WARP_MMA = NCW + 4;         // one per consumer group
   static constexpr int THREADS = (WARP_MMA + 4) * 32;   // (whole warpgroups, for the register budgets)
   // registers of the roles' threads; their sum is the launch's
-  static constexpr int REG_CONSUMER = NWG == 3 ? 120 : 168, REG_COPY = NWG == 3 ? 80 : 104, REG_MMA = NWG == 3 ? 40 : 72;
+  static constexpr int REG_CONSUMER = NWG == 4 ? 96 : NWG == 3 ? 120 : 168, REG_COPY = NWG == 4 ? 72 : NWG == 3 ? 80 : 104;
+  static constexpr int REG_MMA = NWG == 4 ? 24 : NWG == 3 ? 40 : 72;
   static constexpr int REG_LAUNCH = 65536 / THREADS / 8 * 8;
   static_assert(128 * (NWG * REG_CONSUMER + REG_COPY + REG_MMA) <= THREADS * REG_LAUNCH, "registers");
+  // (setmaxnreg.inc to fewer or .dec to more than a warp has is an illegal instruction)
+  static_assert(REG_CONSUMER >= REG_LAUNCH && REG_COPY <= REG_LAUNCH && REG_MMA <= REG_LAUNCH, "registers of a role");
   static constexpr int R = 8 * NT;                 // query rows (padded)
   static constexpr int KS = HD / 64;               // K steps of the fp4 product
-  // passes of the product (pass k accumulates terms k, k + PASSES, ..), groups of 8 columns of S per row block. A pass
-  // reads K's tile from shared memory once more, a group costs the softmax a packed FMA per pair of rows. 16 x 16384
-  // tokens, 8 x 8 heads of 128: 65.1 us with 1 pass, 61.6 with 2, 63.6 with 3; 32 sequences, heads of 64: 43.9, 45.9, 45.9
-  static constexpr int PASSES = HD == 128 ? 2 : 1, CG = QT / PASSES;
+  // Passes of the product (pass k accumulates terms k, k + PASSES, ..), groups of 8 columns of S per row block. A pass
+  // reads K's tile from shared memory once more, a group costs the softmax a packed FMA per pair of rows and registers.
+  // 16 x 16384 tokens, 8 x 8 heads of 128: 65.1 us with 1 pass, 61.6 with 2, 63.6 with 3. 32 sequences, heads of 64: 8 x 8
+  // 51.5, 43.4, 44.4 us, 8 x 16 64.2, 61.2, 60.2 (where a third pass would leave 2^-28 of a row's largest, not 2^-31).
+  static constexpr int PASSES = 2, CG = QT / PASSES;
   static constexpr int NQ = (8 * CG * NT + 15) / 16 * 16;   // columns of S: row block x group x 8 rows
   static constexpr int ROW = HD / 2;               // code bytes of a token
   static constexpr int V_OFF = TILE * ROW;
@@ -84,7 +88,7 @@ struct Smem {
   // Ring slots, NSG per group. A slot has one group and one copy warp, which see every phase
   // of its barriers: a wait on a parity cannot mistake a phase for the one before the last.
   static constexpr int CPG = 4 / NWG;              // copy warps of a group, taking its tiles in turn
-  static constexpr int NSG = (NWG == 3 ? 3 : 4) * (HD == 128 ? 1 : 2);
+  static constexpr int NSG = NWG == 4 ? 5 : (NWG == 3 ? 3 : 4) * (HD == 128 ? 1 : 2);
   static_assert(NSG % CPG == 0, "ring");
   static constexpr int NS = NWG * NSG;
   static constexpr int qOff = NS * SLOT;
@@ -408,23 +412,27 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         const int tok = (t0 + i) * TILE + 32 * wq + lane;               // this lane's token
         const bool cut = (t0 + i + 1) * (long long)TILE > L;            // the sequence ends in this tile
         const bool more = i + NWG < nt;
+        // ---- logits of this token relative to the rows' references (both row blocks at once: one vote, and their chains
+        // overlap; 32 sequences, 8 x 16 heads of 64, 61.2 -> 58.1 us)
+        float e[R];
 #pragma unroll
-        for (int nb = 0; nb < NT; ++nb) {
-          // ---- logits of 8 rows for this token, relative to the references
-          float e[8];
+        for (int r = 0; r < R; r += 2) {
+          e[r] = x[r];
+          e[r + 1] = x[r + 1];
+          sub2(e[r], e[r + 1], m[r], m[r + 1]);
+        }
+        if (cut && tok >= L) {
 #pragma unroll
-          for (int r = 0; r < 8; r += 2) {
-            e[r] = x[8 * nb + r];
-            e[r + 1] = x[8 * nb + r + 1];
-            sub2(e[r], e[r + 1], m[8 * nb + r], m[8 * nb + r + 1]);
-          }
-          if (cut && tok >= L) {
+          for (int r = 0; r < R; ++r) e[r] = -INFINITY;
+        }
+        float top = -INFINITY;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) e[r] = -INFINITY;
-          }
-          const float top = fmaxf(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])), fmaxf(fmaxf(e[4], e[5]), fmaxf(e[6], e[7])));
-          if (__any_sync(0xffffffffu, top > kTop)) {
-            // ---- move the references of the rows that need it
+        for (int r = 0; r < R; r += 8)
+          top = fmaxf(top, fmaxf(fmaxf(fmaxf(e[r], e[r + 1]), fmaxf(e[r + 2], e[r + 3])), fmaxf(fmaxf(e[r + 4], e[r + 5]), fmaxf(e[r + 6], e[r + 7]))));
+        if (__any_sync(0xffffffffu, top > kTop)) {
+          // ---- move the references of the rows that need it
+#pragma unroll
+          for (int nb = 0; nb < NT; ++nb) {
             float a0 = 1.f, a1 = 1.f;                                   // of this lane's output columns, rows 2c and 2c + 1
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
               const float now = best > old + kTop ? best - kBelow : old;
               const float alpha = ex2(old - now);
               m[8 * nb + r] = now;
-              e[r] = cut && tok >= L ? -INFINITY : x[8 * nb + r] - now;
+              e[8 * nb + r] = cut && tok >= L ? -INFINITY : x[8 * nb + r] - now;
               if (r == 2 * c) a0 = alpha;
               if (r == 2 * c + 1) a1 = alpha;
             }
@@ -448,10 +456,16 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
             ol[nb][0] *= a0;
             ol[nb][1] *= a1;
           }
-          // ---- p in f16, a row of the warp's P
-          const uint32_t p0 = f32x2_to_f16x2(ex2(e[0]), ex2(e[1])), p1 = f32x2_to_f16x2(ex2(e[2]), ex2(e[3]));
-          const uint32_t p2 = f32x2_to_f16x2(ex2(e[4]), ex2(e[5])), p3 = f32x2_to_f16x2(ex2(e[6]), ex2(e[7]));
-          sts_i4(psm + 512 * nb + 16 * lane, make_int4(p0, p1, p2, p3));
+        }
+        float ex[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) ex[r] = ex2(e[r]);
+        // ---- p in f16, a row of the warp's P
+#pragma unroll
+        for (int nb = 0; nb < NT; ++nb) {
+          const float* q = ex + 8 * nb;
+          sts_i4(psm + 512 * nb + 16 * lane, make_int4(f32x2_to_f16x2(q[0], q[1]), f32x2_to_f16x2(q[2], q[3]), f32x2_to_f16x2(q[4], q[5]),
+                                                       f32x2_to_f16x2(q[6], q[7])));
         }
         __syncwarp();
         uint32_t pb[NT][4];
