@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       if (!wait_bar(&qfull[qb], (n >> 1) & 1, abort_flag, KERR_TIMEOUT_FULL)) break;
       const int4 inf = lds_i4(sb + S::infoOff + 64 * qb);               // L, first tile, tiles, part (-1: whole)
       const int4 who = lds_i4(sb + S::infoOff + 64 * qb + 16);          // sequence, virtual head
-      const int L = inf.x, t0 = inf.y, nt = inf.z;
+      const int L = inf.x, t0 = inf.y, nt = inf.z, last = (L - 1) / TILE;
       if (nt == 0) break;
 #pragma unroll
       for (int nb = 0; nb < NT; ++nb) {
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       if (merges > 0 && !wait_bar(merged, (merges - 1) & 1, abort_flag, KERR_TIMEOUT_EMPTY)) break;
       for (int i = tn.first; i < nt; i += NWG) {
         const int tok = (t0 + i) * TILE + 32 * wq + lane;               // this lane's token
-        const bool cut = (t0 + i + 1) * (long long)TILE > L;            // the sequence ends in this tile
+        const bool cut = t0 + i == last;                                // the sequence ends in this tile
         const bool more = i + NWG < nt;
         // ---- logits of this token relative to the rows' references (both row blocks at once: one vote, and their chains
         // overlap; 32 sequences, 8 x 16 heads of 64, 61.2 -> 58.1 us)
@@ -421,9 +421,10 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           e[r + 1] = x[r + 1];
           sub2(e[r], e[r + 1], m[r], m[r + 1]);
         }
-        if (cut && tok >= L) {
+        if (cut) {                                     // (of the whole warp: no other tile pays for it)
+          const bool past = tok >= L;
 #pragma unroll
-          for (int r = 0; r < R; ++r) e[r] = -INFINITY;
+          for (int r = 0; r < R; ++r) e[r] = past ? -INFINITY : e[r];
         }
         float top = -INFINITY;
 #pragma unroll
