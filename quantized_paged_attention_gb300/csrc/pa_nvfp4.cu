@@ -6,7 +6,8 @@
 // Bound: the pages' bytes, 2 (D/2 + D/16) per (token, KV head).
 //
 // One persistent CTA per SM, the work (KV head and block of query rows, sequence, tile
-// of 128 tokens) in one list that is cut into equal ranges:
+// of 128 tokens) in one list that is cut into equal ranges, an item's beginning counted as
+// a few tiles:
 //  * 4 copy warps stream the tiles (K and V codes and scales, 18 KB with head_dim
 //    128) into a ring by cp.async, tokens past the end as zeros, and build the item's
 //    query operand.
@@ -80,6 +81,9 @@ struct Smem {
   static constexpr int KS_OFF = 2 * TILE * ROW;    // K scales as V's, then (MMA warp) [KS][token % 32][token / 32][4]
   static constexpr int VS_OFF = KS_OFF + KS * 512; // V scales [token][HD / 16]
   static constexpr int SLOT = VS_OFF + TILE * (HD / 16);
+  // An item's beginning (and the end before it) weighed in tiles when the work is cut. One of 131071 tokens, 4 x 16 heads of
+  // 128: 34.2 us with 0, 30.8 with 2 to 8; 64 ragged 116.8, 114.3 with 5; 32 sequences, 8 x 8 heads of 64, 43.8, 41.0 with 7 to 10.
+  static constexpr int BEGIN = HD == 64 ? 8 : 5;
   static constexpr int NSB = 2 * NWG;              // S buffers, two per group
   static constexpr int qBytes = PASSES * NQ * ROW;
   static constexpr int STG_ROW = HD;               // floats of a staged row
@@ -253,6 +257,7 @@ struct Cursor {
   int s, vh, L, T;
   long long off;      // work of the sequences before s
   int t;              // first tile of the item
+  int v;              // units of its beginning
 };
 
 }  // namespace d4
@@ -296,14 +301,19 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     fence_mbar_init();
   }
   if (warp == S::WARP_MMA) tmem_alloc(tmem_slot, S::TMEM_COLS);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // barriers and tensor memory are there: each role waits for it where it needs them (the copy warps with the first item's
+  // table entries and queries on their way)
+  auto all_set = [&]() {
+    tc_fence_before();
+    asm volatile("bar.sync 0;" ::: "memory");
+    tc_fence_after();
+  };
   const int Hq = Hk * p.qg;
 
   if (warp < NCW) {
     // ======================================================== consumer warps
+    all_set();
+    const uint32_t tmem = *tmem_slot;
     reg_inc<S::REG_CONSUMER>();
     const int wg = warp >> 2, wq = warp & 3;
     const int g = lane >> 2, c = lane & 3;
@@ -623,8 +633,9 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     const size_t chunk = size_t(bs) * (HD / 2 + HD / 16), plane = size_t(Hk) * chunk;
 
     // ---- the CTA's range of units, and the item that holds its first one
-    // work of a sequence of T tiles (32 sequences have at most 2^29 tiles)
-    auto work = [&](int T) -> int { return p.whole ? min(T, 1) : T; };
+    // work of a sequence of T tiles, its beginning counted as BEGIN of them (32 sequences: below 2^30)
+    constexpr int BEGIN = S::BEGIN;
+    auto work = [&](int T) -> int { return p.whole ? min(T, 1) : T > 0 ? T + BEGIN : 0; };
     long long W = 0;
     for (int s0 = 0; s0 < B; s0 += 32)
       W += __reduce_add_sync(0xffffffffu, (unsigned)work(tiles_of(s0 == 0 ? len0 : s0 + lane < B ? seq_len(s0 + lane) : 0)));
@@ -654,22 +665,25 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           c.L = __shfl_sync(0xffffffffu, L, src);
           c.T = __shfl_sync(0xffffffffu, T, src);
           c.off = off + __shfl_sync(0xffffffffu, incl, src) - work(c.T);
-          c.t = (int)(x - c.off);
+          const int in = (int)(x - c.off);
+          c.t = max(0, in - BEGIN);                 // (whole sequences: in is 0)
+          c.v = p.whole ? 0 : max(0, BEGIN - in);
           return c;
         }
         off += __shfl_sync(0xffffffffu, incl, 31);
       }
-      return Cursor{-1, 0, 0, 0, 0, 0};      // (not reached: x < W)
+      return Cursor{-1, 0, 0, 0, 0, 0, 0};   // (not reached: x < W)
     };
-    Cursor cur{-1, 0, 0, 0, 0, 0};
+    Cursor cur{-1, 0, 0, 0, 0, 0, 0};
     if (u < u1) {
       const long long vh = div_nonneg(u, W);
       cur = find(0, 0, u - vh * W);
       cur.vh = (int)vh;
+      if (u1 - u <= cur.v) cur.s = -1;              // (a beginning without a tile is the next range's)
     }
     // the item that begins at unit `at`, behind item c
     auto next = [&](const Cursor& c, long long at) -> Cursor {
-      if (at >= u1) return Cursor{-1, 0, 0, 0, 0, 0};
+      if (u1 - at <= (p.whole ? 0 : BEGIN)) return Cursor{-1, 0, 0, 0, 0, 0, 0};
       const long long off = c.off + work(c.T);
       Cursor n = off < W ? find(c.s + 1, off, off) : find(0, 0, 0);
       n.vh = off < W ? c.vh : c.vh + 1;
@@ -696,14 +710,15 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     uint4 qv[NT];
     load_q(cur, qv);
     int32_t ent0 = load_entries(cur.s, (int)(((long long)cur.t * TILE) >> lbs));
+    all_set();
     Turn tn(pw, S::NSG, NWG * S::CPG, pw / NWG, S::CPG);                // (a warp without a group only builds operands)
     const int wg = pw % NWG;
     int n = 0;
     int4 meta = make_int4(0, 0, 0, 0);
     bool ok = true;
     while (cur.s >= 0 && ok) {
-      const int te = p.whole ? cur.T : (int)min((long long)cur.T, cur.t + (u1 - u)), nt = te - cur.t;
-      const long long behind = u + work(nt);
+      const int te = p.whole ? cur.T : (int)min((long long)cur.T, cur.t + (u1 - u - cur.v)), nt = te - cur.t;
+      const long long behind = u + (p.whole ? 1 : cur.v + nt);
       const int part = cur.t > 0 ? 2 * (int)blockIdx.x : te < cur.T ? 2 * (int)blockIdx.x + 1 : -1;
       const int L = cur.L;
       const uint64_t kbase = reinterpret_cast<uint64_t>(p.kv) + size_t(cur.vh / RB) * chunk;
@@ -868,7 +883,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
       ++n;
       if (cur.t == 0 && te < cur.T) {
         // begins here and goes on: the pieces are this CTA's and those of the ranges up to the sequence's last unit
-        const long long last = u + cur.T - 1, head = rem * (per + 1);
+        const long long last = u + cur.v + cur.T - 1, head = rem * (per + 1);
         const long long cta = last < head ? div_nonneg(last, per + 1) : rem + div_nonneg(last - head, per);
         meta = make_int4((int)cta - (int)blockIdx.x + 1, cur.s, cur.vh, 0);
       }
@@ -893,6 +908,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     cp_async_wait_all();
   } else {
     // ======================================================== MMA warps, one per consumer group
+    all_set();
+    const uint32_t tmem = *tmem_slot;
     reg_dec<S::REG_MMA>();
     const int wg = warp - S::WARP_MMA;
     if (wg < NWG) {
@@ -981,7 +998,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
   __syncthreads();
   if (warp == S::WARP_MMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, S::TMEM_COLS);
+    tmem_dealloc(*tmem_slot, S::TMEM_COLS);
   }
 }
 
