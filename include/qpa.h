@@ -686,7 +686,8 @@ int kv_gather_fp8(const uint8_t* kv_cache, const int32_t* block_table, const int
  * ceil(L/block_size) are read; seq_lens int32 [num_seqs], clamped to
  * [0, max_blocks_per_seq*block_size]. workspace: pa_decode_nvfp4_workspace_size()
  * bytes, 256-byte aligned, no initialisation; calls that may overlap need a
- * workspace each.
+ * workspace each, but for those with max_blocks_per_seq*block_size up to 512, which
+ * do not touch it.
  * Supported: head_dim 64 or 128, query_group 1..64, block_size 16/32/64/128/256.
  * Alignment: q, kv_cache, out 16 bytes. out and workspace may overlap neither each
  * other nor an input (QPA_ERR_OVERLAP). Errors as pa_decode_fp8; an invalid block id

@@ -810,6 +810,7 @@ def nvfp4_desc(q, kv_cache, block_table, query_group, softmax_scale=None):
 
 
 _DECODE4_WORKSPACE = {}                # head_dim -> bytes
+_DECODE4_UNTOUCHED = {}                # (device, head_dim) -> a workspace for calls that do not touch theirs
 
 
 def pa_decode_nvfp4_workspace_size(desc: Nvfp4Desc) -> int:
@@ -841,12 +842,18 @@ def pa_decode_nvfp4(q, kv_cache, block_table, seq_lens, k_scale, v_scale, query_
     elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
         _fail("out must be contiguous bfloat16 of the shape of q")
     if workspace is None:
-        nbytes = _DECODE4_WORKSPACE.get(want.head_dim)
-        if nbytes is None:             # (depends on nothing else; 0: the call will be refused)
-            nbytes = max(pa_decode_nvfp4_workspace_size(want), 256)
-            if nbytes > 256:
-                _DECODE4_WORKSPACE[want.head_dim] = nbytes
-        workspace = _empty(nbytes, torch.uint8, q.device, stream)
+        # (4 us of a call's 20: tables of up to 512 tokens share one that no kernel touches)
+        key = (q.get_device(), want.head_dim) if want.max_blocks_per_seq * want.block_size <= 512 else None
+        workspace = _DECODE4_UNTOUCHED.get(key) if key is not None else None
+        if workspace is None:
+            nbytes = _DECODE4_WORKSPACE.get(want.head_dim)
+            if nbytes is None:         # (depends on nothing else; 0: the call will be refused)
+                nbytes = max(pa_decode_nvfp4_workspace_size(want), 256)
+                if nbytes > 256:
+                    _DECODE4_WORKSPACE[want.head_dim] = nbytes
+            workspace = _empty(nbytes, torch.uint8, q.device, stream)
+            if key is not None and nbytes > 256:
+                _DECODE4_UNTOUCHED[key] = workspace
     elif not workspace.is_contiguous():
         _fail("workspace must be contiguous")
     index = _device_of(q, kv_cache, block_table, seq_lens, k_scale, v_scale, out, workspace)

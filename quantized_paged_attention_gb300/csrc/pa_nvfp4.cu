@@ -35,8 +35,8 @@
 // slots per CTA: a range begins in at most one cut item and ends in another), and a
 // second kernel joins them in order. Where no sequence can have more than 4 tiles
 // (max_blocks_per_seq * block_size <= 512) the list is of whole sequences and the second
-// kernel is not launched: a call of four sequences of up to 200 tokens takes 20 us of wall clock
-// instead of 25, 9 us of a graph.
+// kernel is not launched: a call of four sequences of up to 200 tokens takes 15 us of wall clock,
+// 9 us of a graph (25 us with the second kernel and a workspace made for the call).
 #define QPA_WHOLE_UNIT
 #include "qpa.h"
 #include "common.cuh"
@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         arrive_if(lane == 0, &qfull[qb]);
       }
     }
-    if (pt == 0) p.meta[blockIdx.x] = meta;
+    if (pt == 0 && !p.whole) p.meta[blockIdx.x] = meta;
     cp_async_wait_all();
   } else {
     // ======================================================== MMA warps, one per consumer group

@@ -244,3 +244,15 @@ def test_every_value_read_back_with_many_scales(fp4):
         with np.errstate(invalid="ignore"):
             same_bf16(k, want)
     done()
+
+
+@pytest.mark.parametrize("D,G,bs,cols", [(128, 8, 16, 32), (64, 24, 256, 2), (128, 16, 64, 8)])
+def test_tables_of_512_tokens_leave_the_workspace_alone(D, G, bs, cols):
+    c = Case([bs * cols, 1, 130, 0], 2, G, D, bs)
+    table = t32(c.table[:, :cols])
+    d = qpa.nvfp4_desc(bf16_tensor(c.q, dev()), torch.from_numpy(c.cache).to(dev()), table, G)
+    ws = torch.full((qpa.pa_decode_nvfp4_workspace_size(d),), 0x5A, dtype=torch.uint8, device=dev())
+    outs = [c.run(table=table, workspace=ws), c.run(table=table), c.run(table=table)]
+    done()
+    assert bool((ws == 0x5A).all()) and torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    c.check(outs[0])
