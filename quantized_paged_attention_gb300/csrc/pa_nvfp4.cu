@@ -385,8 +385,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         for (int nb = 0; nb < NT; ++nb) tmem_ld_cols(tl + (2 * wg + (count & 1)) * NQ + 8 * CG * nb, v[nb]);
       };
       // S has come: its groups joined, times the rows' factors (v is free then). The product is rounded before the
-      // reference is taken off, as it is where the reference comes from: a fused one is off by more than 14, f16's
-      // room, from logits of 2^28 on.
+      // reference is taken off, as it is where the reference comes from: a fused one differs by up to half a step of the
+      // logit, which is f16's room and more where logits are large.
       auto join_terms = [&]() {
         tmem_wait_ld();
 #pragma unroll
@@ -450,7 +450,10 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
               // (a masked token does not count; NaN is ignored)
               const float best = warp_max(cut && tok >= L ? -INFINITY : x[8 * nb + r]);
               const float old = m[8 * nb + r];
-              const float now = best > old + kTop ? best - kBelow : old;
+              // (decided by the rounded difference that was voted on; one below best that rounds to more than kTop below, from
+              // 2^27 on, is best itself: p stays within f16)
+              const float below = best - kBelow;
+              const float now = best - old > kTop ? (best - below > kTop ? best : below) : old;
               const float alpha = ex2(old - now);
               m[8 * nb + r] = now;
               e[8 * nb + r] = cut && tok >= L ? -INFINITY : x[8 * nb + r] - now;
