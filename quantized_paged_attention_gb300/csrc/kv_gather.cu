@@ -32,9 +32,9 @@ constexpr int kMaxTile = 64;        // rows of a block
 enum : long long { kSkip = -1, kZero = -2 };
 
 // x * g cut to float32, the last bit set if bits were lost and `keep` is 1
-__device__ __forceinline__ uint32_t mul_sticky(float x, float g, uint32_t keep) {
+__device__ __forceinline__ float mul_sticky(float x, float g, uint32_t keep) {
   const float p = __fmul_rz(x, g);
-  return __float_as_uint(p) | min(__float_as_uint(fmaf(x, g, -p)), keep);
+  return __uint_as_float(__float_as_uint(p) | min(__float_as_uint(fmaf(x, g, -p)), keep));
 }
 // g such that x * g in float32 rounds to bf16 as the exact product does, for the x of at
 // most 6 bits that codes and group scales make; in every lane of a warp.
@@ -52,11 +52,6 @@ __device__ __forceinline__ uint32_t mul_bf16x2(float a, float b, float g) {
   uint32_t r;
   asm("{ .reg .b64 x, y; mov.b64 x, {%1, %2}; mov.b64 y, {%3, %3}; mul.rn.f32x2 x, x, y; .reg .f32 u, v; "
       "mov.b64 {u, v}, x; cvt.rn.bf16x2.f32 %0, v, u; }" : "=r"(r) : "f"(a), "f"(b), "f"(g));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf16x2(uint32_t lo, uint32_t hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(__uint_as_float(lo)), "f"(__uint_as_float(hi)));
   return r;
 }
 
@@ -187,9 +182,13 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const GatherLaunch 
         } else {
           uint32_t w[4];
           if (!FP4 && p.per_token) {
-            const uint32_t keep = fabsf(g[u]) < INFINITY ? 1u : 0u;            // (an infinite g loses no bits, and its residual is NaN)
+            // a small g is taken 2^64 times (a residual would lose its own bits below 2^-149); an infinite one loses no bits, and
+            // its residual is NaN
+            const bool small = fabsf(g[u]) < 8.67361738e-19f;                  // 2^-60
+            const float gs = small ? g[u] * 18446744073709551616.f : g[u], back = small ? 5.42101086e-20f : 1.f;
+            const uint32_t keep = fabsf(gs) < INFINITY ? 1u : 0u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = bf16x2(mul_sticky(x[2 * j], g[u], keep), mul_sticky(x[2 * j + 1], g[u], keep));
+            for (int j = 0; j < 4; ++j) w[j] = mul_bf16x2(mul_sticky(x[2 * j], gs, keep), mul_sticky(x[2 * j + 1], gs, keep), back);
           } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = mul_bf16x2(x[2 * j], x[2 * j + 1], g[u]);

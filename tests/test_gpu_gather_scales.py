@@ -64,3 +64,14 @@ def test_an_infinite_scale_reads_as_it_does_per_tensor():
             for x, y in zip(a, b):
                 assert torch.equal(torch.isnan(x), torch.isnan(y)) and torch.equal(torch.nan_to_num(x, nan=0.0), torch.nan_to_num(y, nan=0.0))
     done()
+
+
+def test_products_next_to_the_smallest_normal_number():
+    """Products a little above a midpoint of bf16 (7 bits behind the point, then 1, then zeros up to a last bit below 2^-149)
+    that are at least 2^-126."""
+    gs = []
+    for x in (1.125, 1.375, 1.625, 1.875, 9 * 2.0 ** -9, 15 * 2.0 ** -9, 7 * 2.0 ** -9):
+        for m in range(257, 512, 2):
+            g = np.float32(m * 2.0 ** -134 / x)
+            gs += [g, np.nextafter(g, np.float32(1))]
+    _check(np.array(gs, dtype=np.float32), lowest=2.0 ** -126)
