@@ -606,11 +606,12 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
             }
           }
           if (inf.w < 0) {
-            const float inv = vscale / l;
+            // (v_scale last: v_scale / l may lie in float32's subnormals where the result does not)
+            const float inv = 1.f / l;
             __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) +
                                  ((long long)who.x * Hq + (long long)kvh * p.qg + rbase + row) * HD + (HD / 32) * lane;
-            if constexpr (HD == 128) store4(dst, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-            else *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
+            if constexpr (HD == 128) store4(dst, acc[0] * inv * vscale, acc[1] * inv * vscale, acc[2] * inv * vscale, acc[3] * inv * vscale);
+            else *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(acc[0] * inv * vscale, acc[1] * inv * vscale);
           } else {
             float* dst = p.part_o + ((long long)inf.w * 16 + row) * HD + (HD / 32) * lane;
             if constexpr (HD == 128) store4(dst, acc[0], acc[1], acc[2], acc[3]);
@@ -1079,7 +1080,7 @@ __global__ void __launch_bounds__(32 * d4::COMBINE_WARPS) decode4_combine_kernel
       den = fmaf(f, s_l[w], den);
     }
     const long long row = (long long)meta.y * p.num_kv_heads * p.qg + (meta.z / p.row_blocks) * p.qg + rbase + r;
-    reinterpret_cast<__nv_bfloat16*>(p.out)[row * HD + threadIdx.x] = __float2bfloat16_rn(num * (vscale / den));
+    reinterpret_cast<__nv_bfloat16*>(p.out)[row * HD + threadIdx.x] = __float2bfloat16_rn(num / den * vscale);
   }
 }
 
