@@ -38,6 +38,8 @@
 // kernel is not launched: a call of four sequences of up to 200 tokens takes 15 us of wall clock,
 // 9 us of a graph (25 us with the second kernel and a workspace made for the call).
 #define QPA_WHOLE_UNIT
+#include <cmath>
+
 #include "qpa.h"
 #include "common.cuh"
 #include "qpa_internal.h"
@@ -129,7 +131,8 @@ struct Params {
   long long q_stride_seq, q_stride_head, table_stride;
   int num_seqs, num_kv_heads, qg, row_blocks, block_size, log2_bs, num_blocks, max_blocks;
   int whole;                        // a unit of work is a sequence, not a tile: no item is cut
-  float softmax_scale;
+  float softmax_mant;               // softmax_scale = softmax_mant 2^softmax_exp
+  int softmax_exp;
 };
 
 // kind::mxf4nvf4 instruction descriptor: e2m1 operands, K-major, unsigned e4m3 scales
@@ -223,6 +226,15 @@ __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
   uint32_t r;
   asm("{ .reg .b8 t; cvt.rn.satfinite.e2m1x2.f32 t, %2, %1; cvt.u32.u8 %0, t; }" : "=r"(r) : "f"(lo), "f"(hi));
   return r;
+}
+
+// x = m 2^e with 1 <= |m| < 2: m, and e added to `exponent`; 0, infinities and NaN as they are
+__device__ __forceinline__ float mantissa(float x, int& exponent) {
+  const bool small = fabsf(x) < 1.17549435e-38f;                        // 2^-126
+  const uint32_t b = __float_as_uint(small ? x * 16777216.f : x), e = (b >> 23) & 255u;
+  if (e == 0 || e == 255u) return x;
+  exponent += (int)e - 127 - (small ? 24 : 0);
+  return __uint_as_float((b & 0x807fffffu) | 0x3f800000u);
 }
 
 // A taker's tiles, every `of`-th of the CTA's: the ring slot (of the group's ns, every by-th) and
@@ -710,7 +722,11 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
     auto load_entries = [&](int s, int e0) -> int32_t {
       return s >= 0 && e0 + lane < p.max_blocks ? __ldg(p.block_table + (long long)s * p.table_stride + e0 + lane) : 0;
     };
-    const float base = kscale * p.softmax_scale * kLog2e;
+    // the logits' factor, its power of two apart: k_scale and the softmax's scale may leave float32's range together where the
+    // logits do not
+    int base_exp = 0;
+    const float base = mantissa(kscale, base_exp) * p.softmax_mant * kLog2e;
+    base_exp += p.softmax_exp;
     uint4 qv[NT];
     load_q(cur, qv);
     int32_t ent0 = load_entries(cur.s, (int)(((long long)cur.t * TILE) >> lbs));
@@ -828,7 +844,8 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
         int er = eb;
 #pragma unroll
         for (int sh = 2; sh < 16; sh <<= 1) er = max(er, __shfl_xor_sync(0xffffffffu, er, sh));
-        if (er == -200) er = 0;
+        const bool zero = er == -200;
+        if (zero) er = 0;
         const int rel = max(eb - er, -17 + 3 * (PASSES - 1));           // scales 2^8 .. 2^-9, those of the last pass too
         // x 2^-(er + rel), in two factors that are floats
         const int sh = -(er + rel), s1 = max(-126, min(126, sh)), s2 = sh - s1;
@@ -870,10 +887,10 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           }
         }
         if (h16 == 0) {
-          // the row's factor takes 2^(er - 8)
-          const int a = er - 8, a1 = max(-126, min(126, a)), a2 = a - a1;
+          // the row's factor takes 2^(er - 8) (past 2^+-252 it is 0 or infinite in any case); of a row of zeros it is 0
+          const int a = er - 8 + base_exp, a1 = max(-126, min(126, a)), a2 = max(-126, min(126, a - a1));
           const float f = base * __uint_as_float(uint32_t(127 + a1) << 23) * __uint_as_float(uint32_t(127 + a2) << 23);
-          const bool used = 16 * (cur.vh % RB) + qrow + 8 * h < p.qg;
+          const bool used = !zero && 16 * (cur.vh % RB) + qrow + 8 * h < p.qg;
           stsf(sb + S::cOff + 4 * (qb * R + 8 * h + qrow), !row_ok ? __int_as_float(0x7fffffff) : used ? f : 0.f);
         }
       }
@@ -1133,7 +1150,8 @@ cudaError_t launch_decode4(const Decode4Launch& a, cudaStream_t stream) {
   while ((1 << p.log2_bs) < a.block_size) ++p.log2_bs;
   p.num_blocks = a.num_blocks;
   p.max_blocks = a.max_blocks;
-  p.softmax_scale = a.softmax_scale;
+  p.softmax_mant = std::frexp(a.softmax_scale, &p.softmax_exp);
+  if (!std::isfinite(a.softmax_scale)) p.softmax_exp = 0;
   // no more CTAs than units there can be
   const long long tiles = ((long long)a.max_blocks * a.block_size + d4::TILE - 1) / d4::TILE;
   p.whole = tiles <= 4;
