@@ -52,7 +52,7 @@ constexpr int TILE = 128;           // tokens per tile
 constexpr int QT = 6;               // e2m1 terms of a query
 constexpr int MAX_CTAS = 160;
 constexpr int COMBINE_WARPS = 4;
-constexpr float kNoMax = -3e38f;    // no token seen yet: finite, so that differences stay defined, and below any logit
+constexpr float kNoMax = -3.40282347e38f;   // no token seen yet: the lowest float, so that no logit is below it
 constexpr float kBelow = 8.f;       // the reference is set this far below the largest logit (p up to 2^8)
 constexpr float kTop = 14.f;        // and moves when a logit is this far above it (p up to 2^14 in f16)
 

@@ -78,3 +78,12 @@ def test_logits_a_few_steps_apart_in_different_tiles(D, G):
         q[:, :, 16] = x * 2.0 ** -6
         out = _decode(q, cache, table, [key1.size] * B, G)
         assert np.all(np.abs(out - 3.0) <= 3.0 * (2.0 ** -8 + 2.0 ** -18)), np.isnan(out).sum()
+
+
+@pytest.mark.parametrize("x", [-3.05e38, -3.3e38, 3.05e38, 3.3e38])
+def test_logits_next_to_the_largest_float(x):
+    q = np.zeros((2, 4, 64))
+    q[:, :, 0] = x
+    cache, table = _pages(300, 64, np.zeros(300, dtype=np.uint8), np.full(300, 5, dtype=np.uint8))
+    out = _decode(q, cache, table, [300, 7], 4)
+    assert np.all(np.abs(out - 3.0) <= 3.0 * (2.0 ** -8 + 2.0 ** -18)), out
