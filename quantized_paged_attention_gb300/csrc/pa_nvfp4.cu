@@ -42,6 +42,7 @@
 
 #include "qpa.h"
 #include "common.cuh"
+#include "kept_answer.h"
 #include "qpa_internal.h"
 #include "tc.cuh"
 
@@ -1116,11 +1117,17 @@ template <int NT, int HD>
 static cudaError_t launch_decode4_t(const d4::Params& p, int grid, cudaStream_t stream) {
   using S = d4::Smem<NT, HD>;
   // the roles' register budgets draw on what the kernel is launched with: built with less, it would wait for ever
-  static const bool built = [] {
+  static std::atomic<int> kept{0};
+  int registers;
+  const cudaError_t e = kept_answer(kept, [](int* n) {
     cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, decode4_kernel<NT, HD>) == cudaSuccess && f.numRegs == S::REG_LAUNCH;
-  }();
-  if (!built) return cudaErrorInvalidConfiguration;
+    const cudaError_t st = cudaFuncGetAttributes(&f, decode4_kernel<NT, HD>);
+    *n = st == cudaSuccess ? f.numRegs : 0;
+    if (st != cudaSuccess) cudaGetLastError();            // (returned here; nobody else's)
+    return st;
+  }, registers);
+  if (e != cudaSuccess) return e;
+  if (registers != S::REG_LAUNCH) return cudaErrorInvalidConfiguration;
   cudaFuncSetAttribute(decode4_kernel<NT, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::total);
   decode4_kernel<NT, HD><<<grid, S::THREADS, S::total, stream>>>(p);
   return cudaGetLastError();
