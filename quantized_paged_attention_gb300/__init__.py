@@ -508,6 +508,12 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _capturing(device, stream):
+    """Whether _empty's memory on `stream` comes from a graph under capture (and has to go with it)."""
+    with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _device_of(*ts):
     """Index of the CUDA device that holds every tensor."""
     index = ts[0].get_device()
@@ -852,7 +858,7 @@ def pa_decode_nvfp4(q, kv_cache, block_table, seq_lens, k_scale, v_scale, query_
                 if nbytes > 256:
                     _DECODE4_WORKSPACE[want.head_dim] = nbytes
             workspace = _empty(nbytes, torch.uint8, q.device, stream)
-            if key is not None and nbytes > 256:
+            if key is not None and nbytes > 256 and q.is_cuda and not _capturing(q.device, stream):
                 _DECODE4_UNTOUCHED[key] = workspace
     elif not workspace.is_contiguous():
         _fail("workspace must be contiguous")
