@@ -700,6 +700,7 @@ def kv_append_nvfp4(k, v, kv_cache, slots, k_scale, v_scale, stream=None):
     T = slots.numel()
     if slots.dtype != torch.int64 or not slots.is_contiguous():
         _fail("slots must be contiguous int64")
+    _below_2_31(T, Hk, NB, bs, D)
     if (planes == 2) != (v is not None) or (v is None) != (v_scale is None):
         _fail("v and v_scale go with a cache of two planes, and only with one")
     if k.dtype != torch.bfloat16 or tuple(k.shape) != (T, Hk, D) or (T and k.stride(2) != 1):
@@ -714,7 +715,6 @@ def kv_append_nvfp4(k, v, kv_cache, slots, k_scale, v_scale, stream=None):
     else:
         index = _device_of(k, kv_cache, slots, k_scale)
         vp = vsp = vt = vh = 0
-    _below_2_31(T, Hk, NB)
     d = Append4Desc(T, Hk, D, bs, NB, planes, _dim_stride(k, 0), _dim_stride(k, 1), vt, vh)
     _launch("kv_append_nvfp4", index, stream, k.data_ptr(), vp, kv_cache.data_ptr(), slots.data_ptr(),
             k_scale.data_ptr(), vsp, ctypes.byref(d))
@@ -739,7 +739,7 @@ def _gather(fn, shape, per_token, kv_cache, block_table, query_start, seq_lens, 
         _fail("query_start must be contiguous int32 with one entry more than requests, seq_lens with one per request")
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         _fail("out_dtype must be bfloat16 or float32")
-    _below_2_31(num_tokens, NB, Hk)
+    _below_2_31(num_tokens, R, NB, Hk, bs, D)
     rows = (num_tokens, Hk, D)
     for o in (out_k, out_v):
         if o is not None and (o.dtype != out_dtype or tuple(o.shape) != rows or not o.is_contiguous()):
@@ -804,8 +804,8 @@ def nvfp4_desc(q, kv_cache, block_table, query_group, softmax_scale=None):
     maxb, stride = _rows(block_table)
     if block_table.shape[0] != B:
         _fail("block_table must have one row per sequence")
-    if not (B < 1 << 31 and NB < 1 << 31 and Hk < 1 << 31 and 0 <= query_group < 1 << 31):
-        _below_2_31(B, NB, Hk, query_group)
+    if not (B < 1 << 31 and NB < 1 << 31 and Hk < 1 << 31 and bs < 1 << 31 and D < 1 << 31 and 0 <= query_group < 1 << 31):
+        _below_2_31(B, NB, Hk, bs, D, query_group)
     if q.is_contiguous():
         return Nvfp4Desc(B, Hk, query_group, D, bs, NB, maxb, 0.0 if softmax_scale is None else float(softmax_scale),
                          0, 0, stride)
