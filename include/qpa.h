@@ -588,6 +588,8 @@ int pa_chunk_fp8(const void* q, const uint8_t* kv_cache, const int32_t* block_ta
  * dim 2i in the low nibble of byte i), then block_size * head_dim/16 e4m3fn
  * scales (head_dim/16 per token, one per 16 dims). A value is
  *     e2m1(code) * e4m3(scale) * g,    g = k_scale[0] or v_scale[0] (float, device).
+ * Scale bytes are 0x00 to 0x7F (0x7F: NaN), as kv_append_nvfp4 writes them. One with the
+ * sign bit set is outside the format: the decode takes K's scales as unsigned.
  * With head_dim 128, block_size 128, one plane and one head a chunk is a page of
  * nvfp4_index_score (which knows no g: append with k_scale = 1).
  * ====================================================================== */
@@ -678,17 +680,30 @@ int kv_gather_fp8(const uint8_t* kv_cache, const int32_t* block_table, const int
  * with k_t and v_t the values of the 4-bit cache (planes = 2). L = 0 gives 0.
  * Codes and scales of tokens past L have no influence, NaN scales included; a NaN
  * scale of a token that is seen makes the rows of its sequence and head NaN (a V
- * scale: the 16 dims of its group).
+ * scale: the 16 dims of its group). A query row that is not finite is NaN.
+ *
+ * Precision: K enters the tensor core as it is, V times its group scales exactly in f16.
+ * A query enters as 6 e2m1 terms of 3 bits each with a power of two per 16 dims: exact
+ * for elements down to 2^-9 of their 16 dims' largest |q|, within 2^-17 of that below,
+ * and within 2^-31 of the row's largest where 16 dims are far smaller than the row. The
+ * probabilities enter as f16: 11 bits down to 2^-22 of the row's largest, within 2^-33 of
+ * it below (keys and values of normal distribution: results are 2e-4 off for it, their
+ * rounding to bf16 1.6e-3). Sums and softmax statistics are float32, and a logit is off
+ * by up to 2^-21 of itself: the weights of tokens whose logits are nearer than that to
+ * each other are that uncertain. Logits past float32's range give NaN. The output is bf16
+ * only: probabilities of 11 bits would leave the rest of a float32 output without
+ * meaning.
  *
  * Layouts: q bf16 [num_seqs][num_kv_heads*query_group][head_dim] with the
  * descriptor's strides (elements, multiples of 8); out bf16, contiguous;
- * block_table int32, row s at s * table_stride elements, only entries below
- * ceil(L/block_size) are read; seq_lens int32 [num_seqs], clamped to
+ * block_table int32, row s at s * table_stride elements, entries from
+ * ceil(L/block_size) on have no influence; seq_lens int32 [num_seqs], clamped to
  * [0, max_blocks_per_seq*block_size]. workspace: pa_decode_nvfp4_workspace_size()
  * bytes, 256-byte aligned, no initialisation; calls that may overlap need a
  * workspace each, but for those with max_blocks_per_seq*block_size up to 512, which
  * do not touch it.
- * Supported: head_dim 64 or 128, query_group 1..64, block_size 16/32/64/128/256.
+ * Supported: head_dim 64 or 128, query_group 1..64 (the pages are read once per 16 of
+ * it), block_size 16/32/64/128/256.
  * Alignment: q, kv_cache, out 16 bytes. out and workspace may overlap neither each
  * other nor an input (QPA_ERR_OVERLAP). Errors as pa_decode_fp8; an invalid block id
  * reads block 0 and raises error word 3.

@@ -3,7 +3,10 @@
 // Mathematics: out = sum_t p_t v_t / sum_t p_t, p_t = 2^(c s_t - m) with s_t the dot
 // product, c the logits' factor in base 2 and m a running reference per row.
 //
-// Bound: the pages' bytes, 2 (D/2 + D/16) per (token, KV head).
+// Bound: the pages' bytes, 2 (D/2 + D/16) per (token, KV head), once per block of 16 query
+// rows (16 x 16384 tokens, 8 heads of 128: 59 us with 8 rows, 76 with 16, 137 with 32 in two
+// passes) and, with more than 8 rows or heads of 64, the instructions of the softmax and of V's
+// conversion.
 //
 // One persistent CTA per SM, the work (KV head and block of query rows, sequence, tile
 // of 128 tokens) in one list that is cut into equal ranges, an item's beginning counted as
@@ -30,13 +33,16 @@
 //    The sum of p is one more row of V, of ones.
 //  * The reference m is put 8 below the largest logit (in base 2) and moves only when one
 //    exceeds it by 14: f16 holds 11 bits of p down to 2^-22 of the largest, and the common
-//    path has no exchange of maxima and no rescaling.
+//    path has no exchange of maxima and no rescaling. (p in f16 is a choice: a result is 2e-4 off
+//    for it, its own rounding to bf16 1.6e-3; a second term of p would double V's products.)
 // An item that its range does not cut is written out; pieces go to the workspace (two
 // slots per CTA: a range begins in at most one cut item and ends in another), and a
 // second kernel joins them in order. Where no sequence can have more than 4 tiles
 // (max_blocks_per_seq * block_size <= 512) the list is of whole sequences and the second
-// kernel is not launched: a call of four sequences of up to 200 tokens takes 15 us of wall clock,
-// 9 us of a graph (25 us with the second kernel and a workspace made for the call).
+// kernel is not launched (whole against cut, graphs in a row, heads of 128: four of up to 200
+// tokens, 2 x 4 heads, 6.9 against 8.7 us; four of 512 8.2, 9.3; 64 of 512, 8 x 8 heads, 22.0, 26.7; but
+// four of 1024 10.0, 9.4; 64 of up to 1024 32.1, 30.7). Wall clock of a call from Python, four of up to
+// 200 tokens: 17 to 21 us; with a table of 512 columns 22 to 24.
 #define QPA_WHOLE_UNIT
 #include <cmath>
 
