@@ -5,8 +5,8 @@
 //
 // Bound: the pages' bytes, 2 (D/2 + D/16) per (token, KV head), once per block of 16 query
 // rows (16 x 16384 tokens, 8 heads of 128: 59 us with 8 rows, 76 with 16, 137 with 32 in two
-// passes) and, with more than 8 rows or heads of 64, the instructions of the softmax and of V's
-// conversion.
+// passes) and, with more than 8 rows or heads of 64, the chains (S, softmax, V's conversion and
+// products) of as many warps as registers allow.
 //
 // One persistent CTA per SM, the work (KV head and block of query rows, sequence, tile
 // of 128 tokens) in one list that is cut into equal ranges, an item's beginning counted as
