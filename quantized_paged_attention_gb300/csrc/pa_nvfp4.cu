@@ -894,10 +894,11 @@ __global__ void __launch_bounds__(d4::Smem<NT, HD>::THREADS, 1) decode4_kernel(c
           }
         }
         if (h16 == 0) {
-          // the row's factor takes 2^(er - 8) (past 2^+-252 it is 0 or infinite in any case); of a row of zeros it is 0
+          // the row's factor takes 2^(er - 8) (past 2^+-252 it is 0 or infinite in any case); of a row of zeros it is 0, or NaN
+          // where the scales are not finite
           const int a = er - 8 + base_exp, a1 = max(-126, min(126, a)), a2 = max(-126, min(126, a - a1));
-          const float f = base * __uint_as_float(uint32_t(127 + a1) << 23) * __uint_as_float(uint32_t(127 + a2) << 23);
-          const bool used = !zero && 16 * (cur.vh % RB) + qrow + 8 * h < p.qg;
+          const float f = base * (zero ? 0.f : __uint_as_float(uint32_t(127 + a1) << 23)) * __uint_as_float(uint32_t(127 + a2) << 23);
+          const bool used = 16 * (cur.vh % RB) + qrow + 8 * h < p.qg;
           stsf(sb + S::cOff + 4 * (qb * R + 8 * h + qrow), !row_ok ? __int_as_float(0x7fffffff) : used ? f : 0.f);
         }
       }

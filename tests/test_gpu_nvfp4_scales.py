@@ -63,3 +63,17 @@ def test_key_and_softmax_scales(k_scale, scale, size, group_scale):
     tol = 2.0 ** -8 * np.abs(want) + bound * (2 * 2.0 ** -11 + 2 * np.expm1(2.0 ** -21 * np.abs(x).max(axis=1))[:, None] + 2.0 ** -18)
     tol += 2.0 ** -33 * (np.abs(V).sum(axis=0) + 7 * np.abs(want))
     assert np.all(np.abs(got - want) <= tol), (np.abs(got - want) / tol).max()
+
+
+@pytest.mark.parametrize("k_scale,scale", [(np.nan, 0.1), (np.inf, 0.1), (-np.inf, 0.1), (1.0, np.nan), (1.0, np.inf)])
+def test_scales_that_are_not_finite(k_scale, scale):
+    """Logits are NaN or infinite: every row is NaN, that of a query of zeros (0 times infinity) too."""
+    r = synth.rng(4)
+    cache = rand_cache(r, 4, 1, 16, 64, smax=60)
+    q = r.standard_normal((2, 3, 64))
+    q[:, 1] = 0.0
+    out = qpa.pa_decode_nvfp4(bf16_tensor(synth.round_to_bf16_bits(q), dev()),
+                              torch.from_numpy(cache).to(dev()), t32([[1, 2], [3, 0]]), t32([32, 9]),
+                              f32(k_scale), f32(1.0), 3, softmax_scale=scale)
+    done()
+    assert bool(torch.isnan(out).all())
